@@ -3,61 +3,26 @@
 // Everything here runs on the host, allocates nothing and never synchronises.
 // Argument errors return before any CUDA call is made.
 #include <stdint.h>
-#include <string.h>
 
 #include <algorithm>
 #include <cmath>
 #include <mutex>
 
+#include "kda_host.cuh"
 #include "kda_internal.cuh"
 
-using kda::segment_shape;
-#include <nvtx3/nvToolsExt.h>
+thread_local char kda::g_last_error[256] = "";
 
 namespace {
 
-thread_local char g_last_error[256] = "";
-
-void set_last_error(const char* msg) {
-    strncpy(g_last_error, msg, sizeof(g_last_error) - 1);
-    g_last_error[sizeof(g_last_error) - 1] = '\0';
-}
-
-// An NVTX range around each entry point (named after it), so a timeline
-// profiler shows every library call; free when no tool is attached.
-struct NvtxRange {
-    explicit NvtxRange(const char* name) { nvtxRangePushA(name); }
-    ~NvtxRange() { nvtxRangePop(); }
-    NvtxRange(const NvtxRange&) = delete;
-    NvtxRange& operator=(const NvtxRange&) = delete;
-};
-
-bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
-bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
-
-// [p, p + n) and [q, q + m) overlap (both non-empty)?
-bool overlaps(const void* p, size_t n, const void* q, size_t m) {
-    if (!p || !q || n == 0 || m == 0) return false;
-    uintptr_t a = reinterpret_cast<uintptr_t>(p), b = reinterpret_cast<uintptr_t>(q);
-    return a < b + m && b < a + n;
-}
-
-// n = a * b * c * d with overflow detection (all factors >= 0).
-bool mul_ok(size_t* out, size_t a, size_t b, size_t c = 1, size_t d = 1) {
-    const size_t lim = (size_t)1 << 62;
-    size_t r = a;
-    for (size_t f : {b, c, d}) {
-        if (f != 0 && r > lim / f) return false;
-        r *= f;
-    }
-    *out = r;
-    return true;
-}
-
-kda_status_t fail(kda_status_t s, const char* why) {
-    set_last_error(why);
-    return s;
-}
+using kda::aligned16;
+using kda::aligned4;
+using kda::fail;
+using kda::mul_ok;
+using kda::NvtxRange;
+using kda::overlaps;
+using kda::segment_shape;
+using kda::set_last_error;
 
 kda_status_t check_dims(int dk, int dv, kda_dtype_t io) {
     if (dk <= 0 || dv <= 0) return fail(KDA_ERR_INVALID_ARG, "dk and dv must be positive");
@@ -87,7 +52,7 @@ const char* kda_status_string(kda_status_t s) {
     return "KDA_ERR_UNKNOWN";
 }
 
-const char* kda_last_error_string(void) { return g_last_error; }
+const char* kda_last_error_string(void) { return kda::g_last_error; }
 
 size_t kda_chunk_fwd_workspace_size(int B, int T, int H, int dk, int dv, kda_dtype_t io) {
     if (B < 0 || T < 0 || H < 0) return (size_t)-1;

@@ -1,0 +1,267 @@
+// Softmax attention on the CUDA cores, with every product and sum in 32 bits.
+//
+//     x_ij = scale q_i . k_j (j <= position of i),  m_i = max_j x_ij,
+//     l_i = sum_j e^{x_ij - m_i},  o_i = sum_j e^{x_ij - m_i} v_j / l_i
+//
+// in one pass over the keys: when a key tile raises m_i, the sums so far are
+// multiplied by e^{m_old - m_new}. A CTA of 256 threads holds 64 rows and takes
+// 64 keys at a time through shared memory; thread (y, x) computes rows
+// 4y .. 4y + 3 against keys x + 16 i, and the same rows of the output.
+// Bound by the FFMA pipe: 8 shared-memory loads of 16 bytes feed 64 FFMA in the
+// first product and 12 feed 128 in the second.
+#include "kda_attn.cuh"
+
+namespace kda {
+namespace {
+
+constexpr int kRows = 64, kKeys = 64, kThreadsSimt = 256;
+
+struct SimtParams {
+    AttnShape s;
+    const void* q;
+    const void* k;
+    const void* v;
+    const int* block_table;
+    void* o;
+    float* lse;
+    long long q_stride, k_stride, v_stride;
+    int num_pages, page, max_pages;
+    float scale;
+    int* d_status;
+};
+
+template <int D>
+constexpr size_t simt_smem() {
+    return (size_t)3 * kRows * (D + 4) * 4;
+}
+
+template <typename T>
+__device__ __forceinline__ float4 load4(const T* p);
+template <>
+__device__ __forceinline__ float4 load4<float>(const float* p) {
+    return *reinterpret_cast<const float4*>(p);
+}
+template <>
+__device__ __forceinline__ float4 load4<__nv_bfloat16>(const __nv_bfloat16* p) {
+    const uint2 w = *reinterpret_cast<const uint2*>(p);
+    return make_float4(__uint_as_float(w.x << 16), __uint_as_float(w.x & 0xffff0000u),
+                       __uint_as_float(w.y << 16), __uint_as_float(w.y & 0xffff0000u));
+}
+__device__ __forceinline__ void store4(float* p, float4 x) { *reinterpret_cast<float4*>(p) = x; }
+__device__ __forceinline__ void store4(__nv_bfloat16* p, float4 x) {
+    __nv_bfloat162 a = __floats2bfloat162_rn(x.x, x.y), b = __floats2bfloat162_rn(x.z, x.w);
+    *reinterpret_cast<uint2*>(p) =
+        make_uint2(*reinterpret_cast<uint32_t*>(&a), *reinterpret_cast<uint32_t*>(&b));
+}
+
+template <typename T, int D>
+__global__ void __launch_bounds__(kThreadsSimt, 2) kda_attn_simt_kernel(const SimtParams p) {
+    constexpr int LD = D + 4, LP = kKeys + 4, C4 = D / 64;  // C4: float4 columns per thread
+    extern __shared__ __align__(16) float sm[];
+    float* sq = sm;
+    float* sk = sq + kRows * LD;  // also the probabilities, once the scores are done
+    float* sv = sk + kKeys * LD;
+    float* sp = sk;
+
+    pdl_wait();
+    const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
+    const AttnShape& s = p.s;
+    const T* gq = static_cast<const T*>(p.q);
+    const T* gk = static_cast<const T*>(p.k);
+    const T* gv = static_cast<const T*>(p.v);
+    T* go = static_cast<T*>(p.o);
+    int flags = 0;
+    AttnWalk walk;
+    AttnItem it;
+    for (long long idx = blockIdx.x; attn_find_item(s, walk, idx, &it); idx += gridDim.x) {
+        const int G = s.G, tok0 = it.t * it.q.tok;
+        const int rows = min(it.q.tok, it.q.q_len - tok0) * G;
+        const int keys = attn_item_keys(it.q, it.t);
+        const size_t first = (size_t)it.q.q0 + tok0;  // packed token of row 0
+        __syncthreads();
+        for (int i = tid; i < kRows * (D / 4); i += kThreadsSimt) {
+            const int r = i / (D / 4), c = (i % (D / 4)) * 4;
+            float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (r < rows)
+                x = load4(gq + (first + r / G) * p.q_stride + (size_t)(it.h * G + r % G) * D + c);
+            *reinterpret_cast<float4*>(sq + r * LD + c) = x;
+        }
+        // Keys that each of this thread's rows sees.
+        int lim[4];
+        float m[4], l[4], acc[4][C4 * 4];
+#pragma unroll
+        for (int i = 0; i < 4; i++) {
+            const int r = ty * 4 + i;
+            lim[i] = r < rows ? max(it.q.kv - it.q.q_len + tok0 + r / G + 1, 0) : 0;
+            m[i] = -INFINITY;
+            l[i] = 0.f;
+#pragma unroll
+            for (int c = 0; c < C4 * 4; c++) acc[i][c] = 0.f;
+        }
+        const int seen_by_all = max(it.q.kv - it.q.q_len + tok0 + 1, 0);
+        for (int k0 = 0; k0 < keys; k0 += kKeys) {
+            __syncthreads();  // the tile before is read
+            for (int i = tid; i < kKeys * (D / 4); i += kThreadsSimt) {
+                const int j = i / (D / 4), c = (i % (D / 4)) * 4, at = k0 + j;
+                float4 xk = make_float4(0.f, 0.f, 0.f, 0.f), xv = xk;
+                if (at < keys) {
+                    if (p.block_table) {
+                        const int id = p.block_table[(size_t)it.r * p.max_pages + at / p.page];
+                        if (id >= 0 && id < p.num_pages) {
+                            const size_t row = ((size_t)id * s.Hkv + it.h) * p.page + at % p.page;
+                            xk = load4(gk + row * D + c);
+                            xv = load4(gv + row * D + c);
+                        } else {
+                            flags |= KDA_DEV_PAGES;
+                        }
+                    } else {
+                        const size_t row = (size_t)it.q.q0 + at;
+                        xk = load4(gk + row * p.k_stride + (size_t)it.h * D + c);
+                        xv = load4(gv + row * p.v_stride + (size_t)it.h * D + c);
+                    }
+                }
+                *reinterpret_cast<float4*>(sk + j * LD + c) = xk;
+                *reinterpret_cast<float4*>(sv + j * LD + c) = xv;
+            }
+            __syncthreads();
+            float x[4][4] = {};
+#pragma unroll 4
+            for (int c = 0; c < D; c += 4) {
+                float4 a[4], b[4];
+#pragma unroll
+                for (int i = 0; i < 4; i++)
+                    a[i] = *reinterpret_cast<const float4*>(sq + (ty * 4 + i) * LD + c);
+#pragma unroll
+                for (int i = 0; i < 4; i++)
+                    b[i] = *reinterpret_cast<const float4*>(sk + (tx + 16 * i) * LD + c);
+#pragma unroll
+                for (int i = 0; i < 4; i++)
+#pragma unroll
+                    for (int j = 0; j < 4; j++) {
+                        x[i][j] = fmaf(a[i].x, b[j].x, x[i][j]);
+                        x[i][j] = fmaf(a[i].y, b[j].y, x[i][j]);
+                        x[i][j] = fmaf(a[i].z, b[j].z, x[i][j]);
+                        x[i][j] = fmaf(a[i].w, b[j].w, x[i][j]);
+                    }
+            }
+            __syncthreads();  // sk becomes sp
+#pragma unroll
+            for (int i = 0; i < 4; i++) {
+                float mx = -INFINITY;
+#pragma unroll
+                for (int j = 0; j < 4; j++) {
+                    x[i][j] = k0 + tx + 16 * j < lim[i] ? x[i][j] * p.scale : -INFINITY;
+                    mx = fmaxf(mx, x[i][j]);
+                }
+#pragma unroll
+                for (int o = 8; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+                const float mn = fmaxf(m[i], mx);
+                const float ref = mn == -INFINITY ? 0.f : mn;  // a row that sees nothing yet
+                const float corr = expf(m[i] - ref);
+                m[i] = mn;
+                float sum = 0.f;
+#pragma unroll
+                for (int j = 0; j < 4; j++) {
+                    const float e = expf(x[i][j] - ref);
+                    sum += e;
+                    sp[(ty * 4 + i) * LP + tx + 16 * j] = e;
+                }
+#pragma unroll
+                for (int o = 8; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+                l[i] = l[i] * corr + sum;
+#pragma unroll
+                for (int c = 0; c < C4 * 4; c++) acc[i][c] *= corr;
+            }
+            __syncthreads();
+            // Rows may see only part of this tile: a weight of zero then adds
+            // nothing, whatever the value beside it holds.
+            const bool edge = k0 + kKeys > seen_by_all;
+            auto add = [&](bool guard) {
+#pragma unroll 2
+                for (int j = 0; j < kKeys; j += 4) {
+                    float4 e[4];
+#pragma unroll
+                    for (int i = 0; i < 4; i++)
+                        e[i] = *reinterpret_cast<const float4*>(sp + (ty * 4 + i) * LP + j);
+#pragma unroll
+                    for (int jj = 0; jj < 4; jj++)
+#pragma unroll
+                        for (int c = 0; c < C4; c++) {
+                            const float4 b = *reinterpret_cast<const float4*>(
+                                sv + (j + jj) * LD + tx * 4 + 64 * c);
+#pragma unroll
+                            for (int i = 0; i < 4; i++) {
+                                const float w = jj == 0 ? e[i].x : jj == 1 ? e[i].y : jj == 2 ? e[i].z : e[i].w;
+                                if (guard && w == 0.f) continue;
+                                acc[i][c * 4] = fmaf(w, b.x, acc[i][c * 4]);
+                                acc[i][c * 4 + 1] = fmaf(w, b.y, acc[i][c * 4 + 1]);
+                                acc[i][c * 4 + 2] = fmaf(w, b.z, acc[i][c * 4 + 2]);
+                                acc[i][c * 4 + 3] = fmaf(w, b.w, acc[i][c * 4 + 3]);
+                            }
+                        }
+                }
+            };
+            if (edge) add(true);
+            else add(false);
+        }
+#pragma unroll
+        for (int i = 0; i < 4; i++) {
+            const int r = ty * 4 + i;
+            if (r >= rows) continue;
+            const size_t tok = first + r / G;
+            const int head = it.h * G + r % G;
+            const float inv = l[i] > 0.f ? 1.f / l[i] : (l[i] == 0.f ? 0.f : l[i]);  // NaN stays
+#pragma unroll
+            for (int c = 0; c < C4; c++) {
+                const float4 y = make_float4(acc[i][c * 4] * inv, acc[i][c * 4 + 1] * inv,
+                                             acc[i][c * 4 + 2] * inv, acc[i][c * 4 + 3] * inv);
+                flags |= finite_flag(y.x) | finite_flag(y.y) | finite_flag(y.z) | finite_flag(y.w);
+                store4(go + (tok * s.Hkv * G + head) * D + tx * 4 + 64 * c, y);
+            }
+            if (p.lse && tx == 0)
+                p.lse[tok * s.Hkv * G + head] = l[i] == 0.f ? -INFINITY : m[i] + logf(l[i]);
+        }
+    }
+    if (walk.bad) flags |= KDA_DEV_LENGTH;
+    report_flags(p.d_status, flags);
+}
+
+template <typename T, int D>
+cudaError_t launch_t(const AttnArgs& a) {
+    const int G = a.Hq / a.Hkv;
+    SimtParams p{};
+    p.s = {a.cu_q, a.kv_len, a.N, a.total_q, a.max_q,
+           (int)min((long long)a.max_pages * a.page, (1LL << 31) - 1), a.Hkv, G, kRows / G,
+           kRows / G, kKeys};
+    p.q = a.q;
+    p.k = a.k;
+    p.v = a.v;
+    p.block_table = a.block_table;
+    p.o = a.o;
+    p.lse = a.lse;
+    p.q_stride = a.q_stride;
+    p.k_stride = a.k_stride;
+    p.v_stride = a.v_stride;
+    p.num_pages = a.num_pages;
+    p.page = a.page;
+    p.max_pages = a.max_pages;
+    p.scale = a.scale;
+    p.d_status = a.d_status;
+    cudaError_t e = cudaFuncSetAttribute(kda_attn_simt_kernel<T, D>,
+                                         cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         (int)simt_smem<D>());
+    if (e != cudaSuccess) return e;
+    long long grid = attn_items_bound(p.s);
+    if (grid > 65535) grid = 65535;
+    return launch_dependent(kda_attn_simt_kernel<T, D>, dim3((unsigned)grid), dim3(kThreadsSimt),
+                            simt_smem<D>(), a.stream, p);
+}
+
+}  // namespace
+
+cudaError_t launch_attn_simt(const AttnArgs& a, kda_dtype_t io) {
+    if (io == KDA_BF16) return a.d == 128 ? launch_t<__nv_bfloat16, 128>(a) : launch_t<__nv_bfloat16, 64>(a);
+    return a.d == 128 ? launch_t<float, 128>(a) : launch_t<float, 64>(a);
+}
+
+}  // namespace kda

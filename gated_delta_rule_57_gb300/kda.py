@@ -32,6 +32,8 @@ KDA_F32 = 1
 KDA_DEV_DECAY_RANGE = 0x1
 KDA_DEV_NONFINITE = 0x2
 KDA_DEV_TIMEOUT = 0x4
+KDA_DEV_PAGES = 0x8
+KDA_DEV_LENGTH = 0x10
 
 _DTYPE = {torch.bfloat16: KDA_BF16, torch.float32: KDA_F32}
 
@@ -113,6 +115,18 @@ def lib(build_if_missing: bool = True) -> ctypes.CDLL:
             L.kda_decode_multi.argtypes = [vp, vp, vp, vp, vp, vp, vp, vp, I, I, I, I, I, I, I,
                                            vp, vp]
             L.kda_decode_multi.restype = I
+            ll, f = ctypes.c_longlong, ctypes.c_float
+            L.kda_kv_plan.argtypes = [vp] * 9 + [I] * 5 + [vp, vp]
+            L.kda_kv_plan.restype = I
+            L.kda_kv_append.argtypes = [vp] * 5 + [I, I, I, ll, ll, I, I, I, vp, vp]
+            L.kda_kv_append.restype = I
+            L.kda_attn_workspace_size.argtypes = [I] * 7
+            L.kda_attn_workspace_size.restype = sz
+            L.kda_attn_prompt.argtypes = [vp] * 6 + [I] * 6 + [ll] * 3 + [f, I, vp, sz, vp, vp]
+            L.kda_attn_prompt.restype = I
+            L.kda_attn_paged.argtypes = [vp] * 8 + [I] * 6 + [ll] + [I] * 3 + [f, I, vp, sz, vp,
+                                                                              vp]
+            L.kda_attn_paged.restype = I
             _lib = L
     return _lib
 
@@ -418,3 +432,157 @@ def kda_decode_multi(q, k, v, g, beta, S, *, ntok: Optional[torch.Tensor] = None
                                   _ptr(status), _stream(stream))
     _check(code)
     return o
+
+
+def _ints(name: str, t: torch.Tensor, shape):
+    """Device address of an int32 tensor of the given shape."""
+    if t.dtype != torch.int32 or t.shape != shape:
+        raise ValueError(f"{name} must be an int32 tensor of shape {tuple(shape)}")
+    return _ptr(t)
+
+
+def _rows(name: str, t: torch.Tensor, dtype=None):
+    """Address and token stride of a [T, H, d] tensor whose heads are
+    contiguous (a view of a fused projection, or a whole tensor)."""
+    if not t.is_cuda:
+        raise ValueError("KDA tensors must live on a CUDA device")
+    if t.dim() != 3 or (dtype is not None and t.dtype != dtype):
+        raise ValueError(f"{name} must be [T, H, d]" + (f" of {dtype}" if dtype else ""))
+    T, H, d = t.shape
+    st, sh, sd = t.stride()
+    if (d > 1 and sd != 1) or (H > 1 and sh != d):
+        raise ValueError(f"{name}: the heads of a token must be contiguous")
+    return t.data_ptr(), st if T > 1 else H * d
+
+
+def kda_kv_plan(old_len, new_len, block_table, free_pages, ring, *, page_size: int,
+                max_tokens: int, kv_len=None, cu_new=None, slot_map=None, ring_out=None,
+                status: Optional[torch.Tensor] = None, stream=None):
+    """Pages of one step of N requests whose lengths go from old_len to new_len.
+
+    old_len, new_len: [N]; block_table: [N, max_pages] and free_pages:
+    [num_pages] (a ring; both updated in place); ring: {first, count} of the
+    free pages; all int32. Returns (kv_len [N], cu_new [N + 1], slot_map
+    [max_tokens], ring_out [2]).
+    """
+    N, max_pages = block_table.shape
+    dev = block_table.device
+    if kv_len is None:
+        kv_len = torch.empty((N,), dtype=torch.int32, device=dev)
+    if cu_new is None:
+        cu_new = torch.empty((N + 1,), dtype=torch.int32, device=dev)
+    if slot_map is None:
+        slot_map = torch.empty((max_tokens,), dtype=torch.int32, device=dev)
+    if ring_out is None:
+        ring_out = torch.empty((2,), dtype=torch.int32, device=dev)
+    _check(lib().kda_kv_plan(
+        _ints("old_len", old_len, (N,)), _ints("new_len", new_len, (N,)),
+        _ints("block_table", block_table, (N, max_pages)),
+        _ints("free_pages", free_pages, (free_pages.numel(),)), _ints("ring", ring, (2,)),
+        _ints("ring_out", ring_out, (2,)), _ints("kv_len", kv_len, (N,)),
+        _ints("cu_new", cu_new, (N + 1,)), _ints("slot_map", slot_map, (max_tokens,)), N,
+        max_pages, free_pages.numel(), page_size, max_tokens, _ptr(status), _stream(stream)))
+    return kv_len, cu_new, slot_map, ring_out
+
+
+def kda_kv_append(k, v, slot_map, k_cache, v_cache, *, status: Optional[torch.Tensor] = None,
+                  stream=None):
+    """Write k, v [T, Hkv, d] (token-strided views allowed) to the slots
+    slot_map [T] (int32; negative: skipped; longer than T: the first T) of the
+    caches [num_pages, Hkv, page_size, d], in place."""
+    pages, Hkv, page, d = k_cache.shape
+    T = k.shape[0]
+    io = _DTYPE.get(k.dtype)
+    if io is None:
+        raise TypeError(f"unsupported k dtype {k.dtype}")
+    if k.shape != (T, Hkv, d) or v.shape != k.shape or v_cache.shape != k_cache.shape or \
+            k_cache.dtype != k.dtype or v_cache.dtype != k.dtype:
+        raise ValueError("k, v [T, Hkv, d] and the caches must agree in shape and dtype")
+    if slot_map.dtype != torch.int32 or slot_map.dim() != 1 or slot_map.numel() < T:
+        raise ValueError("slot_map must be an int32 tensor with an entry per token")
+    kp, ks = _rows("k", k)
+    vp, vs = _rows("v", v, k.dtype)
+    _check(lib().kda_kv_append(kp, vp, _ptr(slot_map), _ptr(k_cache), _ptr(v_cache), T, Hkv, d,
+                               ks, vs, pages, page, io, _ptr(status), _stream(stream)))
+
+
+def kda_attn_workspace_size(N: int, total_q: int, max_q: int, Hq: int, Hkv: int, d: int,
+                            io: torch.dtype = torch.bfloat16) -> int:
+    n = lib().kda_attn_workspace_size(N, total_q, max_q, Hq, Hkv, d, _DTYPE[io])
+    if n == ctypes.c_size_t(-1).value:
+        raise KdaError(KDA_ERR_INVALID_ARG, "unsupported problem size")
+    return int(n)
+
+
+def _attn_buffers(q, N, most, Hkv, o, lse, want_lse, workspace):
+    """Outputs and workspace of an attention call, and its dtype code."""
+    T, Hq, d = q.shape
+    io = _DTYPE.get(q.dtype)
+    if io is None:
+        raise TypeError(f"unsupported q dtype {q.dtype}")
+    if o is None:
+        o = torch.empty((T, Hq, d), dtype=q.dtype, device=q.device)
+    elif o.shape != q.shape or o.dtype != q.dtype:
+        raise ValueError("o must have q's shape and dtype")
+    if lse is None:
+        if want_lse:
+            lse = torch.empty((T, Hq), dtype=torch.float32, device=q.device)
+    elif lse.shape != (T, Hq) or lse.dtype != torch.float32:
+        raise ValueError("lse must be an fp32 tensor [T, Hq]")
+    if workspace is None:
+        need = lib().kda_attn_workspace_size(N, T, most, Hq, Hkv, d, io)
+        if need != ctypes.c_size_t(-1).value and need:  # the call itself reports bad arguments
+            workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+    ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    return io, o, lse, workspace, ws_bytes
+
+
+def kda_attn_prompt(q, k, v, cu_seqlens, *, max_len: Optional[int] = None,
+                    scale: Optional[float] = None, o=None, lse=None, want_lse: bool = True,
+                    workspace=None, status: Optional[torch.Tensor] = None, stream=None):
+    """Causal attention over packed prompts. q: [T, Hq, d]; k, v: [T, Hkv, d]
+    (token-strided views allowed); cu_seqlens: int32 [N + 1] on the device;
+    max_len: the longest prompt (None: T); scale: None for 1 / sqrt(d).
+    Returns (o [T, Hq, d], lse [T, Hq] or None)."""
+    T, Hq, d = q.shape
+    Hkv = k.shape[1]
+    N = cu_seqlens.numel() - 1
+    if k.shape != (T, Hkv, d) or v.shape != k.shape:
+        raise ValueError("k and v must be [T, Hkv, d] with q's T and d")
+    most = T if max_len is None else max_len
+    io, o, lse, workspace, ws_bytes = _attn_buffers(q, N, most, Hkv, o, lse, want_lse, workspace)
+    qp, qs = _rows("q", q)
+    kp, ks = _rows("k", k, q.dtype)
+    vp, vs = _rows("v", v, q.dtype)
+    _check(lib().kda_attn_prompt(qp, kp, vp, _ints("cu_seqlens", cu_seqlens, (N + 1,)), _ptr(o),
+                                 _ptr(lse), N, T, most, Hq, Hkv, d, qs, ks, vs,
+                                 d ** -0.5 if scale is None else scale, io, _ptr(workspace),
+                                 ws_bytes, _ptr(status), _stream(stream)))
+    return o, lse
+
+
+def kda_attn_paged(q, k_cache, v_cache, block_table, cu_q, kv_len, *,
+                   max_q: Optional[int] = None, scale: Optional[float] = None, o=None, lse=None,
+                   want_lse: bool = True, workspace=None,
+                   status: Optional[torch.Tensor] = None, stream=None):
+    """Causal attention of each request's last tokens over its paged cache.
+    q: [T, Hq, d] (token-strided views allowed); caches: [num_pages, Hkv,
+    page_size, d]; block_table: [N, max_pages], cu_q: [N + 1], kv_len: [N],
+    int32 on the device; max_q: the most new tokens of a request (None: T);
+    scale: None for 1 / sqrt(d). Returns (o [T, Hq, d], lse [T, Hq] or None)."""
+    T, Hq, d = q.shape
+    pages, Hkv, page, dc = k_cache.shape
+    N, max_pages = block_table.shape
+    if dc != d or v_cache.shape != k_cache.shape or k_cache.dtype != q.dtype or \
+            v_cache.dtype != q.dtype:
+        raise ValueError("the caches must be [num_pages, Hkv, page_size, d] of q's d and dtype")
+    most = T if max_q is None else max_q
+    io, o, lse, workspace, ws_bytes = _attn_buffers(q, N, most, Hkv, o, lse, want_lse, workspace)
+    qp, qs = _rows("q", q)
+    _check(lib().kda_attn_paged(qp, _ptr(k_cache), _ptr(v_cache),
+                                _ints("block_table", block_table, (N, max_pages)),
+                                _ints("cu_q", cu_q, (N + 1,)), _ints("kv_len", kv_len, (N,)),
+                                _ptr(o), _ptr(lse), N, T, most, Hq, Hkv, d, qs, pages, page,
+                                max_pages, d ** -0.5 if scale is None else scale, io,
+                                _ptr(workspace), ws_bytes, _ptr(status), _stream(stream)))
+    return o, lse

@@ -53,7 +53,7 @@
 extern "C" {
 #endif
 
-#define KDA_ABI_VERSION 2
+#define KDA_ABI_VERSION 3
 
 typedef enum {
     KDA_OK = 0,
@@ -78,6 +78,8 @@ typedef enum { KDA_BF16 = 0, KDA_F32 = 1 } kda_dtype_t;
  * overflows fp32). */
 #define KDA_DEV_NONFINITE 0x2
 #define KDA_DEV_TIMEOUT 0x4     /* an mbarrier wait exceeded its iteration cap */
+#define KDA_DEV_PAGES 0x8       /* pages ran out, or a page id or slot is out of range */
+#define KDA_DEV_LENGTH 0x10     /* a length outside what the call was sized for */
 
 /* Version of this header the library was built from (KDA_ABI_VERSION). */
 int kda_abi_version(void);
@@ -435,6 +437,155 @@ kda_status_t kda_decode_multi(const void* q, const void* k, const void* v, const
                               const float* beta, float* S, void* o, const int* ntok, int N, int K,
                               int H, int dk, int dv, kda_dtype_t io, int commit, int* d_status,
                               void* stream);
+
+/*
+ * The softmax-attention layers of a hybrid stack
+ * ----------------------------------------------
+ * The orkas.ai page "Kimi K3 architecture" (section "Sequence: three quarters
+ * of the layers stopped reading everything") keeps full attention in every
+ * fourth layer; section "The bill arrives in the serving stack" (second
+ * bullet) describes the paged half of the cache that those layers leave. The
+ * four calls below serve such a layer: plan a step's pages, write its keys and
+ * values, and attend, over whole prompts or over the cache. Heads are grouped:
+ * query head i reads key head i / (Hq / Hkv). They share the conventions at
+ * the top of this file, with these differences:
+ *   - q, k and v may be views of one fused projection: token t starts at
+ *     t * stride elements, its heads are contiguous ([H, d]). Strides are
+ *     multiples of 16 bytes.
+ *   - int arrays, lse and d_status need 4-byte alignment; q, k, v, o, the
+ *     caches and the workspace 16.
+ *   - d in {64, 128}, at most 64 query heads per key head.
+ *   - lengths and tables are device data, so what is wrong with them is
+ *     reported in *d_status (KDA_DEV_PAGES, KDA_DEV_LENGTH); no access leaves
+ *     the buffers whatever they hold.
+ */
+
+/*
+ * Plan one step of N requests whose cached lengths go from old_len[n] to
+ * new_len[n]. A request that grows takes the pages it lacks, in the requests'
+ * order, from the head of a ring of free pages; one that shrinks (drafts taken
+ * back; to 0 where it ends) gives the pages it no longer needs back at the
+ * ring's end, for later steps. The result is the same on every run.
+ *
+ *   old_len, new_len : [N] (in)
+ *   block_table : [N, max_pages] (in/out) page ids; the first
+ *                 ceil(old_len / page_size) of a row are read, the entries of
+ *                 taken pages written, the others left as they are
+ *   free_pages  : [num_pages] (in/out) ring of page ids in 0 .. num_pages - 1;
+ *                 the free ones are at (ring_in[0] + i) % num_pages,
+ *                 i < ring_in[1]
+ *   ring_in     : {first, count} of the free pages (in)
+ *   ring_out    : {first, count} after the step (out)
+ *   kv_len      : [N] (out) lengths after the step: new_len, or old_len for a
+ *                 request left as it was
+ *   cu_new      : [N + 1] (out) prefix sums of the new tokens
+ *                 max(new_len - old_len, 0): request n's are the packed tokens
+ *                 cu_new[n] .. cu_new[n + 1] - 1
+ *   slot_map    : [max_tokens] (out) slot page * page_size + offset of each
+ *                 packed token; -1 past the last one and for requests left as
+ *                 they were
+ *
+ * A request is left as it was, and KDA_DEV_PAGES is set, when its row is
+ * shorter than its pages, or the free pages or max_tokens run out before or at
+ * it (it then needs pages or tokens). What is given back in a step is not
+ * taken in it. Outputs must not overlap anything (ring_out and kv_len are not
+ * ring_in and old_len): a step can be repeated or captured into a graph.
+ * Limits: N <= 16384 (KDA_ERR_UNSUPPORTED beyond), num_pages * page_size <
+ * 2^31, any positive page_size. One launch.
+ */
+kda_status_t kda_kv_plan(const int* old_len, const int* new_len, int* block_table,
+                         int* free_pages, const int* ring_in, int* ring_out, int* kv_len,
+                         int* cu_new, int* slot_map, int N, int max_pages, int num_pages,
+                         int page_size, int max_tokens, int* d_status, void* stream);
+
+/*
+ * Write T new tokens' keys and values to their slots.
+ *
+ *   k, v             : [T, Hkv, d] of type io, token strides k_stride, v_stride (in)
+ *   slot_map         : [T] (in) as kda_kv_plan writes it; negative: the token is
+ *                      skipped; past the cache: skipped, KDA_DEV_PAGES
+ *   k_cache, v_cache : [num_pages, Hkv, page_size, d] of type io (in/out)
+ *
+ * Two tokens with one slot leave either's values. HBM-bound: each byte is read
+ * and written once.
+ */
+kda_status_t kda_kv_append(const void* k, const void* v, const int* slot_map, void* k_cache,
+                           void* v_cache, int T, int Hkv, int d, long long k_stride,
+                           long long v_stride, int num_pages, int page_size, kda_dtype_t io,
+                           int* d_status, void* stream);
+
+/*
+ * Causal attention over N packed prompts:
+ *     o_i = sum_{j <= i} p_ij v_j,   p_i = softmax_j(scale q_i . k_j),
+ *     lse_i = log sum_{j <= i} e^{scale q_i . k_j}
+ * with i, j tokens of the same prompt.
+ *
+ *   q          : [total, Hq, d] of type io, token stride q_stride   (in)
+ *   k, v       : [total, Hkv, d] of type io, strides k_stride, v_stride (in)
+ *   cu_seqlens : [N + 1] (in) prompt n is tokens cu_seqlens[n] ..
+ *                cu_seqlens[n + 1] - 1 (none: an empty prompt)
+ *   o          : [total, Hq, d] of type io, contiguous (out); rows of no
+ *                prompt are not written
+ *   lse        : [total, Hq] fp32 or NULL (out)
+ *   max_len    : no prompt is longer; one that is, or a cu_seqlens that
+ *                decreases or passes total, sets KDA_DEV_LENGTH and that
+ *                prompt's rows are not written
+ *   scale      : positive and finite
+ *   workspace, ws_bytes : see kda_attn_workspace_size
+ *
+ * io = KDA_BF16: products on the tensor cores in fp32, probabilities rounded
+ * to bf16 for the second product (their sum is of the unrounded ones), softmax
+ * statistics and sums in fp32. io = KDA_F32: everything in fp32 on the CUDA
+ * cores. What later tokens hold (NaN and Inf too) does not reach earlier
+ * tokens. KDA_DEV_NONFINITE is set where an o is NaN or Inf.
+ */
+kda_status_t kda_attn_prompt(const void* q, const void* k, const void* v, const int* cu_seqlens,
+                             void* o, float* lse, int N, int total, int max_len, int Hq, int Hkv,
+                             int d, long long q_stride, long long k_stride, long long v_stride,
+                             float scale, kda_dtype_t io, void* workspace, size_t ws_bytes,
+                             int* d_status, void* stream);
+
+/*
+ * Causal attention of each request's last tokens over its paged cache: the
+ * q_n = cu_q[n + 1] - cu_q[n] packed tokens of request n (one while decoding,
+ * the drafts of a speculative round, a chunk of a prompt) are the last q_n of
+ * its kv_len[n] cached tokens, so token i of them sees the first
+ * kv_len[n] - q_n + i + 1.
+ *
+ *   q           : [total_q, Hq, d] of type io, token stride q_stride (in)
+ *   k_cache, v_cache : [num_pages, Hkv, page_size, d] of type io (in); what the
+ *                 tokens' own keys and values hold was written before
+ *                 (kda_kv_append). Slots past kv_len may hold anything.
+ *   block_table : [N, max_pages] (in) page ids
+ *   cu_q        : [N + 1] (in);  kv_len : [N] (in)
+ *   o, lse      : as for kda_attn_prompt, [total_q, ...]; a row that sees no key
+ *                 (kv_len < q_n) gets o = 0, lse = -inf
+ *   max_q       : no request has more new tokens (else KDA_DEV_LENGTH, rows not
+ *                 written)
+ *   page_size   : a power of two in 16 .. 1024 (KDA_ERR_UNSUPPORTED otherwise)
+ *
+ * A kv_len below 0 or past max_pages * page_size is clamped (KDA_DEV_LENGTH); a
+ * page id out of range reads as zeros (KDA_DEV_PAGES). The rest as for
+ * kda_attn_prompt.
+ */
+kda_status_t kda_attn_paged(const void* q, const void* k_cache, const void* v_cache,
+                            const int* block_table, const int* cu_q, const int* kv_len, void* o,
+                            float* lse, int N, int total_q, int max_q, int Hq, int Hkv, int d,
+                            long long q_stride, int num_pages, int page_size, int max_pages,
+                            float scale, kda_dtype_t io, void* workspace, size_t ws_bytes,
+                            int* d_status, void* stream);
+
+/*
+ * Bytes of device workspace that let kda_attn_prompt (total_q = total, max_q =
+ * max_len) and kda_attn_paged split a long row of keys among CTAs: partial
+ * results of at most two row tiles per SM of the current device; 0 where
+ * nothing would be split. NULL or a smaller buffer is accepted and runs unsplit; both
+ * give the same results up to rounding. 16-byte aligned, not overlapping any
+ * other argument, not used by another call in flight; contents are scratch.
+ * (size_t)-1 for arguments the calls would reject.
+ */
+size_t kda_attn_workspace_size(int N, int total_q, int max_q, int Hq, int Hkv, int d,
+                               kda_dtype_t io);
 
 #ifdef __cplusplus
 }
