@@ -1,7 +1,8 @@
 """64-bit definitions of the paged-cache and attention operators, one request
 and one head at a time, and the error they allow.
 
-Tolerances. With u = 2^-9 (half a unit in the last place of bf16), rounding the
+Tolerances. With u = 2^-8 (half a unit in the last place of bf16: its significand
+has 8 bits, so rounding moves x by at most 2^-8 |x|), rounding the
 probabilities p_j moves an output by at most u A, A = sum_j p_j |v_j|, and
 rounding the output by at most u (|o| + u A). What is left is fp32: a score
 x = scale q . k carries a relative error of a few sqrt(d) 2^-24 of
@@ -16,7 +17,7 @@ import math
 
 import torch
 
-U = 2.0 ** -9
+U = 2.0 ** -8
 
 
 def attend(q, k, v, kv_len, scale):
