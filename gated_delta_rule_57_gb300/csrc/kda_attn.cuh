@@ -45,8 +45,6 @@ struct AttnArgs {
     cudaStream_t stream;
 };
 
-cudaError_t launch_attn_simt(const AttnArgs& a, kda_dtype_t io);
-
 // What the device side needs to divide the work.
 struct AttnShape {
     const int* cu_q;
@@ -88,30 +86,65 @@ __device__ __forceinline__ int attn_item_keys(const AttnReq& q, int t) {
     return max(q.kv - q.q_len + last, 0);
 }
 
-// The next whole item of a sequence of increasing item numbers: a walk over
-// the requests, a warp together. Items of a request: tiles from the last to
-// the first, key heads inside.
+// sum_{i < n} floor((a i + b) / m) for non-negative arguments: the multiples of
+// m in a and b are taken out, and what is left counts the lattice points under
+// a line, which are those beside it with the axes exchanged (Euclid's steps).
+__device__ __forceinline__ long long attn_floor_sum(long long n, long long m, long long a,
+                                                    long long b) {
+    long long sum = 0;
+    while (n > 0) {
+        sum += n * (n - 1) / 2 * (a / m) + n * (b / m);
+        a %= m;
+        b %= m;
+        const long long top = a * n + b;
+        n = top / m;
+        b = top % m;
+        const long long x = m;
+        m = a;
+        a = x;
+        if (m == 0) break;  // n is 0 then: top < m
+    }
+    return sum;
+}
+
+// Units (key tiles, at least one) of item t of a request, and of its items
+// 0 .. t - 1.
+__device__ __forceinline__ int attn_item_units(const AttnShape& s, const AttnReq& q, int t) {
+    return max((attn_item_keys(q, t) + s.kt - 1) / s.kt, 1);
+}
+__device__ __forceinline__ long long attn_units_before(const AttnShape& s, const AttnReq& q, int t) {
+    if (t <= 0) return 0;
+    const int full = min(t, q.nqt - 1);  // items whose tokens are all there
+    const long long off = (long long)q.kv - q.q_len;
+    // Items that see at most one tile count one each.
+    long long one = off + q.tok <= s.kt ? ((long long)s.kt - off) / q.tok : 0;
+    one = one < full ? one : full;
+    const long long rest = full - one;
+    long long sum = one + attn_floor_sum(rest, s.kt, q.tok, off + (one + 1) * q.tok + s.kt - 1);
+    if (t == q.nqt) sum += attn_item_units(s, q, t - 1);
+    return sum;
+}
+
+// A walk over the requests, a warp together, that finds the request of an item
+// (or of a unit) of a non-decreasing sequence of numbers.
 struct AttnWalk {
     int r0 = 0;          // the 32 requests r0 .. r0 + 31 are looked at
-    long long base = 0;  // items before them
+    long long base = 0;  // items (units) before them
     bool bad = false;    // some request so far had a bad length (lane-wise)
 };
 
-struct AttnItem {
-    int r, t, h;
-    AttnReq q;
-};
-
-// False when there is no item `idx`. idx must not decrease from call to call.
-__device__ __forceinline__ bool attn_find_item(const AttnShape& s, AttnWalk& w, long long idx,
-                                               AttnItem* it) {
+// False when there is no item (unit) `idx`. *in: its number in the request.
+template <bool UNITS>
+__device__ __forceinline__ bool attn_find(const AttnShape& s, AttnWalk& w, long long idx, int* req,
+                                          AttnReq* rq, long long* in) {
     const int lane = threadIdx.x & 31;
     for (; w.r0 < s.N; w.r0 += 32) {
         const int r = w.r0 + lane;
         AttnReq q{};
         if (r < s.N) q = attn_request(s, r);
         w.bad |= q.bad != 0;
-        const long long mine = (long long)q.nqt * s.Hkv;
+        const long long mine =
+            (q.nqt == 0 ? 0 : UNITS ? attn_units_before(s, q, q.nqt) : q.nqt) * s.Hkv;
         long long inc = mine;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
@@ -122,22 +155,83 @@ __device__ __forceinline__ bool attn_find_item(const AttnShape& s, AttnWalk& w, 
         if (idx < w.base + total) {
             const unsigned m = __ballot_sync(0xffffffffu, idx < w.base + inc);
             const int src = __ffs(m) - 1;
-            it->r = w.r0 + src;
-            it->q.q0 = __shfl_sync(0xffffffffu, q.q0, src);
-            it->q.q_len = __shfl_sync(0xffffffffu, q.q_len, src);
-            it->q.kv = __shfl_sync(0xffffffffu, q.kv, src);
-            it->q.tok = __shfl_sync(0xffffffffu, q.tok, src);
-            it->q.nqt = __shfl_sync(0xffffffffu, q.nqt, src);
-            it->q.bad = 0;
-            const int in = (int)(idx - w.base - __shfl_sync(0xffffffffu, inc - mine, src));
-            it->t = it->q.nqt - 1 - in / s.Hkv;
-            it->h = in % s.Hkv;
+            *req = w.r0 + src;
+            rq->q0 = __shfl_sync(0xffffffffu, q.q0, src);
+            rq->q_len = __shfl_sync(0xffffffffu, q.q_len, src);
+            rq->kv = __shfl_sync(0xffffffffu, q.kv, src);
+            rq->tok = __shfl_sync(0xffffffffu, q.tok, src);
+            rq->nqt = __shfl_sync(0xffffffffu, q.nqt, src);
+            rq->bad = 0;
+            *in = idx - w.base - __shfl_sync(0xffffffffu, inc - mine, src);
             return true;
         }
         w.base += total;
     }
     return false;
 }
+
+// Split items: units of a request run key head by key head, row tile by row
+// tile. The item of unit `in` of a request and the tile of it that the unit is.
+__device__ __forceinline__ void attn_unit_item(const AttnShape& s, const AttnReq& q, long long in,
+                                               int* h, int* t, int* tile) {
+    const long long per = attn_units_before(s, q, q.nqt);
+    *h = (int)(in / per);
+    const long long rest = in - *h * per;
+    int lo = 0, hi = q.nqt;  // units_before(lo) <= rest < units_before(hi)
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (attn_units_before(s, q, mid) <= rest) lo = mid;
+        else hi = mid;
+    }
+    *t = lo;
+    *tile = (int)(rest - attn_units_before(s, q, lo));
+}
+
+// Units of a CTA's range, by the whole block: all units of all requests over
+// `ctas`, but at least `least`. s_sum: one word per warp.
+template <int THREADS>
+__device__ __forceinline__ long long attn_units_each(const AttnShape& s, int ctas, int least,
+                                                     long long* s_sum) {
+    long long sum = 0;
+    for (int r = threadIdx.x; r < s.N; r += THREADS) {
+        const AttnReq q = attn_request(s, r);
+        if (q.nqt) sum += attn_units_before(s, q, q.nqt) * s.Hkv;
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    if ((threadIdx.x & 31) == 0) s_sum[threadIdx.x >> 5] = sum;
+    __syncthreads();
+    sum = 0;
+    for (int w = 0; w < THREADS / 32; w++) sum += s_sum[w];
+    const long long each = (sum + ctas - 1) / ctas;
+    return each < least ? least : each;
+}
+
+// Partial results of split items in the workspace: slot 2 c holds the part of
+// CTA c's range that starts where the range does, slot 2 c + 1 the one that
+// ends where it does. Per slot: rows x d outputs (each the softmax over its
+// part), then rows log-sums in base 2.
+struct AttnSplit {
+    float* ws;      // null: whole items
+    int ctas;       // CTAs the units are divided among
+    int least;      // units of a range, at least
+    int rows;       // rows of a slot
+};
+inline __host__ __device__ size_t attn_slot_floats(int rows, int d) { return (size_t)rows * (d + 1); }
+
+// Joins the parts of the split items (io: type of o).
+cudaError_t launch_attn_combine(const AttnShape& s, const AttnSplit& sp, int d, int rows_per_tile,
+                                void* o, float* lse, kda_dtype_t io, int* d_status,
+                                cudaStream_t stream);
+cudaError_t launch_attn_tc(const AttnArgs& a);    // bf16
+cudaError_t launch_attn_simt(const AttnArgs& a);  // fp32
+
+// How a call on `nsm` SMs divides the tensor-core kernel's work: CTAs and rows
+// of a slot of its split form, or ctas = 0 for whole items.
+AttnSplit attn_tc_split(int N, int total_q, int max_q, int Hq, int Hkv, int nsm);
+
+// SMs of the current device, 0 if none is visible.
+int attn_sms();
 
 // Most items there can be, for the grid: every request may leave one tile
 // partly filled.

@@ -57,7 +57,7 @@ kda_status_t run(AttnArgs& a, kda_dtype_t io, size_t n_k, size_t n_v) {
             if (overlaps(outs[i].p, outs[i].n, outs[j].p, outs[j].n))
                 return fail(KDA_ERR_INVALID_ARG, "o, lse and the workspace overlap");
     }
-    return launched(launch_attn_simt(a, io));
+    return launched(io == KDA_BF16 ? launch_attn_tc(a) : launch_attn_simt(a));
 }
 
 }  // namespace
@@ -68,7 +68,10 @@ size_t kda_attn_workspace_size(int N, int total_q, int max_q, int Hq, int Hkv, i
                                kda_dtype_t io) {
     if (N < 0 || total_q < 0 || max_q < 0 || check_heads(Hq, Hkv, d, io) != KDA_OK)
         return (size_t)-1;
-    return 0;
+    if (io != KDA_BF16) return 0;
+    const int most = max_q < total_q ? max_q : total_q;
+    const AttnSplit sp = attn_tc_split(N, total_q, most, Hq, Hkv, attn_sms());
+    return 2 * (size_t)sp.ctas * attn_slot_floats(sp.rows, d) * 4;
 }
 
 kda_status_t kda_attn_prompt(const void* q, const void* k, const void* v, const int* cu_seqlens,
@@ -121,8 +124,8 @@ kda_status_t kda_attn_paged(const void* q, const void* k_cache, const void* v_ca
                             float scale, kda_dtype_t io, void* workspace, size_t ws_bytes,
                             int* d_status, void* stream) {
     NvtxRange nvtx_range("kda_attn_paged");
-    if (N < 0 || total_q < 0 || max_q < 0 || num_pages < 0 || max_pages < 0 || page_size < 1)
-        return fail(KDA_ERR_INVALID_ARG, "sizes must be >= 0 and page_size positive");
+    if (N < 0 || total_q < 0 || max_q < 0 || num_pages < 1 || max_pages < 0 || page_size < 1)
+        return fail(KDA_ERR_INVALID_ARG, "sizes must be >= 0, num_pages and page_size positive");
     kda_status_t st = check_heads(Hq, Hkv, d, io);
     if (st != KDA_OK) return st;
     if (page_size < 16 || page_size > 1024 || (page_size & (page_size - 1)))
@@ -130,7 +133,7 @@ kda_status_t kda_attn_paged(const void* q, const void* k_cache, const void* v_ca
     if ((long long)num_pages * page_size >= (1LL << 31))
         return fail(KDA_ERR_INVALID_ARG, "num_pages * page_size must be below 2^31");
     if (N == 0 || total_q == 0 || max_q == 0 || Hq == 0) return KDA_OK;
-    if (!kv_len || (max_pages > 0 && !block_table) || (num_pages > 0 && (!k_cache || !v_cache)))
+    if (!kv_len || (max_pages > 0 && !block_table) || !k_cache || !v_cache)
         return fail(KDA_ERR_INVALID_ARG, "a NULL pointer");
     size_t n_c;
     if (!mul_ok(&n_c, num_pages, page_size, (size_t)Hkv * d, io == KDA_BF16 ? 2 : 4))

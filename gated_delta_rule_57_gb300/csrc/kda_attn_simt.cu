@@ -1,4 +1,4 @@
-// Softmax attention on the CUDA cores, with every product and sum in 32 bits.
+// Softmax attention of fp32 inputs on the CUDA cores, with every product and sum in 32 bits.
 //
 //     x_ij = scale q_i . k_j (j <= position of i),  m_i = max_j x_ij,
 //     l_i = sum_j e^{x_ij - m_i},  o_i = sum_j e^{x_ij - m_i} v_j / l_i
@@ -35,26 +35,11 @@ constexpr size_t simt_smem() {
     return (size_t)3 * kRows * (D + 4) * 4;
 }
 
-template <typename T>
-__device__ __forceinline__ float4 load4(const T* p);
-template <>
-__device__ __forceinline__ float4 load4<float>(const float* p) {
+__device__ __forceinline__ float4 load4(const float* p) {
     return *reinterpret_cast<const float4*>(p);
 }
-template <>
-__device__ __forceinline__ float4 load4<__nv_bfloat16>(const __nv_bfloat16* p) {
-    const uint2 w = *reinterpret_cast<const uint2*>(p);
-    return make_float4(__uint_as_float(w.x << 16), __uint_as_float(w.x & 0xffff0000u),
-                       __uint_as_float(w.y << 16), __uint_as_float(w.y & 0xffff0000u));
-}
-__device__ __forceinline__ void store4(float* p, float4 x) { *reinterpret_cast<float4*>(p) = x; }
-__device__ __forceinline__ void store4(__nv_bfloat16* p, float4 x) {
-    __nv_bfloat162 a = __floats2bfloat162_rn(x.x, x.y), b = __floats2bfloat162_rn(x.z, x.w);
-    *reinterpret_cast<uint2*>(p) =
-        make_uint2(*reinterpret_cast<uint32_t*>(&a), *reinterpret_cast<uint32_t*>(&b));
-}
 
-template <typename T, int D>
+template <int D>
 __global__ void __launch_bounds__(kThreadsSimt, 2) kda_attn_simt_kernel(const SimtParams p) {
     constexpr int LD = D + 4, LP = kKeys + 4, C4 = D / 64;  // C4: float4 columns per thread
     extern __shared__ __align__(16) float sm[];
@@ -66,14 +51,20 @@ __global__ void __launch_bounds__(kThreadsSimt, 2) kda_attn_simt_kernel(const Si
     pdl_wait();
     const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
     const AttnShape& s = p.s;
-    const T* gq = static_cast<const T*>(p.q);
-    const T* gk = static_cast<const T*>(p.k);
-    const T* gv = static_cast<const T*>(p.v);
-    T* go = static_cast<T*>(p.o);
+    const float* gq = static_cast<const float*>(p.q);
+    const float* gk = static_cast<const float*>(p.k);
+    const float* gv = static_cast<const float*>(p.v);
+    float* go = static_cast<float*>(p.o);
     int flags = 0;
     AttnWalk walk;
-    AttnItem it;
-    for (long long idx = blockIdx.x; attn_find_item(s, walk, idx, &it); idx += gridDim.x) {
+    struct {
+        int r, t, h;
+        AttnReq q;
+    } it;
+    long long in;
+    for (long long idx = blockIdx.x; attn_find<false>(s, walk, idx, &it.r, &it.q, &in); idx += gridDim.x) {
+        it.t = it.q.nqt - 1 - (int)(in / s.Hkv);
+        it.h = (int)(in % s.Hkv);
         const int G = s.G, tok0 = it.t * it.q.tok;
         const int rows = min(it.q.tok, it.q.q_len - tok0) * G;
         const int keys = attn_item_keys(it.q, it.t);
@@ -216,7 +207,7 @@ __global__ void __launch_bounds__(kThreadsSimt, 2) kda_attn_simt_kernel(const Si
                 const float4 y = make_float4(acc[i][c * 4] * inv, acc[i][c * 4 + 1] * inv,
                                              acc[i][c * 4 + 2] * inv, acc[i][c * 4 + 3] * inv);
                 flags |= finite_flag(y.x) | finite_flag(y.y) | finite_flag(y.z) | finite_flag(y.w);
-                store4(go + (tok * s.Hkv * G + head) * D + tx * 4 + 64 * c, y);
+                *reinterpret_cast<float4*>(go + (tok * s.Hkv * G + head) * D + tx * 4 + 64 * c) = y;
             }
             if (p.lse && tx == 0)
                 p.lse[tok * s.Hkv * G + head] = l[i] == 0.f ? -INFINITY : m[i] + logf(l[i]);
@@ -226,7 +217,7 @@ __global__ void __launch_bounds__(kThreadsSimt, 2) kda_attn_simt_kernel(const Si
     report_flags(p.d_status, flags);
 }
 
-template <typename T, int D>
+template <int D>
 cudaError_t launch_t(const AttnArgs& a) {
     const int G = a.Hq / a.Hkv;
     SimtParams p{};
@@ -247,21 +238,20 @@ cudaError_t launch_t(const AttnArgs& a) {
     p.max_pages = a.max_pages;
     p.scale = a.scale;
     p.d_status = a.d_status;
-    cudaError_t e = cudaFuncSetAttribute(kda_attn_simt_kernel<T, D>,
+    cudaError_t e = cudaFuncSetAttribute(kda_attn_simt_kernel<D>,
                                          cudaFuncAttributeMaxDynamicSharedMemorySize,
                                          (int)simt_smem<D>());
     if (e != cudaSuccess) return e;
     long long grid = attn_items_bound(p.s);
     if (grid > 65535) grid = 65535;
-    return launch_dependent(kda_attn_simt_kernel<T, D>, dim3((unsigned)grid), dim3(kThreadsSimt),
+    return launch_dependent(kda_attn_simt_kernel<D>, dim3((unsigned)grid), dim3(kThreadsSimt),
                             simt_smem<D>(), a.stream, p);
 }
 
 }  // namespace
 
-cudaError_t launch_attn_simt(const AttnArgs& a, kda_dtype_t io) {
-    if (io == KDA_BF16) return a.d == 128 ? launch_t<__nv_bfloat16, 128>(a) : launch_t<__nv_bfloat16, 64>(a);
-    return a.d == 128 ? launch_t<float, 128>(a) : launch_t<float, 64>(a);
+cudaError_t launch_attn_simt(const AttnArgs& a) {
+    return a.d == 128 ? launch_t<128>(a) : launch_t<64>(a);
 }
 
 }  // namespace kda

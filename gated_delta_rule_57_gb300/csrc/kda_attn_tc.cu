@@ -1,0 +1,810 @@
+// Softmax attention on the 5th-generation tensor cores (bf16).
+//
+//     S = Q K^T,  P = 2^{c S - m},  O = P V / l,   c = scale log2 e
+//
+// with m a running reference of each row's largest c S and l its running sum.
+// A raised m multiplies what O and l hold by 2^{m_old - m_new}; m is only
+// raised when a row's maximum passes it by more than 8, so P stays below 2^8
+// (bf16 and fp32 keep their relative precision there) and after a few key
+// tiles O is hardly ever touched.
+//
+// One CTA per SM, ten warps:
+//   warps 0..3, 4..7  two softmax groups, one row of S per thread
+//   warp 8            issues the products (and zeroes V past the last key)
+//   warp 9            finds the work and issues the loads
+// A group's loop: S (TMEM, 128 lanes x 128 columns fp32) -> registers, mask,
+// maximum, exponentials, P as bf16 pairs into the first half of S's columns, and
+// the second product reads P from there as its A operand. While one group
+// computes exponentials the tensor core runs the other group's two products.
+// The groups hold either the two row tiles of one item, sharing every key and
+// value tile (prompts and chunks), or the even and the odd key tiles of one
+// row tile (few rows: the two results are merged in TMEM at the end).
+//
+// Tensor memory (512 columns): S of group 0, S of group 1, O of group 0, O of
+// group 1. Shared memory: two Q tiles and a ring of K / V tiles, all "SW128
+// row tiles" of 128 rows, filled by TMA. K tiles are the K-major B operand of
+// the first product, V tiles the MN-major B operand of the second.
+//
+// A key past a row's last one gets P = 0 by a select on S. V past the item's
+// last key (stale cache slots, the next prompt) is zeroed in shared memory, since
+// 0 x NaN is NaN; for keys that some rows of the item see and others do not,
+// a row whose O is not finite is computed again from global memory over
+// exactly the keys it sees, so a NaN or Inf beside zero weights never reaches it.
+#include "kda_attn.cuh"
+#include "sm100_ptx.cuh"
+#include "tensor_map.cuh"
+
+namespace kda {
+namespace {
+
+using namespace ptx;
+
+constexpr int kTile = 128;         // rows of a row tile, keys of a key tile
+constexpr int kThreadsTc = 384;    // three warpgroups; the last two warps only make up the third
+// Registers per thread: launched with 168 (64512 in all), then 200 for the two
+// softmax groups and 104 for the third (64512).
+constexpr int kRegsSoftmax = 200, kRegsOther = 104;
+constexpr int kMmaWarp = 8, kLoadWarp = 9;
+constexpr int kPieces = 4;         // pieces announced ahead
+constexpr float kRaise = 8.f;      // log2 growth of a row maximum that moves its reference
+
+template <int D>
+struct TcCfg {
+    static constexpr int TILE_BYTES = kTile * D * 2;
+    static constexpr int STAGES = D == 128 ? 5 : 8;
+    static constexpr int SMEM = (2 + STAGES) * TILE_BYTES + 1024;
+};
+
+struct TcAttnParams {
+    AttnShape s;
+    AttnSplit sp;
+    const int* block_table;  // null: packed prompts
+    const __nv_bfloat16* q;
+    const __nv_bfloat16* k;
+    const __nv_bfloat16* v;
+    __nv_bfloat16* o;
+    float* lse;
+    long long q_stride, k_stride, v_stride;
+    int num_pages, page, max_pages;
+    int box_q;  // tokens of a Q load
+    float c;    // scale log2 e
+    int* d_status;
+};
+
+// A range of key tiles of one item.
+struct Piece {
+    int r, h;
+    int tok0;       // packed token of row 0
+    int ntok;       // tokens of the item
+    int pos0;       // keys that row 0's token sees, less one (may be negative)
+    int key0;       // packed token of key 0 (prompts)
+    int kv;         // keys of the request
+    int keys;       // keys the item's last token sees
+    int kt0, kt1;   // key tiles
+    int pair;       // two row tiles (1) or one (0)
+    int slot;       // where a part of an item goes; -1: the whole item
+    int end;        // no more pieces
+};
+
+// Key tiles of a softmax group: tiles kt0 + first, + step, ... (n of them).
+struct Share {
+    int n, first, step;
+};
+__device__ __forceinline__ Share group_share(const Piece& p, int w, int tok1) {
+    Share g;
+    if (p.pair) {
+        const int last = min((w + 1) * tok1, p.ntok);  // its last token
+        const int keys = last > w * tok1 ? max(p.pos0 + last, 0) : 0;
+        g.n = max(min(p.kt1, (keys + kTile - 1) / kTile) - p.kt0, 0);
+        g.first = 0;
+        g.step = 1;
+    } else {
+        g.n = (min(p.kt1, (p.keys + kTile - 1) / kTile) - p.kt0 - w + 1) / 2;
+        g.n = max(g.n, 0);
+        g.first = w;
+        g.step = 2;
+    }
+    return g;
+}
+__device__ __forceinline__ int piece_tiles(const Piece& p) {
+    return max(min(p.kt1, (p.keys + kTile - 1) / kTile) - p.kt0, 0);
+}
+
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ uint32_t pack2(float a, float b) {
+    __nv_bfloat162 v = __floats2bfloat162_rn(a, b);
+    return *reinterpret_cast<uint32_t*>(&v);
+}
+// A bounded wait by a whole warp, with one outcome for all its lanes.
+__device__ __forceinline__ void warp_wait(bool& ok, uint64_t* bar, uint32_t parity) {
+    if (ok) ok = mbar_wait(bar, parity);
+    ok = __all_sync(0xffffffffu, ok);
+}
+
+struct Shared {
+    uint64_t kv_full[8], kv_empty[8];
+    uint64_t q_full, q_empty;
+    uint64_t s_full[2], p_full[2], pv_done[2];
+    uint64_t merge;  // both softmax groups
+    uint64_t piece_full[kPieces], piece_empty[kPieces];
+    Piece pieces[kPieces];
+    float2 ml[kTile];  // merging the groups: (reference, sum) of group 1's rows, then both weights
+    long long sum[kThreadsTc / 32];
+    uint32_t tmem;
+};
+
+// One row again, a warp together, over exactly the keys [j0, j1) that it sees,
+// columns c0 .. c0 + 32 V - 1; lane l holds columns c0 + l + 32 e of acc.
+// Returns the sum of exponentials (0: none).
+template <int D, int V>
+__device__ float row_again(const TcAttnParams& p, const Piece& pc, size_t tok, int head, int j0,
+                           int j1, int c0, float* acc) {
+    const int lane = threadIdx.x & 31;
+    constexpr int E = D / 32;
+    float q[E];
+    const __nv_bfloat16* gq = p.q + tok * p.q_stride + (size_t)head * D;
+#pragma unroll
+    for (int e = 0; e < E; e++) q[e] = __bfloat162float(gq[lane + 32 * e]);
+    float m = -INFINITY, l = 0.f;
+#pragma unroll
+    for (int e = 0; e < V; e++) acc[e] = 0.f;
+    for (int j = j0; j < j1; j++) {
+        const __nv_bfloat16 *gk, *gv;
+        if (p.block_table) {
+            const int id = p.block_table[(size_t)pc.r * p.max_pages + j / p.page];
+            if (id < 0 || id >= p.num_pages) {  // reads as zeros
+                gk = gv = nullptr;
+            } else {
+                const size_t at = (((size_t)id * p.s.Hkv + pc.h) * p.page + j % p.page) * D;
+                gk = p.k + at;
+                gv = p.v + at;
+            }
+        } else {
+            gk = p.k + (size_t)(pc.key0 + j) * p.k_stride + (size_t)pc.h * D;
+            gv = p.v + (size_t)(pc.key0 + j) * p.v_stride + (size_t)pc.h * D;
+        }
+        float x = 0.f;
+        if (gk) {
+#pragma unroll
+            for (int e = 0; e < E; e++) x = fmaf(q[e], __bfloat162float(gk[lane + 32 * e]), x);
+        }
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+        x *= p.c;
+        const float mn = x > m ? x : m;
+        const float a = m == -INFINITY ? 0.f : exp2f(m - mn);
+        const float w = mn == -INFINITY ? 0.f : exp2f(x - mn);
+        m = mn;
+        l = l * a + w;
+#pragma unroll
+        for (int e = 0; e < V; e++)
+            acc[e] = acc[e] * a + (gv ? w * __bfloat162float(gv[c0 + lane + 32 * e]) : 0.f);
+    }
+    return l;
+}
+
+template <int D>
+__global__ void __launch_bounds__(kThreadsTc, 1)
+    kda_attn_tc_kernel(const __grid_constant__ CUtensorMap map_q,
+                       const __grid_constant__ CUtensorMap map_k,
+                       const __grid_constant__ CUtensorMap map_v,
+                       const __grid_constant__ TcAttnParams p) {
+    using C = TcCfg<D>;
+    constexpr int NS = C::STAGES, HALVES = D / 64;
+    constexpr uint32_t TM_S = 0, TM_O = 256;
+    extern __shared__ __align__(1024) unsigned char smem_raw[];
+    unsigned char* sm = smem_raw + ((1024u - (smem_addr(smem_raw) & 1023u)) & 1023u);
+    unsigned char* sq = sm;                        // two Q tiles
+    unsigned char* skv = sm + 2 * C::TILE_BYTES;   // the ring
+    __shared__ Shared sh;
+
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    if (tid == 0) {
+        for (int i = 0; i < NS; i++) {
+            mbar_init(&sh.kv_full[i], 1);
+            mbar_init(&sh.kv_empty[i], 1);
+        }
+        mbar_init(&sh.q_full, 1);
+        mbar_init(&sh.q_empty, 1);
+        for (int w = 0; w < 2; w++) {
+            mbar_init(&sh.s_full[w], 1);
+            mbar_init(&sh.p_full[w], 128);
+            mbar_init(&sh.pv_done[w], 1);
+        }
+        mbar_init(&sh.merge, 256);
+        for (int i = 0; i < kPieces; i++) {
+            mbar_init(&sh.piece_full[i], 1);
+            mbar_init(&sh.piece_empty[i], 9);
+        }
+        fence_mbarrier_init();
+        prefetch_tensormap(&map_q);
+        prefetch_tensormap(&map_k);
+        prefetch_tensormap(&map_v);
+    }
+    if (warp == 0) {
+        tmem_alloc(&sh.tmem, 512);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    pdl_wait();
+    // Units of this CTA's range (split items); also the barrier after the setup.
+    long long each = 0;
+    if (p.sp.ws) each = attn_units_each<kThreadsTc>(p.s, p.sp.ctas, p.sp.least, sh.sum);
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tbase = sh.tmem;
+    const int G = p.s.G, tok1 = p.s.tok1;
+    int flags = 0;
+    bool ok = true;
+
+    if (warp >= 8) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsOther));
+        if (warp == kLoadWarp) {
+            // ------------------------------------------------------------ work and loads
+            int stage = 0, kv_phase = 0, q_phase = 0, np = 0;
+            auto load_kv = [&](const Piece& pc, const CUtensorMap* map, int kt) {
+                warp_wait(ok, &sh.kv_empty[stage], kv_phase ^ 1);
+                if (!ok) return;
+                unsigned char* dst = skv + stage * C::TILE_BYTES;
+                uint64_t* bar = &sh.kv_full[stage];
+                if (lane == 0) mbar_arrive_expect_tx(bar, C::TILE_BYTES);
+                __syncwarp();
+                if (!p.block_table) {
+                    if (lane < HALVES)
+                        tma_load_3d(dst + lane * (kTile * 128), map, bar, 64 * lane, pc.h,
+                                    pc.key0 + kt * kTile);
+                } else {
+                    const int per = p.page < kTile ? kTile / p.page : 1;  // pages of a tile
+                    if (lane < per * HALVES) {
+                        const int pg = lane % per, half = lane / per;
+                        const int j = kt * kTile + pg * p.page;  // first key of the page's part
+                        // past the keys, or no page: beyond the cache, which loads zeros
+                        int id = p.num_pages;
+                        if (j < pc.kv) {
+                            id = p.block_table[(size_t)pc.r * p.max_pages + j / p.page];
+                            if (id < 0 || id >= p.num_pages) {
+                                id = p.num_pages;
+                                flags |= KDA_DEV_PAGES;
+                            }
+                        }
+                        tma_load_4d(dst + half * (kTile * 128) + pg * p.page * 128, map, bar, 64 * half,
+                                    j % p.page, pc.h, id);
+                    }
+                }
+                if (++stage == NS) {
+                    stage = 0;
+                    kv_phase ^= 1;
+                }
+            };
+            auto announce = [&](const Piece& pc) {
+                const int i = np % kPieces;
+                warp_wait(ok, &sh.piece_empty[i], ((np / kPieces) & 1) ^ 1);
+                if (!ok) return;
+                if (lane == 0) {
+                    sh.pieces[i] = pc;
+                    mbar_arrive(&sh.piece_full[i]);
+                }
+                np++;
+                __syncwarp();
+            };
+            auto process = [&](const Piece& pc) {
+                announce(pc);
+                const int n = piece_tiles(pc), lead = pc.pair ? 1 : 2;
+                if (n == 0 || !ok) return;
+                warp_wait(ok, &sh.q_empty, q_phase ^ 1);
+                if (!ok) return;
+                q_phase ^= 1;
+                if (lane == 0)
+                    mbar_arrive_expect_tx(&sh.q_full, (1 + pc.pair) * HALVES * p.box_q * G * 128);
+                __syncwarp();
+                if (lane < HALVES * (1 + pc.pair)) {
+                    const int w = lane / HALVES, half = lane % HALVES;
+                    tma_load_3d(sq + w * C::TILE_BYTES + half * (kTile * 128), &map_q, &sh.q_full,
+                                64 * half, pc.h * G, pc.tok0 + w * tok1);
+                }
+                for (int j = 0; j < lead && j < n; j++) load_kv(pc, &map_k, pc.kt0 + j);
+                for (int j = 0; j < n; j++) {
+                    load_kv(pc, &map_v, pc.kt0 + j);
+                    if (j + lead < n) load_kv(pc, &map_k, pc.kt0 + j + lead);
+                }
+            };
+            auto piece_of = [&](int r, const AttnReq& q, int h, int t) {
+                Piece pc;
+                pc.r = r;
+                pc.h = h;
+                const int at = t * q.tok;
+                pc.tok0 = q.q0 + at;
+                pc.ntok = min(q.tok, q.q_len - at);
+                pc.pos0 = q.kv - q.q_len + at;
+                pc.key0 = q.q0;
+                pc.kv = q.kv;
+                pc.keys = attn_item_keys(q, t);
+                pc.kt0 = 0;
+                pc.kt1 = attn_item_units(p.s, q, t);
+                pc.pair = q.tok > tok1;
+                pc.slot = -1;
+                pc.end = 0;
+                return pc;
+            };
+            // Whole items: numbers blockIdx.x, + gridDim.x, ...; split ones: the units
+            // [cur, end), item by item.
+            AttnWalk walk;
+            AttnReq q{};
+            int r = 0, h = 0, t = 0, tile = 0;
+            long long in;
+            const bool split = p.sp.ws != nullptr;
+            long long cur = split ? blockIdx.x * each : blockIdx.x;
+            const long long start = cur, end = cur + each;
+            bool have = false;  // (q, h, t, tile) is where `cur` is
+            while (ok && (!split || cur < end)) {
+                if (!have) {
+                    if (!(split ? attn_find<true>(p.s, walk, cur, &r, &q, &in)
+                                : attn_find<false>(p.s, walk, cur, &r, &q, &in)))
+                        break;
+                    if (split) {
+                        attn_unit_item(p.s, q, in, &h, &t, &tile);
+                    } else {
+                        t = q.nqt - 1 - (int)(in / p.s.Hkv);
+                        h = (int)(in % p.s.Hkv);
+                    }
+                }
+                Piece pc = piece_of(r, q, h, t);
+                if (split) {
+                    const int n = pc.kt1, take = (int)min((long long)(n - tile), end - cur);
+                    pc.kt0 = tile;
+                    pc.kt1 = tile + take;
+                    if (take < n) pc.slot = 2 * blockIdx.x + (cur > start ? 1 : 0);
+                    cur += take;
+                    tile = 0;
+                    if (++t == q.nqt) {
+                        t = 0;
+                        h++;
+                    }
+                    have = h < p.s.Hkv;
+                } else {
+                    cur += gridDim.x;
+                }
+                process(pc);
+            }
+            if (blockIdx.x == 0) {  // lengths of requests this CTA had no work of
+                for (int i = lane; i < p.s.N; i += 32) walk.bad |= attn_request(p.s, i).bad != 0;
+                if (walk.bad) flags |= KDA_DEV_LENGTH;
+            }
+            Piece last{};
+            last.end = 1;
+            announce(last);
+            if (!ok) {
+                flags |= KDA_DEV_TIMEOUT;
+                // copies in flight land before the CTA leaves
+                for (int i = 0; i < NS; i++)
+                    mbar_wait(&sh.kv_full[i], (i < stage ? kv_phase : kv_phase ^ 1), 1LL << 24);
+                mbar_wait(&sh.q_full, q_phase ^ 1, 1LL << 24);
+            }
+        } else if (warp == kMmaWarp) {
+            // ------------------------------------------------------------ products
+            int stage = 0, kv_phase = 0, q_phase = 0, np = 0;
+            int tiles[2] = {0, 0};  // tiles of each group so far
+            const uint32_t idesc_s = idesc_bf16(kTile, kTile, 0, 0);
+            const uint32_t idesc_o = idesc_bf16(kTile, D, 0, 1);
+            const uint32_t aq = smem_addr(sq), akv = smem_addr(skv);
+            auto next = [&] {
+                if (++stage == NS) {
+                    stage = 0;
+                    kv_phase ^= 1;
+                }
+            };
+            auto wait = [&](uint64_t* bar, uint32_t parity) {
+                warp_wait(ok, bar, parity);
+                return ok;
+            };
+            auto scores = [&](int w, int pair, uint32_t kstage) {  // S_w = Q_w K^T
+                if (lane == 0) {
+                    const uint64_t a = desc_kmajor(aq + (pair ? w : 0) * C::TILE_BYTES);
+                    const uint64_t b = desc_kmajor(akv + kstage * C::TILE_BYTES);
+    #pragma unroll
+                    for (int kk = 0; kk < D / 16; kk++)
+                        mma_bf16(tbase + TM_S + w * kTile, a + kstep_kmajor(kTile, kk),
+                                 b + kstep_kmajor(kTile, kk), idesc_s, kk > 0);
+                    mma_commit(&sh.s_full[w]);
+                }
+                __syncwarp();
+            };
+            auto outputs = [&](int w, uint32_t vstage, bool first) {  // O_w += P_w V
+                if (lane == 0) {
+                    const uint64_t b = desc_mnmajor(akv + vstage * C::TILE_BYTES, kTile);
+    #pragma unroll
+                    for (int kk = 0; kk < kTile / 16; kk++)
+                        mma_bf16_ta(tbase + TM_O + w * D, tbase + TM_S + w * kTile + 8 * kk,
+                                    b + kstep_mnmajor(kk), idesc_o, !first || kk > 0);
+                    mma_commit(&sh.pv_done[w]);
+                }
+                __syncwarp();
+            };
+            auto release = [&](uint64_t* bar) {
+                if (lane == 0) mma_commit(bar);
+                __syncwarp();
+            };
+            while (ok) {
+                const int i = np % kPieces;
+                if (!wait(&sh.piece_full[i], (np / kPieces) & 1)) break;
+                const Piece pc = sh.pieces[i];
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&sh.piece_empty[i]);
+                np++;
+                if (pc.end) break;
+                const int n = piece_tiles(pc), lead = pc.pair ? 1 : 2;
+                if (n == 0) continue;
+                const Share g[2] = {group_share(pc, 0, tok1), group_share(pc, 1, tok1)};
+                if (!wait(&sh.q_full, q_phase)) break;
+                q_phase ^= 1;
+                for (int j = 0; j < lead && j < n; j++) {
+                    if (!wait(&sh.kv_full[stage], kv_phase)) break;
+                    tc_fence_after();
+    #pragma unroll
+                    for (int w = 0; w < 2; w++)
+                        if (pc.pair ? g[w].n > 0 : w == j) scores(w, pc.pair, stage);
+                    release(&sh.kv_empty[stage]);
+                    next();
+                }
+                if (n <= lead) release(&sh.q_empty);
+                for (int j = 0; j < n && ok; j++) {
+                    const int vs = stage;
+                    if (!wait(&sh.kv_full[vs], kv_phase)) break;
+                    next();
+                    const int dead = pc.keys - (pc.kt0 + j) * kTile;  // first row past the keys
+                    if (dead < kTile) {
+                        unsigned char* v = skv + vs * C::TILE_BYTES;
+    #pragma unroll
+                        for (int half = 0; half < HALVES; half++)
+                            for (int b = dead * 128 + lane * 16; b < kTile * 128; b += 512)
+                                *reinterpret_cast<uint4*>(v + half * (kTile * 128) + b) =
+                                    make_uint4(0, 0, 0, 0);
+                        fence_proxy_async_smem();
+                        __syncwarp();
+                    }
+                    const bool more = j + lead < n;
+                    const int ks = stage;
+                    bool have_k = false;
+    #pragma unroll
+                    for (int w = 0; w < 2; w++) {
+                        if (pc.pair ? j >= g[w].n : w != (j & 1)) continue;
+                        if (!wait(&sh.p_full[w], tiles[w] & 1)) break;
+                        tiles[w]++;
+                        tc_fence_after();
+                        outputs(w, vs, pc.pair ? j == 0 : j < 2);
+                        if (pc.pair ? j + 1 < g[w].n : more) {
+                            if (!have_k && !wait(&sh.kv_full[ks], kv_phase)) break;
+                            have_k = true;
+                            scores(w, pc.pair, ks);
+                        }
+                    }
+                    if (!ok) break;
+                    release(&sh.kv_empty[vs]);
+                    if (more) {
+                        release(&sh.kv_empty[ks]);
+                        next();
+                        if (j + lead == n - 1) release(&sh.q_empty);
+                    }
+                }
+            }
+            if (!ok) {
+                flags |= KDA_DEV_TIMEOUT;
+                // products in flight end before the tensor memory is freed
+                if (lane == 0) mma_commit(&sh.q_empty);
+                __nanosleep(1000000);
+            }
+        }
+    } else {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoftmax));
+        // ------------------------------------------------------------ softmax
+        const int w = warp >> 2, quarter = warp & 3;
+        const int row = 32 * quarter + lane;  // of the row tile, and the TMEM lane
+        const int rtok = row / G, rhead = row % G;
+        const uint32_t ts = tmem_at(tbase, 32 * quarter, TM_S + w * kTile);
+        const uint32_t to = tmem_at(tbase, 32 * quarter, TM_O);
+        int np = 0, merges = 0;
+        int mine = 0, theirs = 0;  // key tiles of this group and of the other so far
+        auto meet = [&] {          // of both groups
+            mbar_arrive(&sh.merge);
+            warp_wait(ok, &sh.merge, merges++ & 1);
+        };
+        auto wait = [&](uint64_t* bar, uint32_t parity) {
+            warp_wait(ok, bar, parity);
+            return ok;
+        };
+        while (ok) {
+            const int i = np % kPieces;
+            if (!wait(&sh.piece_full[i], (np / kPieces) & 1)) break;
+            const Piece pc = sh.pieces[i];
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&sh.piece_empty[i]);
+            np++;
+            if (pc.end) break;
+            const Share g = group_share(pc, w, tok1);
+            const int tok = (pc.pair ? w * tok1 : 0) + rtok;
+            const bool live = row < tok1 * G && tok < pc.ntok;
+            const bool warp_live = __any_sync(0xffffffffu, live);
+            // Keys this row sees; a row of nothing masks nothing (never stored).
+            const int lim = live ? max(pc.pos0 + tok + 1, 0) : 0x7fffffff;
+            float m = -INFINITY, l = 0.f;  // reference (c S) and sum
+            for (int n = 0; n < g.n; n++) {
+                const int base = (pc.kt0 + g.first + n * g.step) * kTile;
+                if (!wait(&sh.s_full[w], mine & 1)) break;
+                tc_fence_after();
+                if (warp_live) {
+                    float x[kTile];
+#pragma unroll
+                    for (int b = 0; b < kTile; b += 32) tmem_ld32(ts + b, x + b);
+                    if (__any_sync(0xffffffffu, base + kTile > lim)) {
+#pragma unroll
+                        for (int e = 0; e < kTile; e++) x[e] = base + e < lim ? x[e] : -INFINITY;
+                    }
+                    float mx[4] = {x[0], x[1], x[2], x[3]};
+#pragma unroll
+                    for (int e = 4; e < kTile; e++) mx[e & 3] = fmaxf(mx[e & 3], x[e]);
+                    const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * p.c;
+                    if (n == 0) {
+                        m = top;
+                    } else if (__any_sync(0xffffffffu, top > m + kRaise)) {
+                        const float mn = fmaxf(m, top);
+                        const float a = mn == -INFINITY ? 1.f : ex2(m - mn);
+                        m = mn;
+                        l *= a;
+                        if (!wait(&sh.pv_done[w], (mine - 1) & 1)) break;
+                        tc_fence_after();
+#pragma unroll
+                        for (int b = 0; b < D; b += 32) {
+                            float y[32];
+                            tmem_ld32(to + w * D + b, y);
+#pragma unroll
+                            for (int e = 0; e < 32; e++) y[e] *= a;
+                            tmem_st16(to + w * D + b, y);
+                            tmem_st16(to + w * D + b + 16, y + 16);
+                        }
+                    }
+                    const float ref = m == -INFINITY ? 0.f : m;
+                    float sum[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                    for (int b = 0; b < kTile; b += 32) {
+                        float pk[16];
+#pragma unroll
+                        for (int e = 0; e < 32; e += 2) {
+                            const float u = ex2(fmaf(x[b + e], p.c, -ref));
+                            const float v = ex2(fmaf(x[b + e + 1], p.c, -ref));
+                            sum[e & 2] += u;
+                            sum[(e & 2) + 1] += v;
+                            pk[e / 2] = __uint_as_float(pack2(u, v));
+                        }
+                        tmem_st16(ts + b / 2, pk);
+                    }
+                    l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+                    tmem_wait_st();
+                }
+                mine++;
+                tc_fence_before();
+                mbar_arrive(&sh.p_full[w]);
+            }
+            if (!ok) break;
+
+            // ------------------------------------------------ the piece's results
+            // Columns [c0, c0 + cn) of the row: all of them, or half when the
+            // two groups hold the same rows.
+            const Share g1 = group_share(pc, 1 - w, tok1);
+            theirs += g1.n;
+            int c0 = 0, cn = D;
+            float a0 = 0.f, a1 = 0.f;  // weights of this group's O and the other's
+            if (pc.pair) {
+                a0 = l == 0.f ? 0.f : 1.f / l;
+            } else {
+                if (w == 1) sh.ml[row] = make_float2(m, l);
+                meet();
+                if (w == 0) {
+                    const float2 other = sh.ml[row];
+                    const float mn = fmaxf(m, other.x);
+                    a0 = m == -INFINITY ? 0.f : ex2(m - mn);
+                    a1 = other.x == -INFINITY ? 0.f : ex2(other.x - mn);
+                    // a NaN sum keeps its NaN through either weight
+                    l = (l == 0.f ? 0.f : l * a0) + (other.y == 0.f ? 0.f : other.y * a1);
+                    m = mn;
+                    const float inv = l == 0.f ? 0.f : 1.f / l;
+                    a0 *= inv;
+                    a1 *= inv;
+                    sh.ml[row] = make_float2(a0, a1);
+                }
+                meet();
+                if (w == 1) {
+                    const float2 both = sh.ml[row];
+                    a0 = both.y;
+                    a1 = both.x;
+                }
+                cn = D / 2;
+                c0 = w * cn;
+                if (g1.n > 0) wait(&sh.pv_done[1 - w], (theirs - 1) & 1);
+            }
+            if (g.n > 0) wait(&sh.pv_done[w], (mine - 1) & 1);
+            if (!ok) break;
+            tc_fence_after();
+            const size_t at = ((size_t)pc.tok0 + tok) * p.s.Hkv * G + (size_t)pc.h * G + rhead;
+            const int srow = (pc.pair ? w * kTile : 0) + row;
+            float* part = pc.slot >= 0 ? p.sp.ws + attn_slot_floats(p.sp.rows, D) * pc.slot : nullptr;
+            if (warp_live) {
+                float fin = 0.f;  // NaN once a value is not finite
+                for (int b = c0; b < c0 + cn; b += 32) {
+                    float y[32];
+                    if (g.n > 0) {
+                        tmem_ld32(to + w * D + b, y);
+#pragma unroll
+                        for (int e = 0; e < 32; e++) y[e] = a0 == 0.f ? 0.f : y[e] * a0;
+                    } else {
+#pragma unroll
+                        for (int e = 0; e < 32; e++) y[e] = 0.f;
+                    }
+                    if (!pc.pair && g1.n > 0) {
+                        float z[32];
+                        tmem_ld32(to + (1 - w) * D + b, z);
+#pragma unroll
+                        for (int e = 0; e < 32; e++) y[e] += a1 == 0.f ? 0.f : z[e] * a1;
+                    }
+#pragma unroll
+                    for (int e = 0; e < 32; e++) fin = fmaf(y[e], 0.f, fin);
+                    if (live) {
+                        if (part) {
+                            float4* dst = reinterpret_cast<float4*>(part + (size_t)srow * D + b);
+#pragma unroll
+                            for (int e = 0; e < 8; e++)
+                                dst[e] = make_float4(y[4 * e], y[4 * e + 1], y[4 * e + 2], y[4 * e + 3]);
+                        } else {
+                            uint4* dst = reinterpret_cast<uint4*>(p.o + at * D + b);
+#pragma unroll
+                            for (int e = 0; e < 4; e++)
+                                dst[e] = make_uint4(pack2(y[8 * e], y[8 * e + 1]),
+                                                    pack2(y[8 * e + 2], y[8 * e + 3]),
+                                                    pack2(y[8 * e + 4], y[8 * e + 5]),
+                                                    pack2(y[8 * e + 6], y[8 * e + 7]));
+                        }
+                    }
+                }
+                if (live && (pc.pair || w == 0)) {
+                    if (part)
+                        part[(size_t)p.sp.rows * D + srow] = l == 0.f ? -INFINITY : m + log2f(l);
+                    else if (p.lse)
+                        p.lse[at] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.69314718056f;
+                }
+                // Rows that are not finite, again over the keys they see.
+                unsigned bad = __ballot_sync(0xffffffffu, live && !(fin == 0.f));
+                while (bad) {
+                    const int src = __ffs(bad) - 1;
+                    bad &= bad - 1;
+                    const int stok = __shfl_sync(0xffffffffu, tok, src);
+                    const int shead = __shfl_sync(0xffffffffu, rhead, src);
+                    const int slim = __shfl_sync(0xffffffffu, lim, src);
+                    const int ssrow = __shfl_sync(0xffffffffu, srow, src);
+                    const int j0 = pc.kt0 * kTile, j1 = min(pc.kt1 * kTile, slim);
+                    const size_t tk = (size_t)pc.tok0 + stok;
+                    const int head = pc.h * G + shead;
+                    for (int b = c0; b < c0 + cn; b += 32) {
+                        float y[1];
+                        const float sum = row_again<D, 1>(p, pc, tk, head, j0, j1, b, y);
+                        y[0] *= sum == 0.f ? 0.f : 1.f / sum;
+                        flags |= finite_flag(y[0]);
+                        if (part) part[(size_t)ssrow * D + b + lane] = y[0];
+                        else p.o[(tk * p.s.Hkv * G + head) * D + b + lane] = __float2bfloat16_rn(y[0]);
+                    }
+                }
+            }
+            tc_fence_before();
+            if (!pc.pair) meet();  // both groups have read both results
+        }
+        if (!ok) flags |= KDA_DEV_TIMEOUT;
+    }
+    __syncwarp();
+    report_flags(p.d_status, flags);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (warp == 0) tmem_dealloc(tbase, 512);
+}
+
+// Rows of packed tokens: [tokens][heads][d], boxes of 64 x heads x tokens.
+bool make_rows(CUtensorMap* m, const void* ptr, int d, int heads, int tokens, long long stride,
+               int box_heads, int box_tokens) {
+    auto enc = tensor_map_encoder();
+    if (!enc) return false;
+    cuuint64_t dims[3] = {(cuuint64_t)d, (cuuint64_t)heads, (cuuint64_t)tokens};
+    cuuint64_t strides[2] = {(cuuint64_t)d * 2, (cuuint64_t)stride * 2};
+    cuuint32_t box[3] = {64, (cuuint32_t)box_heads, (cuuint32_t)box_tokens};
+    cuuint32_t es[3] = {1, 1, 1};
+    return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(ptr), dims, strides, box,
+               es, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+               CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// A cache: [pages][heads][page][d], boxes of 64 x (page or 128) tokens.
+bool make_cache(CUtensorMap* m, const void* ptr, int d, int page, int heads, int pages) {
+    auto enc = tensor_map_encoder();
+    if (!enc) return false;
+    cuuint64_t dims[4] = {(cuuint64_t)d, (cuuint64_t)page, (cuuint64_t)heads, (cuuint64_t)pages};
+    cuuint64_t strides[3] = {(cuuint64_t)d * 2, (cuuint64_t)page * d * 2,
+                             (cuuint64_t)heads * page * d * 2};
+    cuuint32_t box[4] = {64, (cuuint32_t)(page < kTile ? page : kTile), 1, 1};
+    cuuint32_t es[4] = {1, 1, 1, 1};
+    return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(ptr), dims, strides, box,
+               es, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+               CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int D>
+cudaError_t launch_t(const AttnArgs& a) {
+    const int G = a.Hq / a.Hkv, tok1 = kTile / G;
+    const int nsm = attn_sms();
+    TcAttnParams p{};
+    p.s = {a.cu_q, a.kv_len, a.N, a.total_q, a.max_q,
+           (int)min((long long)a.max_pages * a.page, (1LL << 31) - 1), a.Hkv, G, tok1, 2 * tok1,
+           kTile};
+    p.sp = attn_tc_split(a.N, a.total_q, a.max_q, a.Hq, a.Hkv, nsm);
+    if (p.sp.ctas && a.ws &&
+        a.ws_bytes >= 2 * (size_t)p.sp.ctas * attn_slot_floats(p.sp.rows, D) * 4)
+        p.sp.ws = a.ws;
+    p.block_table = a.block_table;
+    p.q = static_cast<const __nv_bfloat16*>(a.q);
+    p.k = static_cast<const __nv_bfloat16*>(a.k);
+    p.v = static_cast<const __nv_bfloat16*>(a.v);
+    p.o = static_cast<__nv_bfloat16*>(a.o);
+    p.lse = a.lse;
+    p.q_stride = a.q_stride;
+    p.k_stride = a.k_stride;
+    p.v_stride = a.v_stride;
+    p.num_pages = a.num_pages;
+    p.page = a.page;
+    p.max_pages = a.max_pages;
+    p.box_q = a.max_q < tok1 ? a.max_q : tok1;
+    p.c = a.scale * 1.44269504089f;
+    p.d_status = a.d_status;
+
+    CUtensorMap mq, mk, mv;
+    bool ok = make_rows(&mq, a.q, D, a.Hq, a.total_q, a.q_stride, G, p.box_q);
+    if (a.kv_len)
+        ok = ok && make_cache(&mk, a.k, D, a.page, a.Hkv, a.num_pages) &&
+             make_cache(&mv, a.v, D, a.page, a.Hkv, a.num_pages);
+    else
+        ok = ok && make_rows(&mk, a.k, D, a.Hkv, a.total_q, a.k_stride, 1, kTile) &&
+             make_rows(&mv, a.v, D, a.Hkv, a.total_q, a.v_stride, 1, kTile);
+    if (!ok) return cudaErrorInvalidValue;
+    auto kernel = kda_attn_tc_kernel<D>;
+    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         TcCfg<D>::SMEM);
+    if (e != cudaSuccess) return e;
+    long long grid = p.sp.ws ? p.sp.ctas : attn_items_bound(p.s);
+    if (grid > nsm) grid = nsm;
+    e = launch_dependent(kernel, dim3((unsigned)grid), dim3(kThreadsTc), TcCfg<D>::SMEM, a.stream,
+                         mq, mk, mv, p);
+    if (e != cudaSuccess || !p.sp.ws) return e;
+    return launch_attn_combine(p.s, p.sp, D, kTile, a.o, a.lse, KDA_BF16, a.d_status, a.stream);
+}
+
+}  // namespace
+
+AttnSplit attn_tc_split(int N, int total_q, int max_q, int Hq, int Hkv, int nsm) {
+    AttnSplit sp{};
+    if (N == 0 || total_q == 0 || max_q == 0 || Hkv == 0 || nsm == 0) return sp;
+    const int G = Hq / Hkv, tok1 = kTile / G;
+    // Enough items to fill the SMs evenly on their own: whole ones.
+    const long long items = (long long)total_q / (2 * tok1) * Hkv;
+    if (max_q > tok1 && items >= 8LL * nsm) return sp;
+    sp.ctas = nsm;
+    sp.least = 2;
+    sp.rows = max_q <= tok1 ? (max_q * G + 3) & ~3 : 2 * kTile;  // whole 16-byte vectors
+    return sp;
+}
+
+cudaError_t launch_attn_tc(const AttnArgs& a) {
+    return a.d == 128 ? launch_t<128>(a) : launch_t<64>(a);
+}
+
+}  // namespace kda
