@@ -86,23 +86,25 @@ __device__ __forceinline__ int attn_item_keys(const AttnReq& q, int t) {
     return max(q.kv - q.q_len + last, 0);
 }
 
-// sum_{i < n} floor((a i + b) / m) for non-negative arguments: the multiples of
-// m in a and b are taken out, and what is left counts the lattice points under
-// a line, which are those beside it with the axes exchanged (Euclid's steps).
-__device__ __forceinline__ long long attn_floor_sum(long long n, long long m, long long a,
-                                                    long long b) {
+// sum_{i < n} floor((a i + b) / m): the multiples of m in a and b are taken out,
+// and what is left counts the lattice points under a line, which are those
+// beside it with the axes exchanged (Euclid's steps; two or three for the tile
+// sizes here). a n + b below 2^32.
+__device__ __forceinline__ long long attn_floor_sum(uint32_t n, uint32_t m, uint32_t a,
+                                                    uint32_t b) {
     long long sum = 0;
     while (n > 0) {
-        sum += n * (n - 1) / 2 * (a / m) + n * (b / m);
-        a %= m;
-        b %= m;
-        const long long top = a * n + b;
+        const uint32_t qa = a / m, qb = b / m;
+        sum += ((long long)n * (n - 1) >> 1) * qa + (long long)n * qb;
+        a -= qa * m;
+        b -= qb * m;
+        if (a == 0) break;
+        const uint32_t top = a * n + b;
         n = top / m;
-        b = top % m;
-        const long long x = m;
+        b = top - n * m;
+        const uint32_t x = m;
         m = a;
         a = x;
-        if (m == 0) break;  // n is 0 then: top < m
     }
     return sum;
 }
@@ -114,13 +116,13 @@ __device__ __forceinline__ int attn_item_units(const AttnShape& s, const AttnReq
 }
 __device__ __forceinline__ long long attn_units_before(const AttnShape& s, const AttnReq& q, int t) {
     if (t <= 0) return 0;
+    if (q.nqt == 1) return attn_item_units(s, q, 0);
     const int full = min(t, q.nqt - 1);  // items whose tokens are all there
-    const long long off = (long long)q.kv - q.q_len;
+    const int off = q.kv - q.q_len;
     // Items that see at most one tile count one each.
-    long long one = off + q.tok <= s.kt ? ((long long)s.kt - off) / q.tok : 0;
-    one = one < full ? one : full;
-    const long long rest = full - one;
-    long long sum = one + attn_floor_sum(rest, s.kt, q.tok, off + (one + 1) * q.tok + s.kt - 1);
+    int one = off + q.tok <= s.kt ? (s.kt - off) / q.tok : 0;
+    one = min(one, full);
+    long long sum = one + attn_floor_sum(full - one, s.kt, q.tok, off + (one + 1) * q.tok + s.kt - 1);
     if (t == q.nqt) sum += attn_item_units(s, q, t - 1);
     return sum;
 }
@@ -177,11 +179,13 @@ __device__ __forceinline__ void attn_unit_item(const AttnShape& s, const AttnReq
     const long long per = attn_units_before(s, q, q.nqt);
     *h = (int)(in / per);
     const long long rest = in - *h * per;
-    int lo = 0, hi = q.nqt;  // units_before(lo) <= rest < units_before(hi)
+    // units_before(lo) <= rest < units_before(hi); 32 places at a time
+    int lo = 0, hi = q.nqt;
     while (hi - lo > 1) {
-        const int mid = (lo + hi) >> 1;
-        if (attn_units_before(s, q, mid) <= rest) lo = mid;
-        else hi = mid;
+        const int step = (hi - lo + 31) >> 5, at = lo + (int)(threadIdx.x & 31) * step;
+        const bool below = at < hi && attn_units_before(s, q, at) <= rest;
+        lo += (__popc(__ballot_sync(0xffffffffu, below)) - 1) * step;
+        hi = min(lo + step, hi);
     }
     *t = lo;
     *tile = (int)(rest - attn_units_before(s, q, lo));

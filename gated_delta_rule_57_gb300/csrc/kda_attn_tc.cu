@@ -8,10 +8,11 @@
 // (bf16 and fp32 keep their relative precision there) and after a few key
 // tiles O is hardly ever touched.
 //
-// One CTA per SM, ten warps:
+// One CTA per SM:
 //   warps 0..3, 4..7  two softmax groups, one row of S per thread
-//   warp 8            issues the products (and zeroes V past the last key)
+//   warp 8            issues the products
 //   warp 9            finds the work and issues the loads
+//   warp 10           zeroes V past the last key
 // A group's loop: S (TMEM, 128 lanes x 128 columns fp32) -> registers, mask,
 // maximum, exponentials, P as bf16 pairs into the first half of S's columns, and
 // the second product reads P from there as its A operand. While one group
@@ -40,11 +41,11 @@ namespace {
 using namespace ptx;
 
 constexpr int kTile = 128;         // rows of a row tile, keys of a key tile
-constexpr int kThreadsTc = 384;    // three warpgroups; the last two warps only make up the third
+constexpr int kThreadsTc = 384;    // three warpgroups; the last warp only makes up the third
 // Registers per thread: launched with 168 (64512 in all), then 200 for the two
 // softmax groups and 104 for the third (64512).
 constexpr int kRegsSoftmax = 200, kRegsOther = 104;
-constexpr int kMmaWarp = 8, kLoadWarp = 9;
+constexpr int kMmaWarp = 8, kLoadWarp = 9, kTailWarp = 10;
 constexpr int kPieces = 4;         // pieces announced ahead
 constexpr float kRaise = 8.f;      // log2 growth of a row maximum that moves its reference
 
@@ -119,6 +120,25 @@ __device__ __forceinline__ uint32_t pack2(float a, float b) {
     __nv_bfloat162 v = __floats2bfloat162_rn(a, b);
     return *reinterpret_cast<uint32_t*>(&v);
 }
+// Two fp32 operations in one instruction.
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+    float2 d;
+    asm("{\n\t.reg .b64 a, b, c, d;\n\t"
+        "mov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\tmov.b64 c, {%6, %7};\n\t"
+        "fma.rn.f32x2 d, a, b, c;\n\tmov.b64 {%0, %1}, d;\n\t}"
+        : "=f"(d.x), "=f"(d.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+    return d;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+    float2 d;
+    asm("{\n\t.reg .b64 a, b, d;\n\t"
+        "mov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\t"
+        "add.rn.f32x2 d, a, b;\n\tmov.b64 {%0, %1}, d;\n\t}"
+        : "=f"(d.x), "=f"(d.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+    return d;
+}
 // A bounded wait by a whole warp, with one outcome for all its lanes.
 __device__ __forceinline__ void warp_wait(bool& ok, uint64_t* bar, uint32_t parity) {
     if (ok) ok = mbar_wait(bar, parity);
@@ -128,7 +148,9 @@ __device__ __forceinline__ void warp_wait(bool& ok, uint64_t* bar, uint32_t pari
 struct Shared {
     uint64_t kv_full[8], kv_empty[8];
     uint64_t q_full, q_empty;
-    uint64_t s_full[2], p_full[2], pv_done[2];
+    uint64_t s_full[2], p_full[2][2];  // of each group; P per half of the keys
+    uint64_t o_full[2];             // a piece's last product
+    uint64_t v_clean[8];            // a V tile of the ring has zeros past the keys
     uint64_t merge;  // both softmax groups
     uint64_t piece_full[kPieces], piece_empty[kPieces];
     Piece pieces[kPieces];
@@ -202,23 +224,26 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
     unsigned char* skv = sm + 2 * C::TILE_BYTES;   // the ring
     __shared__ Shared sh;
 
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int tid = threadIdx.x, lane = tid & 31;
+    const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);  // uniform, and known to be
     if (tid == 0) {
         for (int i = 0; i < NS; i++) {
             mbar_init(&sh.kv_full[i], 1);
-            mbar_init(&sh.kv_empty[i], 1);
+            mbar_init(&sh.kv_empty[i], 2);  // read by the products, seen by the V warp
+            mbar_init(&sh.v_clean[i], 1);
         }
         mbar_init(&sh.q_full, 1);
         mbar_init(&sh.q_empty, 1);
         for (int w = 0; w < 2; w++) {
             mbar_init(&sh.s_full[w], 1);
-            mbar_init(&sh.p_full[w], 128);
-            mbar_init(&sh.pv_done[w], 1);
+            mbar_init(&sh.p_full[w][0], 128);
+            mbar_init(&sh.p_full[w][1], 128);
+            mbar_init(&sh.o_full[w], 1);
         }
         mbar_init(&sh.merge, 256);
         for (int i = 0; i < kPieces; i++) {
             mbar_init(&sh.piece_full[i], 1);
-            mbar_init(&sh.piece_empty[i], 9);
+            mbar_init(&sh.piece_empty[i], 10);  // softmax, products, V
         }
         fence_mbarrier_init();
         prefetch_tensormap(&map_q);
@@ -386,11 +411,17 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
             }
         } else if (warp == kMmaWarp) {
             // ------------------------------------------------------------ products
+            // What this warp does between two products shows as idle tensor core.
+            // All of it is uniform, so that stages and descriptors stay in uniform
+            // registers, and one elected lane issues.
             int stage = 0, kv_phase = 0, q_phase = 0, np = 0;
-            int tiles[2] = {0, 0};  // tiles of each group so far
-            const uint32_t idesc_s = idesc_bf16(kTile, kTile, 0, 0);
-            const uint32_t idesc_o = idesc_bf16(kTile, D, 0, 1);
-            const uint32_t aq = smem_addr(sq), akv = smem_addr(skv);
+            int tiles0 = 0, tiles1 = 0;  // parities of the groups' tiles so far
+            uint32_t cleaned = 0;        // parity of v_clean, a bit per tile of the ring
+            constexpr uint32_t idesc_s = idesc_bf16(kTile, kTile, 0, 0);
+            constexpr uint32_t idesc_o = idesc_bf16(kTile, D, 0, 1);
+            const uint64_t dq = desc_kmajor(smem_addr(sq));
+            const uint64_t dk = desc_kmajor(smem_addr(skv)), dv = desc_mnmajor(smem_addr(skv), kTile);
+            constexpr uint32_t TILE = C::TILE_BYTES >> 4;  // a tile in descriptor units
             auto next = [&] {
                 if (++stage == NS) {
                     stage = 0;
@@ -398,14 +429,14 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
                 }
             };
             auto wait = [&](uint64_t* bar, uint32_t parity) {
-                warp_wait(ok, bar, parity);
+                if (!__all_sync(0xffffffffu, mbar_wait(bar, parity))) ok = false;
                 return ok;
             };
-            auto scores = [&](int w, int pair, uint32_t kstage) {  // S_w = Q_w K^T
-                if (lane == 0) {
-                    const uint64_t a = desc_kmajor(aq + (pair ? w : 0) * C::TILE_BYTES);
-                    const uint64_t b = desc_kmajor(akv + kstage * C::TILE_BYTES);
-    #pragma unroll
+            auto uniform = [](int x) { return __shfl_sync(0xffffffffu, x, 0); };
+            auto scores = [&](int w, uint32_t qtile, uint32_t kstage) {  // S_w = Q_w K^T
+                const uint64_t a = dq + qtile * TILE, b = dk + kstage * TILE;
+                if (elect_one()) {
+#pragma unroll
                     for (int kk = 0; kk < D / 16; kk++)
                         mma_bf16(tbase + TM_S + w * kTile, a + kstep_kmajor(kTile, kk),
                                  b + kstep_kmajor(kTile, kk), idesc_s, kk > 0);
@@ -413,90 +444,173 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
                 }
                 __syncwarp();
             };
-            auto outputs = [&](int w, uint32_t vstage, bool first) {  // O_w += P_w V
-                if (lane == 0) {
-                    const uint64_t b = desc_mnmajor(akv + vstage * C::TILE_BYTES, kTile);
-    #pragma unroll
-                    for (int kk = 0; kk < kTile / 16; kk++)
+            // O_w += P_w V over one half of the key tile
+            auto outputs = [&](int w, uint32_t vstage, int half, uint32_t add) {
+                const uint64_t b = dv + vstage * TILE;
+                if (elect_one()) {
+#pragma unroll
+                    for (int i = 0; i < kTile / 32; i++) {
+                        const int kk = half * (kTile / 32) + i;
                         mma_bf16_ta(tbase + TM_O + w * D, tbase + TM_S + w * kTile + 8 * kk,
-                                    b + kstep_mnmajor(kk), idesc_o, !first || kk > 0);
-                    mma_commit(&sh.pv_done[w]);
+                                    b + kstep_mnmajor(kk), idesc_o, kk > 0 ? 1 : add);
+                    }
                 }
                 __syncwarp();
             };
-            auto release = [&](uint64_t* bar) {
-                if (lane == 0) mma_commit(bar);
+            auto commit = [&](uint64_t* bar) {
+                if (elect_one()) mma_commit(bar);
                 __syncwarp();
             };
             while (ok) {
                 const int i = np % kPieces;
                 if (!wait(&sh.piece_full[i], (np / kPieces) & 1)) break;
-                const Piece pc = sh.pieces[i];
-                __syncwarp();
+                const Piece& pc = sh.pieces[i];
+                const int end = uniform(pc.end), n = uniform(piece_tiles(pc)), pair = uniform(pc.pair);
+                const int n0 = uniform(group_share(pc, 0, tok1).n), n1 = uniform(group_share(pc, 1, tok1).n);
+                const int tail = uniform(pc.keys < (pc.kt0 + n) * kTile);
                 if (lane == 0) mbar_arrive(&sh.piece_empty[i]);
                 np++;
-                if (pc.end) break;
-                const int n = piece_tiles(pc), lead = pc.pair ? 1 : 2;
+                if (end) break;
                 if (n == 0) continue;
-                const Share g[2] = {group_share(pc, 0, tok1), group_share(pc, 1, tok1)};
                 if (!wait(&sh.q_full, q_phase)) break;
                 q_phase ^= 1;
-                for (int j = 0; j < lead && j < n; j++) {
+                if (pair) {
+                    // Two row tiles on every key tile.
                     if (!wait(&sh.kv_full[stage], kv_phase)) break;
                     tc_fence_after();
-    #pragma unroll
-                    for (int w = 0; w < 2; w++)
-                        if (pc.pair ? g[w].n > 0 : w == j) scores(w, pc.pair, stage);
-                    release(&sh.kv_empty[stage]);
+                    if (n0 > 0) scores(0, 0, stage);
+                    if (n1 > 0) scores(1, 1, stage);
+                    commit(&sh.kv_empty[stage]);
                     next();
-                }
-                if (n <= lead) release(&sh.q_empty);
-                for (int j = 0; j < n && ok; j++) {
-                    const int vs = stage;
-                    if (!wait(&sh.kv_full[vs], kv_phase)) break;
-                    next();
-                    const int dead = pc.keys - (pc.kt0 + j) * kTile;  // first row past the keys
-                    if (dead < kTile) {
-                        unsigned char* v = skv + vs * C::TILE_BYTES;
-    #pragma unroll
-                        for (int half = 0; half < HALVES; half++)
-                            for (int b = dead * 128 + lane * 16; b < kTile * 128; b += 512)
-                                *reinterpret_cast<uint4*>(v + half * (kTile * 128) + b) =
-                                    make_uint4(0, 0, 0, 0);
-                        fence_proxy_async_smem();
-                        __syncwarp();
-                    }
-                    const bool more = j + lead < n;
-                    const int ks = stage;
-                    bool have_k = false;
-    #pragma unroll
-                    for (int w = 0; w < 2; w++) {
-                        if (pc.pair ? j >= g[w].n : w != (j & 1)) continue;
-                        if (!wait(&sh.p_full[w], tiles[w] & 1)) break;
-                        tiles[w]++;
-                        tc_fence_after();
-                        outputs(w, vs, pc.pair ? j == 0 : j < 2);
-                        if (pc.pair ? j + 1 < g[w].n : more) {
-                            if (!have_k && !wait(&sh.kv_full[ks], kv_phase)) break;
-                            have_k = true;
-                            scores(w, pc.pair, ks);
+                    if (n == 1) commit(&sh.q_empty);
+                    for (int j = 0; j < n; j++) {
+                        const int vs = stage;
+                        if (!wait(&sh.kv_full[vs], kv_phase)) break;
+                        next();
+                        const bool more = j + 1 < n;
+                        const int ks = stage;
+                        if (more) {
+                            if (!wait(&sh.kv_full[ks], kv_phase)) break;
+                        } else if (tail) {
+                            if (!wait(&sh.v_clean[vs], cleaned >> vs & 1)) break;
+                            cleaned ^= 1u << vs;
+                        }
+                        if (j < n0) {
+                            if (!wait(&sh.p_full[0][0], tiles0)) break;
+                            tc_fence_after();
+                            outputs(0, vs, 0, j > 0);
+                            if (!wait(&sh.p_full[0][1], tiles0)) break;
+                            tc_fence_after();
+                            outputs(0, vs, 1, 1);
+                            tiles0 ^= 1;
+                            if (j + 1 < n0) scores(0, 0, ks);
+                            else commit(&sh.o_full[0]);
+                        }
+                        if (j < n1) {
+                            if (!wait(&sh.p_full[1][0], tiles1)) break;
+                            tc_fence_after();
+                            outputs(1, vs, 0, j > 0);
+                            if (!wait(&sh.p_full[1][1], tiles1)) break;
+                            tc_fence_after();
+                            outputs(1, vs, 1, 1);
+                            tiles1 ^= 1;
+                            if (j + 1 < n1) scores(1, 1, ks);
+                            else commit(&sh.o_full[1]);
+                        }
+                        commit(&sh.kv_empty[vs]);
+                        if (more) {
+                            commit(&sh.kv_empty[ks]);
+                            next();
+                            if (j + 2 == n) commit(&sh.q_empty);
                         }
                     }
-                    if (!ok) break;
-                    release(&sh.kv_empty[vs]);
-                    if (more) {
-                        release(&sh.kv_empty[ks]);
+                } else {
+                    // One row tile, key tiles in turn to the two groups.
+                    for (int j = 0; j < 2 && j < n; j++) {
+                        if (!wait(&sh.kv_full[stage], kv_phase)) break;
+                        tc_fence_after();
+                        scores(j, 0, stage);
+                        commit(&sh.kv_empty[stage]);
                         next();
-                        if (j + lead == n - 1) release(&sh.q_empty);
+                    }
+                    if (n <= 2) commit(&sh.q_empty);
+                    for (int j = 0; j < n && ok; j++) {
+                        const int vs = stage, w = j & 1;
+                        if (!wait(&sh.kv_full[vs], kv_phase)) break;
+                        next();
+                        const bool more = j + 2 < n;
+                        const int ks = stage;
+                        if (j + 1 == n && tail) {
+                            if (!wait(&sh.v_clean[vs], cleaned >> vs & 1)) break;
+                            cleaned ^= 1u << vs;
+                        }
+                        const int parity = w ? tiles1 : tiles0;
+                        if (!wait(&sh.p_full[w][0], parity)) break;
+                        tc_fence_after();
+                        outputs(w, vs, 0, j > 1);
+                        if (!wait(&sh.p_full[w][1], parity)) break;
+                        tc_fence_after();
+                        outputs(w, vs, 1, 1);
+                        tiles0 ^= w ^ 1;
+                        tiles1 ^= w;
+                        commit(&sh.kv_empty[vs]);
+                        if (more) {
+                            if (!wait(&sh.kv_full[ks], kv_phase)) break;
+                            scores(w, 0, ks);
+                            commit(&sh.kv_empty[ks]);
+                            next();
+                            if (j + 3 == n) commit(&sh.q_empty);
+                        } else {
+                            commit(&sh.o_full[w]);
+                        }
                     }
                 }
             }
             if (!ok) {
                 flags |= KDA_DEV_TIMEOUT;
                 // products in flight end before the tensor memory is freed
-                if (lane == 0) mma_commit(&sh.q_empty);
+                commit(&sh.q_empty);
                 __nanosleep(1000000);
             }
+        } else if (warp == kTailWarp) {
+            // ------------------------------------------------------------ V past the keys
+            // It sees every tile of the ring go by (so that no phase of a barrier
+            // passes unseen), and the last one of a piece is its last V tile.
+            int stage = 0, kv_phase = 0, np = 0;
+            while (ok) {
+                const int i = np % kPieces;
+                warp_wait(ok, &sh.piece_full[i], (np / kPieces) & 1);
+                if (!ok) break;
+                const Piece pc = sh.pieces[i];
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&sh.piece_empty[i]);
+                np++;
+                if (pc.end) break;
+                const int n = piece_tiles(pc);
+                const int dead = pc.keys - (pc.kt0 + n - 1) * kTile;  // first row past the keys
+                for (int j = 0; j < 2 * n; j++) {
+                    warp_wait(ok, &sh.kv_full[stage], kv_phase);
+                    if (!ok) break;
+                    if (j == 2 * n - 1 && dead < kTile) {
+                        unsigned char* v = skv + stage * C::TILE_BYTES;
+#pragma unroll
+                        for (int half = 0; half < HALVES; half++)
+                            for (int b = dead * 128 + lane * 16; b < kTile * 128; b += 512)
+                                *reinterpret_cast<uint4*>(v + half * (kTile * 128) + b) =
+                                    make_uint4(0, 0, 0, 0);
+                        fence_proxy_async_smem();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(&sh.v_clean[stage]);
+                    }
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&sh.kv_empty[stage]);
+                    if (++stage == NS) {
+                        stage = 0;
+                        kv_phase ^= 1;
+                    }
+                }
+            }
+            if (!ok) flags |= KDA_DEV_TIMEOUT;
         }
     } else {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoftmax));
@@ -507,7 +621,8 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
         const uint32_t ts = tmem_at(tbase, 32 * quarter, TM_S + w * kTile);
         const uint32_t to = tmem_at(tbase, 32 * quarter, TM_O);
         int np = 0, merges = 0;
-        int mine = 0, theirs = 0;  // key tiles of this group and of the other so far
+        int mine = 0;              // key tiles of this group so far
+        int done = 0, theirs = 0;  // pieces with some, of this group and of the other
         auto meet = [&] {          // of both groups
             mbar_arrive(&sh.merge);
             warp_wait(ok, &sh.merge, merges++ & 1);
@@ -536,16 +651,32 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
                 if (!wait(&sh.s_full[w], mine & 1)) break;
                 tc_fence_after();
                 if (warp_live) {
-                    float x[kTile];
+                    uint32_t xr[kTile];
+                    float* x = reinterpret_cast<float*>(xr);
+                    // The second half is on its way while the first is looked at.
+                    tmem_ld64_async(ts, xr);
+                    tmem_wait_ld();
+                    tmem_landed<64>(xr);
+                    tmem_ld64_async(ts + 64, xr + 64);
+                    const bool edge = __any_sync(0xffffffffu, base + kTile > lim);
+                    float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-                    for (int b = 0; b < kTile; b += 32) tmem_ld32(ts + b, x + b);
-                    if (__any_sync(0xffffffffu, base + kTile > lim)) {
+                    for (int b = 0; b < kTile; b += 64) {
+                        if (b > 0) {
+                            tmem_wait_ld();
+                            tmem_landed<64>(xr + 64);
+                        }
+                        if (edge) {
 #pragma unroll
-                        for (int e = 0; e < kTile; e++) x[e] = base + e < lim ? x[e] : -INFINITY;
+                            for (int e = b; e < b + 64; e++)
+                                x[e] = base + e < lim ? x[e] : -INFINITY;
+                        }
+#pragma unroll
+                        for (int e = b; e < b + 64; e += 8)
+#pragma unroll
+                            for (int i = 0; i < 4; i++)
+                                mx[i] = fmaxf(fmaxf(mx[i], x[e + i]), x[e + i + 4]);
                     }
-                    float mx[4] = {x[0], x[1], x[2], x[3]};
-#pragma unroll
-                    for (int e = 4; e < kTile; e++) mx[e & 3] = fmaxf(mx[e & 3], x[e]);
                     const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * p.c;
                     if (n == 0) {
                         m = top;
@@ -554,8 +685,7 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
                         const float a = mn == -INFINITY ? 1.f : ex2(m - mn);
                         m = mn;
                         l *= a;
-                        if (!wait(&sh.pv_done[w], (mine - 1) & 1)) break;
-                        tc_fence_after();
+                        // (S of this tile is there, so the products before it are done)
 #pragma unroll
                         for (int b = 0; b < D; b += 32) {
                             float y[32];
@@ -567,26 +697,34 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
                         }
                     }
                     const float ref = m == -INFINITY ? 0.f : m;
-                    float sum[4] = {0.f, 0.f, 0.f, 0.f};
+                    const float2 c2 = make_float2(p.c, p.c), ref2 = make_float2(-ref, -ref);
+                    float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
                     for (int b = 0; b < kTile; b += 32) {
                         float pk[16];
 #pragma unroll
                         for (int e = 0; e < 32; e += 2) {
-                            const float u = ex2(fmaf(x[b + e], p.c, -ref));
-                            const float v = ex2(fmaf(x[b + e + 1], p.c, -ref));
-                            sum[e & 2] += u;
-                            sum[(e & 2) + 1] += v;
-                            pk[e / 2] = __uint_as_float(pack2(u, v));
+                            float2 u = fma2(make_float2(x[b + e], x[b + e + 1]), c2, ref2);
+                            u.x = ex2(u.x);
+                            u.y = ex2(u.y);
+                            sum[(e >> 1) & 1] = add2(sum[(e >> 1) & 1], u);
+                            pk[e / 2] = __uint_as_float(pack2(u.x, u.y));
                         }
                         tmem_st16(ts + b / 2, pk);
+                        if (b == kTile / 2 - 32) {  // the second product may start on this half
+                            tmem_wait_st();
+                            tc_fence_before();
+                            mbar_arrive(&sh.p_full[w][0]);
+                        }
                     }
-                    l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+                    l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
                     tmem_wait_st();
+                } else {
+                    mbar_arrive(&sh.p_full[w][0]);
                 }
                 mine++;
                 tc_fence_before();
-                mbar_arrive(&sh.p_full[w]);
+                mbar_arrive(&sh.p_full[w][1]);
             }
             if (!ok) break;
 
@@ -594,7 +732,8 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
             // Columns [c0, c0 + cn) of the row: all of them, or half when the
             // two groups hold the same rows.
             const Share g1 = group_share(pc, 1 - w, tok1);
-            theirs += g1.n;
+            done += g.n > 0;
+            theirs += g1.n > 0;
             int c0 = 0, cn = D;
             float a0 = 0.f, a1 = 0.f;  // weights of this group's O and the other's
             if (pc.pair) {
@@ -623,9 +762,9 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
                 }
                 cn = D / 2;
                 c0 = w * cn;
-                if (g1.n > 0) wait(&sh.pv_done[1 - w], (theirs - 1) & 1);
+                if (g1.n > 0) wait(&sh.o_full[1 - w], (theirs - 1) & 1);
             }
-            if (g.n > 0) wait(&sh.pv_done[w], (mine - 1) & 1);
+            if (g.n > 0) wait(&sh.o_full[w], (done - 1) & 1);
             if (!ok) break;
             tc_fence_after();
             const size_t at = ((size_t)pc.tok0 + tok) * p.s.Hkv * G + (size_t)pc.h * G + rhead;
