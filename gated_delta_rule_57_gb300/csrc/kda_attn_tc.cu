@@ -8,11 +8,13 @@
 // (bf16 and fp32 keep their relative precision there) and after a few key
 // tiles O is hardly ever touched.
 //
-// One CTA per SM:
+// One CTA per SM, four warpgroups:
 //   warps 0..3, 4..7  two softmax groups, one row of S per thread
 //   warp 8            issues the products
 //   warp 9            finds the work and issues the loads
-//   warp 10           zeroes V past the last key
+//   warp 10           zeroes V past the last key (warp 11 idles)
+//   warps 12..15      the results: O / l, merging, stores
+// Every wait has a limit, after which the kernel reports KDA_DEV_TIMEOUT.
 // A group's loop: S (TMEM, 128 lanes x 128 columns fp32) -> registers, mask,
 // maximum, exponentials, P as bf16 pairs into the first half of S's columns, and
 // the second product reads P from there as its A operand. While one group
@@ -41,10 +43,10 @@ namespace {
 using namespace ptx;
 
 constexpr int kTile = 128;         // rows of a row tile, keys of a key tile
-constexpr int kThreadsTc = 384;    // three warpgroups; the last warp only makes up the third
-// Registers per thread: launched with 168 (64512 in all), then 200 for the two
-// softmax groups and 104 for the third (64512).
-constexpr int kRegsSoftmax = 200, kRegsOther = 104;
+constexpr int kThreadsTc = 512;
+// Registers per thread: launched with 128 (65536 in all), then by warpgroup.
+constexpr int kRegsSoftmax = 192, kRegsOther = 64, kRegsResult = 64;
+static_assert(2 * kRegsSoftmax + kRegsOther + kRegsResult <= 4 * 128, "more than launched with");
 constexpr int kMmaWarp = 8, kLoadWarp = 9, kTailWarp = 10;
 constexpr int kPieces = 4;         // pieces announced ahead
 constexpr float kRaise = 8.f;      // log2 growth of a row maximum that moves its reference
@@ -53,7 +55,7 @@ template <int D>
 struct TcCfg {
     static constexpr int TILE_BYTES = kTile * D * 2;
     static constexpr int STAGES = D == 128 ? 5 : 8;
-    static constexpr int SMEM = (2 + STAGES) * TILE_BYTES + 1024;
+    static constexpr int TILES = (2 + STAGES) * TILE_BYTES;
 };
 
 struct TcAttnParams {
@@ -147,24 +149,29 @@ __device__ __forceinline__ void warp_wait(bool& ok, uint64_t* bar, uint32_t pari
 
 struct Shared {
     uint64_t kv_full[8], kv_empty[8];
+    uint64_t v_clean[8];            // a V tile of the ring has zeros past the keys
     uint64_t q_full, q_empty;
     uint64_t s_full[2], p_full[2][2];  // of each group; P per half of the keys
-    uint64_t o_full[2];             // a piece's last product
-    uint64_t v_clean[8];            // a V tile of the ring has zeros past the keys
-    uint64_t merge;  // both softmax groups
+    uint64_t o_full[2];             // a piece's last product of a group
+    uint64_t ml_full[2];            // and its references and sums
+    uint64_t o_free[2];             // both have been read
     uint64_t piece_full[kPieces], piece_empty[kPieces];
     Piece pieces[kPieces];
-    float2 ml[kTile];  // merging the groups: (reference, sum) of group 1's rows, then both weights
+    float2 ml[2][kTile];            // reference and sum of each row
     long long sum[kThreadsTc / 32];
     uint32_t tmem;
 };
+template <int D>
+constexpr int tc_smem() {
+    return TcCfg<D>::TILES + (int)sizeof(Shared);
+}
+static_assert(tc_smem<128>() <= 227 * 1024, "shared memory of a CTA");
 
-// One row again, a warp together, over exactly the keys [j0, j1) that it sees,
-// columns c0 .. c0 + 32 V - 1; lane l holds columns c0 + l + 32 e of acc.
-// Returns the sum of exponentials (0: none).
-template <int D, int V>
+// One row again, a warp together, over exactly the keys [j0, j1) that it sees;
+// lane l holds columns l + 32 e of acc. Returns the sum of exponentials.
+template <int D>
 __device__ float row_again(const TcAttnParams& p, const Piece& pc, size_t tok, int head, int j0,
-                           int j1, int c0, float* acc) {
+                           int j1, float* acc) {
     const int lane = threadIdx.x & 31;
     constexpr int E = D / 32;
     float q[E];
@@ -173,7 +180,7 @@ __device__ float row_again(const TcAttnParams& p, const Piece& pc, size_t tok, i
     for (int e = 0; e < E; e++) q[e] = __bfloat162float(gq[lane + 32 * e]);
     float m = -INFINITY, l = 0.f;
 #pragma unroll
-    for (int e = 0; e < V; e++) acc[e] = 0.f;
+    for (int e = 0; e < E; e++) acc[e] = 0.f;
     for (int j = j0; j < j1; j++) {
         const __nv_bfloat16 *gk, *gv;
         if (p.block_table) {
@@ -203,8 +210,8 @@ __device__ float row_again(const TcAttnParams& p, const Piece& pc, size_t tok, i
         m = mn;
         l = l * a + w;
 #pragma unroll
-        for (int e = 0; e < V; e++)
-            acc[e] = acc[e] * a + (gv ? w * __bfloat162float(gv[c0 + lane + 32 * e]) : 0.f);
+        for (int e = 0; e < E; e++)
+            acc[e] = acc[e] * a + (gv ? w * __bfloat162float(gv[lane + 32 * e]) : 0.f);
     }
     return l;
 }
@@ -218,11 +225,14 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
     using C = TcCfg<D>;
     constexpr int NS = C::STAGES, HALVES = D / 64;
     constexpr uint32_t TM_S = 0, TM_O = 256;
-    extern __shared__ __align__(1024) unsigned char smem_raw[];
-    unsigned char* sm = smem_raw + ((1024u - (smem_addr(smem_raw) & 1023u)) & 1023u);
+    extern __shared__ __align__(1024) unsigned char sm[];  // 128-byte swizzle: 1024-byte tiles
     unsigned char* sq = sm;                        // two Q tiles
     unsigned char* skv = sm + 2 * C::TILE_BYTES;   // the ring
-    __shared__ Shared sh;
+    Shared& sh = *reinterpret_cast<Shared*>(sm + C::TILES);
+    if (smem_addr(sm) & 1023u) {  // never, by the declaration above
+        if (threadIdx.x == 0 && p.d_status) atomicOr(p.d_status, KDA_DEV_TIMEOUT);
+        return;
+    }
 
     const int tid = threadIdx.x, lane = tid & 31;
     const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);  // uniform, and known to be
@@ -239,11 +249,12 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
             mbar_init(&sh.p_full[w][0], 128);
             mbar_init(&sh.p_full[w][1], 128);
             mbar_init(&sh.o_full[w], 1);
+            mbar_init(&sh.ml_full[w], 128);
+            mbar_init(&sh.o_free[w], 128);
         }
-        mbar_init(&sh.merge, 256);
         for (int i = 0; i < kPieces; i++) {
             mbar_init(&sh.piece_full[i], 1);
-            mbar_init(&sh.piece_empty[i], 10);  // softmax, products, V
+            mbar_init(&sh.piece_empty[i], 14);  // softmax 8, products, V, results 4
         }
         fence_mbarrier_init();
         prefetch_tensormap(&map_q);
@@ -266,39 +277,43 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
     int flags = 0;
     bool ok = true;
 
-    if (warp >= 8) {
+    if (warp >= 8 && warp < 12) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsOther));
         if (warp == kLoadWarp) {
             // ------------------------------------------------------------ work and loads
             int stage = 0, kv_phase = 0, q_phase = 0, np = 0;
-            auto load_kv = [&](const Piece& pc, const CUtensorMap* map, int kt) {
+            // Paged: a tile is `per` pages (or part of one); lane `pg` of each half
+            // loads one. Their ids are read a tile or more ahead of their use.
+            const int log2_page = __ffs(p.page) - 1;
+            const int per = p.block_table && p.page < kTile ? kTile >> log2_page : 1;
+            const int pg = lane & (per - 1), half = lane / per;
+            auto page_id = [&](const Piece& pc, int kt) {
+                // past the keys, or no page: beyond the cache, which loads zeros
+                int id = p.num_pages;
+                const int j = kt * kTile + (pg << log2_page);  // first key of the lane's part
+                if (half < HALVES && j < pc.kv) {
+                    id = p.block_table[(size_t)pc.r * p.max_pages + (j >> log2_page)];
+                    if (id < 0 || id >= p.num_pages) {
+                        id = p.num_pages;
+                        flags |= KDA_DEV_PAGES;
+                    }
+                }
+                return id;
+            };
+            auto load_kv = [&](const Piece& pc, const CUtensorMap* map, int kt, int id) {
                 warp_wait(ok, &sh.kv_empty[stage], kv_phase ^ 1);
                 if (!ok) return;
                 unsigned char* dst = skv + stage * C::TILE_BYTES;
                 uint64_t* bar = &sh.kv_full[stage];
                 if (lane == 0) mbar_arrive_expect_tx(bar, C::TILE_BYTES);
                 __syncwarp();
-                if (!p.block_table) {
-                    if (lane < HALVES)
-                        tma_load_3d(dst + lane * (kTile * 128), map, bar, 64 * lane, pc.h,
-                                    pc.key0 + kt * kTile);
-                } else {
-                    const int per = p.page < kTile ? kTile / p.page : 1;  // pages of a tile
-                    if (lane < per * HALVES) {
-                        const int pg = lane % per, half = lane / per;
-                        const int j = kt * kTile + pg * p.page;  // first key of the page's part
-                        // past the keys, or no page: beyond the cache, which loads zeros
-                        int id = p.num_pages;
-                        if (j < pc.kv) {
-                            id = p.block_table[(size_t)pc.r * p.max_pages + j / p.page];
-                            if (id < 0 || id >= p.num_pages) {
-                                id = p.num_pages;
-                                flags |= KDA_DEV_PAGES;
-                            }
-                        }
-                        tma_load_4d(dst + half * (kTile * 128) + pg * p.page * 128, map, bar, 64 * half,
-                                    j % p.page, pc.h, id);
-                    }
+                if (half < HALVES) {
+                    dst += half * (kTile * 128);
+                    if (!p.block_table)
+                        tma_load_3d(dst, map, bar, 64 * half, pc.h, pc.key0 + kt * kTile);
+                    else
+                        tma_load_4d(dst + (pg << log2_page) * 128, map, bar, 64 * half,
+                                    (kt * kTile) & (p.page - 1), pc.h, id);
                 }
                 if (++stage == NS) {
                     stage = 0;
@@ -331,10 +346,20 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
                     tma_load_3d(sq + w * C::TILE_BYTES + half * (kTile * 128), &map_q, &sh.q_full,
                                 64 * half, pc.h * G, pc.tok0 + w * tok1);
                 }
-                for (int j = 0; j < lead && j < n; j++) load_kv(pc, &map_k, pc.kt0 + j);
+                // Ids of tiles j, j + 1, j + 2 in id[0..2].
+                int id[3] = {0, 0, 0};
+                if (p.block_table) {
+#pragma unroll
+                    for (int j = 0; j < 3; j++) id[j] = page_id(pc, pc.kt0 + j);
+                }
+                load_kv(pc, &map_k, pc.kt0, id[0]);
+                if (lead == 2 && n > 1) load_kv(pc, &map_k, pc.kt0 + 1, id[1]);
                 for (int j = 0; j < n; j++) {
-                    load_kv(pc, &map_v, pc.kt0 + j);
-                    if (j + lead < n) load_kv(pc, &map_k, pc.kt0 + j + lead);
+                    load_kv(pc, &map_v, pc.kt0 + j, id[0]);
+                    if (j + lead < n) load_kv(pc, &map_k, pc.kt0 + j + lead, lead == 1 ? id[1] : id[2]);
+                    id[0] = id[1];
+                    id[1] = id[2];
+                    if (p.block_table && j + 3 < n) id[2] = page_id(pc, pc.kt0 + j + 3);
                 }
             };
             auto piece_of = [&](int r, const AttnReq& q, int h, int t) {
@@ -461,71 +486,123 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
                 if (elect_one()) mma_commit(bar);
                 __syncwarp();
             };
-            while (ok) {
+            struct Next {  // the piece after this one
+                int end, n, pair, n0, n1, tail;
+            };
+            auto take = [&](Next& x) {  // from the queue
                 const int i = np % kPieces;
-                if (!wait(&sh.piece_full[i], (np / kPieces) & 1)) break;
+                if (!wait(&sh.piece_full[i], (np / kPieces) & 1)) return false;
                 const Piece& pc = sh.pieces[i];
-                const int end = uniform(pc.end), n = uniform(piece_tiles(pc)), pair = uniform(pc.pair);
-                const int n0 = uniform(group_share(pc, 0, tok1).n), n1 = uniform(group_share(pc, 1, tok1).n);
-                const int tail = uniform(pc.keys < (pc.kt0 + n) * kTile);
+                x.end = uniform(pc.end);
+                x.n = uniform(piece_tiles(pc));
+                x.pair = uniform(pc.pair);
+                x.n0 = uniform(group_share(pc, 0, tok1).n);
+                x.n1 = uniform(group_share(pc, 1, tok1).n);
+                x.tail = uniform(pc.keys < (pc.kt0 + x.n) * kTile);
                 if (lane == 0) mbar_arrive(&sh.piece_empty[i]);
                 np++;
-                if (end) break;
-                if (n == 0) continue;
-                if (!wait(&sh.q_full, q_phase)) break;
-                q_phase ^= 1;
-                if (pair) {
-                    // Two row tiles on every key tile.
-                    if (!wait(&sh.kv_full[stage], kv_phase)) break;
-                    tc_fence_after();
-                    if (n0 > 0) scores(0, 0, stage);
-                    if (n1 > 0) scores(1, 1, stage);
-                    commit(&sh.kv_empty[stage]);
-                    next();
-                    if (n == 1) commit(&sh.q_empty);
+                return true;
+            };
+            // Group w's O may be written: the results before are out. Waited for
+            // once per piece and group.
+            auto o_free = [&](int w, int piece) { return wait(&sh.o_free[w], (piece & 1) ^ 1); };
+            auto half_by_half = [&](int w, int parity, uint32_t vs, uint32_t add) {
+                if (!wait(&sh.p_full[w][0], parity)) return false;
+                tc_fence_after();
+                outputs(w, vs, 0, add);
+                if (!wait(&sh.p_full[w][1], parity)) return false;
+                tc_fence_after();
+                outputs(w, vs, 1, 1);
+                return true;
+            };
+            Next x{};
+            take(x);
+            bool primed = false;  // x's first scores are on their way
+            for (int piece = 0; ok && !x.end; piece++) {
+                const int n = x.n;
+                if (n == 0) {
+                    if (!o_free(0, piece) || !o_free(1, piece) || !take(x)) break;
+                    continue;
+                }
+                if (x.pair) {
+                    // Two row tiles on every key tile. The last tile's step starts the
+                    // next piece's first scores, if that is a pair too, as any other
+                    // step starts the next tile's.
+                    const int n0 = x.n0, n1 = x.n1, tail = x.tail;
+                    if (!primed) {
+                        if (!wait(&sh.q_full, q_phase)) break;
+                        q_phase ^= 1;
+                        if (!wait(&sh.kv_full[stage], kv_phase)) break;
+                        tc_fence_after();
+                        if (n0 > 0) scores(0, 0, stage);
+                        if (n1 > 0) scores(1, 1, stage);
+                        commit(&sh.kv_empty[stage]);
+                        next();
+                        if (n == 1) commit(&sh.q_empty);
+                    }
+                    primed = false;
                     for (int j = 0; j < n; j++) {
                         const int vs = stage;
                         if (!wait(&sh.kv_full[vs], kv_phase)) break;
                         next();
-                        const bool more = j + 1 < n;
+                        bool s0 = j + 1 < n0, s1 = j + 1 < n1;  // scores to start
+                        if (j + 1 == n) {
+                            if (tail) {
+                                if (!wait(&sh.v_clean[vs], cleaned >> vs & 1)) break;
+                                cleaned ^= 1u << vs;
+                            }
+                            if (!take(x)) break;
+                            primed = !x.end && x.pair && x.n > 0;
+                            s0 = primed && x.n0 > 0;
+                            s1 = primed && x.n1 > 0;
+                        }
+                        const bool more = j + 1 < n || primed;
                         const int ks = stage;
-                        if (more) {
-                            if (!wait(&sh.kv_full[ks], kv_phase)) break;
-                        } else if (tail) {
-                            if (!wait(&sh.v_clean[vs], cleaned >> vs & 1)) break;
-                            cleaned ^= 1u << vs;
-                        }
+                        bool have = false;
+                        auto keys = [&] {  // the key tile (and the rows) of the next scores
+                            if (have) return true;
+                            have = true;
+                            if (j + 1 == n) {
+                                if (!wait(&sh.q_full, q_phase)) return false;
+                                q_phase ^= 1;
+                            }
+                            if (!wait(&sh.kv_full[ks], kv_phase)) return false;
+                            tc_fence_after();
+                            return true;
+                        };
+                        if (j == 0 && !o_free(0, piece)) break;
                         if (j < n0) {
-                            if (!wait(&sh.p_full[0][0], tiles0)) break;
-                            tc_fence_after();
-                            outputs(0, vs, 0, j > 0);
-                            if (!wait(&sh.p_full[0][1], tiles0)) break;
-                            tc_fence_after();
-                            outputs(0, vs, 1, 1);
+                            if (!half_by_half(0, tiles0, vs, j > 0)) break;
                             tiles0 ^= 1;
-                            if (j + 1 < n0) scores(0, 0, ks);
-                            else commit(&sh.o_full[0]);
+                            if (j + 1 == n0) commit(&sh.o_full[0]);
                         }
+                        if (s0) {
+                            if (!keys()) break;
+                            scores(0, 0, ks);
+                        }
+                        if (j == 0 && !o_free(1, piece)) break;
                         if (j < n1) {
-                            if (!wait(&sh.p_full[1][0], tiles1)) break;
-                            tc_fence_after();
-                            outputs(1, vs, 0, j > 0);
-                            if (!wait(&sh.p_full[1][1], tiles1)) break;
-                            tc_fence_after();
-                            outputs(1, vs, 1, 1);
+                            if (!half_by_half(1, tiles1, vs, j > 0)) break;
                             tiles1 ^= 1;
-                            if (j + 1 < n1) scores(1, 1, ks);
-                            else commit(&sh.o_full[1]);
+                            if (j + 1 == n1) commit(&sh.o_full[1]);
+                        }
+                        if (s1) {
+                            if (!keys()) break;
+                            scores(1, 1, ks);
                         }
                         commit(&sh.kv_empty[vs]);
                         if (more) {
                             commit(&sh.kv_empty[ks]);
                             next();
-                            if (j + 2 == n) commit(&sh.q_empty);
                         }
+                        // the rows' last scores are issued
+                        if (j + 2 == n || (j + 1 == n && primed && x.n == 1)) commit(&sh.q_empty);
                     }
                 } else {
                     // One row tile, key tiles in turn to the two groups.
+                    const int tail = x.tail;
+                    if (!wait(&sh.q_full, q_phase)) break;
+                    q_phase ^= 1;
                     for (int j = 0; j < 2 && j < n; j++) {
                         if (!wait(&sh.kv_full[stage], kv_phase)) break;
                         tc_fence_after();
@@ -534,6 +611,7 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
                         next();
                     }
                     if (n <= 2) commit(&sh.q_empty);
+                    if (!ok || !o_free(0, piece) || !o_free(1, piece)) break;
                     for (int j = 0; j < n && ok; j++) {
                         const int vs = stage, w = j & 1;
                         if (!wait(&sh.kv_full[vs], kv_phase)) break;
@@ -544,18 +622,13 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
                             if (!wait(&sh.v_clean[vs], cleaned >> vs & 1)) break;
                             cleaned ^= 1u << vs;
                         }
-                        const int parity = w ? tiles1 : tiles0;
-                        if (!wait(&sh.p_full[w][0], parity)) break;
-                        tc_fence_after();
-                        outputs(w, vs, 0, j > 1);
-                        if (!wait(&sh.p_full[w][1], parity)) break;
-                        tc_fence_after();
-                        outputs(w, vs, 1, 1);
+                        if (!half_by_half(w, w ? tiles1 : tiles0, vs, j > 1)) break;
                         tiles0 ^= w ^ 1;
                         tiles1 ^= w;
                         commit(&sh.kv_empty[vs]);
                         if (more) {
                             if (!wait(&sh.kv_full[ks], kv_phase)) break;
+                            tc_fence_after();
                             scores(w, 0, ks);
                             commit(&sh.kv_empty[ks]);
                             next();
@@ -564,6 +637,7 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
                             commit(&sh.o_full[w]);
                         }
                     }
+                    if (!ok || !take(x)) break;
                 }
             }
             if (!ok) {
@@ -612,42 +686,36 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
             }
             if (!ok) flags |= KDA_DEV_TIMEOUT;
         }
-    } else {
+    } else if (warp < 8) {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoftmax));
         // ------------------------------------------------------------ softmax
         const int w = warp >> 2, quarter = warp & 3;
         const int row = 32 * quarter + lane;  // of the row tile, and the TMEM lane
-        const int rtok = row / G, rhead = row % G;
+        const int rtok = row / G;
         const uint32_t ts = tmem_at(tbase, 32 * quarter, TM_S + w * kTile);
-        const uint32_t to = tmem_at(tbase, 32 * quarter, TM_O);
-        int np = 0, merges = 0;
-        int mine = 0;              // key tiles of this group so far
-        int done = 0, theirs = 0;  // pieces with some, of this group and of the other
-        auto meet = [&] {          // of both groups
-            mbar_arrive(&sh.merge);
-            warp_wait(ok, &sh.merge, merges++ & 1);
-        };
+        const uint32_t to = tmem_at(tbase, 32 * quarter, TM_O + w * D);
+        int mine = 0;  // key tiles of this group so far
         auto wait = [&](uint64_t* bar, uint32_t parity) {
             warp_wait(ok, bar, parity);
             return ok;
         };
-        while (ok) {
+        for (int np = 0; ok; np++) {
             const int i = np % kPieces;
             if (!wait(&sh.piece_full[i], (np / kPieces) & 1)) break;
-            const Piece pc = sh.pieces[i];
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&sh.piece_empty[i]);
-            np++;
-            if (pc.end) break;
+            const Piece& pc = sh.pieces[i];
+            const int end = pc.end, pair = pc.pair, kt0 = pc.kt0;
             const Share g = group_share(pc, w, tok1);
-            const int tok = (pc.pair ? w * tok1 : 0) + rtok;
+            const int tok = (pair ? w * tok1 : 0) + rtok;
             const bool live = row < tok1 * G && tok < pc.ntok;
-            const bool warp_live = __any_sync(0xffffffffu, live);
             // Keys this row sees; a row of nothing masks nothing (never stored).
             const int lim = live ? max(pc.pos0 + tok + 1, 0) : 0x7fffffff;
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&sh.piece_empty[i]);
+            if (end) break;
+            const bool warp_live = __any_sync(0xffffffffu, live);
             float m = -INFINITY, l = 0.f;  // reference (c S) and sum
             for (int n = 0; n < g.n; n++) {
-                const int base = (pc.kt0 + g.first + n * g.step) * kTile;
+                const int base = (kt0 + g.first + n * g.step) * kTile;
                 if (!wait(&sh.s_full[w], mine & 1)) break;
                 tc_fence_after();
                 if (warp_live) {
@@ -689,11 +757,11 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
 #pragma unroll
                         for (int b = 0; b < D; b += 32) {
                             float y[32];
-                            tmem_ld32(to + w * D + b, y);
+                            tmem_ld32(to + b, y);
 #pragma unroll
                             for (int e = 0; e < 32; e++) y[e] *= a;
-                            tmem_st16(to + w * D + b, y);
-                            tmem_st16(to + w * D + b + 16, y + 16);
+                            tmem_st16(to + b, y);
+                            tmem_st16(to + b + 16, y + 16);
                         }
                     }
                     const float ref = m == -INFINITY ? 0.f : m;
@@ -726,88 +794,106 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
                 tc_fence_before();
                 mbar_arrive(&sh.p_full[w][1]);
             }
+            if (!wait(&sh.o_free[w], (np & 1) ^ 1)) break;  // ml of the piece before is read
+            sh.ml[w][row] = make_float2(m, l);
+            mbar_arrive(&sh.ml_full[w]);
+        }
+        if (!ok) flags |= KDA_DEV_TIMEOUT;
+    } else {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsResult));
+        // ------------------------------------------------------------ results
+        const int row = tid & 127;  // of the row tile, and the TMEM lane
+        const int rtok = row / G, rhead = row % G;
+        const uint32_t to = tmem_at(tbase, row & 96, TM_O);
+        int done[2] = {0, 0};  // pieces with key tiles of each group so far
+        for (int np = 0; ok; np++) {
+            const int i = np % kPieces;
+            warp_wait(ok, &sh.piece_full[i], (np / kPieces) & 1);
             if (!ok) break;
-
-            // ------------------------------------------------ the piece's results
-            // Columns [c0, c0 + cn) of the row: all of them, or half when the
-            // two groups hold the same rows.
-            const Share g1 = group_share(pc, 1 - w, tok1);
-            done += g.n > 0;
-            theirs += g1.n > 0;
-            int c0 = 0, cn = D;
-            float a0 = 0.f, a1 = 0.f;  // weights of this group's O and the other's
-            if (pc.pair) {
-                a0 = l == 0.f ? 0.f : 1.f / l;
-            } else {
-                if (w == 1) sh.ml[row] = make_float2(m, l);
-                meet();
-                if (w == 0) {
-                    const float2 other = sh.ml[row];
-                    const float mn = fmaxf(m, other.x);
+            const Piece pc = sh.pieces[i];
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&sh.piece_empty[i]);
+            if (pc.end) break;
+            float* part = pc.slot >= 0 ? p.sp.ws + attn_slot_floats(p.sp.rows, D) * pc.slot : nullptr;
+            const int n[2] = {group_share(pc, 0, tok1).n, group_share(pc, 1, tok1).n};
+            // Two row tiles, one after the other; or the two halves of one.
+#pragma unroll
+            for (int w = 0; w < 2; w++) {
+                if (w == 1 && !pc.pair) break;
+                float a0, a1 = 0.f;  // weights of O_w (and of O_1)
+                float m, l;
+                {
+                    warp_wait(ok, &sh.ml_full[w], np & 1);
+                    const float2 x = sh.ml[w][row];
+                    m = x.x;
+                    l = x.y;
+                    if (n[w] > 0) warp_wait(ok, &sh.o_full[w], done[w]++ & 1);
+                }
+                if (w == 0 && !pc.pair) {
+                    warp_wait(ok, &sh.ml_full[1], np & 1);
+                    const float2 x = sh.ml[1][row];
+                    if (n[1] > 0) warp_wait(ok, &sh.o_full[1], done[1]++ & 1);
+                    const float mn = fmaxf(m, x.x);
                     a0 = m == -INFINITY ? 0.f : ex2(m - mn);
-                    a1 = other.x == -INFINITY ? 0.f : ex2(other.x - mn);
+                    a1 = x.x == -INFINITY ? 0.f : ex2(x.x - mn);
                     // a NaN sum keeps its NaN through either weight
-                    l = (l == 0.f ? 0.f : l * a0) + (other.y == 0.f ? 0.f : other.y * a1);
+                    l = (l == 0.f ? 0.f : l * a0) + (x.y == 0.f ? 0.f : x.y * a1);
                     m = mn;
                     const float inv = l == 0.f ? 0.f : 1.f / l;
                     a0 *= inv;
                     a1 *= inv;
-                    sh.ml[row] = make_float2(a0, a1);
+                } else {
+                    a0 = l == 0.f ? 0.f : 1.f / l;
                 }
-                meet();
-                if (w == 1) {
-                    const float2 both = sh.ml[row];
-                    a0 = both.y;
-                    a1 = both.x;
-                }
-                cn = D / 2;
-                c0 = w * cn;
-                if (g1.n > 0) wait(&sh.o_full[1 - w], (theirs - 1) & 1);
-            }
-            if (g.n > 0) wait(&sh.o_full[w], (done - 1) & 1);
-            if (!ok) break;
-            tc_fence_after();
-            const size_t at = ((size_t)pc.tok0 + tok) * p.s.Hkv * G + (size_t)pc.h * G + rhead;
-            const int srow = (pc.pair ? w * kTile : 0) + row;
-            float* part = pc.slot >= 0 ? p.sp.ws + attn_slot_floats(p.sp.rows, D) * pc.slot : nullptr;
-            if (warp_live) {
+                if (!ok) break;
+                tc_fence_after();
+                const int tok = w * tok1 + rtok, srow = w * kTile + row;
+                const bool live = row < tok1 * G && tok < pc.ntok;
+                const size_t at = ((size_t)pc.tok0 + tok) * p.s.Hkv * G + (size_t)pc.h * G + rhead;
                 float fin = 0.f;  // NaN once a value is not finite
-                for (int b = c0; b < c0 + cn; b += 32) {
-                    float y[32];
-                    if (g.n > 0) {
-                        tmem_ld32(to + w * D + b, y);
+                if (__any_sync(0xffffffffu, live)) {
+                    for (int b = 0; b < D; b += 16) {
+                        float y[16];
+                        if (n[w] > 0) {
+                            tmem_ld16(to + w * D + b, y);
 #pragma unroll
-                        for (int e = 0; e < 32; e++) y[e] = a0 == 0.f ? 0.f : y[e] * a0;
-                    } else {
-#pragma unroll
-                        for (int e = 0; e < 32; e++) y[e] = 0.f;
-                    }
-                    if (!pc.pair && g1.n > 0) {
-                        float z[32];
-                        tmem_ld32(to + (1 - w) * D + b, z);
-#pragma unroll
-                        for (int e = 0; e < 32; e++) y[e] += a1 == 0.f ? 0.f : z[e] * a1;
-                    }
-#pragma unroll
-                    for (int e = 0; e < 32; e++) fin = fmaf(y[e], 0.f, fin);
-                    if (live) {
-                        if (part) {
-                            float4* dst = reinterpret_cast<float4*>(part + (size_t)srow * D + b);
-#pragma unroll
-                            for (int e = 0; e < 8; e++)
-                                dst[e] = make_float4(y[4 * e], y[4 * e + 1], y[4 * e + 2], y[4 * e + 3]);
+                            for (int e = 0; e < 16; e++) y[e] = a0 == 0.f ? 0.f : y[e] * a0;
                         } else {
-                            uint4* dst = reinterpret_cast<uint4*>(p.o + at * D + b);
 #pragma unroll
-                            for (int e = 0; e < 4; e++)
-                                dst[e] = make_uint4(pack2(y[8 * e], y[8 * e + 1]),
-                                                    pack2(y[8 * e + 2], y[8 * e + 3]),
-                                                    pack2(y[8 * e + 4], y[8 * e + 5]),
-                                                    pack2(y[8 * e + 6], y[8 * e + 7]));
+                            for (int e = 0; e < 16; e++) y[e] = 0.f;
+                        }
+                        if (w == 0 && !pc.pair && n[1] > 0) {
+                            float z[16];
+                            tmem_ld16(to + D + b, z);
+#pragma unroll
+                            for (int e = 0; e < 16; e++) y[e] += a1 == 0.f ? 0.f : z[e] * a1;
+                        }
+#pragma unroll
+                        for (int e = 0; e < 16; e++) fin = fmaf(y[e], 0.f, fin);
+                        if (live) {
+                            if (part) {
+                                float4* dst = reinterpret_cast<float4*>(part + (size_t)srow * D + b);
+#pragma unroll
+                                for (int e = 0; e < 4; e++)
+                                    dst[e] = make_float4(y[4 * e], y[4 * e + 1], y[4 * e + 2],
+                                                         y[4 * e + 3]);
+                            } else {
+                                uint4* dst = reinterpret_cast<uint4*>(p.o + at * D + b);
+#pragma unroll
+                                for (int e = 0; e < 2; e++)
+                                    dst[e] = make_uint4(pack2(y[8 * e], y[8 * e + 1]),
+                                                        pack2(y[8 * e + 2], y[8 * e + 3]),
+                                                        pack2(y[8 * e + 4], y[8 * e + 5]),
+                                                        pack2(y[8 * e + 6], y[8 * e + 7]));
+                            }
                         }
                     }
                 }
-                if (live && (pc.pair || w == 0)) {
+                // The groups may go on to the next piece.
+                tc_fence_before();
+                mbar_arrive(&sh.o_free[w]);
+                if (!pc.pair) mbar_arrive(&sh.o_free[1]);
+                if (live) {
                     if (part)
                         part[(size_t)p.sp.rows * D + srow] = l == 0.f ? -INFINITY : m + log2f(l);
                     else if (p.lse)
@@ -820,23 +906,24 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
                     bad &= bad - 1;
                     const int stok = __shfl_sync(0xffffffffu, tok, src);
                     const int shead = __shfl_sync(0xffffffffu, rhead, src);
-                    const int slim = __shfl_sync(0xffffffffu, lim, src);
                     const int ssrow = __shfl_sync(0xffffffffu, srow, src);
-                    const int j0 = pc.kt0 * kTile, j1 = min(pc.kt1 * kTile, slim);
+                    const int j0 = pc.kt0 * kTile;
+                    const int j1 = min(pc.kt1 * kTile, max(pc.pos0 + stok + 1, 0));
                     const size_t tk = (size_t)pc.tok0 + stok;
                     const int head = pc.h * G + shead;
-                    for (int b = c0; b < c0 + cn; b += 32) {
-                        float y[1];
-                        const float sum = row_again<D, 1>(p, pc, tk, head, j0, j1, b, y);
-                        y[0] *= sum == 0.f ? 0.f : 1.f / sum;
-                        flags |= finite_flag(y[0]);
-                        if (part) part[(size_t)ssrow * D + b + lane] = y[0];
-                        else p.o[(tk * p.s.Hkv * G + head) * D + b + lane] = __float2bfloat16_rn(y[0]);
+                    float y[D / 32];
+                    const float sum = row_again<D>(p, pc, tk, head, j0, j1, y);
+#pragma unroll
+                    for (int e = 0; e < D / 32; e++) {
+                        const float x = y[e] * (sum == 0.f ? 0.f : 1.f / sum);
+                        flags |= finite_flag(x);
+                        const int c = lane + 32 * e;
+                        if (part) part[(size_t)ssrow * D + c] = x;
+                        else p.o[(tk * p.s.Hkv * G + head) * D + c] = __float2bfloat16_rn(x);
                     }
                 }
             }
-            tc_fence_before();
-            if (!pc.pair) meet();  // both groups have read both results
+            if (!ok) break;
         }
         if (!ok) flags |= KDA_DEV_TIMEOUT;
     }
@@ -917,11 +1004,11 @@ cudaError_t launch_t(const AttnArgs& a) {
     if (!ok) return cudaErrorInvalidValue;
     auto kernel = kda_attn_tc_kernel<D>;
     cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         TcCfg<D>::SMEM);
+                                         tc_smem<D>());
     if (e != cudaSuccess) return e;
     long long grid = p.sp.ws ? p.sp.ctas : attn_items_bound(p.s);
     if (grid > nsm) grid = nsm;
-    e = launch_dependent(kernel, dim3((unsigned)grid), dim3(kThreadsTc), TcCfg<D>::SMEM, a.stream,
+    e = launch_dependent(kernel, dim3((unsigned)grid), dim3(kThreadsTc), tc_smem<D>(), a.stream,
                          mq, mk, mv, p);
     if (e != cudaSuccess || !p.sp.ws) return e;
     return launch_attn_combine(p.s, p.sp, D, kTile, a.o, a.lse, KDA_BF16, a.d_status, a.stream);
