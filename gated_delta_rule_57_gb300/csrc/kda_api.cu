@@ -17,6 +17,7 @@ namespace {
 
 using kda::aligned16;
 using kda::aligned4;
+using kda::device_sms;
 using kda::fail;
 using kda::mul_ok;
 using kda::NvtxRange;
@@ -101,18 +102,6 @@ cudaError_t seg_scratch_address(void** out) {
 }  // namespace
 
 namespace {
-
-// SMs of the current device, 0 if none is visible.
-int device_sms() {
-    int dev = 0, nsm = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess ||
-        cudaDeviceGetAttribute(&nsm, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess ||
-        nsm <= 0) {
-        cudaGetLastError();
-        return 0;
-    }
-    return nsm;
-}
 
 // Device-planned split (nseg = 0): plans of up to min(32, chunks) segments;
 // the workspace holds their states, then the decay probe (kPlanSamples chunks

@@ -191,18 +191,28 @@ __device__ __forceinline__ void attn_unit_item(const AttnShape& s, const AttnReq
     *tile = (int)(rest - attn_units_before(s, q, lo));
 }
 
+// Sums of the units of 32 requests each, for a walk to start from.
+constexpr int kAttnGroups = 256;
+
 // Units of a CTA's range, by the whole block: all units of all requests over
-// `ctas`, but at least `least`. s_sum: one word per warp.
+// `ctas`, but at least `least`. groups[i]: units of requests 32 i .. 32 i + 31;
+// s_sum: one word per warp. The caller synchronises before groups is read.
 template <int THREADS>
 __device__ __forceinline__ long long attn_units_each(const AttnShape& s, int ctas, int least,
-                                                     long long* s_sum) {
+                                                     long long* groups, long long* s_sum) {
     long long sum = 0;
-    for (int r = threadIdx.x; r < s.N; r += THREADS) {
-        const AttnReq q = attn_request(s, r);
-        if (q.nqt) sum += attn_units_before(s, q, q.nqt) * s.Hkv;
-    }
+    for (int r0 = threadIdx.x & ~31; r0 < s.N; r0 += THREADS) {
+        const int r = r0 + (threadIdx.x & 31);
+        long long mine = 0;
+        if (r < s.N) {
+            const AttnReq q = attn_request(s, r);
+            if (q.nqt) mine = attn_units_before(s, q, q.nqt) * s.Hkv;
+        }
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+        for (int o = 16; o > 0; o >>= 1) mine += __shfl_xor_sync(0xffffffffu, mine, o);
+        if ((threadIdx.x & 31) == 0 && (r0 >> 5) < kAttnGroups) groups[r0 >> 5] = mine;
+        sum += mine;
+    }
     if ((threadIdx.x & 31) == 0) s_sum[threadIdx.x >> 5] = sum;
     __syncthreads();
     sum = 0;
@@ -211,38 +221,58 @@ __device__ __forceinline__ long long attn_units_each(const AttnShape& s, int cta
     return each < least ? least : each;
 }
 
+// A walk that starts at the 32 requests that hold unit `idx` (or, beyond the
+// groups there are sums of, at the first ones without).
+__device__ __forceinline__ AttnWalk attn_walk_at(const AttnShape& s, const long long* groups,
+                                                 long long idx) {
+    const int n = min((s.N + 31) >> 5, kAttnGroups);
+    AttnWalk w;
+    int i = 0;
+    for (; i < n && w.base + groups[i] <= idx; i++) w.base += groups[i];
+    w.r0 = 32 * i;
+    return w;
+}
+
 // Partial results of split items in the workspace: slot 2 c holds the part of
 // CTA c's range that starts where the range does, slot 2 c + 1 the one that
 // ends where it does. Per slot: rows x d outputs (each the softmax over its
-// part), then rows log-sums in base 2.
+// part), then rows log-sums in base 2. After the slots, one AttnCut per CTA.
 struct AttnSplit {
     float* ws;      // null: whole items
     int ctas;       // CTAs the units are divided among
     int least;      // units of a range, at least
     int rows;       // rows of a slot
 };
+// Where a CTA's range starts: which unit of which item.
+struct AttnCut {
+    long long each;  // units of a range
+    int tok0, ntok;  // the item's tokens (0: no work at or after the start)
+    int h, tile, n;  // key head; unit of the item that the range starts at; units of the item
+    int pad;
+};
 inline __host__ __device__ size_t attn_slot_floats(int rows, int d) { return (size_t)rows * (d + 1); }
+inline __host__ __device__ AttnCut* attn_cuts(const AttnSplit& sp, int d) {
+    return reinterpret_cast<AttnCut*>(sp.ws + 2 * (size_t)sp.ctas * attn_slot_floats(sp.rows, d));
+}
+inline size_t attn_split_bytes(const AttnSplit& sp, int d) {
+    return sp.ctas * (2 * attn_slot_floats(sp.rows, d) * sizeof(float) + sizeof(AttnCut));
+}
 
-// Joins the parts of the split items (io: type of o).
-cudaError_t launch_attn_combine(const AttnShape& s, const AttnSplit& sp, int d, int rows_per_tile,
+// Joins the parts of the split items (io: type of o); G query heads per key head.
+cudaError_t launch_attn_combine(const AttnSplit& sp, int Hkv, int G, int d, int rows_per_tile,
                                 void* o, float* lse, kda_dtype_t io, int* d_status,
                                 cudaStream_t stream);
 cudaError_t launch_attn_tc(const AttnArgs& a);    // bf16
 cudaError_t launch_attn_simt(const AttnArgs& a);  // fp32
 
 // How a call on `nsm` SMs divides the tensor-core kernel's work: CTAs and rows
-// of a slot of its split form, or ctas = 0 for whole items.
-AttnSplit attn_tc_split(int N, int total_q, int max_q, int Hq, int Hkv, int nsm);
+// of a slot of its split form, or ctas = 0 for whole items. max_keys: no request
+// has more keys.
+AttnSplit attn_tc_split(int N, int total_q, int max_q, long long max_keys, int Hq, int Hkv, int nsm);
 
-// SMs of the current device, 0 if none is visible.
-int attn_sms();
-
-// Most items there can be, for the grid: every request may leave one tile
-// partly filled.
+// Most items there can be: every request may leave one partly filled.
 inline long long attn_items_bound(const AttnShape& s) {
-    const long long full = (long long)s.total_q / s.tok1;
-    const long long some = full + s.N;
-    return some * s.Hkv;
+    return ((long long)s.total_q / s.tok2 + s.N) * s.Hkv;
 }
 
 }  // namespace kda

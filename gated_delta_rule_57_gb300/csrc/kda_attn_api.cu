@@ -1,4 +1,5 @@
 // Entry points of softmax attention: argument checks and dispatch.
+#include <limits.h>
 #include <math.h>
 
 #include "kda_attn.cuh"
@@ -70,8 +71,7 @@ size_t kda_attn_workspace_size(int N, int total_q, int max_q, int Hq, int Hkv, i
         return (size_t)-1;
     if (io != KDA_BF16) return 0;
     const int most = max_q < total_q ? max_q : total_q;
-    const AttnSplit sp = attn_tc_split(N, total_q, most, Hq, Hkv, attn_sms());
-    return 2 * (size_t)sp.ctas * attn_slot_floats(sp.rows, d) * 4;
+    return attn_split_bytes(attn_tc_split(N, total_q, most, INT_MAX, Hq, Hkv, device_sms()), d);
 }
 
 kda_status_t kda_attn_prompt(const void* q, const void* k, const void* v, const int* cu_seqlens,

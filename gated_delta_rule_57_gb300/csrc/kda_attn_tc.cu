@@ -33,7 +33,10 @@
 // 0 x NaN is NaN; for keys that some rows of the item see and others do not,
 // a row whose O is not finite is computed again from global memory over
 // exactly the keys it sees, so a NaN or Inf beside zero weights never reaches it.
+#include <atomic>
+
 #include "kda_attn.cuh"
+#include "kda_host.cuh"
 #include "sm100_ptx.cuh"
 #include "tensor_map.cuh"
 
@@ -157,7 +160,10 @@ struct Shared {
     uint64_t o_free[2];             // both have been read
     uint64_t piece_full[kPieces], piece_empty[kPieces];
     Piece pieces[kPieces];
-    float2 ml[2][kTile];            // reference and sum of each row
+    union {
+        float2 ml[2][kTile];            // reference and sum of each row
+        long long groups[kAttnGroups];  // before the first piece
+    };
     long long sum[kThreadsTc / 32];
     uint32_t tmem;
 };
@@ -269,7 +275,7 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
     pdl_wait();
     // Units of this CTA's range (split items); also the barrier after the setup.
     long long each = 0;
-    if (p.sp.ws) each = attn_units_each<kThreadsTc>(p.s, p.sp.ctas, p.sp.least, sh.sum);
+    if (p.sp.ws) each = attn_units_each<kThreadsTc>(p.s, p.sp.ctas, p.sp.least, sh.groups, sh.sum);
     __syncthreads();
     tc_fence_after();
     const uint32_t tbase = sh.tmem;
@@ -382,7 +388,6 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
             };
             // Whole items: numbers blockIdx.x, + gridDim.x, ...; split ones: the units
             // [cur, end), item by item.
-            AttnWalk walk;
             AttnReq q{};
             int r = 0, h = 0, t = 0, tile = 0;
             long long in;
@@ -390,6 +395,22 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
             long long cur = split ? blockIdx.x * each : blockIdx.x;
             const long long start = cur, end = cur + each;
             bool have = false;  // (q, h, t, tile) is where `cur` is
+            AttnWalk walk;
+            if (split) {
+                walk = attn_walk_at(p.s, sh.groups, cur);
+                AttnCut cut{each, 0, 0, 0, 0, 0, 0};
+                have = attn_find<true>(p.s, walk, cur, &r, &q, &in);
+                if (have) {
+                    attn_unit_item(p.s, q, in, &h, &t, &tile);
+                    cut.tok0 = q.q0 + t * q.tok;
+                    cut.ntok = min(q.tok, q.q_len - t * q.tok);
+                    cut.h = h;
+                    cut.tile = tile;
+                    cut.n = attn_item_units(p.s, q, t);
+                }
+                if (lane == 0) attn_cuts(p.sp, D)[blockIdx.x] = cut;
+                if (!have) cur = end;
+            }
             while (ok && (!split || cur < end)) {
                 if (!have) {
                     if (!(split ? attn_find<true>(p.s, walk, cur, &r, &q, &in)
@@ -968,15 +989,15 @@ bool make_cache(CUtensorMap* m, const void* ptr, int d, int page, int heads, int
 template <int D>
 cudaError_t launch_t(const AttnArgs& a) {
     const int G = a.Hq / a.Hkv, tok1 = kTile / G;
-    const int nsm = attn_sms();
+    int dev = 0;
+    const int nsm = device_sms(&dev);
+    if (nsm == 0) return cudaErrorNoDevice;
     TcAttnParams p{};
     p.s = {a.cu_q, a.kv_len, a.N, a.total_q, a.max_q,
            (int)min((long long)a.max_pages * a.page, (1LL << 31) - 1), a.Hkv, G, tok1, 2 * tok1,
            kTile};
-    p.sp = attn_tc_split(a.N, a.total_q, a.max_q, a.Hq, a.Hkv, nsm);
-    if (p.sp.ctas && a.ws &&
-        a.ws_bytes >= 2 * (size_t)p.sp.ctas * attn_slot_floats(p.sp.rows, D) * 4)
-        p.sp.ws = a.ws;
+    p.sp = attn_tc_split(a.N, a.total_q, a.max_q, a.kv_len ? p.s.kv_cap : a.max_q, a.Hq, a.Hkv, nsm);
+    if (p.sp.ctas && a.ws && a.ws_bytes >= attn_split_bytes(p.sp, D)) p.sp.ws = a.ws;
     p.block_table = a.block_table;
     p.q = static_cast<const __nv_bfloat16*>(a.q);
     p.k = static_cast<const __nv_bfloat16*>(a.k);
@@ -1003,23 +1024,30 @@ cudaError_t launch_t(const AttnArgs& a) {
              make_rows(&mv, a.v, D, a.Hkv, a.total_q, a.v_stride, 1, kTile);
     if (!ok) return cudaErrorInvalidValue;
     auto kernel = kda_attn_tc_kernel<D>;
-    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         tc_smem<D>());
-    if (e != cudaSuccess) return e;
+    static std::atomic<uint64_t> ready{0};  // devices that know the kernel's shared memory
+    const uint64_t bit = dev < 64 ? 1ull << dev : 0;
+    cudaError_t e = cudaSuccess;
+    if (!(ready.load(std::memory_order_relaxed) & bit)) {
+        e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, tc_smem<D>());
+        if (e != cudaSuccess) return e;
+        ready.fetch_or(bit, std::memory_order_relaxed);
+    }
     long long grid = p.sp.ws ? p.sp.ctas : attn_items_bound(p.s);
     if (grid > nsm) grid = nsm;
     e = launch_dependent(kernel, dim3((unsigned)grid), dim3(kThreadsTc), tc_smem<D>(), a.stream,
                          mq, mk, mv, p);
     if (e != cudaSuccess || !p.sp.ws) return e;
-    return launch_attn_combine(p.s, p.sp, D, kTile, a.o, a.lse, KDA_BF16, a.d_status, a.stream);
+    return launch_attn_combine(p.sp, a.Hkv, G, D, kTile, a.o, a.lse, KDA_BF16, a.d_status, a.stream);
 }
 
 }  // namespace
 
-AttnSplit attn_tc_split(int N, int total_q, int max_q, int Hq, int Hkv, int nsm) {
+AttnSplit attn_tc_split(int N, int total_q, int max_q, long long max_keys, int Hq, int Hkv, int nsm) {
     AttnSplit sp{};
     if (N == 0 || total_q == 0 || max_q == 0 || Hkv == 0 || nsm == 0) return sp;
     const int G = Hq / Hkv, tok1 = kTile / G;
+    // Rows of keys too short to be worth a second launch: whole items.
+    if (max_keys <= KDA_ATTN_SHORT_KEYS) return sp;
     // Enough items to fill the SMs evenly on their own: whole ones.
     const long long items = (long long)total_q / (2 * tok1) * Hkv;
     if (max_q > tok1 && items >= 8LL * nsm) return sp;

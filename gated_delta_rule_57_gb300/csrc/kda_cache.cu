@@ -1,6 +1,8 @@
 // Paged key/value cache of the softmax-attention layers: the plan of a step
 // (block tables, slot map and free list from request lengths) and the write of
 // new keys and values to their slots. Kernels and entry points.
+#include <algorithm>
+
 #include "kda_host.cuh"
 #include "kda_internal.cuh"
 
@@ -270,14 +272,6 @@ __global__ void __launch_bounds__(kAppendWarps * 32) kda_kv_append_kernel(const 
     }
 }
 
-int sm_count() {
-    int dev = 0, n = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess ||
-        cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
-        cudaGetLastError();
-    return n > 0 ? n : 1;
-}
-
 }  // namespace
 }  // namespace kda
 
@@ -334,7 +328,7 @@ kda_status_t kda_kv_plan(const int* old_len, const int* new_len, int* block_tabl
     // One CTA for up to 2048 tokens' slots: at a few thousand the redundant
     // scans cost nothing beside the launch.
     long long grid = ((long long)max_tokens + 4 * kPlanThreads - 1) / (4 * kPlanThreads);
-    const long long most = sm_count();
+    const long long most = std::max(device_sms(), 1);
     grid = grid < 1 ? 1 : (grid > most ? most : grid);
     return launched(launch_dependent(kda_kv_plan_kernel, dim3((unsigned)grid), dim3(kPlanThreads),
                                      smem, static_cast<cudaStream_t>(stream), p));

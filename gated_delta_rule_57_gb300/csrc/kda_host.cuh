@@ -5,6 +5,8 @@
 #include <stdint.h>
 #include <string.h>
 
+#include <atomic>
+
 #include <nvtx3/nvToolsExt.h>
 
 #include "kda_internal.cuh"
@@ -60,6 +62,25 @@ inline kda_status_t launched(cudaError_t e) {
     if (e == cudaSuccess) return KDA_OK;
     set_last_error(cudaGetErrorString(e));
     return KDA_ERR_CUDA;
+}
+
+// SMs of the current device, 0 if none is visible; *device (if not null): its
+// number.
+inline int device_sms(int* device = nullptr) {
+    static std::atomic<int> known[64];
+    int dev = 0, n = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) {
+        cudaGetLastError();
+        return 0;
+    }
+    if (device) *device = dev;
+    if (dev < 64 && (n = known[dev].load(std::memory_order_relaxed)) > 0) return n;
+    if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n <= 0) {
+        cudaGetLastError();
+        return 0;
+    }
+    if (dev < 64) known[dev].store(n, std::memory_order_relaxed);
+    return n;
 }
 
 }  // namespace kda

@@ -116,3 +116,10 @@ def test_binding_refuses():
         kda.kda_kv_append(x, x[:2], i, x[None], x[None])
     with pytest.raises(ValueError):
         kda.kda_kv_plan(i.long(), i, i[:, None], i, i[:2], page_size=16, max_tokens=4)
+
+
+def test_short_keys_matches_header():
+    import re
+    from gated_delta_rule_57_gb300 import build
+    text = open(build.INCLUDE + "/kda.h").read()
+    assert kda.KDA_ATTN_SHORT_KEYS == int(re.search(r"#define KDA_ATTN_SHORT_KEYS (\d+)", text).group(1))
