@@ -155,10 +155,14 @@ struct Shared {
     uint64_t v_clean[8];            // a V tile of the ring has zeros past the keys
     uint64_t q_full, q_empty;
     uint64_t s_full[2], p_full[2][2];  // of each group; P per half of the keys
-    uint64_t o_full[2];             // a piece's last product of a group
-    uint64_t ml_full[2];            // and its references and sums
-    uint64_t o_free[2];             // both have been read
+    // Of each group, for each piece: its references and sums are there, are read;
+    // for each piece in which it has key tiles: its O is complete, is read. (A
+    // group without tiles runs ahead of the products, so it may not count in
+    // what they wait for.)
+    uint64_t ml_full[2], ml_free[2], o_full[2], o_free[2];
     uint64_t piece_full[kPieces], piece_empty[kPieces];
+    uint64_t next_full;             // the number of the next whole item
+    alignas(16) uint4 next;
     Piece pieces[kPieces];
     union {
         float2 ml[2][kTile];            // reference and sum of each row
@@ -248,6 +252,7 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
             mbar_init(&sh.kv_empty[i], 2);  // read by the products, seen by the V warp
             mbar_init(&sh.v_clean[i], 1);
         }
+        mbar_init(&sh.next_full, 1);
         mbar_init(&sh.q_full, 1);
         mbar_init(&sh.q_empty, 1);
         for (int w = 0; w < 2; w++) {
@@ -256,6 +261,7 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
             mbar_init(&sh.p_full[w][1], 128);
             mbar_init(&sh.o_full[w], 1);
             mbar_init(&sh.ml_full[w], 128);
+            mbar_init(&sh.ml_free[w], 128);
             mbar_init(&sh.o_free[w], 128);
         }
         for (int i = 0; i < kPieces; i++) {
@@ -386,8 +392,9 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
                 pc.end = 0;
                 return pc;
             };
-            // Whole items: numbers blockIdx.x, + gridDim.x, ...; split ones: the units
-            // [cur, end), item by item.
+            // Whole items: a CTA per item, of which those that run take over the ones
+            // that have not started, in their order (longest rows of a request first),
+            // asking ahead. Split ones: the units [cur, end), item by item.
             AttnReq q{};
             int r = 0, h = 0, t = 0, tile = 0;
             long long in;
@@ -411,35 +418,55 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
                 if (lane == 0) attn_cuts(p.sp, D)[blockIdx.x] = cut;
                 if (!have) cur = end;
             }
+            int asked = 0;
             while (ok && (!split || cur < end)) {
+                if (!split) {
+                    if (lane == 0) {
+                        mbar_arrive_expect_tx(&sh.next_full, 16);
+                        clc_try_cancel(&sh.next, &sh.next_full);
+                    }
+                    __syncwarp();
+                    if (cur < walk.base) walk = AttnWalk{};
+                }
                 if (!have) {
-                    if (!(split ? attn_find<true>(p.s, walk, cur, &r, &q, &in)
-                                : attn_find<false>(p.s, walk, cur, &r, &q, &in)))
-                        break;
-                    if (split) {
+                    have = split ? attn_find<true>(p.s, walk, cur, &r, &q, &in)
+                                 : attn_find<false>(p.s, walk, cur, &r, &q, &in);
+                    if (split && have) {
                         attn_unit_item(p.s, q, in, &h, &t, &tile);
-                    } else {
+                    } else if (have) {
                         t = q.nqt - 1 - (int)(in / p.s.Hkv);
                         h = (int)(in % p.s.Hkv);
                     }
                 }
-                Piece pc = piece_of(r, q, h, t);
-                if (split) {
-                    const int n = pc.kt1, take = (int)min((long long)(n - tile), end - cur);
-                    pc.kt0 = tile;
-                    pc.kt1 = tile + take;
-                    if (take < n) pc.slot = 2 * blockIdx.x + (cur > start ? 1 : 0);
-                    cur += take;
-                    tile = 0;
-                    if (++t == q.nqt) {
-                        t = 0;
-                        h++;
+                if (have) {
+                    Piece pc = piece_of(r, q, h, t);
+                    if (split) {
+                        const int n = pc.kt1, take = (int)min((long long)(n - tile), end - cur);
+                        pc.kt0 = tile;
+                        pc.kt1 = tile + take;
+                        if (take < n) pc.slot = 2 * blockIdx.x + (cur > start ? 1 : 0);
+                        cur += take;
+                        tile = 0;
+                        if (++t == q.nqt) {
+                            t = 0;
+                            h++;
+                        }
+                        have = h < p.s.Hkv;
                     }
-                    have = h < p.s.Hkv;
-                } else {
-                    cur += gridDim.x;
+                    process(pc);
+                } else if (split) {
+                    break;
                 }
-                process(pc);
+                if (!split) {
+                    have = false;
+                    warp_wait(ok, &sh.next_full, asked++ & 1);
+                    const int x = ok ? __shfl_sync(0xffffffffu, clc_answer(&sh.next), 0) : -1;
+                    if (x < 0) break;
+                    cur = x;
+                    // the answer is read before the next one is written
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                }
             }
             if (blockIdx.x == 0) {  // lengths of requests this CTA had no work of
                 for (int i = lane; i < p.s.N; i += 32) walk.bad |= attn_request(p.s, i).bad != 0;
@@ -524,9 +551,10 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
                 np++;
                 return true;
             };
-            // Group w's O may be written: the results before are out. Waited for
-            // once per piece and group.
-            auto o_free = [&](int w, int piece) { return wait(&sh.o_free[w], (piece & 1) ^ 1); };
+            // Group w's O may be written: what it held is read. Waited for once per
+            // piece in which the group has key tiles.
+            int uses0 = 0, uses1 = 0;
+            auto o_free = [&](int w) { return wait(&sh.o_free[w], ((w ? uses1++ : uses0++) & 1) ^ 1); };
             auto half_by_half = [&](int w, int parity, uint32_t vs, uint32_t add) {
                 if (!wait(&sh.p_full[w][0], parity)) return false;
                 tc_fence_after();
@@ -539,10 +567,10 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
             Next x{};
             take(x);
             bool primed = false;  // x's first scores are on their way
-            for (int piece = 0; ok && !x.end; piece++) {
+            while (ok && !x.end) {
                 const int n = x.n;
                 if (n == 0) {
-                    if (!o_free(0, piece) || !o_free(1, piece) || !take(x)) break;
+                    if (!take(x)) break;
                     continue;
                 }
                 if (x.pair) {
@@ -591,7 +619,7 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
                             tc_fence_after();
                             return true;
                         };
-                        if (j == 0 && !o_free(0, piece)) break;
+                        if (j == 0 && n0 > 0 && !o_free(0)) break;
                         if (j < n0) {
                             if (!half_by_half(0, tiles0, vs, j > 0)) break;
                             tiles0 ^= 1;
@@ -601,7 +629,7 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
                             if (!keys()) break;
                             scores(0, 0, ks);
                         }
-                        if (j == 0 && !o_free(1, piece)) break;
+                        if (j == 0 && n1 > 0 && !o_free(1)) break;
                         if (j < n1) {
                             if (!half_by_half(1, tiles1, vs, j > 0)) break;
                             tiles1 ^= 1;
@@ -632,7 +660,7 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
                         next();
                     }
                     if (n <= 2) commit(&sh.q_empty);
-                    if (!ok || !o_free(0, piece) || !o_free(1, piece)) break;
+                    if (!ok || !o_free(0) || (n > 1 && !o_free(1))) break;
                     for (int j = 0; j < n && ok; j++) {
                         const int vs = stage, w = j & 1;
                         if (!wait(&sh.kv_full[vs], kv_phase)) break;
@@ -815,7 +843,7 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
                 tc_fence_before();
                 mbar_arrive(&sh.p_full[w][1]);
             }
-            if (!wait(&sh.o_free[w], (np & 1) ^ 1)) break;  // ml of the piece before is read
+            if (!wait(&sh.ml_free[w], (np & 1) ^ 1)) break;  // of the piece before
             sh.ml[w][row] = make_float2(m, l);
             mbar_arrive(&sh.ml_full[w]);
         }
@@ -846,6 +874,7 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
                 {
                     warp_wait(ok, &sh.ml_full[w], np & 1);
                     const float2 x = sh.ml[w][row];
+                    mbar_arrive(&sh.ml_free[w]);
                     m = x.x;
                     l = x.y;
                     if (n[w] > 0) warp_wait(ok, &sh.o_full[w], done[w]++ & 1);
@@ -853,6 +882,7 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
                 if (w == 0 && !pc.pair) {
                     warp_wait(ok, &sh.ml_full[1], np & 1);
                     const float2 x = sh.ml[1][row];
+                    mbar_arrive(&sh.ml_free[1]);
                     if (n[1] > 0) warp_wait(ok, &sh.o_full[1], done[1]++ & 1);
                     const float mn = fmaxf(m, x.x);
                     a0 = m == -INFINITY ? 0.f : ex2(m - mn);
@@ -912,8 +942,8 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
                 }
                 // The groups may go on to the next piece.
                 tc_fence_before();
-                mbar_arrive(&sh.o_free[w]);
-                if (!pc.pair) mbar_arrive(&sh.o_free[1]);
+                if (n[w] > 0) mbar_arrive(&sh.o_free[w]);
+                if (!pc.pair && n[1] > 0) mbar_arrive(&sh.o_free[1]);
                 if (live) {
                     if (part)
                         part[(size_t)p.sp.rows * D + srow] = l == 0.f ? -INFINITY : m + log2f(l);
@@ -1032,8 +1062,8 @@ cudaError_t launch_t(const AttnArgs& a) {
         if (e != cudaSuccess) return e;
         ready.fetch_or(bit, std::memory_order_relaxed);
     }
-    long long grid = p.sp.ws ? p.sp.ctas : attn_items_bound(p.s);
-    if (grid > nsm) grid = nsm;
+    const long long grid = p.sp.ws ? p.sp.ctas : attn_items_bound(p.s);
+    if (grid >= 1LL << 31) return cudaErrorInvalidValue;
     e = launch_dependent(kernel, dim3((unsigned)grid), dim3(kThreadsTc), tc_smem<D>(), a.stream,
                          mq, mk, mv, p);
     if (e != cudaSuccess || !p.sp.ws) return e;

@@ -121,6 +121,35 @@ __device__ __forceinline__ void fence_proxy_async_smem() {
 }
 
 // ---------------------------------------------------------------------------
+// Cluster launch control: a running CTA takes over one that has not started
+// ---------------------------------------------------------------------------
+// Asks for the next CTA of this grid that has not started; the 16-byte answer
+// arrives at `resp` (16-byte aligned shared memory) with 16 bytes on `bar`. Not to
+// be asked again after a refusal.
+__device__ __forceinline__ void clc_try_cancel(void* resp, uint64_t* bar) {
+    asm volatile(
+        "clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128 [%0], "
+        "[%1];" ::"r"(smem_addr(resp)),
+        "r"(smem_addr(bar))
+        : "memory");
+}
+// blockIdx.x of the CTA taken over, or -1: none was left.
+__device__ __forceinline__ int clc_answer(const void* resp) {
+    uint32_t got, x;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t.reg .b128 r;\n\t"
+        "ld.shared.b128 r, [%2];\n\t"
+        "clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 p, r;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t"
+        "mov.u32 %1, 0;\n\t"
+        "@p clusterlaunchcontrol.query_cancel.get_first_ctaid.v4.b32.b128 {%1, _, _, _}, r;\n\t}"
+        : "=r"(got), "=r"(x)
+        : "r"(smem_addr(resp))
+        : "memory");
+    return got ? (int)x : -1;
+}
+
+// ---------------------------------------------------------------------------
 // tcgen05: tensor memory
 // ---------------------------------------------------------------------------
 // Whole warp. Writes the TMEM base address of `ncols` columns (power of two,

@@ -263,3 +263,26 @@ def test_cache_built_step_by_step_equals_the_prompt(io):
     torch.cuda.synchronize()
     assert have == lens and int(status) == 0
     attn_ref.check(whole, whole_lse, ref)
+
+
+@pytest.mark.parametrize("q_lens,kv_lens,hq,hkv,d,page", [([300], [2300], 4, 1, 64, 1024), ([70, 1], [1200, 1100], 8, 2, 128, 32),
+                                                         ([40, 260, 1], [1111, 1500, 3], 6, 1, 128, 16)])
+def test_ranges_of_few_key_tiles(q_lens, kv_lens, hq, hkv, d, page):
+    """Ranges so short that a softmax group gets pieces without key tiles: every
+    part is written before it is joined (the workspace starts as NaN), no wait
+    runs out, and repeats give the same bits."""
+    q, kc, vc, table = cached(q_lens, kv_lens, hq, hkv, d, page, BF, seed=d)
+    ref = attn_ref.paged(q, kc, vc, table, q_lens, kv_lens, d ** -0.5)
+    need = kda.kda_attn_workspace_size(len(q_lens), sum(q_lens), max(q_lens), hq, hkv, d)
+    assert need > 0
+    status, first = ints([0]), None
+    for _ in range(30):
+        ws = torch.full((need // 4,), float("nan"), device=DEV)
+        o, lse = kda.kda_attn_paged(q, kc, vc, table, cumulative(q_lens), ints(kv_lens), max_q=max(q_lens),
+                                    workspace=ws, status=status)
+        torch.cuda.synchronize()
+        assert int(status) == 0
+        if first is None:
+            first = (o, lse)
+            attn_ref.check(o, lse, ref)
+        assert torch.equal(o, first[0]) and torch.equal(lse, first[1])
