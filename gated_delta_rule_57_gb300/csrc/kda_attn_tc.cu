@@ -797,7 +797,7 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
                     const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * p.c;
                     if (n == 0) {
                         m = top;
-                    } else if (__any_sync(0xffffffffu, top > m + kRaise)) {
+                    } else if (__any_sync(0xffffffffu, live && top > m + kRaise)) {
                         const float mn = fmaxf(m, top);
                         const float a = mn == -INFINITY ? 1.f : ex2(m - mn);
                         m = mn;
