@@ -265,10 +265,12 @@ cudaError_t launch_attn_combine(const AttnSplit& sp, int Hkv, int G, int d, int 
 cudaError_t launch_attn_tc(const AttnArgs& a);    // bf16
 cudaError_t launch_attn_simt(const AttnArgs& a);  // fp32
 
-// How a call on `nsm` SMs divides the tensor-core kernel's work: CTAs and rows
-// of a slot of its split form, or ctas = 0 for whole items. max_keys: no request
-// has more keys.
-AttnSplit attn_tc_split(int N, int total_q, int max_q, long long max_keys, int Hq, int Hkv, int nsm);
+// How a call on `nsm` SMs divides a kernel's work: CTAs and rows of a slot of its
+// split form, or ctas = 0 for whole items. max_keys: no request has more keys.
+AttnSplit attn_tc_split(int N, int total_q, int max_q, long long max_keys, int Hq, int Hkv,
+                        int nsm);
+AttnSplit attn_simt_split(int N, int total_q, int max_q, long long max_keys, int Hq, int Hkv,
+                          int nsm);
 
 // Most items there can be: every request may leave one partly filled.
 inline long long attn_items_bound(const AttnShape& s) {

@@ -69,9 +69,9 @@ size_t kda_attn_workspace_size(int N, int total_q, int max_q, int Hq, int Hkv, i
                                kda_dtype_t io) {
     if (N < 0 || total_q < 0 || max_q < 0 || check_heads(Hq, Hkv, d, io) != KDA_OK)
         return (size_t)-1;
-    if (io != KDA_BF16) return 0;
     const int most = max_q < total_q ? max_q : total_q;
-    return attn_split_bytes(attn_tc_split(N, total_q, most, INT_MAX, Hq, Hkv, device_sms()), d);
+    const auto split = io == KDA_BF16 ? attn_tc_split : attn_simt_split;
+    return attn_split_bytes(split(N, total_q, most, INT_MAX, Hq, Hkv, device_sms()), d);
 }
 
 kda_status_t kda_attn_prompt(const void* q, const void* k, const void* v, const int* cu_seqlens,

@@ -1,23 +1,30 @@
 // Softmax attention of fp32 inputs on the CUDA cores, with every product and sum in 32 bits.
 //
-//     x_ij = scale q_i . k_j (j <= position of i),  m_i = max_j x_ij,
-//     l_i = sum_j e^{x_ij - m_i},  o_i = sum_j e^{x_ij - m_i} v_j / l_i
+//     x_ij = scale log2(e) q_i . k_j (j <= position of i),  m_i = max_j x_ij,
+//     l_i = sum_j 2^{x_ij - m_i},  o_i = sum_j 2^{x_ij - m_i} v_j / l_i
 //
 // in one pass over the keys: when a key tile raises m_i, the sums so far are
-// multiplied by e^{m_old - m_new}. A CTA of 256 threads holds 64 rows and takes
+// multiplied by 2^{m_old - m_new}. A CTA of 256 threads holds 64 rows and takes
 // 64 keys at a time through shared memory; thread (y, x) computes rows
-// 4y .. 4y + 3 against keys x + 16 i, and the same rows of the output.
-// Bound by the FFMA pipe: 8 shared-memory loads of 16 bytes feed 64 FFMA in the
+// 4y .. 4y + 3 against keys x + 16 i, and the same rows of the output. Two CTAs
+// per SM, so that one's loads and softmax pass beside the other's products; long
+// rows are cut into ranges as the header of kda_attn.cuh says. Bound by the FFMA pipe: 8 shared-memory loads of 16 bytes feed 64 FFMA in the
 // first product and 12 feed 128 in the second.
+#include <algorithm>
+
 #include "kda_attn.cuh"
+#include "kda_host.cuh"
 
 namespace kda {
 namespace {
 
 constexpr int kRows = 64, kKeys = 64, kThreadsSimt = 256;
 
+constexpr int kCtasPerSm = 2;
+
 struct SimtParams {
     AttnShape s;
+    AttnSplit sp;
     const void* q;
     const void* k;
     const void* v;
@@ -40,7 +47,7 @@ __device__ __forceinline__ float4 load4(const float* p) {
 }
 
 template <int D>
-__global__ void __launch_bounds__(kThreadsSimt, 2) kda_attn_simt_kernel(const SimtParams p) {
+__global__ void __launch_bounds__(kThreadsSimt, kCtasPerSm) kda_attn_simt_kernel(const SimtParams p) {
     constexpr int LD = D + 4, LP = kKeys + 4, C4 = D / 64;  // C4: float4 columns per thread
     extern __shared__ __align__(16) float sm[];
     float* sq = sm;
@@ -48,6 +55,7 @@ __global__ void __launch_bounds__(kThreadsSimt, 2) kda_attn_simt_kernel(const Si
     float* sv = sk + kKeys * LD;
     float* sp = sk;
 
+    __shared__ long long s_groups[kAttnGroups], s_sum[kThreadsSimt / 32];
     pdl_wait();
     const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
     const AttnShape& s = p.s;
@@ -55,19 +63,54 @@ __global__ void __launch_bounds__(kThreadsSimt, 2) kda_attn_simt_kernel(const Si
     const float* gk = static_cast<const float*>(p.k);
     const float* gv = static_cast<const float*>(p.v);
     float* go = static_cast<float*>(p.o);
+    const float c = p.scale * 1.44269504089f;  // scores in base 2
     int flags = 0;
     AttnWalk walk;
     struct {
         int r, t, h;
         AttnReq q;
-    } it;
-    long long in;
-    for (long long idx = blockIdx.x; attn_find<false>(s, walk, idx, &it.r, &it.q, &in); idx += gridDim.x) {
-        it.t = it.q.nqt - 1 - (int)(in / s.Hkv);
-        it.h = (int)(in % s.Hkv);
+    } it{};
+    long long in, each = 0;
+    const bool split = p.sp.ws != nullptr;
+    if (split) {
+        each = attn_units_each<kThreadsSimt>(s, p.sp.ctas, p.sp.least, s_groups, s_sum);
+        __syncthreads();
+    }
+    // Whole items: numbers blockIdx.x, + gridDim.x, ...; split ones: units
+    // [cur, end). Every warp walks by itself, to the same places.
+    long long cur = split ? blockIdx.x * each : blockIdx.x;
+    const long long start = cur, end = cur + each;
+    if (split) walk = attn_walk_at(s, s_groups, cur);
+    bool have = false;
+    int tile = 0;
+    while (!split || cur < end) {
+        if (!have) {
+            if (!(split ? attn_find<true>(s, walk, cur, &it.r, &it.q, &in)
+                        : attn_find<false>(s, walk, cur, &it.r, &it.q, &in))) {
+                if (split && cur == start && tid == 0) attn_cuts(p.sp, D)[blockIdx.x] = AttnCut{};
+                break;
+            }
+            if (split) {
+                attn_unit_item(s, it.q, in, &it.h, &it.t, &tile);
+            } else {
+                it.t = it.q.nqt - 1 - (int)(in / s.Hkv);
+                it.h = (int)(in % s.Hkv);
+            }
+        }
         const int G = s.G, tok0 = it.t * it.q.tok;
         const int rows = min(it.q.tok, it.q.q_len - tok0) * G;
-        const int keys = attn_item_keys(it.q, it.t);
+        const int units = attn_item_units(s, it.q, it.t);
+        // Keys [key0, keys) of the item are this CTA's.
+        const int take = split ? (int)min((long long)(units - tile), end - cur) : units;
+        const int key0 = tile * kKeys, keys = min(attn_item_keys(it.q, it.t), (tile + take) * kKeys);
+        float* part = nullptr;
+        if (split) {
+            if (cur == start && tid == 0)
+                attn_cuts(p.sp, D)[blockIdx.x] =
+                    AttnCut{each, it.q.q0 + tok0, rows / G, it.h, tile, units, 0};
+            if (take < units)
+                part = p.sp.ws + attn_slot_floats(p.sp.rows, D) * (2 * blockIdx.x + (cur > start ? 1 : 0));
+        }
         const size_t first = (size_t)it.q.q0 + tok0;  // packed token of row 0
         __syncthreads();
         for (int i = tid; i < kRows * (D / 4); i += kThreadsSimt) {
@@ -90,7 +133,7 @@ __global__ void __launch_bounds__(kThreadsSimt, 2) kda_attn_simt_kernel(const Si
             for (int c = 0; c < C4 * 4; c++) acc[i][c] = 0.f;
         }
         const int seen_by_all = max(it.q.kv - it.q.q_len + tok0 + 1, 0);
-        for (int k0 = 0; k0 < keys; k0 += kKeys) {
+        for (int k0 = key0; k0 < keys; k0 += kKeys) {
             __syncthreads();  // the tile before is read
             for (int i = tid; i < kKeys * (D / 4); i += kThreadsSimt) {
                 const int j = i / (D / 4), c = (i % (D / 4)) * 4, at = k0 + j;
@@ -117,14 +160,14 @@ __global__ void __launch_bounds__(kThreadsSimt, 2) kda_attn_simt_kernel(const Si
             __syncthreads();
             float x[4][4] = {};
 #pragma unroll 4
-            for (int c = 0; c < D; c += 4) {
+            for (int e = 0; e < D; e += 4) {
                 float4 a[4], b[4];
 #pragma unroll
                 for (int i = 0; i < 4; i++)
-                    a[i] = *reinterpret_cast<const float4*>(sq + (ty * 4 + i) * LD + c);
+                    a[i] = *reinterpret_cast<const float4*>(sq + (ty * 4 + i) * LD + e);
 #pragma unroll
                 for (int i = 0; i < 4; i++)
-                    b[i] = *reinterpret_cast<const float4*>(sk + (tx + 16 * i) * LD + c);
+                    b[i] = *reinterpret_cast<const float4*>(sk + (tx + 16 * i) * LD + e);
 #pragma unroll
                 for (int i = 0; i < 4; i++)
 #pragma unroll
@@ -141,25 +184,22 @@ __global__ void __launch_bounds__(kThreadsSimt, 2) kda_attn_simt_kernel(const Si
                 float mx = -INFINITY;
 #pragma unroll
                 for (int j = 0; j < 4; j++) {
-                    x[i][j] = k0 + tx + 16 * j < lim[i] ? x[i][j] * p.scale : -INFINITY;
+                    x[i][j] = k0 + tx + 16 * j < lim[i] ? x[i][j] * c : -INFINITY;
                     mx = fmaxf(mx, x[i][j]);
                 }
 #pragma unroll
                 for (int o = 8; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
                 const float mn = fmaxf(m[i], mx);
                 const float ref = mn == -INFINITY ? 0.f : mn;  // a row that sees nothing yet
-                const float corr = expf(m[i] - ref);
+                const float corr = exp2f(m[i] - ref);
                 m[i] = mn;
-                float sum = 0.f;
+                l[i] *= corr;
 #pragma unroll
                 for (int j = 0; j < 4; j++) {
-                    const float e = expf(x[i][j] - ref);
-                    sum += e;
+                    const float e = exp2f(x[i][j] - ref);
+                    l[i] += e;  // of this thread's keys
                     sp[(ty * 4 + i) * LP + tx + 16 * j] = e;
                 }
-#pragma unroll
-                for (int o = 8; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-                l[i] = l[i] * corr + sum;
 #pragma unroll
                 for (int c = 0; c < C4 * 4; c++) acc[i][c] *= corr;
             }
@@ -198,21 +238,41 @@ __global__ void __launch_bounds__(kThreadsSimt, 2) kda_attn_simt_kernel(const Si
 #pragma unroll
         for (int i = 0; i < 4; i++) {
             const int r = ty * 4 + i;
+#pragma unroll
+            for (int o = 8; o > 0; o >>= 1) l[i] += __shfl_xor_sync(0xffffffffu, l[i], o);
             if (r >= rows) continue;
-            const size_t tok = first + r / G;
-            const int head = it.h * G + r % G;
+            const size_t at = (first + r / G) * s.Hkv * G + it.h * G + r % G;
+            float* dst = part ? part + (size_t)r * D : go + at * D;
             const float inv = l[i] > 0.f ? 1.f / l[i] : (l[i] == 0.f ? 0.f : l[i]);  // NaN stays
 #pragma unroll
             for (int c = 0; c < C4; c++) {
                 const float4 y = make_float4(acc[i][c * 4] * inv, acc[i][c * 4 + 1] * inv,
                                              acc[i][c * 4 + 2] * inv, acc[i][c * 4 + 3] * inv);
                 flags |= finite_flag(y.x) | finite_flag(y.y) | finite_flag(y.z) | finite_flag(y.w);
-                *reinterpret_cast<float4*>(go + (tok * s.Hkv * G + head) * D + tx * 4 + 64 * c) = y;
+                *reinterpret_cast<float4*>(dst + tx * 4 + 64 * c) = y;
             }
-            if (p.lse && tx == 0)
-                p.lse[tok * s.Hkv * G + head] = l[i] == 0.f ? -INFINITY : m[i] + logf(l[i]);
+            if (tx == 0) {
+                if (part)
+                    part[(size_t)p.sp.rows * D + r] =
+                        l[i] == 0.f ? -INFINITY : m[i] + log2f(l[i]);
+                else if (p.lse)
+                    p.lse[at] = l[i] == 0.f ? -INFINITY : (m[i] + log2f(l[i])) * 0.69314718056f;
+            }
+        }
+        if (split) {
+            cur += take;
+            tile = 0;
+            if (++it.t == it.q.nqt) {
+                it.t = 0;
+                it.h++;
+            }
+            have = it.h < s.Hkv;
+        } else {
+            cur += gridDim.x;
         }
     }
+    if (blockIdx.x == 0)  // lengths of requests this CTA had no work of
+        for (int i = tid; i < s.N; i += kThreadsSimt) walk.bad |= attn_request(s, i).bad != 0;
     if (walk.bad) flags |= KDA_DEV_LENGTH;
     report_flags(p.d_status, flags);
 }
@@ -242,13 +302,31 @@ cudaError_t launch_t(const AttnArgs& a) {
                                          cudaFuncAttributeMaxDynamicSharedMemorySize,
                                          (int)simt_smem<D>());
     if (e != cudaSuccess) return e;
-    long long grid = attn_items_bound(p.s);
-    if (grid > 65535) grid = 65535;
-    return launch_dependent(kda_attn_simt_kernel<D>, dim3((unsigned)grid), dim3(kThreadsSimt),
-                            simt_smem<D>(), a.stream, p);
+    const int nsm = device_sms();
+    p.sp = attn_simt_split(a.N, a.total_q, a.max_q, a.kv_len ? p.s.kv_cap : a.max_q, a.Hq, a.Hkv, nsm);
+    if (p.sp.ctas && a.ws && a.ws_bytes >= attn_split_bytes(p.sp, D)) p.sp.ws = a.ws;
+    const long long grid = p.sp.ws ? p.sp.ctas : std::min(attn_items_bound(p.s), 1LL << 20);
+    e = launch_dependent(kda_attn_simt_kernel<D>, dim3((unsigned)grid), dim3(kThreadsSimt),
+                         simt_smem<D>(), a.stream, p);
+    if (e != cudaSuccess || !p.sp.ws) return e;
+    return launch_attn_combine(p.sp, a.Hkv, G, D, kRows, a.o, a.lse, KDA_F32, a.d_status, a.stream);
 }
 
 }  // namespace
+
+AttnSplit attn_simt_split(int N, int total_q, int max_q, long long max_keys, int Hq, int Hkv,
+                          int nsm) {
+    AttnSplit sp{};
+    if (N == 0 || total_q == 0 || max_q == 0 || Hkv == 0 || nsm == 0) return sp;
+    const int G = Hq / Hkv, tok = kRows / G;
+    // Rows of a few key tiles, or enough items to fill the SMs evenly: whole ones.
+    if (max_keys <= KDA_ATTN_SHORT_KEYS / 4) return sp;
+    if ((long long)total_q / tok * Hkv >= 16LL * kCtasPerSm * nsm) return sp;
+    sp.ctas = kCtasPerSm * nsm;
+    sp.least = 1;
+    sp.rows = (std::min(max_q, tok) * G + 3) & ~3;  // whole 16-byte vectors
+    return sp;
+}
 
 cudaError_t launch_attn_simt(const AttnArgs& a) {
     return a.d == 128 ? launch_t<128>(a) : launch_t<64>(a);

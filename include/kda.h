@@ -575,14 +575,14 @@ kda_status_t kda_attn_paged(const void* q, const void* k_cache, const void* v_ca
                             float scale, kda_dtype_t io, void* workspace, size_t ws_bytes,
                             int* d_status, void* stream);
 
-/* Requests of at most this many keys (max_len, or max_pages * page_size) are
- * never split: those calls need no workspace. */
+/* Requests of at most this many keys (max_len, or max_pages * page_size; a quarter
+ * of it for KDA_F32) are never split: those calls need no workspace. */
 #define KDA_ATTN_SHORT_KEYS 1024
 
 /*
  * Bytes of device workspace that let kda_attn_prompt (total_q = total, max_q =
  * max_len) and kda_attn_paged split a long row of keys among CTAs: partial
- * results of at most two row tiles per SM of the current device; 0 where
+ * results of a few row tiles per SM of the current device; 0 where
  * nothing would be split. NULL or a smaller buffer is accepted and runs unsplit; both
  * give the same results up to rounding. 16-byte aligned, not overlapping any
  * other argument, not used by another call in flight; contents are scratch.
