@@ -177,7 +177,7 @@ __device__ __forceinline__ bool attn_find(const AttnShape& s, AttnWalk& w, long 
 __device__ __forceinline__ void attn_unit_item(const AttnShape& s, const AttnReq& q, long long in,
                                                int* h, int* t, int* tile) {
     const long long per = attn_units_before(s, q, q.nqt);
-    *h = (int)(in / per);
+    *h = in < 1LL << 32 && per < 1LL << 32 ? (int)((uint32_t)in / (uint32_t)per) : (int)(in / per);
     const long long rest = in - *h * per;
     // units_before(lo) <= rest < units_before(hi); 32 places at a time
     int lo = 0, hi = q.nqt;

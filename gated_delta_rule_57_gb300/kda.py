@@ -449,6 +449,14 @@ def _ints(name: str, t: torch.Tensor, shape):
     return _ptr(t)
 
 
+def _ints_out(name: str, t, n: int, like):
+    """An int32 output of n entries, made here when not given, and its address."""
+    if t is None:
+        t = torch.empty(n, dtype=torch.int32, device=like.device)
+        return t, t.data_ptr()
+    return t, _ints(name, t, (n,))
+
+
 def _rows(name: str, t: torch.Tensor, dtype=None):
     """Address and token stride of a [T, H, d] tensor whose heads are
     contiguous (a view of a fused projection, or a whole tensor)."""
@@ -475,22 +483,16 @@ def kda_kv_plan(old_len, new_len, block_table, free_pages, ring, *, page_size: i
     """
     N, max_pages = block_table.shape
     pages = free_pages.numel()
-    row, two = (N,), (2,)
-    if kv_len is None:
-        kv_len = old_len.new_empty(N)
-    if cu_new is None:
-        cu_new = old_len.new_empty(N + 1)
-    if slot_map is None:
-        slot_map = old_len.new_empty(max_tokens)
-    if ring_out is None:
-        ring_out = old_len.new_empty(2)
+    kv_len, kv_p = _ints_out("kv_len", kv_len, N, old_len)
+    cu_new, cu_p = _ints_out("cu_new", cu_new, N + 1, old_len)
+    slot_map, slot_p = _ints_out("slot_map", slot_map, max_tokens, old_len)
+    ring_out, ring_p = _ints_out("ring_out", ring_out, 2, old_len)
+    row = (N,)
     _check((_lib or lib()).kda_kv_plan(
         _ints("old_len", old_len, row), _ints("new_len", new_len, row),
         _ints("block_table", block_table, (N, max_pages)),
-        _ints("free_pages", free_pages, (pages,)), _ints("ring", ring, two),
-        _ints("ring_out", ring_out, two), _ints("kv_len", kv_len, row),
-        _ints("cu_new", cu_new, (N + 1,)), _ints("slot_map", slot_map, (max_tokens,)), N,
-        max_pages, pages, page_size, max_tokens, _ptr(status), _stream(stream)))
+        _ints("free_pages", free_pages, (pages,)), _ints("ring", ring, (2,)), ring_p, kv_p, cu_p,
+        slot_p, N, max_pages, pages, page_size, max_tokens, _ptr(status), _stream(stream)))
     return kv_len, cu_new, slot_map, ring_out
 
 
@@ -530,18 +532,18 @@ def _attn_buffers(q, N, most, keys, Hkv, o, lse, want_lse, workspace):
     if io is None:
         raise TypeError(f"unsupported q dtype {q.dtype}")
     if o is None:
-        o = q.new_empty((T, Hq, d))
+        o = torch.empty((T, Hq, d), dtype=q.dtype, device=q.device)
     elif o.shape != q.shape or o.dtype != q.dtype:
         raise ValueError("o must have q's shape and dtype")
     if lse is None:
         if want_lse:
-            lse = q.new_empty((T, Hq), dtype=torch.float32)
+            lse = torch.empty((T, Hq), dtype=torch.float32, device=q.device)
     elif lse.shape != (T, Hq) or lse.dtype != torch.float32:
         raise ValueError("lse must be an fp32 tensor [T, Hq]")
     if workspace is None and keys > KDA_ATTN_SHORT_KEYS // (4 if io == KDA_F32 else 1):
         need = (_lib or lib()).kda_attn_workspace_size(N, T, most, Hq, Hkv, d, io)
         if need != ctypes.c_size_t(-1).value and need:  # the call itself reports bad arguments
-            workspace = q.new_empty(need, dtype=torch.uint8)
+            workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
     ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
     return io, o, lse, workspace, ws_bytes
 
