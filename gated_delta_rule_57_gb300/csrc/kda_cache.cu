@@ -85,6 +85,8 @@ struct PlanParams {
     int* d_status;
 };
 
+// EACH: requests of a thread, their lengths held in registers.
+template <int EACH>
 __global__ void __launch_bounds__(kPlanThreads) kda_kv_plan_kernel(const PlanParams p) {
     extern __shared__ unsigned s_pre[];
     unsigned* s_tok = s_pre;
@@ -122,15 +124,25 @@ __global__ void __launch_bounds__(kPlanThreads) kda_kv_plan_kernel(const PlanPar
                (b > a && s_tok[r + 1] > (unsigned)p.max_tokens);
     };
 
-    // Each thread owns a run of consecutive requests.
-    const int each = (N + kPlanThreads - 1) / kPlanThreads;
-    const int r0 = min(tid * each, N), r1 = min(r0 + each, N);
+    // Each thread owns EACH consecutive requests.
+    const int r0 = tid * EACH;
+    unsigned a[EACH], b[EACH], held[EACH], want[EACH];
+#pragma unroll
+    for (int e = 0; e < EACH; e++) {
+        a[e] = b[e] = 0;
+        if (r0 + e < N) {
+            a[e] = length(p.old_len, r0 + e);
+            b[e] = length(p.new_len, r0 + e);
+        }
+    }
     unsigned tok = 0, take = 0, back = 0, sum;
     if (tid == 0) s_taken = 0;
-    for (int r = r0; r < r1; r++) {
-        const unsigned a = length(p.old_len, r), b = length(p.new_len, r);
-        tok = sat_add(tok, b > a ? b - a : 0u);
-        take = sat_add(take, takes(pages(a), pages(b)));
+#pragma unroll
+    for (int e = 0; e < EACH; e++) {
+        held[e] = pages(a[e]);
+        want[e] = pages(b[e]);
+        tok = sat_add(tok, b[e] > a[e] ? b[e] - a[e] : 0u);
+        take = sat_add(take, takes(held[e], want[e]));
     }
     tok = block_scan(tok, s_warp, &sum);
     const unsigned tokens = sum;
@@ -140,36 +152,40 @@ __global__ void __launch_bounds__(kPlanThreads) kda_kv_plan_kernel(const PlanPar
         s_take[N] = sum;
         if (tokens >= kLenCap) flags |= KDA_DEV_LENGTH;
     }
-    for (int r = r0; r < r1; r++) {
-        const unsigned a = length(p.old_len, r), b = length(p.new_len, r);
-        s_tok[r] = tok;
-        s_take[r] = take;
-        tok = sat_add(tok, b > a ? b - a : 0u);
-        take = sat_add(take, takes(pages(a), pages(b)));
+#pragma unroll
+    for (int e = 0; e < EACH; e++) {
+        if (r0 + e < N) {
+            s_tok[r0 + e] = tok;
+            s_take[r0 + e] = take;
+        }
+        tok = sat_add(tok, b[e] > a[e] ? b[e] - a[e] : 0u);
+        take = sat_add(take, takes(held[e], want[e]));
     }
     __syncthreads();
-    for (int r = r0; r < r1; r++) {
-        const unsigned a = length(p.old_len, r), b = length(p.new_len, r);
-        const unsigned held = pages(a), want = pages(b);
-        const bool no = refused(r, a, b, held, want);
+    unsigned gives[EACH];
+#pragma unroll
+    for (int e = 0; e < EACH; e++) {
+        const int r = r0 + e;
+        gives[e] = 0;
+        if (r >= N) continue;
+        const bool no = refused(r, a[e], b[e], held[e], want[e]);
         if (no) flags |= KDA_DEV_PAGES;
-        else if (want > held) atomicMax(&s_taken, s_take[r + 1]);
+        else if (want[e] > held[e]) atomicMax(&s_taken, s_take[r + 1]);
         // Entries past the row's end were never pages.
-        if (!no && want < held && want < (unsigned)p.max_pages)
-            back = sat_add(back, min(held, (unsigned)p.max_pages) - want);
+        if (!no && want[e] < held[e] && want[e] < (unsigned)p.max_pages)
+            gives[e] = min(held[e], (unsigned)p.max_pages) - want[e];
+        back = sat_add(back, gives[e]);
         if (blockIdx.x == 0) {
-            p.kv_len[r] = (int)(no ? a : b);
+            p.kv_len[r] = (int)(no ? a[e] : b[e]);
             p.cu[r] = (int)s_tok[r];
         }
     }
-    unsigned b0 = block_scan(back, s_warp, &sum);
+    back = block_scan(back, s_warp, &sum);
     unsigned given = sum;
-    for (int r = r0; r < r1; r++) {
-        const unsigned a = length(p.old_len, r), b = length(p.new_len, r);
-        const unsigned held = pages(a), want = pages(b);
-        s_back[r] = b0;
-        if (!refused(r, a, b, held, want) && want < held && want < (unsigned)p.max_pages)
-            b0 = sat_add(b0, min(held, (unsigned)p.max_pages) - want);
+#pragma unroll
+    for (int e = 0; e < EACH; e++) {
+        if (r0 + e < N) s_back[r0 + e] = back;
+        back = sat_add(back, gives[e]);
     }
     if (tid == 0) s_back[N] = given;
     __syncthreads();
@@ -320,9 +336,11 @@ kda_status_t kda_kv_plan(const int* old_len, const int* new_len, int* block_tabl
     PlanParams p{old_len, new_len, block_table, free_pages, ring_in, ring_out, kv_len, cu_new,
                  slot_map, N, max_pages, num_pages, page_size, max_tokens, d_status};
     const size_t smem = 3 * ((size_t)N + 1) * 4;
+    auto kernel = N <= kPlanThreads        ? kda_kv_plan_kernel<1>
+                  : N <= 4 * kPlanThreads ? kda_kv_plan_kernel<4>
+                                          : kda_kv_plan_kernel<kPlanMaxN / kPlanThreads>;
     if (smem > 48 * 1024) {
-        cudaError_t e = cudaFuncSetAttribute(kda_kv_plan_kernel,
-                                             cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+        cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
         if (e != cudaSuccess) return launched(e);
     }
     // One CTA for up to 2048 tokens' slots: at a few thousand the redundant
@@ -330,7 +348,7 @@ kda_status_t kda_kv_plan(const int* old_len, const int* new_len, int* block_tabl
     long long grid = ((long long)max_tokens + 4 * kPlanThreads - 1) / (4 * kPlanThreads);
     const long long most = std::max(device_sms(), 1);
     grid = grid < 1 ? 1 : (grid > most ? most : grid);
-    return launched(launch_dependent(kda_kv_plan_kernel, dim3((unsigned)grid), dim3(kPlanThreads),
+    return launched(launch_dependent(kernel, dim3((unsigned)grid), dim3(kPlanThreads),
                                      smem, static_cast<cudaStream_t>(stream), p));
 }
 
