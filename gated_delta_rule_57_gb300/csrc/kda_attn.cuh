@@ -16,8 +16,9 @@
 //     concurrent CTAs share the keys of one request in L2 and the short
 //     items fill the end.
 //   Split items: the key tiles of all items laid end to end are cut into
-//     equal ranges, one per CTA, so few rows over a long cache use every SM
-//     and ragged lengths balance exactly. An item cut by a boundary leaves
+//     ranges of equal cost, one per CTA, so few rows over a long cache use every
+//     SM and ragged lengths balance exactly (a tile belongs to the range that
+//     its first unit of cost is in). An item cut by a boundary leaves
 //     partial results in the workspace (at most two per CTA) that
 //     kda_attn_combine joins.
 #pragma once
@@ -53,12 +54,14 @@ struct AttnShape {
     int Hkv, G;
     int tok1, tok2;  // tokens of an item: tok1 for requests that fit it, else tok2
     int kt;          // keys of a key tile
+    int cost1, cost2;  // of a key tile of either kind of item, in any unit
 };
 
 // One request: its packed tokens, keys, and items.
 struct AttnReq {
     int q0, q_len, kv;  // first packed token, new tokens, keys
     int tok, nqt;       // tokens per item, items per key head
+    int cost;           // of a key tile
     int bad;            // lengths outside what the call was sized for
 };
 
@@ -77,6 +80,7 @@ __device__ __forceinline__ AttnReq attn_request(const AttnShape& s, int r) {
     }
     q.tok = n <= s.tok1 ? s.tok1 : s.tok2;
     q.nqt = (n + q.tok - 1) / q.tok;
+    q.cost = n <= s.tok1 ? s.cost1 : s.cost2;
     return q;
 }
 
@@ -128,15 +132,15 @@ __device__ __forceinline__ long long attn_units_before(const AttnShape& s, const
 }
 
 // A walk over the requests, a warp together, that finds the request of an item
-// (or of a unit) of a non-decreasing sequence of numbers.
+// (or of a unit of cost) of a non-decreasing sequence of numbers.
 struct AttnWalk {
     int r0 = 0;          // the 32 requests r0 .. r0 + 31 are looked at
-    long long base = 0;  // items (units) before them
+    long long base = 0;  // items (cost) before them
     bool bad = false;    // some request so far had a bad length (lane-wise)
 };
 
-// False when there is no item (unit) `idx`. *in: its number in the request.
-template <bool UNITS>
+// False when there is no item (unit of cost) `idx`. *in: its number in the request.
+template <bool COST>
 __device__ __forceinline__ bool attn_find(const AttnShape& s, AttnWalk& w, long long idx, int* req,
                                           AttnReq* rq, long long* in) {
     const int lane = threadIdx.x & 31;
@@ -146,7 +150,7 @@ __device__ __forceinline__ bool attn_find(const AttnShape& s, AttnWalk& w, long 
         if (r < s.N) q = attn_request(s, r);
         w.bad |= q.bad != 0;
         const long long mine =
-            (q.nqt == 0 ? 0 : UNITS ? attn_units_before(s, q, q.nqt) : q.nqt) * s.Hkv;
+            (q.nqt == 0 ? 0 : COST ? attn_units_before(s, q, q.nqt) * q.cost : q.nqt) * s.Hkv;
         long long inc = mine;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
@@ -163,6 +167,7 @@ __device__ __forceinline__ bool attn_find(const AttnShape& s, AttnWalk& w, long 
             rq->kv = __shfl_sync(0xffffffffu, q.kv, src);
             rq->tok = __shfl_sync(0xffffffffu, q.tok, src);
             rq->nqt = __shfl_sync(0xffffffffu, q.nqt, src);
+            rq->cost = __shfl_sync(0xffffffffu, q.cost, src);
             rq->bad = 0;
             *in = idx - w.base - __shfl_sync(0xffffffffu, inc - mine, src);
             return true;
@@ -172,33 +177,44 @@ __device__ __forceinline__ bool attn_find(const AttnShape& s, AttnWalk& w, long 
     return false;
 }
 
-// Split items: units of a request run key head by key head, row tile by row
-// tile. The item of unit `in` of a request and the tile of it that the unit is.
-__device__ __forceinline__ void attn_unit_item(const AttnShape& s, const AttnReq& q, long long in,
-                                               int* h, int* t, int* tile) {
-    const long long per = attn_units_before(s, q, q.nqt);
-    *h = in < 1LL << 32 && per < 1LL << 32 ? (int)((uint32_t)in / (uint32_t)per) : (int)(in / per);
-    const long long rest = in - *h * per;
+// Split items: the tiles of a request run key head by key head, row tile by row
+// tile. The first tile at or after the unit of cost `cur`, by a warp together:
+// its request, key head, row tile and number in the item. cur moves to its
+// start. False when there is none.
+__device__ __forceinline__ bool attn_first_tile(const AttnShape& s, AttnWalk& w, long long* cur,
+                                                int* r, AttnReq* q, int* h, int* t, int* tile) {
+    long long in, per, at;
+    for (;;) {
+        if (!attn_find<true>(s, w, *cur, r, q, &in)) return false;
+        per = attn_units_before(s, *q, q->nqt);
+        // its number among the request's tiles
+        at = in < 1LL << 32 ? (uint32_t)(in + q->cost - 1) / (uint32_t)q->cost : (in + q->cost - 1) / q->cost;
+        *cur += at * q->cost - in;
+        if (at < per * s.Hkv) break;  // else the next request's first
+    }
+    *h = at < 1LL << 32 && per < 1LL << 32 ? (int)((uint32_t)at / (uint32_t)per) : (int)(at / per);
+    const long long rest = at - *h * per;
     // units_before(lo) <= rest < units_before(hi); 32 places at a time
-    int lo = 0, hi = q.nqt;
+    int lo = 0, hi = q->nqt;
     while (hi - lo > 1) {
-        const int step = (hi - lo + 31) >> 5, at = lo + (int)(threadIdx.x & 31) * step;
-        const bool below = at < hi && attn_units_before(s, q, at) <= rest;
+        const int step = (hi - lo + 31) >> 5, x = lo + (int)(threadIdx.x & 31) * step;
+        const bool below = x < hi && attn_units_before(s, *q, x) <= rest;
         lo += (__popc(__ballot_sync(0xffffffffu, below)) - 1) * step;
         hi = min(lo + step, hi);
     }
     *t = lo;
-    *tile = (int)(rest - attn_units_before(s, q, lo));
+    *tile = (int)(rest - attn_units_before(s, *q, lo));
+    return true;
 }
 
-// Sums of the units of 32 requests each, for a walk to start from.
+// Sums of the cost of 32 requests each, for a walk to start from.
 constexpr int kAttnGroups = 256;
 
-// Units of a CTA's range, by the whole block: all units of all requests over
-// `ctas`, but at least `least`. groups[i]: units of requests 32 i .. 32 i + 31;
+// Cost of a CTA's range, by the whole block: that of all requests over `ctas`, but
+// at least `least`. groups[i]: cost of requests 32 i .. 32 i + 31;
 // s_sum: one word per warp. The caller synchronises before groups is read.
 template <int THREADS>
-__device__ __forceinline__ long long attn_units_each(const AttnShape& s, int ctas, int least,
+__device__ __forceinline__ long long attn_cost_each(const AttnShape& s, int ctas, int least,
                                                      long long* groups, long long* s_sum) {
     long long sum = 0;
     for (int r0 = threadIdx.x & ~31; r0 < s.N; r0 += THREADS) {
@@ -206,7 +222,7 @@ __device__ __forceinline__ long long attn_units_each(const AttnShape& s, int cta
         long long mine = 0;
         if (r < s.N) {
             const AttnReq q = attn_request(s, r);
-            if (q.nqt) mine = attn_units_before(s, q, q.nqt) * s.Hkv;
+            if (q.nqt) mine = attn_units_before(s, q, q.nqt) * q.cost * s.Hkv;
         }
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) mine += __shfl_xor_sync(0xffffffffu, mine, o);
@@ -221,7 +237,7 @@ __device__ __forceinline__ long long attn_units_each(const AttnShape& s, int cta
     return each < least ? least : each;
 }
 
-// A walk that starts at the 32 requests that hold unit `idx` (or, beyond the
+// A walk that starts at the 32 requests that hold unit of cost `idx` (or, beyond the
 // groups there are sums of, at the first ones without).
 __device__ __forceinline__ AttnWalk attn_walk_at(const AttnShape& s, const long long* groups,
                                                  long long idx) {
@@ -239,16 +255,17 @@ __device__ __forceinline__ AttnWalk attn_walk_at(const AttnShape& s, const long 
 // part), then rows log-sums in base 2. After the slots, one AttnCut per CTA.
 struct AttnSplit {
     float* ws;      // null: whole items
-    int ctas;       // CTAs the units are divided among
-    int least;      // units of a range, at least
+    int ctas;       // CTAs the tiles are divided among
+    int least;      // cost of a range, at least (no less than a tile's)
     int rows;       // rows of a slot
 };
-// Where a CTA's range starts: which unit of which item.
+// The first tile of a CTA's range.
 struct AttnCut {
-    long long each;  // units of a range
-    int tok0, ntok;  // the item's tokens (0: no work at or after the start)
-    int h, tile, n;  // key head; unit of the item that the range starts at; units of the item
-    int pad;
+    long long each;  // cost of a range
+    long long u0;    // cost before the tile's item
+    int tok0, ntok;  // the item's tokens (ntok 0: no tile in the range)
+    int h, tile, n;  // key head; the tile's number in the item; tiles of the item
+    int cost;        // of a tile
 };
 inline __host__ __device__ size_t attn_slot_floats(int rows, int d) { return (size_t)rows * (d + 1); }
 inline __host__ __device__ AttnCut* attn_cuts(const AttnSplit& sp, int d) {

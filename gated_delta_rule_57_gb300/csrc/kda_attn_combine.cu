@@ -24,8 +24,12 @@ __global__ void __launch_bounds__(kCombineWarps * 32)
     const int b = blockIdx.x + 1;
     const AttnCut cut = attn_cuts(sp, D)[b];
     if (cut.ntok == 0 || cut.tile == 0) return;  // no work, or the boundary is an item's too
-    const long long u0 = b * cut.each - cut.tile, u1 = u0 + cut.n;
-    const int c0 = (int)(u0 / cut.each), c1 = (int)((u1 - 1) / cut.each);  // CTAs with a part
+    // CTAs with a part: the ranges of the item's first and last tile.
+    const int c0 = (int)(cut.u0 / cut.each);
+    const int c1 = (int)((cut.u0 + (long long)(cut.n - 1) * cut.cost) / cut.each);
+    // The first part may be its range's first too.
+    const AttnCut start = attn_cuts(sp, D)[c0];
+    const int late = !(start.u0 == cut.u0 && start.tile == 0);
     const int lane = threadIdx.x & 31, rows = cut.ntok * G, per = tile_rows / G;
     const int first = ((b - 1 - c0) * gridDim.y + blockIdx.y) * kCombineWarps + (threadIdx.x >> 5);
     const int step = (c1 - c0) * gridDim.y * kCombineWarps;
@@ -47,7 +51,7 @@ __global__ void __launch_bounds__(kCombineWarps * 32)
         }
 #pragma unroll 2
         for (int c = c0; c <= c1; c++) {
-            const float* p = sp.ws + slot * (2 * (size_t)c + (u0 > c * cut.each ? 1 : 0));
+            const float* p = sp.ws + slot * (2 * (size_t)c + (c == c0 ? late : 0));
             float x[kBatch], y[kBatch][V];
 #pragma unroll
             for (int k = 0; k < kBatch; k++) {

@@ -73,11 +73,11 @@ __global__ void __launch_bounds__(kThreadsSimt, kCtasPerSm) kda_attn_simt_kernel
     long long in, each = 0;
     const bool split = p.sp.ws != nullptr;
     if (split) {
-        each = attn_units_each<kThreadsSimt>(s, p.sp.ctas, p.sp.least, s_groups, s_sum);
+        each = attn_cost_each<kThreadsSimt>(s, p.sp.ctas, p.sp.least, s_groups, s_sum);
         __syncthreads();
     }
-    // Whole items: numbers blockIdx.x, + gridDim.x, ...; split ones: units
-    // [cur, end). Every warp walks by itself, to the same places.
+    // Whole items: numbers blockIdx.x, + gridDim.x, ...; split ones: tiles
+    // that start in [cur, end), a tile costing 1. Every warp walks by itself, to the same places.
     long long cur = split ? blockIdx.x * each : blockIdx.x;
     const long long start = cur, end = cur + each;
     if (split) walk = attn_walk_at(s, s_groups, cur);
@@ -85,14 +85,12 @@ __global__ void __launch_bounds__(kThreadsSimt, kCtasPerSm) kda_attn_simt_kernel
     int tile = 0;
     while (!split || cur < end) {
         if (!have) {
-            if (!(split ? attn_find<true>(s, walk, cur, &it.r, &it.q, &in)
+            if (!(split ? attn_first_tile(s, walk, &cur, &it.r, &it.q, &it.h, &it.t, &tile)
                         : attn_find<false>(s, walk, cur, &it.r, &it.q, &in))) {
                 if (split && cur == start && tid == 0) attn_cuts(p.sp, D)[blockIdx.x] = AttnCut{};
                 break;
             }
-            if (split) {
-                attn_unit_item(s, it.q, in, &it.h, &it.t, &tile);
-            } else {
+            if (!split) {
                 it.t = it.q.nqt - 1 - (int)(in / s.Hkv);
                 it.h = (int)(in % s.Hkv);
             }
@@ -107,7 +105,7 @@ __global__ void __launch_bounds__(kThreadsSimt, kCtasPerSm) kda_attn_simt_kernel
         if (split) {
             if (cur == start && tid == 0)
                 attn_cuts(p.sp, D)[blockIdx.x] =
-                    AttnCut{each, it.q.q0 + tok0, rows / G, it.h, tile, units, 0};
+                    AttnCut{each, cur - tile, it.q.q0 + tok0, rows / G, it.h, tile, units, 1};
             if (take < units)
                 part = p.sp.ws + attn_slot_floats(p.sp.rows, D) * (2 * blockIdx.x + (cur > start ? 1 : 0));
         }
@@ -283,7 +281,7 @@ cudaError_t launch_t(const AttnArgs& a) {
     SimtParams p{};
     p.s = {a.cu_q, a.kv_len, a.N, a.total_q, a.max_q,
            (int)min((long long)a.max_pages * a.page, (1LL << 31) - 1), a.Hkv, G, kRows / G,
-           kRows / G, kKeys};
+           kRows / G, kKeys, 1, 1};
     p.q = a.q;
     p.k = a.k;
     p.v = a.v;

@@ -52,6 +52,9 @@ constexpr int kRegsSoftmax = 192, kRegsOther = 64, kRegsResult = 64;
 static_assert(2 * kRegsSoftmax + kRegsOther + kRegsResult <= 4 * 128, "more than launched with");
 constexpr int kMmaWarp = 8, kLoadWarp = 9, kTailWarp = 10;
 constexpr int kPieces = 4;         // pieces announced ahead
+// Relative time of a key tile for one row tile and for a pair: about 1750 and 2500
+// clocks, measured in a step of two prompts' chunks among single tokens.
+constexpr int kCostSingle = 5, kCostPair = 7;
 constexpr float kRaise = 8.f;      // log2 growth of a row maximum that moves its reference
 
 template <int D>
@@ -279,9 +282,9 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
     }
     tc_fence_before();
     pdl_wait();
-    // Units of this CTA's range (split items); also the barrier after the setup.
+    // Cost of this CTA's range (split items); also the barrier after the setup.
     long long each = 0;
-    if (p.sp.ws) each = attn_units_each<kThreadsTc>(p.s, p.sp.ctas, p.sp.least, sh.groups, sh.sum);
+    if (p.sp.ws) each = attn_cost_each<kThreadsTc>(p.s, p.sp.ctas, p.sp.least, sh.groups, sh.sum);
     __syncthreads();
     tc_fence_after();
     const uint32_t tbase = sh.tmem;
@@ -394,26 +397,29 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
             };
             // Whole items: a CTA per item, of which those that run take over the ones
             // that have not started, in their order (longest rows of a request first),
-            // asking ahead. Split ones: the units [cur, end), item by item.
+            // asking ahead. Split ones: the tiles that start in [cur, end), item by item.
             AttnReq q{};
             int r = 0, h = 0, t = 0, tile = 0;
             long long in;
             const bool split = p.sp.ws != nullptr;
             long long cur = split ? blockIdx.x * each : blockIdx.x;
-            const long long start = cur, end = cur + each;
+            const long long end = cur + each;
+            long long start = cur;
             bool have = false;  // (q, h, t, tile) is where `cur` is
             AttnWalk walk;
             if (split) {
                 walk = attn_walk_at(p.s, sh.groups, cur);
-                AttnCut cut{each, 0, 0, 0, 0, 0, 0};
-                have = attn_find<true>(p.s, walk, cur, &r, &q, &in);
+                AttnCut cut{each, 0, 0, 0, 0, 0, 0, 0};
+                have = attn_first_tile(p.s, walk, &cur, &r, &q, &h, &t, &tile) && cur < end;
+                start = cur;
                 if (have) {
-                    attn_unit_item(p.s, q, in, &h, &t, &tile);
+                    cut.u0 = cur - (long long)tile * q.cost;
                     cut.tok0 = q.q0 + t * q.tok;
                     cut.ntok = min(q.tok, q.q_len - t * q.tok);
                     cut.h = h;
                     cut.tile = tile;
                     cut.n = attn_item_units(p.s, q, t);
+                    cut.cost = q.cost;
                 }
                 if (lane == 0) attn_cuts(p.sp, D)[blockIdx.x] = cut;
                 if (!have) cur = end;
@@ -429,11 +435,9 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
                     if (cur < walk.base) walk = AttnWalk{};
                 }
                 if (!have) {
-                    have = split ? attn_find<true>(p.s, walk, cur, &r, &q, &in)
+                    have = split ? attn_first_tile(p.s, walk, &cur, &r, &q, &h, &t, &tile)
                                  : attn_find<false>(p.s, walk, cur, &r, &q, &in);
-                    if (split && have) {
-                        attn_unit_item(p.s, q, in, &h, &t, &tile);
-                    } else if (have) {
+                    if (!split && have) {
                         t = q.nqt - 1 - (int)(in / p.s.Hkv);
                         h = (int)(in % p.s.Hkv);
                     }
@@ -441,11 +445,12 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
                 if (have) {
                     Piece pc = piece_of(r, q, h, t);
                     if (split) {
-                        const int n = pc.kt1, take = (int)min((long long)(n - tile), end - cur);
+                        const int n = pc.kt1;
+                        const int take = (int)min((long long)(n - tile), (end - cur + q.cost - 1) / q.cost);
                         pc.kt0 = tile;
                         pc.kt1 = tile + take;
                         if (take < n) pc.slot = 2 * blockIdx.x + (cur > start ? 1 : 0);
-                        cur += take;
+                        cur += (long long)take * q.cost;
                         tile = 0;
                         if (++t == q.nqt) {
                             t = 0;
@@ -1025,7 +1030,7 @@ cudaError_t launch_t(const AttnArgs& a) {
     TcAttnParams p{};
     p.s = {a.cu_q, a.kv_len, a.N, a.total_q, a.max_q,
            (int)min((long long)a.max_pages * a.page, (1LL << 31) - 1), a.Hkv, G, tok1, 2 * tok1,
-           kTile};
+           kTile, kCostSingle, kCostPair};
     p.sp = attn_tc_split(a.N, a.total_q, a.max_q, a.kv_len ? p.s.kv_cap : a.max_q, a.Hq, a.Hkv, nsm);
     if (p.sp.ctas && a.ws && a.ws_bytes >= attn_split_bytes(p.sp, D)) p.sp.ws = a.ws;
     p.block_table = a.block_table;
@@ -1082,7 +1087,7 @@ AttnSplit attn_tc_split(int N, int total_q, int max_q, long long max_keys, int H
     const long long items = (long long)total_q / (2 * tok1) * Hkv;
     if (max_q > tok1 && items >= 8LL * nsm) return sp;
     sp.ctas = nsm;
-    sp.least = 2;
+    sp.least = 2 * kCostPair;
     sp.rows = max_q <= tok1 ? (max_q * G + 3) & ~3 : 2 * kTile;  // whole 16-byte vectors
     return sp;
 }
