@@ -54,14 +54,14 @@ struct AttnShape {
     int Hkv, G;
     int tok1, tok2;  // tokens of an item: tok1 for requests that fit it, else tok2
     int kt;          // keys of a key tile
-    int cost1, cost2;  // of a key tile of either kind of item, in any unit
+    int cost1, cost2;  // of a key of either kind of item, in any unit
 };
 
 // One request: its packed tokens, keys, and items.
 struct AttnReq {
     int q0, q_len, kv;  // first packed token, new tokens, keys
     int tok, nqt;       // tokens per item, items per key head
-    int cost;           // of a key tile
+    int cost;           // of a key
     int bad;            // lengths outside what the call was sized for
 };
 
@@ -90,45 +90,20 @@ __device__ __forceinline__ int attn_item_keys(const AttnReq& q, int t) {
     return max(q.kv - q.q_len + last, 0);
 }
 
-// sum_{i < n} floor((a i + b) / m): the multiples of m in a and b are taken out,
-// and what is left counts the lattice points under a line, which are those
-// beside it with the axes exchanged (Euclid's steps; two or three for the tile
-// sizes here). a n + b below 2^32.
-__device__ __forceinline__ long long attn_floor_sum(uint32_t n, uint32_t m, uint32_t a,
-                                                    uint32_t b) {
-    long long sum = 0;
-    while (n > 0) {
-        const uint32_t qa = a / m, qb = b / m;
-        sum += ((long long)n * (n - 1) >> 1) * qa + (long long)n * qb;
-        a -= qa * m;
-        b -= qb * m;
-        if (a == 0) break;
-        const uint32_t top = a * n + b;
-        n = top / m;
-        b = top - n * m;
-        const uint32_t x = m;
-        m = a;
-        a = x;
-    }
-    return sum;
-}
-
-// Units (key tiles, at least one) of item t of a request, and of its items
-// 0 .. t - 1.
-__device__ __forceinline__ int attn_item_units(const AttnShape& s, const AttnReq& q, int t) {
+// Key tiles of item t of a request, at least one.
+__device__ __forceinline__ int attn_item_tiles(const AttnShape& s, const AttnReq& q, int t) {
     return max((attn_item_keys(q, t) + s.kt - 1) / s.kt, 1);
 }
-__device__ __forceinline__ long long attn_units_before(const AttnShape& s, const AttnReq& q, int t) {
-    if (t <= 0) return 0;
-    if (q.nqt == 1) return attn_item_units(s, q, 0);
-    const int full = min(t, q.nqt - 1);  // items whose tokens are all there
-    const int off = q.kv - q.q_len;
-    // Items that see at most one tile count one each.
-    int one = off + q.tok <= s.kt ? (s.kt - off) / q.tok : 0;
-    one = min(one, full);
-    long long sum = one + attn_floor_sum(full - one, s.kt, q.tok, off + (one + 1) * q.tok + s.kt - 1);
-    if (t == q.nqt) sum += attn_item_units(s, q, t - 1);
-    return sum;
+
+// Cost. A key tile costs q.cost kt; item t of a request is counted as
+//     q.cost (max(kv - q_len, 0) + (t + 1) tok + kt - 1),
+// its keys rounded up to where its last tile must end: never less than its
+// tiles', at most about one tile more, and linear in t, so that the cost before
+// an item is a product and not a sum of quotients (those, by Euclid's steps,
+// took 1200 clocks each time). Tile k of an item starts at k q.cost kt.
+__device__ __forceinline__ long long attn_cost_before(const AttnShape& s, const AttnReq& q, int t) {
+    const long long first = (long long)max(q.kv - q.q_len, 0) + s.kt - 1;
+    return ((long long)t * first + (long long)q.tok * t * (t + 1) / 2) * q.cost;
 }
 
 // A walk over the requests, a warp together, that finds the request of an item
@@ -150,7 +125,7 @@ __device__ __forceinline__ bool attn_find(const AttnShape& s, AttnWalk& w, long 
         if (r < s.N) q = attn_request(s, r);
         w.bad |= q.bad != 0;
         const long long mine =
-            (q.nqt == 0 ? 0 : COST ? attn_units_before(s, q, q.nqt) * q.cost : q.nqt) * s.Hkv;
+            (COST ? attn_cost_before(s, q, q.nqt) : q.nqt) * s.Hkv;
         long long inc = mine;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
@@ -177,34 +152,52 @@ __device__ __forceinline__ bool attn_find(const AttnShape& s, AttnWalk& w, long 
     return false;
 }
 
-// Split items: the tiles of a request run key head by key head, row tile by row
-// tile. The first tile at or after the unit of cost `cur`, by a warp together:
+// a / b, in 32 bits where that does (a quarter of the time).
+__device__ __forceinline__ int attn_quotient(long long a, long long b) {
+    return (unsigned long long)a < 1ull << 32 && b < 1LL << 32 ? (int)((uint32_t)a / (uint32_t)b) : (int)(a / b);
+}
+
+// Split items: the items of a request run key head by key head, row tile by row
+// tile. The first key tile that starts at or after `cur`, by a warp together:
 // its request, key head, row tile and number in the item. cur moves to its
 // start. False when there is none.
 __device__ __forceinline__ bool attn_first_tile(const AttnShape& s, AttnWalk& w, long long* cur,
                                                 int* r, AttnReq* q, int* h, int* t, int* tile) {
-    long long in, per, at;
-    for (;;) {
-        if (!attn_find<true>(s, w, *cur, r, q, &in)) return false;
-        per = attn_units_before(s, *q, q->nqt);
-        // its number among the request's tiles
-        at = in < 1LL << 32 ? (uint32_t)(in + q->cost - 1) / (uint32_t)q->cost : (in + q->cost - 1) / q->cost;
-        *cur += at * q->cost - in;
-        if (at < per * s.Hkv) break;  // else the next request's first
+    long long in;
+    while (attn_find<true>(s, w, *cur, r, q, &in)) {
+        const long long base = *cur - in, per = attn_cost_before(s, *q, q->nqt);
+        *h = attn_quotient(in, per);
+        const long long rest = in - *h * per;
+        // cost_before(lo) <= rest < cost_before(hi); 32 places at a time
+        int lo = 0, hi = q->nqt;
+        while (hi - lo > 1) {
+            const int step = (hi - lo + 31) >> 5, x = lo + (int)(threadIdx.x & 31) * step;
+            const bool below = x < hi && attn_cost_before(s, *q, x) <= rest;
+            lo += (__popc(__ballot_sync(0xffffffffu, below)) - 1) * step;
+            hi = min(lo + step, hi);
+        }
+        const int each = s.kt * q->cost;
+        const long long before = attn_cost_before(s, *q, lo);
+        *tile = attn_quotient(rest - before + each - 1, each);
+        if (*tile >= attn_item_tiles(s, *q, lo)) {  // the next item's first
+            *tile = 0;
+            if (++lo == q->nqt) {
+                lo = 0;
+                ++*h;
+            }
+        }
+        *t = lo;
+        *cur = base + *h * per + (*tile ? before + (long long)*tile * each : attn_cost_before(s, *q, lo));
+        if (*h < s.Hkv) return true;
     }
-    *h = at < 1LL << 32 && per < 1LL << 32 ? (int)((uint32_t)at / (uint32_t)per) : (int)(at / per);
-    const long long rest = at - *h * per;
-    // units_before(lo) <= rest < units_before(hi); 32 places at a time
-    int lo = 0, hi = q->nqt;
-    while (hi - lo > 1) {
-        const int step = (hi - lo + 31) >> 5, x = lo + (int)(threadIdx.x & 31) * step;
-        const bool below = x < hi && attn_units_before(s, *q, x) <= rest;
-        lo += (__popc(__ballot_sync(0xffffffffu, below)) - 1) * step;
-        hi = min(lo + step, hi);
-    }
-    *t = lo;
-    *tile = (int)(rest - attn_units_before(s, *q, lo));
-    return true;
+    return false;
+}
+// Tiles of an item of `n` that starts at u0 that start before `end`.
+__device__ __forceinline__ int attn_tiles_until(const AttnShape& s, const AttnReq& q, long long u0,
+                                                int n, long long end) {
+    const int each = s.kt * q.cost;
+    const long long room = end - u0;
+    return room >= (long long)n * each ? n : attn_quotient(room + each - 1, each);
 }
 
 // Sums of the cost of 32 requests each, for a walk to start from.
@@ -222,7 +215,7 @@ __device__ __forceinline__ long long attn_cost_each(const AttnShape& s, int ctas
         long long mine = 0;
         if (r < s.N) {
             const AttnReq q = attn_request(s, r);
-            if (q.nqt) mine = attn_units_before(s, q, q.nqt) * q.cost * s.Hkv;
+            mine = attn_cost_before(s, q, q.nqt) * s.Hkv;
         }
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) mine += __shfl_xor_sync(0xffffffffu, mine, o);

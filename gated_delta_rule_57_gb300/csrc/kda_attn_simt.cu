@@ -77,19 +77,22 @@ __global__ void __launch_bounds__(kThreadsSimt, kCtasPerSm) kda_attn_simt_kernel
         __syncthreads();
     }
     // Whole items: numbers blockIdx.x, + gridDim.x, ...; split ones: tiles
-    // that start in [cur, end), a tile costing 1. Every warp walks by itself, to the same places.
+    // that start in [cur, end), a key costing 1. Every warp walks by itself, to the same places.
     long long cur = split ? blockIdx.x * each : blockIdx.x;
-    const long long start = cur, end = cur + each;
+    const long long end = cur + each;
+    long long start = cur;
     if (split) walk = attn_walk_at(s, s_groups, cur);
     bool have = false;
     int tile = 0;
     while (!split || cur < end) {
         if (!have) {
-            if (!(split ? attn_first_tile(s, walk, &cur, &it.r, &it.q, &it.h, &it.t, &tile)
+            const bool first = split && cur == start;
+            if (!(split ? attn_first_tile(s, walk, &cur, &it.r, &it.q, &it.h, &it.t, &tile) && cur < end
                         : attn_find<false>(s, walk, cur, &it.r, &it.q, &in))) {
-                if (split && cur == start && tid == 0) attn_cuts(p.sp, D)[blockIdx.x] = AttnCut{};
+                if (first && tid == 0) attn_cuts(p.sp, D)[blockIdx.x] = AttnCut{};
                 break;
             }
+            if (first) start = cur;
             if (!split) {
                 it.t = it.q.nqt - 1 - (int)(in / s.Hkv);
                 it.h = (int)(in % s.Hkv);
@@ -97,16 +100,17 @@ __global__ void __launch_bounds__(kThreadsSimt, kCtasPerSm) kda_attn_simt_kernel
         }
         const int G = s.G, tok0 = it.t * it.q.tok;
         const int rows = min(it.q.tok, it.q.q_len - tok0) * G;
-        const int units = attn_item_units(s, it.q, it.t);
+        const int tiles = attn_item_tiles(s, it.q, it.t);
         // Keys [key0, keys) of the item are this CTA's.
-        const int take = split ? (int)min((long long)(units - tile), end - cur) : units;
-        const int key0 = tile * kKeys, keys = min(attn_item_keys(it.q, it.t), (tile + take) * kKeys);
+        const long long u0 = cur - tile * kKeys;
+        const int last = split ? attn_tiles_until(s, it.q, u0, tiles, end) : tiles;
+        const int key0 = tile * kKeys, keys = min(attn_item_keys(it.q, it.t), last * kKeys);
         float* part = nullptr;
         if (split) {
             if (cur == start && tid == 0)
                 attn_cuts(p.sp, D)[blockIdx.x] =
-                    AttnCut{each, cur - tile, it.q.q0 + tok0, rows / G, it.h, tile, units, 1};
-            if (take < units)
+                    AttnCut{each, u0, it.q.q0 + tok0, rows / G, it.h, tile, tiles, kKeys};
+            if (last - tile < tiles)
                 part = p.sp.ws + attn_slot_floats(p.sp.rows, D) * (2 * blockIdx.x + (cur > start ? 1 : 0));
         }
         const size_t first = (size_t)it.q.q0 + tok0;  // packed token of row 0
@@ -258,7 +262,8 @@ __global__ void __launch_bounds__(kThreadsSimt, kCtasPerSm) kda_attn_simt_kernel
             }
         }
         if (split) {
-            cur += take;
+            cur = last < tiles ? end
+                               : u0 + attn_cost_before(s, it.q, it.t + 1) - attn_cost_before(s, it.q, it.t);
             tile = 0;
             if (++it.t == it.q.nqt) {
                 it.t = 0;
@@ -321,7 +326,7 @@ AttnSplit attn_simt_split(int N, int total_q, int max_q, long long max_keys, int
     if (max_keys <= KDA_ATTN_SHORT_KEYS / 4) return sp;
     if ((long long)total_q / tok * Hkv >= 16LL * kCtasPerSm * nsm) return sp;
     sp.ctas = kCtasPerSm * nsm;
-    sp.least = 1;
+    sp.least = kKeys;
     sp.rows = (std::min(max_q, tok) * G + 3) & ~3;  // whole 16-byte vectors
     return sp;
 }

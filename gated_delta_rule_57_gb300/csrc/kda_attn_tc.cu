@@ -389,7 +389,7 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
                 pc.kv = q.kv;
                 pc.keys = attn_item_keys(q, t);
                 pc.kt0 = 0;
-                pc.kt1 = attn_item_units(p.s, q, t);
+                pc.kt1 = attn_item_tiles(p.s, q, t);
                 pc.pair = q.tok > tok1;
                 pc.slot = -1;
                 pc.end = 0;
@@ -413,13 +413,13 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
                 have = attn_first_tile(p.s, walk, &cur, &r, &q, &h, &t, &tile) && cur < end;
                 start = cur;
                 if (have) {
-                    cut.u0 = cur - (long long)tile * q.cost;
+                    cut.cost = q.cost * kTile;
+                    cut.u0 = cur - (long long)tile * cut.cost;
                     cut.tok0 = q.q0 + t * q.tok;
                     cut.ntok = min(q.tok, q.q_len - t * q.tok);
                     cut.h = h;
                     cut.tile = tile;
-                    cut.n = attn_item_units(p.s, q, t);
-                    cut.cost = q.cost;
+                    cut.n = attn_item_tiles(p.s, q, t);
                 }
                 if (lane == 0) attn_cuts(p.sp, D)[blockIdx.x] = cut;
                 if (!have) cur = end;
@@ -446,11 +446,12 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
                     Piece pc = piece_of(r, q, h, t);
                     if (split) {
                         const int n = pc.kt1;
-                        const int take = (int)min((long long)(n - tile), (end - cur + q.cost - 1) / q.cost);
+                        const long long u0 = cur - (long long)tile * q.cost * kTile;
                         pc.kt0 = tile;
-                        pc.kt1 = tile + take;
-                        if (take < n) pc.slot = 2 * blockIdx.x + (cur > start ? 1 : 0);
-                        cur += (long long)take * q.cost;
+                        pc.kt1 = attn_tiles_until(p.s, q, u0, n, end);
+                        if (pc.kt1 - pc.kt0 < n) pc.slot = 2 * blockIdx.x + (cur > start ? 1 : 0);
+                        cur = pc.kt1 < n ? end
+                                         : u0 + attn_cost_before(p.s, q, t + 1) - attn_cost_before(p.s, q, t);
                         tile = 0;
                         if (++t == q.nqt) {
                             t = 0;
@@ -1087,7 +1088,7 @@ AttnSplit attn_tc_split(int N, int total_q, int max_q, long long max_keys, int H
     const long long items = (long long)total_q / (2 * tok1) * Hkv;
     if (max_q > tok1 && items >= 8LL * nsm) return sp;
     sp.ctas = nsm;
-    sp.least = 2 * kCostPair;
+    sp.least = 2 * kCostPair * kTile;
     sp.rows = max_q <= tok1 ? (max_q * G + 3) & ~3 : 2 * kTile;  // whole 16-byte vectors
     return sp;
 }
