@@ -29,6 +29,8 @@ kda_status_t run(AttnArgs& a, kda_dtype_t io, size_t n_k, size_t n_v) {
     const size_t row = (size_t)a.Hq * a.d;
     if (!(a.scale > 0.f) || !isfinite(a.scale))
         return fail(KDA_ERR_INVALID_ARG, "scale must be positive and finite");
+    if (a.total_q > (1 << 30) || a.N > (1 << 30))
+        return fail(KDA_ERR_INVALID_ARG, "at most 2^30 tokens and requests");
     if (!a.q || !a.cu_q || !a.o) return fail(KDA_ERR_INVALID_ARG, "a NULL pointer");
     for (const void* p : {a.q, a.k, a.v, (const void*)a.o, (const void*)a.ws})
         if (!aligned16(p)) return fail(KDA_ERR_INVALID_ARG, "pointers must be 16-byte aligned");

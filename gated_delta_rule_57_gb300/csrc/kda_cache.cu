@@ -201,6 +201,7 @@ __global__ void __launch_bounds__(kPlanThreads) kda_kv_plan_kernel(const PlanPar
         p.ring_out[1] = (int)(count - taken + given);
     }
 
+    const unsigned after = head + count < P ? head + count : head + count - P;  // the ring's end
     const unsigned first = blockIdx.x * kPlanThreads + tid, step = gridDim.x * kPlanThreads;
     for (unsigned t = first; t < (unsigned)p.max_tokens; t += step) {
         int slot = -1;
@@ -225,7 +226,7 @@ __global__ void __launch_bounds__(kPlanThreads) kda_kv_plan_kernel(const PlanPar
     }
     for (unsigned i = first; i < given; i += step) {
         const int r = find(s_back, N, i);
-        p.ring[(head + count + i) % P] =
+        p.ring[(after + i) % P] =
             p.table[(size_t)r * p.max_pages + pages(length(p.new_len, r)) + i - s_back[r]];
     }
     report_flags(p.d_status, flags);
@@ -361,6 +362,7 @@ kda_status_t kda_kv_append(const void* k, const void* v, const int* slot_map, vo
         return fail(KDA_ERR_INVALID_ARG, "T, Hkv and num_pages must be >= 0, page_size positive");
     if (io != KDA_BF16 && io != KDA_F32) return fail(KDA_ERR_INVALID_ARG, "unknown io dtype");
     if (d != 64 && d != 128) return fail(KDA_ERR_UNSUPPORTED, "d must be 64 or 128");
+    if (T > (1 << 30)) return fail(KDA_ERR_INVALID_ARG, "T must be at most 2^30");
     if (Hkv > (1 << 16)) return fail(KDA_ERR_INVALID_ARG, "Hkv must be at most 65536");
     if ((long long)num_pages * page_size >= (1LL << 31))
         return fail(KDA_ERR_INVALID_ARG, "num_pages * page_size must be below 2^31");
