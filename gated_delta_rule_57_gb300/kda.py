@@ -525,7 +525,7 @@ def kda_attn_workspace_size(N: int, total_q: int, max_q: int, Hq: int, Hkv: int,
     return int(n)
 
 
-def _attn_buffers(q, N, most, keys, Hkv, o, lse, want_lse, workspace):
+def _attn_buffers(q, N, most, keys, Hkv, o, lse, want_lse, workspace, stream):
     """Outputs and workspace of an attention call, and its dtype code."""
     T, Hq, d = q.shape
     io = _DTYPE.get(q.dtype)
@@ -544,6 +544,8 @@ def _attn_buffers(q, N, most, keys, Hkv, o, lse, want_lse, workspace):
         need = (_lib or lib()).kda_attn_workspace_size(N, T, most, Hq, Hkv, d, io)
         if need != ctypes.c_size_t(-1).value and need:  # the call itself reports bad arguments
             workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+            if stream is not None:  # freed when this call returns: not before its stream is done
+                workspace.record_stream(stream)
     ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
     return io, o, lse, workspace, ws_bytes
 
@@ -561,7 +563,8 @@ def kda_attn_prompt(q, k, v, cu_seqlens, *, max_len: Optional[int] = None,
     if k.shape != (T, Hkv, d) or v.shape != k.shape:
         raise ValueError("k and v must be [T, Hkv, d] with q's T and d")
     most = T if max_len is None else max_len
-    io, o, lse, workspace, ws_bytes = _attn_buffers(q, N, most, most, Hkv, o, lse, want_lse, workspace)
+    io, o, lse, workspace, ws_bytes = _attn_buffers(q, N, most, most, Hkv, o, lse, want_lse, workspace,
+                                                    stream)
     qp, qs = _rows("q", q)
     kp, ks = _rows("k", k, q.dtype)
     vp, vs = _rows("v", v, q.dtype)
@@ -589,7 +592,7 @@ def kda_attn_paged(q, k_cache, v_cache, block_table, cu_q, kv_len, *,
         raise ValueError("the caches must be [num_pages, Hkv, page_size, d] of q's d and dtype")
     most = T if max_q is None else max_q
     io, o, lse, workspace, ws_bytes = _attn_buffers(q, N, most, max_pages * page, Hkv, o, lse,
-                                                    want_lse, workspace)
+                                                    want_lse, workspace, stream)
     qp, qs = _rows("q", q)
     _check((_lib or lib()).kda_attn_paged(qp, _ptr(k_cache), _ptr(v_cache),
                                 _ints("block_table", block_table, (N, max_pages)),
