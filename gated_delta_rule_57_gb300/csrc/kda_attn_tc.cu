@@ -55,6 +55,8 @@ constexpr int kPieces = 4;         // pieces announced ahead
 // Relative time of a key tile for one row tile and for a pair: about 1750 and 2500
 // clocks, measured in a step of two prompts' chunks among single tokens.
 constexpr int kCostSingle = 5, kCostPair = 7;
+// Limit of a wait (about 4 s): rows computed again over a million keys pass it by far.
+constexpr long long kWaitClocks = 1LL << 33;
 constexpr float kRaise = 8.f;      // log2 growth of a row maximum that moves its reference
 
 template <int D>
@@ -149,7 +151,7 @@ __device__ __forceinline__ float2 add2(float2 a, float2 b) {
 }
 // A bounded wait by a whole warp, with one outcome for all its lanes.
 __device__ __forceinline__ void warp_wait(bool& ok, uint64_t* bar, uint32_t parity) {
-    if (ok) ok = mbar_wait(bar, parity);
+    if (ok) ok = mbar_wait(bar, parity, kWaitClocks);
     ok = __all_sync(0xffffffffu, ok);
 }
 
@@ -180,6 +182,38 @@ constexpr int tc_smem() {
 }
 static_assert(tc_smem<128>() <= 227 * 1024, "shared memory of a CTA");
 
+// Keys and values of key j of a piece; null where its page id is out of range
+// (such pages read as zeros).
+__device__ __forceinline__ void key_at(const TcAttnParams& p, const Piece& pc, int d, int j,
+                                       const __nv_bfloat16** k, const __nv_bfloat16** v) {
+    if (p.block_table) {
+        const int id = p.block_table[(size_t)pc.r * p.max_pages + j / p.page];
+        const bool there = id >= 0 && id < p.num_pages;
+        const size_t at = (((size_t)id * p.s.Hkv + pc.h) * p.page + j % p.page) * d;
+        *k = there ? p.k + at : nullptr;
+        *v = there ? p.v + at : nullptr;
+    } else {
+        *k = p.k + (size_t)(pc.key0 + j) * p.k_stride + (size_t)pc.h * d;
+        *v = p.v + (size_t)(pc.key0 + j) * p.v_stride + (size_t)pc.h * d;
+    }
+}
+
+// Whether a value of keys [j0, j1) is not finite, a warp together.
+template <int D>
+__device__ bool odd_values(const TcAttnParams& p, const Piece& pc, int j0, int j1) {
+    bool odd = false;
+    for (int j = j0; j < j1; j++) {
+        const __nv_bfloat16 *gk, *gv;
+        key_at(p, pc, D, j, &gk, &gv);
+        if (gv) {
+#pragma unroll
+            for (int e = 0; e < D; e += 32)
+                odd |= finite_flag(__bfloat162float(gv[(threadIdx.x & 31) + e])) != 0;
+        }
+    }
+    return __any_sync(0xffffffffu, odd);
+}
+
 // One row again, a warp together, over exactly the keys [j0, j1) that it sees;
 // lane l holds columns l + 32 e of acc. Returns the sum of exponentials.
 template <int D>
@@ -196,19 +230,7 @@ __device__ float row_again(const TcAttnParams& p, const Piece& pc, size_t tok, i
     for (int e = 0; e < E; e++) acc[e] = 0.f;
     for (int j = j0; j < j1; j++) {
         const __nv_bfloat16 *gk, *gv;
-        if (p.block_table) {
-            const int id = p.block_table[(size_t)pc.r * p.max_pages + j / p.page];
-            if (id < 0 || id >= p.num_pages) {  // reads as zeros
-                gk = gv = nullptr;
-            } else {
-                const size_t at = (((size_t)id * p.s.Hkv + pc.h) * p.page + j % p.page) * D;
-                gk = p.k + at;
-                gv = p.v + at;
-            }
-        } else {
-            gk = p.k + (size_t)(pc.key0 + j) * p.k_stride + (size_t)pc.h * D;
-            gv = p.v + (size_t)(pc.key0 + j) * p.v_stride + (size_t)pc.h * D;
-        }
+        key_at(p, pc, D, j, &gk, &gv);
         float x = 0.f;
         if (gk) {
 #pragma unroll
@@ -297,6 +319,7 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
         if (warp == kLoadWarp) {
             // ------------------------------------------------------------ work and loads
             int stage = 0, kv_phase = 0, q_phase = 0, np = 0;
+            int asked = 0;  // for further items
             // Paged: a tile is `per` pages (or part of one); lane `pg` of each half
             // loads one. Their ids are read a tile or more ahead of their use.
             const int log2_page = __ffs(p.page) - 1;
@@ -424,13 +447,13 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
                 if (lane == 0) attn_cuts(p.sp, D)[blockIdx.x] = cut;
                 if (!have) cur = end;
             }
-            int asked = 0;
             while (ok && (!split || cur < end)) {
                 if (!split) {
                     if (lane == 0) {
                         mbar_arrive_expect_tx(&sh.next_full, 16);
                         clc_try_cancel(&sh.next, &sh.next_full);
                     }
+                    asked++;
                     __syncwarp();
                     if (cur < walk.base) walk = AttnWalk{};
                 }
@@ -465,7 +488,7 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
                 }
                 if (!split) {
                     have = false;
-                    warp_wait(ok, &sh.next_full, asked++ & 1);
+                    warp_wait(ok, &sh.next_full, (asked - 1) & 1);
                     const int x = ok ? __shfl_sync(0xffffffffu, clc_answer(&sh.next), 0) : -1;
                     if (x < 0) break;
                     cur = x;
@@ -487,6 +510,7 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
                 for (int i = 0; i < NS; i++)
                     mbar_wait(&sh.kv_full[i], (i < stage ? kv_phase : kv_phase ^ 1), 1LL << 24);
                 mbar_wait(&sh.q_full, q_phase ^ 1, 1LL << 24);
+                if (asked) mbar_wait(&sh.next_full, (asked - 1) & 1, 1LL << 24);
             }
         } else if (warp == kMmaWarp) {
             // ------------------------------------------------------------ products
@@ -508,7 +532,7 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
                 }
             };
             auto wait = [&](uint64_t* bar, uint32_t parity) {
-                if (!__all_sync(0xffffffffu, mbar_wait(bar, parity))) ok = false;
+                if (!__all_sync(0xffffffffu, mbar_wait(bar, parity, kWaitClocks))) ok = false;
                 return ok;
             };
             auto uniform = [](int x) { return __shfl_sync(0xffffffffu, x, 0); };
@@ -956,16 +980,22 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
                     else if (p.lse)
                         p.lse[at] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.69314718056f;
                 }
-                // Rows that are not finite, again over the keys they see.
+                // Rows that are not finite: where a value that they do not see is at
+                // fault (0 x NaN), again over the keys they see.
                 unsigned bad = __ballot_sync(0xffffffffu, live && !(fin == 0.f));
+                __syncwarp();  // their first results are written
                 while (bad) {
                     const int src = __ffs(bad) - 1;
                     bad &= bad - 1;
                     const int stok = __shfl_sync(0xffffffffu, tok, src);
                     const int shead = __shfl_sync(0xffffffffu, rhead, src);
                     const int ssrow = __shfl_sync(0xffffffffu, srow, src);
-                    const int j0 = pc.kt0 * kTile;
-                    const int j1 = min(pc.kt1 * kTile, max(pc.pos0 + stok + 1, 0));
+                    const int j0 = pc.kt0 * kTile, end = min(pc.kt1 * kTile, pc.keys);
+                    const int j1 = min(end, max(pc.pos0 + stok + 1, 0));
+                    if (!odd_values<D>(p, pc, max(j0, j1), end)) {
+                        flags |= KDA_DEV_NONFINITE;
+                        continue;
+                    }
                     const size_t tk = (size_t)pc.tok0 + stok;
                     const int head = pc.h * G + shead;
                     float y[D / 32];

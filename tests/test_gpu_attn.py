@@ -286,3 +286,40 @@ def test_ranges_of_few_key_tiles(q_lens, kv_lens, hq, hkv, d, page):
             first = (o, lse)
             attn_ref.check(o, lse, ref)
         assert torch.equal(o, first[0]) and torch.equal(lse, first[1])
+
+
+@pytest.mark.parametrize("io", [BF, F32])
+@pytest.mark.parametrize("at", [3, 140, 256])
+def test_one_bad_value_reaches_only_its_column(io, at):
+    """A NaN in one channel of one token's value: that channel of the rows that
+    see it, and nothing else."""
+    lens = [300, 70]
+    q, k, v = (x.contiguous() for x in packed(lens, 8, 2, 128, io, seed=at))
+    ref = attn_ref.prompt(q, k, v, lens, 128 ** -0.5)
+    v[at, 1, 5] = float("nan")
+    status = ints([0])
+    o, lse = kda.kda_attn_prompt(q, k, v, cumulative(lens), status=status)
+    torch.cuda.synchronize()
+    hit = torch.zeros_like(o, dtype=torch.bool)
+    hit[at:300, 4:, 5] = True
+    assert torch.isnan(o[hit]).all() and int(status) == kda.KDA_DEV_NONFINITE
+    attn_ref.check(torch.where(hit, ref[0].to(io), o), lse, ref)
+
+
+@pytest.mark.parametrize("io", [BF, F32])
+def test_a_call_on_a_stream_of_its_own(io):
+    """stream= given while another stream is current: the workspace made by the
+    call is not reused before that stream is done."""
+    q_lens, kv_lens = [1, 3], [4000, 2500]
+    q, kc, vc, table = cached(q_lens, kv_lens, 8, 2, 128, 64, io)
+    cu, kv = cumulative(q_lens), ints(kv_lens)
+    ref = attn_ref.paged(q, kc, vc, table, q_lens, kv_lens, 128 ** -0.5)
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    outs = []
+    for _ in range(20):
+        outs.append(kda.kda_attn_paged(q, kc, vc, table, cu, kv, max_q=3, stream=s))
+        torch.full((1 << 22,), float("nan"), device=DEV)  # takes what the allocator thinks is free
+    s.synchronize()
+    for o, lse in outs:
+        attn_ref.check(o, lse, ref)
