@@ -6,7 +6,7 @@
     python -m gated_delta_rule_57_gb300.profile_cases long    [--T 65536] [--nseg 5|decay] [--calls 4]
     python -m gated_delta_rule_57_gb300.profile_cases t4k     [--nseg 4|decay|1] [--calls 4]
     python -m gated_delta_rule_57_gb300.profile_cases prompt  [--B 2] [--calls 4]
-    python -m gated_delta_rule_57_gb300.profile_cases paged   [--B 64] [--T 4096] [--calls 4]
+    python -m gated_delta_rule_57_gb300.profile_cases paged   --T 4096 [--B 64] [--calls 4]
 
 Draws the seeded synthetic inputs on the GPU, then makes `calls` back-to-back
 calls of kda_chunk_fwd (prefill: B x 8192 tokens x 32 heads, d = 128, bf16)
