@@ -55,6 +55,7 @@ struct AttnShape {
     int tok1, tok2;  // tokens of an item: tok1 for requests that fit it, else tok2
     int kt;          // keys of a key tile
     int cost1, cost2;  // of a key of either kind of item, in any unit
+    int extra;         // keys whose cost an item adds by starting and ending
 };
 
 // One request: its packed tokens, keys, and items.
@@ -96,13 +97,13 @@ __device__ __forceinline__ int attn_item_tiles(const AttnShape& s, const AttnReq
 }
 
 // Cost. A key tile costs q.cost kt; item t of a request is counted as
-//     q.cost (max(kv - q_len, 0) + (t + 1) tok + kt - 1),
-// its keys rounded up to where its last tile must end: never less than its
-// tiles', at most about one tile more, and linear in t, so that the cost before
+//     q.cost (max(kv - q_len, 0) + (t + 1) tok + kt - 1 + extra),
+// its keys rounded up to where its last tile must end and what it costs beside
+// them: never less than its tiles', and linear in t, so that the cost before
 // an item is a product and not a sum of quotients (those, by Euclid's steps,
 // took 1200 clocks each time). Tile k of an item starts at k q.cost kt.
 __device__ __forceinline__ long long attn_cost_before(const AttnShape& s, const AttnReq& q, int t) {
-    const long long first = (long long)max(q.kv - q.q_len, 0) + s.kt - 1;
+    const long long first = (long long)max(q.kv - q.q_len, 0) + s.kt - 1 + s.extra;
     return ((long long)t * first + (long long)q.tok * t * (t + 1) / 2) * q.cost;
 }
 
@@ -277,10 +278,10 @@ cudaError_t launch_attn_simt(const AttnArgs& a);  // fp32
 
 // How a call on `nsm` SMs divides a kernel's work: CTAs and rows of a slot of its
 // split form, or ctas = 0 for whole items. max_keys: no request has more keys.
-AttnSplit attn_tc_split(int N, int total_q, int max_q, long long max_keys, int Hq, int Hkv,
-                        int nsm);
-AttnSplit attn_simt_split(int N, int total_q, int max_q, long long max_keys, int Hq, int Hkv,
-                          int nsm);
+AttnSplit attn_tc_split(int N, int total_q, int max_q, long long max_keys, bool prompt, int Hq,
+                        int Hkv, int nsm);
+AttnSplit attn_simt_split(int N, int total_q, int max_q, long long max_keys, bool prompt, int Hq,
+                          int Hkv, int nsm);
 
 // Most items there can be: every request may leave one partly filled.
 inline long long attn_items_bound(const AttnShape& s) {

@@ -73,7 +73,7 @@ size_t kda_attn_workspace_size(int N, int total_q, int max_q, int Hq, int Hkv, i
         return (size_t)-1;
     const int most = max_q < total_q ? max_q : total_q;
     const auto split = io == KDA_BF16 ? attn_tc_split : attn_simt_split;
-    return attn_split_bytes(split(N, total_q, most, INT_MAX, Hq, Hkv, device_sms()), d);
+    return attn_split_bytes(split(N, total_q, most, INT_MAX, false, Hq, Hkv, device_sms()), d);
 }
 
 kda_status_t kda_attn_prompt(const void* q, const void* k, const void* v, const int* cu_seqlens,

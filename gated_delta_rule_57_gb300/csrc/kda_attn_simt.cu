@@ -286,7 +286,7 @@ cudaError_t launch_t(const AttnArgs& a) {
     SimtParams p{};
     p.s = {a.cu_q, a.kv_len, a.N, a.total_q, a.max_q,
            (int)min((long long)a.max_pages * a.page, (1LL << 31) - 1), a.Hkv, G, kRows / G,
-           kRows / G, kKeys, 1, 1};
+           kRows / G, kKeys, 1, 1, 0};
     p.q = a.q;
     p.k = a.k;
     p.v = a.v;
@@ -306,7 +306,8 @@ cudaError_t launch_t(const AttnArgs& a) {
                                          (int)simt_smem<D>());
     if (e != cudaSuccess) return e;
     const int nsm = device_sms();
-    p.sp = attn_simt_split(a.N, a.total_q, a.max_q, a.kv_len ? p.s.kv_cap : a.max_q, a.Hq, a.Hkv, nsm);
+    p.sp = attn_simt_split(a.N, a.total_q, a.max_q, a.kv_len ? p.s.kv_cap : a.max_q, !a.kv_len, a.Hq,
+                           a.Hkv, nsm);
     if (p.sp.ctas && a.ws && a.ws_bytes >= attn_split_bytes(p.sp, D)) p.sp.ws = a.ws;
     const long long grid = p.sp.ws ? p.sp.ctas : std::min(attn_items_bound(p.s), 1LL << 20);
     e = launch_dependent(kda_attn_simt_kernel<D>, dim3((unsigned)grid), dim3(kThreadsSimt),
@@ -317,13 +318,16 @@ cudaError_t launch_t(const AttnArgs& a) {
 
 }  // namespace
 
-AttnSplit attn_simt_split(int N, int total_q, int max_q, long long max_keys, int Hq, int Hkv,
+// Ranges unless rows have a key tile or two, or there are enough items to fill the
+// SMs evenly. Measured, ranges against whole items, us (8 / 2 heads): d = 64, prompts
+// of 200 19/24, 500 32/45, 1000 50/84, 16 x 1000 499/538; d = 128, one token over
+// 256 keys 22/46, 4000 58/631.
+AttnSplit attn_simt_split(int N, int total_q, int max_q, long long max_keys, bool, int Hq, int Hkv,
                           int nsm) {
     AttnSplit sp{};
     if (N == 0 || total_q == 0 || max_q == 0 || Hkv == 0 || nsm == 0) return sp;
     const int G = Hq / Hkv, tok = kRows / G;
-    // Rows of a few key tiles, or enough items to fill the SMs evenly: whole ones.
-    if (max_keys <= KDA_ATTN_SHORT_KEYS / 4) return sp;
+    if (max_keys <= KDA_ATTN_SHORT_KEYS / 16) return sp;
     if ((long long)total_q / tok * Hkv >= 16LL * kCtasPerSm * nsm) return sp;
     sp.ctas = kCtasPerSm * nsm;
     sp.least = kKeys;

@@ -55,6 +55,8 @@ constexpr int kPieces = 4;         // pieces announced ahead
 // Relative time of a key tile for one row tile and for a pair: about 1750 and 2500
 // clocks, measured in a step of two prompts' chunks among single tokens.
 constexpr int kCostSingle = 5, kCostPair = 7;
+// An item beside its key tiles: 4700 clocks of a pair's, measured over 8192 causal tokens.
+constexpr int kItemKeys = 256;
 // Limit of a wait (about 4 s): rows computed again over a million keys pass it by far.
 constexpr long long kWaitClocks = 1LL << 33;
 constexpr float kRaise = 8.f;      // log2 growth of a row maximum that moves its reference
@@ -1061,8 +1063,9 @@ cudaError_t launch_t(const AttnArgs& a) {
     TcAttnParams p{};
     p.s = {a.cu_q, a.kv_len, a.N, a.total_q, a.max_q,
            (int)min((long long)a.max_pages * a.page, (1LL << 31) - 1), a.Hkv, G, tok1, 2 * tok1,
-           kTile, kCostSingle, kCostPair};
-    p.sp = attn_tc_split(a.N, a.total_q, a.max_q, a.kv_len ? p.s.kv_cap : a.max_q, a.Hq, a.Hkv, nsm);
+           kTile, kCostSingle, kCostPair, kItemKeys};
+    p.sp = attn_tc_split(a.N, a.total_q, a.max_q, a.kv_len ? p.s.kv_cap : a.max_q, !a.kv_len, a.Hq,
+                         a.Hkv, nsm);
     if (p.sp.ctas && a.ws && a.ws_bytes >= attn_split_bytes(p.sp, D)) p.sp.ws = a.ws;
     p.block_table = a.block_table;
     p.q = static_cast<const __nv_bfloat16*>(a.q);
@@ -1108,15 +1111,28 @@ cudaError_t launch_t(const AttnArgs& a) {
 
 }  // namespace
 
-AttnSplit attn_tc_split(int N, int total_q, int max_q, long long max_keys, int Hq, int Hkv, int nsm) {
+// Whole items or ranges. Ranges balance any lengths, but cost a second launch,
+// the parts' stores and a longer start: about 10 us over single tokens, 25 us over
+// pairs of row tiles (18 of their key tiles). Measured, ranges against whole items, us
+// (32 / 8 heads, d = 128, one H = Hkv otherwise):
+//   one token, equal lengths:  1 x 1024 17/12, 1 x 2048 18/17, 1 x 4096 21/27,
+//     16 x 2048 36/26, 64 x 2048 90/84;  lengths to 8192: 32 requests 80/99, 256 618/615
+//   prompts: 2048 54/38, 4 x 2048 152/109, 8192 339/320;  H = 2: 2048 35/28, 8192
+//     106/112;  H = 1: 4096 38/51, 8192 73/86, 16384 177/213
+//   512 new tokens over 32768: 197/323;  2 x 4096 over 16384 1515/1530
+AttnSplit attn_tc_split(int N, int total_q, int max_q, long long max_keys, bool prompt, int Hq,
+                        int Hkv, int nsm) {
     AttnSplit sp{};
     if (N == 0 || total_q == 0 || max_q == 0 || Hkv == 0 || nsm == 0) return sp;
     const int G = Hq / Hkv, tok1 = kTile / G;
-    // Rows of keys too short to be worth a second launch: whole items.
     if (max_keys <= KDA_ATTN_SHORT_KEYS) return sp;
-    // Enough items to fill the SMs evenly on their own: whole ones.
     const long long items = (long long)total_q / (2 * tok1) * Hkv;
-    if (max_q > tok1 && items >= 8LL * nsm) return sp;
+    if (max_q > tok1) {
+        // Prompts: half the longest item is the mean one. Whole unless the longest
+        // passes an even share of all of them by more than what ranges cost.
+        const long long longest = (max_keys + kTile - 1) / kTile;
+        if (prompt ? longest - longest * items / (2 * nsm) <= 18 : items >= 8LL * nsm) return sp;
+    }
     sp.ctas = nsm;
     sp.least = 2 * kCostPair * kTile;
     sp.rows = max_q <= tok1 ? (max_q * G + 3) & ~3 : 2 * kTile;  // whole 16-byte vectors

@@ -29,8 +29,8 @@ KDA_ERR_TIMEOUT = 7
 KDA_BF16 = 0
 KDA_F32 = 1
 
-# Requests of at most this many keys (a quarter of it in fp32) are never split.
-KDA_ATTN_SHORT_KEYS = 1024
+# Requests of at most this many keys (a sixteenth of it in fp32) are never split.
+KDA_ATTN_SHORT_KEYS = 2048
 
 KDA_DEV_DECAY_RANGE = 0x1
 KDA_DEV_NONFINITE = 0x2
@@ -540,7 +540,7 @@ def _attn_buffers(q, N, most, keys, Hkv, o, lse, want_lse, workspace, stream):
             lse = torch.empty((T, Hq), dtype=torch.float32, device=q.device)
     elif lse.shape != (T, Hq) or lse.dtype != torch.float32:
         raise ValueError("lse must be an fp32 tensor [T, Hq]")
-    if workspace is None and keys > KDA_ATTN_SHORT_KEYS // (4 if io == KDA_F32 else 1):
+    if workspace is None and keys > KDA_ATTN_SHORT_KEYS // (16 if io == KDA_F32 else 1):
         need = (_lib or lib()).kda_attn_workspace_size(N, T, most, Hq, Hkv, d, io)
         if need != ctypes.c_size_t(-1).value and need:  # the call itself reports bad arguments
             workspace = torch.empty(need, dtype=torch.uint8, device=q.device)

@@ -575,9 +575,9 @@ kda_status_t kda_attn_paged(const void* q, const void* k_cache, const void* v_ca
                             float scale, kda_dtype_t io, void* workspace, size_t ws_bytes,
                             int* d_status, void* stream);
 
-/* Requests of at most this many keys (max_len, or max_pages * page_size; a quarter
- * of it for KDA_F32) are never split: those calls need no workspace. */
-#define KDA_ATTN_SHORT_KEYS 1024
+/* Requests of at most this many keys (max_len, or max_pages * page_size; a
+ * sixteenth of it for KDA_F32) are never split: those calls need no workspace. */
+#define KDA_ATTN_SHORT_KEYS 2048
 
 /*
  * Bytes of device workspace that let kda_attn_prompt (total_q = total, max_q =

@@ -323,3 +323,39 @@ def test_a_call_on_a_stream_of_its_own(io):
     s.synchronize()
     for o, lse in outs:
         attn_ref.check(o, lse, ref)
+
+
+@pytest.mark.parametrize("io", [BF, F32])
+@pytest.mark.parametrize("q_lens,kv_lens,hq,hkv,d,page", [([70, 1], [1200, 1100], 8, 2, 128, 32), ([40, 260, 1], [1111, 1500, 3], 6, 1, 128, 16),
+                                                          ([1, 1, 1], [700, 588, 83], 8, 2, 64, 16), ([33] * 9, [33, 300, 129, 64, 1000, 95, 40, 511, 77], 4, 4, 64, 64)])
+def test_short_requests_in_wide_tables(io, q_lens, kv_lens, hq, hkv, d, page):
+    """Tables with room for long requests, so that the work is cut into ranges
+    whatever the lengths are; the workspace starts as NaN."""
+    q, kc, vc, table = cached(q_lens, kv_lens, hq, hkv, d, page, io, seed=page)
+    wide = torch.full((table.shape[0], 9000 // page), -1, dtype=torch.int32, device=DEV)
+    wide[:, :table.shape[1]] = table
+    ref = attn_ref.paged(q, kc, vc, table, q_lens, kv_lens, d ** -0.5)
+    need = kda.kda_attn_workspace_size(len(q_lens), sum(q_lens), max(q_lens), hq, hkv, d, io)
+    status, first = ints([0]), None
+    for _ in range(10):
+        ws = torch.full((need // 4,), float("nan"), device=DEV)
+        o, lse = kda.kda_attn_paged(q, kc, vc, wide, cumulative(q_lens), ints(kv_lens), max_q=max(q_lens),
+                                    workspace=ws, status=status)
+        torch.cuda.synchronize()
+        assert int(status) == 0
+        if first is None:
+            first = (o, lse)
+            attn_ref.check(o, lse, ref)
+        assert torch.equal(o, first[0]) and torch.equal(lse, first[1])
+
+
+@pytest.mark.parametrize("lens,hq,hkv", [([5000], 4, 1), ([3000, 2900, 17], 2, 1), ([2500, 1, 2600], 6, 2)])
+def test_prompts_cut_into_ranges(lens, hq, hkv):
+    """Few long prompts of few heads, whose items are cut."""
+    q, k, v = packed(lens, hq, hkv, 128, BF, seed=sum(lens))
+    need = kda.kda_attn_workspace_size(len(lens), sum(lens), max(lens), hq, hkv, 128)
+    ws, status = torch.full((need // 4,), float("nan"), device=DEV), ints([0])
+    o, lse = kda.kda_attn_prompt(q, k, v, cumulative(lens), max_len=max(lens), workspace=ws, status=status)
+    torch.cuda.synchronize()
+    attn_ref.check(o, lse, attn_ref.prompt(q, k, v, lens, 128 ** -0.5))
+    assert int(status) == 0
