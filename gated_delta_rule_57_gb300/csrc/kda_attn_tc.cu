@@ -251,7 +251,8 @@ __device__ float row_again(const TcAttnParams& p, const Piece& pc, size_t tok, i
         x *= p.c;
         const float mn = x > m ? x : m;
         const float a = m == -INFINITY ? 0.f : exp2f(m - mn);
-        const float w = mn == -INFINITY ? 0.f : exp2f(x - mn);
+        // a NaN score is a NaN weight, before any other key is seen too
+        const float w = x != x ? x : mn == -INFINITY ? 0.f : exp2f(x - mn);
         m = mn;
         l = l * a + w;
 #pragma unroll
