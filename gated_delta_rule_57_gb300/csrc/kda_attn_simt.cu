@@ -208,8 +208,8 @@ __global__ void __launch_bounds__(kThreadsSimt, kCtasPerSm) kda_attn_simt_kernel
                 for (int c = 0; c < C4 * 4; c++) acc[i][c] *= corr;
             }
             __syncthreads();
-            // Rows may see only part of this tile: a weight of zero then adds
-            // nothing, whatever the value beside it holds.
+            // Rows may see only part of this tile: the other keys add nothing,
+            // whatever their values hold.
             const bool edge = k0 + kKeys > seen_by_all;
             auto add = [&](bool guard) {
 #pragma unroll 2
@@ -227,7 +227,7 @@ __global__ void __launch_bounds__(kThreadsSimt, kCtasPerSm) kda_attn_simt_kernel
 #pragma unroll
                             for (int i = 0; i < 4; i++) {
                                 const float w = jj == 0 ? e[i].x : jj == 1 ? e[i].y : jj == 2 ? e[i].z : e[i].w;
-                                if (guard && w == 0.f) continue;
+                                if (guard && k0 + j + jj >= lim[i]) continue;
                                 acc[i][c * 4] = fmaf(w, b.x, acc[i][c * 4]);
                                 acc[i][c * 4 + 1] = fmaf(w, b.y, acc[i][c * 4 + 1]);
                                 acc[i][c * 4 + 2] = fmaf(w, b.z, acc[i][c * 4 + 2]);

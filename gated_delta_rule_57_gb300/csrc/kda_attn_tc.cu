@@ -910,7 +910,11 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
 #pragma unroll
             for (int w = 0; w < 2; w++) {
                 if (w == 1 && !pc.pair) break;
-                float a0, a1 = 0.f;  // weights of O_w (and of O_1)
+                // Weights of O_w (and of O_1), and whether they hold anything: what a group
+                // of no weight at all accumulated (0 x NaN) is left out, but a weight that
+                // is zero only in 32 bits keeps the NaN or Inf of a seen value.
+                float a0, a1 = 0.f;
+                bool any0, any1 = false;
                 float m, l;
                 {
                     warp_wait(ok, &sh.ml_full[w], np & 1);
@@ -918,6 +922,7 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
                     mbar_arrive(&sh.ml_free[w]);
                     m = x.x;
                     l = x.y;
+                    any0 = n[w] > 0 && l != 0.f;
                     if (n[w] > 0) warp_wait(ok, &sh.o_full[w], done[w]++ & 1);
                 }
                 if (w == 0 && !pc.pair) {
@@ -925,6 +930,7 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
                     const float2 x = sh.ml[1][row];
                     mbar_arrive(&sh.ml_free[1]);
                     if (n[1] > 0) warp_wait(ok, &sh.o_full[1], done[1]++ & 1);
+                    any1 = n[1] > 0 && x.y != 0.f;
                     const float mn = fmaxf(m, x.x);
                     a0 = m == -INFINITY ? 0.f : ex2(m - mn);
                     a1 = x.x == -INFINITY ? 0.f : ex2(x.x - mn);
@@ -949,7 +955,7 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
                         if (n[w] > 0) {
                             tmem_ld16(to + w * D + b, y);
 #pragma unroll
-                            for (int e = 0; e < 16; e++) y[e] = a0 == 0.f ? 0.f : y[e] * a0;
+                            for (int e = 0; e < 16; e++) y[e] = any0 ? y[e] * a0 : 0.f;
                         } else {
 #pragma unroll
                             for (int e = 0; e < 16; e++) y[e] = 0.f;
@@ -958,7 +964,7 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
                             float z[16];
                             tmem_ld16(to + D + b, z);
 #pragma unroll
-                            for (int e = 0; e < 16; e++) y[e] += a1 == 0.f ? 0.f : z[e] * a1;
+                            for (int e = 0; e < 16; e++) y[e] += any1 ? z[e] * a1 : 0.f;
                         }
 #pragma unroll
                         for (int e = 0; e < 16; e++) fin = fmaf(y[e], 0.f, fin);

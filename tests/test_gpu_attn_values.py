@@ -53,3 +53,39 @@ def test_nan_query_beside_a_bad_later_value(io):
     assert torch.isnan(o[310:]).all()
     rows_match(o, lse, ref, ~hit)
     assert int(status) == kda.KDA_DEV_NONFINITE
+
+
+def far_apart(n, hq, hkv, d, io, low):
+    """Keys whose scores are 128, those of `low` -128: e^-256 of the others' weight, zero in
+    32 bits but not by the definition."""
+    q = torch.full((n, hq, d), 4.0, device=DEV).to(io)
+    k = torch.full((n, hkv, d), 32.0 / d, device=DEV).to(io)
+    k[low] = -32.0 / d
+    return q, k, torch.randn(n, hkv, d, generator=torch.Generator(device=DEV).manual_seed(n), device=DEV).to(io)
+
+
+@pytest.mark.parametrize("io", [BF, F32])
+@pytest.mark.parametrize("bad", [NAN, INF])
+@pytest.mark.parametrize("n,low,at", [(60, slice(5, 6), 5), (60, slice(0, 1), 0), (250, slice(0, 128), 70), (250, slice(128, 250), 130),
+                                      (900, slice(0, 512), 500)])
+def test_a_bad_value_of_no_weight_reaches_its_rows(io, bad, n, low, at):
+    """The weight of a seen key is positive, however small: what its value holds
+    stays, in a prompt and for single tokens over a cache."""
+    hq, hkv, d, page = 4, 2, 64, 64
+    q, k, v = far_apart(n, hq, hkv, d, io, low)
+    v[at, 1, 3] = bad
+    hit = torch.zeros(n, hq, d, dtype=torch.bool, device=DEV)
+    hit[at:, 2:, 3] = True
+    status = ints([0])
+    o, _ = kda.kda_attn_prompt(q, k, v, ints([0, n]), scale=1.0, status=status)
+    torch.cuda.synchronize()
+    assert torch.equal(~torch.isfinite(o), hit) and int(status) == kda.KDA_DEV_NONFINITE
+    per = -(-n // page)
+    kc, vc = (torch.zeros(per, hkv, page, d, dtype=io, device=DEV) for _ in range(2))
+    kda.kda_kv_append(k, v, torch.arange(n, dtype=torch.int32, device=DEV), kc, vc)
+    table = torch.arange(64, dtype=torch.int32, device=DEV)[None].contiguous()  # wide: cut into ranges
+    for ws in (None, torch.empty(0, dtype=torch.uint8, device=DEV)):
+        status.zero_()
+        o, _ = kda.kda_attn_paged(q[-1:], kc, vc, table, ints([0, 1]), ints([n]), scale=1.0, workspace=ws, status=status)
+        torch.cuda.synchronize()
+        assert torch.equal(~torch.isfinite(o), hit[-1:]) and int(status) == kda.KDA_DEV_NONFINITE
