@@ -4,6 +4,10 @@ Argument marshalling only: every step of the computation runs in the CUDA
 kernels of ``libkda.so``. PyTorch provides device memory and streams. There is
 no CPU fallback: if the library is missing or a tensor is not on a CUDA
 device, the call raises.
+
+Calls run on the current stream, or on `stream`: what they then make (outputs,
+workspace) is that stream's memory, and ordering it after the work that writes the
+inputs, and the use of the outputs after it, is the caller's (wait_stream, events).
 """
 from __future__ import annotations
 
@@ -165,6 +169,20 @@ def _stream(stream):
     return stream.cuda_stream
 
 
+def _empty(shape, dtype, like, stream, scratch=False):
+    """A tensor that a call on `stream` makes (an output, or scratch that is dropped
+    when the call returns). It comes from that stream's memory, so that work which
+    still uses it elsewhere cannot meet the call, nor the call whoever gets it next; an
+    output given back while the caller's current stream uses it waits for that too."""
+    if stream is None or stream.cuda_stream == _stream(None):
+        return torch.empty(shape, dtype=dtype, device=like.device)
+    with torch.cuda.stream(stream):
+        t = torch.empty(shape, dtype=dtype, device=like.device)
+    if not scratch:
+        t.record_stream(torch.cuda.current_stream())
+    return t
+
+
 def kda_chunk_fwd_workspace_size(B: int, T: int, H: int, dk: int, dv: int,
                                  io: torch.dtype = torch.bfloat16) -> int:
     n = lib().kda_chunk_fwd_workspace_size(B, T, H, dk, dv, _DTYPE[io])
@@ -187,12 +205,12 @@ def kda_chunk_fwd(q, k, v, g, beta, h0=None, *, o=None, hT=None, want_hT: bool =
     if io is None:
         raise TypeError(f"unsupported q dtype {q.dtype}")
     if o is None:
-        o = torch.empty((B, T, H, dv), dtype=q.dtype, device=q.device)
+        o = _empty((B, T, H, dv), q.dtype, q, stream)
     if hT is None and want_hT:
-        hT = torch.empty((B, H, dk, dv), dtype=torch.float32, device=q.device)
+        hT = _empty((B, H, dk, dv), torch.float32, q, stream)
     need = kda_chunk_fwd_workspace_size(B, T, H, dk, dv, q.dtype)
     if need and workspace is None:
-        workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+        workspace = _empty(need, torch.uint8, q, stream, scratch=True)
     ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
     code = lib().kda_chunk_fwd(_ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(beta), _ptr(h0),
                                _ptr(o), _ptr(hT), B, T, H, dk, dv, io, _ptr(workspace),
@@ -218,7 +236,7 @@ def kda_chunk_fwd_decay_probe(g, nsample: int = 16, out=None, stream=None):
     planner then picks the same split."""
     B, T, H, dk = g.shape
     if out is None:
-        out = torch.empty((B, nsample, H), dtype=torch.float32, device=g.device)
+        out = _empty((B, nsample, H), torch.float32, g, stream)
     _check(lib().kda_chunk_fwd_decay_probe(_ptr(g), B, T, H, dk, nsample, _ptr(out),
                                            _stream(stream)))
     return out
@@ -285,12 +303,12 @@ def kda_chunk_fwd_segmented(q, k, v, g, beta, h0=None, *, nseg=None,
     elif nseg == "decay":
         nseg = 0
     if o is None:
-        o = torch.empty((B, T, H, dv), dtype=q.dtype, device=q.device)
+        o = _empty((B, T, H, dv), q.dtype, q, stream)
     if hT is None and want_hT:
-        hT = torch.empty((B, H, dk, dv), dtype=torch.float32, device=q.device)
+        hT = _empty((B, H, dk, dv), torch.float32, q, stream)
     need = kda_chunk_fwd_segmented_workspace_size(B, T, H, dk, dv, q.dtype, nseg)
     if need and workspace is None:
-        workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+        workspace = _empty(need, torch.uint8, q, stream, scratch=True)
     ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
     code = lib().kda_chunk_fwd_segmented(_ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(beta),
                                          _ptr(h0), _ptr(o), _ptr(hT), B, T, H, dk, dv, io, nseg,
@@ -311,9 +329,9 @@ def kda_chunk_fwd_segmented_noalloc(q, k, v, g, beta, h0=None, *, nseg: int,
     if io is None:
         raise TypeError(f"unsupported q dtype {q.dtype}")
     if o is None:
-        o = torch.empty((B, T, H, dv), dtype=q.dtype, device=q.device)
+        o = _empty((B, T, H, dv), q.dtype, q, stream)
     if hT is None and want_hT:
-        hT = torch.empty((B, H, dk, dv), dtype=torch.float32, device=q.device)
+        hT = _empty((B, H, dk, dv), torch.float32, q, stream)
     code = lib().kda_chunk_fwd_segmented_noalloc(_ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(beta),
                                                  _ptr(h0), _ptr(o), _ptr(hT), B, T, H, dk, dv, io,
                                                  nseg, 0 if lead is None else lead, _ptr(status),
@@ -331,7 +349,7 @@ def kda_chunk_fwd_slice_transition(q, k, g, beta, *, M=None,
     if io is None:
         raise TypeError(f"unsupported q dtype {q.dtype}")
     if M is None:
-        M = torch.empty((B, H, dk, dk), dtype=torch.float32, device=q.device)
+        M = _empty((B, H, dk, dk), torch.float32, q, stream)
     _check(lib().kda_chunk_fwd_slice_transition(_ptr(q), _ptr(k), _ptr(g), _ptr(beta), _ptr(M),
                                                 B, T, H, dk, io, _ptr(status), _stream(stream)))
     return M
@@ -359,9 +377,9 @@ def kda_state_scan(s0, m=None, *, x_in=None, hT=None, want_hT: bool = True, stre
     states of slices 1.., hT [B,H,dk,dv])."""
     n, B, H, dk, dv = s0.shape
     if x_in is None and n > 1:
-        x_in = torch.empty((n - 1, B, H, dk, dv), dtype=torch.float32, device=s0.device)
+        x_in = _empty((n - 1, B, H, dk, dv), torch.float32, s0, stream)
     if hT is None and want_hT:
-        hT = torch.empty((B, H, dk, dv), dtype=torch.float32, device=s0.device)
+        hT = _empty((B, H, dk, dv), torch.float32, s0, stream)
     _check(lib().kda_state_scan(_ptr(s0), _ptr(m), _ptr(x_in), _ptr(hT), n, B, H, dk, dv,
                                 _stream(stream)))
     return x_in, hT
@@ -386,12 +404,12 @@ def kda_chunk_fwd_ckpt(q, k, v, g, beta, h0=None, *, ckpt_every: int, o=None, hT
     if io is None:
         raise TypeError(f"unsupported q dtype {q.dtype}")
     if o is None:
-        o = torch.empty((B, T, H, dv), dtype=q.dtype, device=q.device)
+        o = _empty((B, T, H, dv), q.dtype, q, stream)
     if hT is None and want_hT:
-        hT = torch.empty((B, H, dk, dv), dtype=torch.float32, device=q.device)
+        hT = _empty((B, H, dk, dv), torch.float32, q, stream)
     if ckpt is None:
         n = T // ckpt_every if ckpt_every > 0 else 0
-        ckpt = torch.empty((B, H, max(n, 0), dk, dv), dtype=torch.float32, device=q.device)
+        ckpt = _empty((B, H, max(n, 0), dk, dv), torch.float32, q, stream)
     code = lib().kda_chunk_fwd_ckpt(_ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(beta), _ptr(h0),
                                     _ptr(o), _ptr(hT), _ptr(ckpt), int(ckpt_every), B, T, H, dk,
                                     dv, io, _ptr(status), _stream(stream))
@@ -409,7 +427,7 @@ def kda_decode_step(q, k, v, g, beta, S, *, o=None, status: Optional[torch.Tenso
     if io is None:
         raise TypeError(f"unsupported q dtype {q.dtype}")
     if o is None:
-        o = torch.empty((N, H, dv), dtype=q.dtype, device=q.device)
+        o = _empty((N, H, dv), q.dtype, q, stream)
     code = lib().kda_decode_step(_ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(beta), _ptr(S),
                                  _ptr(o), N, H, dk, dv, io, _ptr(status), _stream(stream))
     _check(code)
@@ -434,7 +452,7 @@ def kda_decode_multi(q, k, v, g, beta, S, *, ntok: Optional[torch.Tensor] = None
     if ntok is not None and (ntok.dtype != torch.int32 or ntok.numel() != N):
         raise ValueError("ntok must be an int32 tensor with N entries")
     if o is None and (want_o or not commit):
-        o = torch.empty((N, K, H, dv), dtype=q.dtype, device=q.device)
+        o = _empty((N, K, H, dv), q.dtype, q, stream)
     code = lib().kda_decode_multi(_ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(beta), _ptr(S),
                                   _ptr(o), _ptr(ntok), N, K, H, dk, dv, io, int(bool(commit)),
                                   _ptr(status), _stream(stream))
@@ -449,10 +467,10 @@ def _ints(name: str, t: torch.Tensor, shape):
     return _ptr(t)
 
 
-def _ints_out(name: str, t, n: int, like):
+def _ints_out(name: str, t, n: int, like, stream):
     """An int32 output of n entries, made here when not given, and its address."""
     if t is None:
-        t = torch.empty(n, dtype=torch.int32, device=like.device)
+        t = _empty(n, torch.int32, like, stream)
         return t, t.data_ptr()
     return t, _ints(name, t, (n,))
 
@@ -483,10 +501,10 @@ def kda_kv_plan(old_len, new_len, block_table, free_pages, ring, *, page_size: i
     """
     N, max_pages = block_table.shape
     pages = free_pages.numel()
-    kv_len, kv_p = _ints_out("kv_len", kv_len, N, old_len)
-    cu_new, cu_p = _ints_out("cu_new", cu_new, N + 1, old_len)
-    slot_map, slot_p = _ints_out("slot_map", slot_map, max_tokens, old_len)
-    ring_out, ring_p = _ints_out("ring_out", ring_out, 2, old_len)
+    kv_len, kv_p = _ints_out("kv_len", kv_len, N, old_len, stream)
+    cu_new, cu_p = _ints_out("cu_new", cu_new, N + 1, old_len, stream)
+    slot_map, slot_p = _ints_out("slot_map", slot_map, max_tokens, old_len, stream)
+    ring_out, ring_p = _ints_out("ring_out", ring_out, 2, old_len, stream)
     row = (N,)
     _check((_lib or lib()).kda_kv_plan(
         _ints("old_len", old_len, row), _ints("new_len", new_len, row),
@@ -532,20 +550,18 @@ def _attn_buffers(q, N, most, keys, Hkv, o, lse, want_lse, workspace, stream):
     if io is None:
         raise TypeError(f"unsupported q dtype {q.dtype}")
     if o is None:
-        o = torch.empty((T, Hq, d), dtype=q.dtype, device=q.device)
+        o = _empty((T, Hq, d), q.dtype, q, stream)
     elif o.shape != q.shape or o.dtype != q.dtype:
         raise ValueError("o must have q's shape and dtype")
     if lse is None:
         if want_lse:
-            lse = torch.empty((T, Hq), dtype=torch.float32, device=q.device)
+            lse = _empty((T, Hq), torch.float32, q, stream)
     elif lse.shape != (T, Hq) or lse.dtype != torch.float32:
         raise ValueError("lse must be an fp32 tensor [T, Hq]")
     if workspace is None and keys > KDA_ATTN_SHORT_KEYS // (16 if io == KDA_F32 else 1):
         need = (_lib or lib()).kda_attn_workspace_size(N, T, most, Hq, Hkv, d, io)
         if need != ctypes.c_size_t(-1).value and need:  # the call itself reports bad arguments
-            workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
-            if stream is not None:  # freed when this call returns: not before its stream is done
-                workspace.record_stream(stream)
+            workspace = _empty(need, torch.uint8, q, stream, scratch=True)
     ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
     return io, o, lse, workspace, ws_bytes
 
