@@ -12,7 +12,8 @@
 //   warps 0..3, 4..7  two softmax groups, one row of S per thread
 //   warp 8            issues the products
 //   warp 9            finds the work and issues the loads
-//   warp 10           zeroes V past the last key (warp 11 idles)
+//   warp 10           clears V of what some rows must not see
+//   warp 11           adds that to the finished rows which see it
 //   warps 12..15      the results: O / l, merging, stores
 // Every wait has a limit, after which the kernel reports KDA_DEV_TIMEOUT.
 // A group's loop: S (TMEM, 128 lanes x 128 columns fp32) -> registers, mask,
@@ -28,11 +29,12 @@
 // row tiles" of 128 rows, filled by TMA. K tiles are the K-major B operand of
 // the first product, V tiles the MN-major B operand of the second.
 //
-// A key past a row's last one gets P = 0 by a select on S. V past the item's
-// last key (stale cache slots, the next prompt) is zeroed in shared memory, since
-// 0 x NaN is NaN; for keys that some rows of the item see and others do not,
-// a row whose O is not finite is computed again from global memory over
-// exactly the keys it sees, so a NaN or Inf beside zero weights never reaches it.
+// A key past a row's last one gets P = 0 by a select on S. 0 x NaN is NaN, so V is
+// cleared in shared memory before the product: past the item's last key (stale cache
+// slots, the next prompt) all of it; of the keys that some rows of the item see and
+// others do not (fewer than it has tokens, at its end) the values that are not finite.
+// Those are noted, and added to the finished o of the rows that see them: p > 0 times
+// NaN or Inf is what it was.
 //
 // What bounds it: for prompts the tensor pipe (78 % active), whose gaps are the chain
 // of one group (scores, exponentials, second product) against the other group's two
@@ -58,14 +60,15 @@ constexpr int kThreadsTc = 512;
 // Registers per thread: launched with 128 (65536 in all), then by warpgroup.
 constexpr int kRegsSoftmax = 192, kRegsOther = 64, kRegsResult = 64;
 static_assert(2 * kRegsSoftmax + kRegsOther + kRegsResult <= 4 * 128, "more than launched with");
-constexpr int kMmaWarp = 8, kLoadWarp = 9, kTailWarp = 10;
+constexpr int kMmaWarp = 8, kLoadWarp = 9, kEdgeWarp = 10;  // and warp 11
 constexpr int kPieces = 4;         // pieces announced ahead
 // Relative time of a key tile for one row tile and for a pair: about 1750 and 2500
 // clocks, measured in a step of two prompts' chunks among single tokens.
 constexpr int kCostSingle = 5, kCostPair = 7;
 // An item beside its key tiles: 4700 clocks of a pair's, measured over 8192 causal tokens.
 constexpr int kItemKeys = 256;
-// Limit of a wait (about 4 s): rows computed again over a million keys pass it by far.
+// Limit of a wait (about 4 s). The longest is for the results of a piece, while its key
+// tiles go by at 1.4 us each: some 2.8 million tiles, 360 million keys.
 constexpr long long kWaitClocks = 1LL << 33;
 constexpr float kRaise = 8.f;      // log2 growth of a row maximum that moves its reference
 
@@ -130,6 +133,13 @@ __device__ __forceinline__ Share group_share(const Piece& p, int w, int tok1) {
 __device__ __forceinline__ int piece_tiles(const Piece& p) {
     return max(min(p.kt1, (p.keys + kTile - 1) / kTile) - p.kt0, 0);
 }
+// Keys that every row of the item sees: those of its first token.
+__device__ __forceinline__ int seen_by_all(const Piece& p) { return min(max(p.pos0 + 1, 0), p.keys); }
+// The first of a piece's n key tiles with keys that some row does not see; V of this
+// one and those after it is cleared.
+__device__ __forceinline__ int edge_tile(const Piece& p, int n) {
+    return min(max(seen_by_all(p) / kTile - p.kt0, 0), n);
+}
 
 __device__ __forceinline__ float ex2(float x) {
     float y;
@@ -167,7 +177,7 @@ __device__ __forceinline__ void warp_wait(bool& ok, uint64_t* bar, uint32_t pari
 
 struct Shared {
     uint64_t kv_full[8], kv_empty[8];
-    uint64_t v_clean[8];            // a V tile of the ring has zeros past the keys
+    uint64_t v_ready[8];            // a tile of the ring has been seen: V is cleared
     uint64_t q_full, q_empty;
     uint64_t s_full[2], p_full[2][2];  // of each group; P per half of the keys
     // Of each group, for each piece: its references and sums are there, are read;
@@ -176,9 +186,13 @@ struct Shared {
     // what they wait for.)
     uint64_t ml_full[2], ml_free[2], o_full[2], o_free[2];
     uint64_t piece_full[kPieces], piece_empty[kPieces];
+    uint64_t odd_full[kPieces];     // all V tiles of a piece are cleared
+    uint64_t rows_full[kPieces];    // all its rows are written
     uint64_t next_full;             // the number of the next whole item
     alignas(16) uint4 next;
     Piece pieces[kPieces];
+    // Keys of a piece with values that were cleared: bit i, key seen_by_all + i.
+    uint32_t odd[kPieces][8];
     union {
         float2 ml[2][kTile];            // reference and sum of each row
         long long groups[kAttnGroups];  // before the first piece
@@ -192,74 +206,99 @@ constexpr int tc_smem() {
 }
 static_assert(tc_smem<128>() <= 227 * 1024, "shared memory of a CTA");
 
-// Keys and values of key j of a piece; null where its page id is out of range
-// (such pages read as zeros).
-__device__ __forceinline__ void key_at(const TcAttnParams& p, const Piece& pc, int d, int j,
-                                       const __nv_bfloat16** k, const __nv_bfloat16** v) {
-    if (p.block_table) {
-        const int id = p.block_table[(size_t)pc.r * p.max_pages + j / p.page];
-        const bool there = id >= 0 && id < p.num_pages;
-        const size_t at = (((size_t)id * p.s.Hkv + pc.h) * p.page + j % p.page) * d;
-        *k = there ? p.k + at : nullptr;
-        *v = there ? p.v + at : nullptr;
-    } else {
-        *k = p.k + (size_t)(pc.key0 + j) * p.k_stride + (size_t)pc.h * d;
-        *v = p.v + (size_t)(pc.key0 + j) * p.v_stride + (size_t)pc.h * d;
-    }
+// Values of key j of a piece; null where its page id is out of range (such pages
+// read as zeros).
+__device__ __forceinline__ const __nv_bfloat16* values_at(const TcAttnParams& p, const Piece& pc,
+                                                          int d, int j) {
+    if (!p.block_table)
+        return p.v + (size_t)(pc.key0 + j) * p.v_stride + (size_t)pc.h * d;
+    const int id = p.block_table[(size_t)pc.r * p.max_pages + j / p.page];
+    if (id < 0 || id >= p.num_pages) return nullptr;
+    return p.v + (((size_t)id * p.s.Hkv + pc.h) * p.page + j % p.page) * d;
 }
 
-// Whether a value of keys [j0, j1) is not finite, a warp together.
-template <int D>
-__device__ bool odd_values(const TcAttnParams& p, const Piece& pc, int j0, int j1) {
-    bool odd = false;
-    for (int j = j0; j < j1; j++) {
-        const __nv_bfloat16 *gk, *gv;
-        key_at(p, pc, D, j, &gk, &gv);
-        if (gv) {
-#pragma unroll
-            for (int e = 0; e < D; e += 32)
-                odd |= finite_flag(__bfloat162float(gv[(threadIdx.x & 31) + e])) != 0;
-        }
-    }
-    return __any_sync(0xffffffffu, odd);
+// Sign bits set where a bf16 of a pair has all exponent bits: NaN or Inf.
+__device__ __forceinline__ uint32_t odd_pair(uint32_t x) {
+    return ((x & 0x7f807f80u) + 0x00800080u) & 0x80008000u;
+}
+__device__ __forceinline__ uint32_t odd_vector(uint4 x) {
+    return odd_pair(x.x) | odd_pair(x.y) | odd_pair(x.z) | odd_pair(x.w);
+}
+__device__ __forceinline__ uint32_t finite_pair(uint32_t x) {  // zeros for the others
+    const uint32_t odd = odd_pair(x);
+    return x & ~((odd >> 15 & 0x00010001u) * 0xffffu);
 }
 
-// One row again, a warp together, over exactly the keys [j0, j1) that it sees;
-// lane l holds columns l + 32 e of acc. Returns the sum of exponentials.
+// Clears a V tile, a warp together: rows from r1 on, and what is not finite in rows
+// [r0, r1). odd: a bit for each such row, row r0 being bit `bit0`.
 template <int D>
-__device__ float row_again(const TcAttnParams& p, const Piece& pc, size_t tok, int head, int j0,
-                           int j1, float* acc) {
+__device__ __forceinline__ void clear_values(unsigned char* v, int r0, int r1, uint32_t* odd,
+                                             int bit0) {
     const int lane = threadIdx.x & 31;
-    constexpr int E = D / 32;
-    float q[E];
-    const __nv_bfloat16* gq = p.q + tok * p.q_stride + (size_t)head * D;
+    uint32_t any = 0;
 #pragma unroll
-    for (int e = 0; e < E; e++) q[e] = __bfloat162float(gq[lane + 32 * e]);
-    float m = -INFINITY, l = 0.f;
-#pragma unroll
-    for (int e = 0; e < E; e++) acc[e] = 0.f;
-    for (int j = j0; j < j1; j++) {
-        const __nv_bfloat16 *gk, *gv;
-        key_at(p, pc, D, j, &gk, &gv);
-        float x = 0.f;
-        if (gk) {
-#pragma unroll
-            for (int e = 0; e < E; e++) x = fmaf(q[e], __bfloat162float(gk[lane + 32 * e]), x);
-        }
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
-        x *= p.c;
-        const float mn = x > m ? x : m;
-        const float a = m == -INFINITY ? 0.f : exp2f(m - mn);
-        // a NaN score is a NaN weight, before any other key is seen too
-        const float w = x != x ? x : mn == -INFINITY ? 0.f : exp2f(x - mn);
-        m = mn;
-        l = l * a + w;
-#pragma unroll
-        for (int e = 0; e < E; e++)
-            acc[e] = acc[e] * a + (gv ? w * __bfloat162float(gv[lane + 32 * e]) : 0.f);
+    for (int half = 0; half < D / 64; half++) {
+        const unsigned char* t = v + half * (kTile * 128);
+#pragma unroll 1  // (four at a time took issue slots from the softmax: ragged prompts 0.3 %)
+        for (int b = r0 * 128 + lane * 16; b < r1 * 128; b += 512)
+            any |= odd_vector(*reinterpret_cast<const uint4*>(t + b));
     }
-    return l;
+    if (__any_sync(0xffffffffu, any)) {
+        for (int half = 0; half < D / 64; half++)
+            for (int b = r0 * 128 + lane * 16; b < r1 * 128; b += 512) {
+                uint4& x = *reinterpret_cast<uint4*>(v + half * (kTile * 128) + b);
+                if (!odd_vector(x)) continue;
+                x = make_uint4(finite_pair(x.x), finite_pair(x.y), finite_pair(x.z), finite_pair(x.w));
+                const int bit = bit0 + b / 128 - r0;
+                atomicOr(odd + (bit >> 5), 1u << (bit & 31));
+            }
+    }
+#pragma unroll
+    for (int half = 0; half < D / 64; half++)
+        for (int b = r1 * 128 + lane * 16; b < kTile * 128; b += 512)
+            *reinterpret_cast<uint4*>(v + half * (kTile * 128) + b) = make_uint4(0, 0, 0, 0);
+}
+
+// Adds the cleared values to the rows that see them, by a warp once the rows are
+// written. odd: lane i holds word i of the piece's bits (zero from lane 8 on). Rows see
+// more keys from one to the next, so each value is read once for a row tile.
+template <int D>
+__device__ __forceinline__ int add_cleared(const TcAttnParams& p, const Piece& pc, uint32_t odd,
+                                           float* part) {
+    const int lane = threadIdx.x & 31, all = seen_by_all(pc), G = p.s.G, tok1 = p.s.tok1;
+    constexpr int E = D / 32;
+    int flags = 0;
+    for (int w = 0; w <= pc.pair; w++) {
+        float sum[E];  // of columns lane + 32 e: zero, or not finite
+#pragma unroll
+        for (int e = 0; e < E; e++) sum[e] = 0.f;
+        int i = 0;  // cleared keys below all + i are in the sums
+        for (int r = 0; r < tok1 * G; r++) {
+            const int tok = w * tok1 + r / G;
+            if (tok >= pc.ntok) break;
+            const int sees = min(pc.pos0 + tok + 1 - all, 256);
+            for (; i < sees; i++) {
+                if (!(__shfl_sync(0xffffffffu, odd, i >> 5) >> (i & 31) & 1)) continue;
+                const __nv_bfloat16* v = values_at(p, pc, D, all + i);
+                if (!v) continue;
+#pragma unroll
+                for (int e = 0; e < E; e++) {
+                    const float x = __bfloat162float(v[lane + 32 * e]);
+                    if (finite_flag(x)) sum[e] += x;
+                }
+            }
+            const size_t at = ((size_t)pc.tok0 + tok) * p.s.Hkv * G + (size_t)pc.h * G + r % G;
+#pragma unroll
+            for (int e = 0; e < E; e++) {
+                if (!finite_flag(sum[e])) continue;
+                flags = KDA_DEV_NONFINITE;
+                const int c = lane + 32 * e;
+                if (part) part[(size_t)(w * kTile + r) * D + c] += sum[e];
+                else p.o[at * D + c] = __float2bfloat16_rn(__bfloat162float(p.o[at * D + c]) + sum[e]);
+            }
+        }
+    }
+    return flags;
 }
 
 template <int D>
@@ -286,7 +325,7 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
         for (int i = 0; i < NS; i++) {
             mbar_init(&sh.kv_full[i], 1);
             mbar_init(&sh.kv_empty[i], 2);  // read by the products, seen by the V warp
-            mbar_init(&sh.v_clean[i], 1);
+            mbar_init(&sh.v_ready[i], 1);
         }
         mbar_init(&sh.next_full, 1);
         mbar_init(&sh.q_full, 1);
@@ -302,7 +341,9 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
         }
         for (int i = 0; i < kPieces; i++) {
             mbar_init(&sh.piece_full[i], 1);
-            mbar_init(&sh.piece_empty[i], 14);  // softmax 8, products, V, results 4
+            mbar_init(&sh.piece_empty[i], 15);  // softmax 8, products, V 2, results 4
+            mbar_init(&sh.odd_full[i], 1);
+            mbar_init(&sh.rows_full[i], 4);
         }
         fence_mbarrier_init();
         prefetch_tensormap(&map_q);
@@ -530,7 +571,6 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
             // registers, and one elected lane issues.
             int stage = 0, kv_phase = 0, q_phase = 0, np = 0;
             int tiles0 = 0, tiles1 = 0;  // parities of the groups' tiles so far
-            uint32_t cleaned = 0;        // parity of v_clean, a bit per tile of the ring
             constexpr uint32_t idesc_s = idesc_bf16(kTile, kTile, 0, 0);
             constexpr uint32_t idesc_o = idesc_bf16(kTile, D, 0, 1);
             const uint64_t dq = desc_kmajor(smem_addr(sq));
@@ -576,7 +616,7 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
                 __syncwarp();
             };
             struct Next {  // the piece after this one
-                int end, n, pair, n0, n1, tail;
+                int end, n, pair, n0, n1;
             };
             auto take = [&](Next& x) {  // from the queue
                 const int i = np % kPieces;
@@ -587,7 +627,6 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
                 x.pair = uniform(pc.pair);
                 x.n0 = uniform(group_share(pc, 0, tok1).n);
                 x.n1 = uniform(group_share(pc, 1, tok1).n);
-                x.tail = uniform(pc.keys < (pc.kt0 + x.n) * kTile);
                 if (lane == 0) mbar_arrive(&sh.piece_empty[i]);
                 np++;
                 return true;
@@ -618,7 +657,7 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
                     // Two row tiles on every key tile. The last tile's step starts the
                     // next piece's first scores, if that is a pair too, as any other
                     // step starts the next tile's.
-                    const int n0 = x.n0, n1 = x.n1, tail = x.tail;
+                    const int n0 = x.n0, n1 = x.n1;
                     if (!primed) {
                         if (!wait(&sh.q_full, q_phase)) break;
                         q_phase ^= 1;
@@ -633,14 +672,10 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
                     primed = false;
                     for (int j = 0; j < n; j++) {
                         const int vs = stage;
-                        if (!wait(&sh.kv_full[vs], kv_phase)) break;
+                        if (!wait(&sh.v_ready[vs], kv_phase)) break;
                         next();
                         bool s0 = j + 1 < n0, s1 = j + 1 < n1;  // scores to start
                         if (j + 1 == n) {
-                            if (tail) {
-                                if (!wait(&sh.v_clean[vs], cleaned >> vs & 1)) break;
-                                cleaned ^= 1u << vs;
-                            }
                             if (!take(x)) break;
                             primed = !x.end && x.pair && x.n > 0;
                             s0 = primed && x.n0 > 0;
@@ -690,7 +725,6 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
                     }
                 } else {
                     // One row tile, key tiles in turn to the two groups.
-                    const int tail = x.tail;
                     if (!wait(&sh.q_full, q_phase)) break;
                     q_phase ^= 1;
                     for (int j = 0; j < 2 && j < n; j++) {
@@ -704,14 +738,10 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
                     if (!ok || !o_free(0) || (n > 1 && !o_free(1))) break;
                     for (int j = 0; j < n && ok; j++) {
                         const int vs = stage, w = j & 1;
-                        if (!wait(&sh.kv_full[vs], kv_phase)) break;
+                        if (!wait(&sh.v_ready[vs], kv_phase)) break;
                         next();
                         const bool more = j + 2 < n;
                         const int ks = stage;
-                        if (j + 1 == n && tail) {
-                            if (!wait(&sh.v_clean[vs], cleaned >> vs & 1)) break;
-                            cleaned ^= 1u << vs;
-                        }
                         if (!half_by_half(w, w ? tiles1 : tiles0, vs, j > 1)) break;
                         tiles0 ^= w ^ 1;
                         tiles1 ^= w;
@@ -736,10 +766,12 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
                 commit(&sh.q_empty);
                 __nanosleep(1000000);
             }
-        } else if (warp == kTailWarp) {
-            // ------------------------------------------------------------ V past the keys
+        } else if (warp == kEdgeWarp) {
+            // ------------------------------------------------------------ V at the edge
             // It sees every tile of the ring go by (so that no phase of a barrier
-            // passes unseen), and the last one of a piece is its last V tile.
+            // passes unseen) and clears the V tiles of a piece from its edge on. The
+            // products wait for V through this warp: one wait for every tile, where a
+            // second one for those at the edge cost long prompts 0.5 %.
             int stage = 0, kv_phase = 0, np = 0;
             while (ok) {
                 const int i = np % kPieces;
@@ -750,29 +782,59 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
                 if (lane == 0) mbar_arrive(&sh.piece_empty[i]);
                 np++;
                 if (pc.end) break;
-                const int n = piece_tiles(pc);
-                const int dead = pc.keys - (pc.kt0 + n - 1) * kTile;  // first row past the keys
-                for (int j = 0; j < 2 * n; j++) {
+                if (lane < 8) sh.odd[i][lane] = 0;  // (those of the piece before are done with)
+                __syncwarp();
+                const int n = piece_tiles(pc), edge = edge_tile(pc, n), all = seen_by_all(pc);
+                int j = 0;                             // the next V tile
+                int v_at = pc.pair || n == 1 ? 1 : 2;  // and its place: one or two K tiles lead
+                for (int at = 0; at < 2 * n; at++) {
                     warp_wait(ok, &sh.kv_full[stage], kv_phase);
                     if (!ok) break;
-                    if (j == 2 * n - 1 && dead < kTile) {
-                        unsigned char* v = skv + stage * C::TILE_BYTES;
-#pragma unroll
-                        for (int half = 0; half < HALVES; half++)
-                            for (int b = dead * 128 + lane * 16; b < kTile * 128; b += 512)
-                                *reinterpret_cast<uint4*>(v + half * (kTile * 128) + b) =
-                                    make_uint4(0, 0, 0, 0);
-                        fence_proxy_async_smem();
-                        __syncwarp();
-                        if (lane == 0) mbar_arrive(&sh.v_clean[stage]);
+                    if (at == v_at) {
+                        if (j >= edge) {
+                            const int base = (pc.kt0 + j) * kTile;
+                            const int r0 = max(all - base, 0), r1 = min(pc.keys - base, kTile);
+                            clear_values<D>(skv + stage * C::TILE_BYTES, r0, r1, sh.odd[i],
+                                            base + r0 - all);
+                            fence_proxy_async_smem();
+                        }
+                        j++;
+                        v_at = min(v_at + 2, 2 * n - 1);
                     }
                     __syncwarp();
-                    if (lane == 0) mbar_arrive(&sh.kv_empty[stage]);
+                    if (lane == 0) {
+                        mbar_arrive(&sh.v_ready[stage]);
+                        mbar_arrive(&sh.kv_empty[stage]);
+                    }
                     if (++stage == NS) {
                         stage = 0;
                         kv_phase ^= 1;
                     }
                 }
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&sh.odd_full[i]);
+            }
+            if (!ok) flags |= KDA_DEV_TIMEOUT;
+        } else {
+            // ------------------------------------------------------------ cleared values
+            // In a warp of its own: beside the results' code it cost ragged prompts 3 %
+            // without ever running.
+            for (int np = 0; ok; np++) {
+                const int i = np % kPieces;
+                warp_wait(ok, &sh.piece_full[i], (np / kPieces) & 1);
+                if (!ok) break;
+                const Piece& pc = sh.pieces[i];  // (stays until this warp is done with it)
+                if (pc.end) break;
+                warp_wait(ok, &sh.odd_full[i], (np / kPieces) & 1);
+                warp_wait(ok, &sh.rows_full[i], (np / kPieces) & 1);
+                if (!ok) break;
+                const uint32_t odd = lane < 8 ? sh.odd[i][lane] : 0;
+                if (__any_sync(0xffffffffu, odd != 0))
+                    flags |= add_cleared<D>(
+                        p, pc, odd,
+                        pc.slot >= 0 ? p.sp.ws + attn_slot_floats(p.sp.rows, D) * pc.slot : nullptr);
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&sh.piece_empty[i]);
             }
             if (!ok) flags |= KDA_DEV_TIMEOUT;
         }
@@ -997,37 +1059,11 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
                     else if (p.lse)
                         p.lse[at] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.69314718056f;
                 }
-                // Rows that are not finite: where a value that they do not see is at
-                // fault (0 x NaN), again over the keys they see.
-                unsigned bad = __ballot_sync(0xffffffffu, live && !(fin == 0.f));
-                __syncwarp();  // their first results are written
-                while (bad) {
-                    const int src = __ffs(bad) - 1;
-                    bad &= bad - 1;
-                    const int stok = __shfl_sync(0xffffffffu, tok, src);
-                    const int shead = __shfl_sync(0xffffffffu, rhead, src);
-                    const int ssrow = __shfl_sync(0xffffffffu, srow, src);
-                    const int j0 = pc.kt0 * kTile, end = min(pc.kt1 * kTile, pc.keys);
-                    const int j1 = min(end, max(pc.pos0 + stok + 1, 0));
-                    if (!odd_values<D>(p, pc, max(j0, j1), end)) {
-                        flags |= KDA_DEV_NONFINITE;
-                        continue;
-                    }
-                    const size_t tk = (size_t)pc.tok0 + stok;
-                    const int head = pc.h * G + shead;
-                    float y[D / 32];
-                    const float sum = row_again<D>(p, pc, tk, head, j0, j1, y);
-#pragma unroll
-                    for (int e = 0; e < D / 32; e++) {
-                        const float x = y[e] * (sum == 0.f ? 0.f : 1.f / sum);
-                        flags |= finite_flag(x);
-                        const int c = lane + 32 * e;
-                        if (part) part[(size_t)ssrow * D + c] = x;
-                        else p.o[(tk * p.s.Hkv * G + head) * D + c] = __float2bfloat16_rn(x);
-                    }
-                }
+                if (live && !(fin == 0.f)) flags |= KDA_DEV_NONFINITE;
             }
             if (!ok) break;
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&sh.rows_full[i]);
         }
         if (!ok) flags |= KDA_DEV_TIMEOUT;
     }
