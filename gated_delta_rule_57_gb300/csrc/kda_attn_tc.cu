@@ -481,6 +481,9 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
             const long long end = cur + each;
             long long start = cur;
             bool have = false;  // (q, h, t, tile) is where `cur` is
+            // One CTA reports on the lengths of all requests: the one that has item 0.
+            // CTA 0 is not always that, as one that has not started may be taken over.
+            bool reports = blockIdx.x == 0;
             AttnWalk walk;
             if (split) {
                 walk = attn_walk_at(p.s, sh.groups, cur);
@@ -544,12 +547,13 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
                     const int x = ok ? __shfl_sync(0xffffffffu, clc_answer(&sh.next), 0) : -1;
                     if (x < 0) break;
                     cur = x;
+                    reports |= x == 0;
                     // the answer is read before the next one is written
                     fence_proxy_async_smem();
                     __syncwarp();
                 }
             }
-            if (blockIdx.x == 0) {  // lengths of requests this CTA had no work of
+            if (reports) {  // lengths of requests this CTA had no work of too
                 for (int i = lane; i < p.s.N; i += 32) walk.bad |= attn_request(p.s, i).bad != 0;
                 if (walk.bad) flags |= KDA_DEV_LENGTH;
             }
