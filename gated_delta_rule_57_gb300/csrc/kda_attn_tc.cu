@@ -1148,14 +1148,9 @@ cudaError_t launch_t(const AttnArgs& a) {
              make_rows(&mv, a.v, D, a.Hkv, a.total_q, a.v_stride, 1, kTile);
     if (!ok) return cudaErrorInvalidValue;
     auto kernel = kda_attn_tc_kernel<D>;
-    static std::atomic<uint64_t> ready{0};  // devices that know the kernel's shared memory
-    const uint64_t bit = dev < 64 ? 1ull << dev : 0;
-    cudaError_t e = cudaSuccess;
-    if (!(ready.load(std::memory_order_relaxed) & bit)) {
-        e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, tc_smem<D>());
-        if (e != cudaSuccess) return e;
-        ready.fetch_or(bit, std::memory_order_relaxed);
-    }
+    static std::atomic<uint64_t> ready{0};
+    cudaError_t e = allow_shared(kernel, tc_smem<D>(), ready, dev);
+    if (e != cudaSuccess) return e;
     const long long grid = p.sp.ws ? p.sp.ctas : attn_items_bound(p.s);
     if (grid >= 1LL << 31) return cudaErrorInvalidValue;
     e = launch_dependent(kernel, dim3((unsigned)grid), dim3(kThreadsTc), tc_smem<D>(), a.stream,

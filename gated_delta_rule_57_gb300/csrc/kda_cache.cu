@@ -2,6 +2,7 @@
 // (block tables, slot map and free list from request lengths) and the write of
 // new keys and values to their slots. Kernels and entry points.
 #include <algorithm>
+#include <atomic>
 
 #include "kda_host.cuh"
 #include "kda_internal.cuh"
@@ -342,14 +343,16 @@ kda_status_t kda_kv_plan(const int* old_len, const int* new_len, int* block_tabl
     auto kernel = N <= kPlanThreads        ? kda_kv_plan_kernel<1>
                   : N <= 4 * kPlanThreads ? kda_kv_plan_kernel<4>
                                           : kda_kv_plan_kernel<kPlanMaxN / kPlanThreads>;
-    if (smem > 48 * 1024) {
-        cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    int dev = -1;
+    const long long most = std::max(device_sms(&dev), 1);
+    if (smem > 48 * 1024) {  // the last of the kernels
+        static std::atomic<uint64_t> ready{0};
+        const cudaError_t e = allow_shared(kernel, 3 * ((size_t)kPlanMaxN + 1) * 4, ready, dev);
         if (e != cudaSuccess) return launched(e);
     }
     // A CTA for 2048 tokens' slots: 253 k tokens took 13.0 us so, as with 512 or
     // 1024, and 18.5 us with 4096; fewer tokens leave the scans, alike for any grid.
     long long grid = ((long long)max_tokens + 4 * kPlanThreads - 1) / (4 * kPlanThreads);
-    const long long most = std::max(device_sms(), 1);
     grid = grid < 1 ? 1 : (grid > most ? most : grid);
     return launched(launch_dependent(kernel, dim3((unsigned)grid), dim3(kPlanThreads),
                                      smem, static_cast<cudaStream_t>(stream), p));

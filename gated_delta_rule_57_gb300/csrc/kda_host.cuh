@@ -83,4 +83,17 @@ inline int device_sms(int* device = nullptr) {
     return n;
 }
 
+// Lets a kernel be launched with up to `bytes` of dynamic shared memory on the current
+// device, once per device. One limit for all calls of a kernel: a limit of the call's
+// own size could be lowered by another thread before the launch.
+template <typename Kernel>
+inline cudaError_t allow_shared(Kernel kernel, size_t bytes, std::atomic<uint64_t>& ready, int dev) {
+    const uint64_t bit = dev >= 0 && dev < 64 ? 1ull << dev : 0;
+    if (ready.load(std::memory_order_relaxed) & bit) return cudaSuccess;
+    const cudaError_t e =
+        cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+    if (e == cudaSuccess) ready.fetch_or(bit, std::memory_order_relaxed);
+    return e;
+}
+
 }  // namespace kda
