@@ -50,7 +50,7 @@ struct AttnArgs {
 struct AttnShape {
     const int* cu_q;
     const int* kv_len;
-    int N, total_q, max_q, kv_cap;  // kv_cap: tokens a block-table row can hold
+    int N, total_q, max_q, kv_cap;  // kv_cap: keys of a request, at most
     int Hkv, G;
     int tok1, tok2;  // tokens of an item: tok1 for requests that fit it, else tok2
     int kt;          // keys of a key tile
@@ -282,6 +282,13 @@ AttnSplit attn_tc_split(int N, int total_q, int max_q, long long max_keys, bool 
                         int Hkv, int nsm);
 AttnSplit attn_simt_split(int N, int total_q, int max_q, long long max_keys, bool prompt, int Hq,
                           int Hkv, int nsm);
+
+// Keys a request can have: what a row of the block table holds, up to 2^30, so that
+// key numbers a few tiles past the end stay inside 32 bits.
+inline int attn_kv_cap(const AttnArgs& a) {
+    const long long row = (long long)a.max_pages * a.page;
+    return (int)(row < (1LL << 30) ? row : 1LL << 30);
+}
 
 // Most items there can be: every request may leave one partly filled.
 inline long long attn_items_bound(const AttnShape& s) {

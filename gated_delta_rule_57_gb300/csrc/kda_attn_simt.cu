@@ -287,7 +287,7 @@ cudaError_t launch_t(const AttnArgs& a) {
     const int G = a.Hq / a.Hkv;
     SimtParams p{};
     p.s = {a.cu_q, a.kv_len, a.N, a.total_q, a.max_q,
-           (int)min((long long)a.max_pages * a.page, (1LL << 31) - 1), a.Hkv, G, kRows / G,
+           attn_kv_cap(a), a.Hkv, G, kRows / G,
            kRows / G, kKeys, 1, 1, 0};
     p.q = a.q;
     p.k = a.k;

@@ -1117,7 +1117,7 @@ cudaError_t launch_t(const AttnArgs& a) {
     if (nsm == 0) return cudaErrorNoDevice;
     TcAttnParams p{};
     p.s = {a.cu_q, a.kv_len, a.N, a.total_q, a.max_q,
-           (int)min((long long)a.max_pages * a.page, (1LL << 31) - 1), a.Hkv, G, tok1, 2 * tok1,
+           attn_kv_cap(a), a.Hkv, G, tok1, 2 * tok1,
            kTile, kCostSingle, kCostPair, kItemKeys};
     p.sp = attn_tc_split(a.N, a.total_q, a.max_q, a.kv_len ? p.s.kv_cap : a.max_q, !a.kv_len, a.Hq,
                          a.Hkv, nsm);

@@ -564,8 +564,8 @@ kda_status_t kda_attn_prompt(const void* q, const void* k, const void* v, const 
  *                 written)
  *   page_size   : a power of two in 16 .. 1024 (KDA_ERR_UNSUPPORTED otherwise)
  *
- * A kv_len below 0 or past max_pages * page_size is clamped (KDA_DEV_LENGTH); a
- * page id out of range reads as zeros (KDA_DEV_PAGES). The rest as for
+ * A kv_len below 0, past max_pages * page_size or past 2^30 is clamped
+ * (KDA_DEV_LENGTH); a page id out of range reads as zeros (KDA_DEV_PAGES). The rest as for
  * kda_attn_prompt.
  */
 kda_status_t kda_attn_paged(const void* q, const void* k_cache, const void* v_cache,

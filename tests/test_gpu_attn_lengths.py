@@ -99,3 +99,19 @@ def test_more_new_tokens_than_announced(io):
         assert (o[3:12] == 7).all() and (lse[3:12] == 7).all()
         for s in (slice(0, 3), slice(12, 13)):
             attn_ref.check(o[s], lse[s], tuple(x[s] for x in ref))
+
+
+@pytest.mark.parametrize("io", [BF, F32])
+def test_lengths_near_2_to_31(io):
+    """A table of 2^31 slots and a length at its end: clamped to 2^30 and reported, and
+    key numbers past the end stay positive. No page of it exists, so every score and
+    value is 0."""
+    kc, vc = (torch.ones(1, 1, 1024, 64, dtype=io, device=DEV) for _ in range(2))
+    table = torch.full((1, 1 << 21), -1, dtype=torch.int32, device=DEV)
+    q = torch.ones(1, 1, 64, device=DEV).to(io)
+    for kv in ((1 << 31) - 1, (1 << 31) - 128, (1 << 31) - 200):
+        status = ints([0])
+        o, lse = kda.kda_attn_paged(q, kc, vc, table, ints([0, 1]), ints([kv]), max_q=1, status=status)
+        torch.cuda.synchronize()
+        assert int(status) == kda.KDA_DEV_LENGTH | kda.KDA_DEV_PAGES
+        assert not o.any() and abs(float(lse) - 30 * 0.6931471805599453) <= 1e-4
