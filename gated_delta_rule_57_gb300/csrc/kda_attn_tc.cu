@@ -189,6 +189,7 @@ struct Shared {
     uint64_t odd_full[kPieces];     // all V tiles of a piece are cleared
     uint64_t rows_full[kPieces];    // all its rows are written
     uint64_t next_full;             // the number of the next whole item
+    uint64_t drained;               // all products have ended
     alignas(16) uint4 next;
     Piece pieces[kPieces];
     // Keys of a piece with values that were cleared: bit i, key seen_by_all + i.
@@ -328,6 +329,7 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
             mbar_init(&sh.v_ready[i], 1);
         }
         mbar_init(&sh.next_full, 1);
+        mbar_init(&sh.drained, 1);
         mbar_init(&sh.q_full, 1);
         mbar_init(&sh.q_empty, 1);
         for (int w = 0; w < 2; w++) {
@@ -764,12 +766,11 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
                     if (!ok || !take(x)) break;
                 }
             }
-            if (!ok) {
-                flags |= KDA_DEV_TIMEOUT;
-                // products in flight end before the tensor memory is freed
-                commit(&sh.q_empty);
-                __nanosleep(1000000);
-            }
+            // Products in flight, which write the tensor memory that is freed below and
+            // arrive on this CTA's barriers, end before it leaves.
+            commit(&sh.drained);
+            if (!__all_sync(0xffffffffu, mbar_wait(&sh.drained, 0, 1LL << 24))) ok = false;
+            if (!ok) flags |= KDA_DEV_TIMEOUT;
         } else if (warp == kEdgeWarp) {
             // ------------------------------------------------------------ V at the edge
             // It sees every tile of the ring go by (so that no phase of a barrier
