@@ -58,10 +58,10 @@
 // writes o (and hT) once. The <true> instantiation also runs the passes of
 // the time-segmented evaluation and of a sequence split across devices (see
 // TcParams).
-#include <cudaTypedefs.h>
 
 #include "kda_internal.cuh"
 #include "sm100_ptx.cuh"
+#include "tensor_map.cuh"
 
 namespace kda {
 namespace {
@@ -206,17 +206,6 @@ __device__ __forceinline__ void tmem_ld16x2(uint32_t ta, uint32_t tb, float* va,
     }
 }
 
-// D[tmem] (+)= A[tmem] * B[smem]: A is M lanes x K, two bf16 per 32-bit column
-// (k = 2c in the low half of column c), so a K = 16 step advances 8 columns.
-__device__ __forceinline__ void mma_bf16_ta(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc,
-                                            uint32_t idesc, uint32_t accumulate) {
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "setp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
-        "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
-        : "memory");
-}
 __device__ __forceinline__ void tmem_st8(uint32_t taddr, const float* v) {
     asm volatile(
         "tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(taddr),
@@ -283,20 +272,6 @@ __device__ __forceinline__ void st_row8(unsigned char* tile, int r, int c0, int 
                                         const float* x) {
     *reinterpret_cast<uint4*>(tile + sw128_offset(r, c0, R)) = pack8(x);
 }
-
-// Descriptors for the two operand orientations of an SW128 tile with R rows;
-// k-step kk covers 16 elements of K. The start address is the low 14-bit
-// field (in 16-byte units), so advancing an operand is a plain add.
-__device__ __forceinline__ uint64_t desc_kmajor(uint32_t base) {
-    return sdesc_sw128(base, 16, 1024);
-}
-__device__ __forceinline__ uint64_t kstep_kmajor(int R, int kk) {
-    return (uint64_t)(((uint32_t)(kk >> 2) * (uint32_t)R * 128u + (uint32_t)(kk & 3) * 32u) >> 4);
-}
-__device__ __forceinline__ uint64_t desc_mnmajor(uint32_t base, int R) {
-    return sdesc_sw128(base, (uint32_t)R * 128u, 1024);
-}
-__device__ __forceinline__ uint64_t kstep_mnmajor(int kk) { return (uint64_t)(kk * 128); }
 
 // Warp-level TF32 MMA (m16n8k8, fp32 accumulate) for the 16-row blocks of
 // the triangular inverse: tcgen05 needs M >= 64, these products are 16 x 16.
@@ -1293,25 +1268,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (warp == 0) tmem_dealloc(tbase, TM_COLS);
 }
 
-PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
-    static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
-    if (!fn) {
-        void* f = nullptr;
-        cudaDriverEntryPointQueryResult qr;
-        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault,
-                                             &qr) == cudaSuccess &&
-            qr == cudaDriverEntryPointSuccess)
-            fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(f);
-    }
-    return fn;
-}
-
 // 4-D map over [B, T, H, d] (innermost first: d, H, T, B), boxes of
 // box_inner x 1 x 64 x 1 with the 128-byte swizzle. Rows past T read as zero.
 bool make_map(CUtensorMap* m, const void* ptr, CUtensorMapDataType dt, int esz, int B, int T,
               int H, int d, int box_inner,
               CUtensorMapSwizzle swz = CU_TENSOR_MAP_SWIZZLE_128B) {
-    auto enc = encode_fn();
+    auto enc = tensor_map_encoder();
     if (!enc) return false;
     cuuint64_t dims[4] = {(cuuint64_t)d, (cuuint64_t)H, (cuuint64_t)T, (cuuint64_t)B};
     cuuint64_t strides[3] = {(cuuint64_t)d * esz, (cuuint64_t)H * d * esz,
