@@ -345,7 +345,8 @@ kda_status_t kda_kv_plan(const int* old_len, const int* new_len, int* block_tabl
                                           : kda_kv_plan_kernel<kPlanMaxN / kPlanThreads>;
     int dev = -1;
     const long long most = std::max(device_sms(&dev), 1);
-    if (smem > 48 * 1024) {  // the last of the kernels
+    // Past 48 KB, of which the static part takes some (only the last kernel gets there).
+    if (smem > 47 * 1024) {
         static std::atomic<uint64_t> ready{0};
         const cudaError_t e = allow_shared(kernel, 3 * ((size_t)kPlanMaxN + 1) * 4, ready, dev);
         if (e != cudaSuccess) return launched(e);
