@@ -25,7 +25,8 @@ namespace {
 // launch to do it, then takes its share of the tokens and pages, each found by
 // a binary search in the prefix sums in shared memory.
 // Bound by latency (the bytes of the larger step are 0.3 us of HBM time): 4.0 us for 256
-// requests that gain a token each, 10.9 us for 2048 mixed ones with 253 k new tokens.
+// requests that gain a token each, 10.9 us for 2048 mixed ones with 253 k new tokens (2048
+// that gain a token each: 9.6 us, so it is the scans and their loads, not the tokens).
 // ---------------------------------------------------------------------------
 constexpr int kPlanThreads = 512;
 constexpr int kPlanMaxN = 16384;           // three prefix arrays in shared memory
@@ -86,8 +87,11 @@ struct PlanParams {
     int* d_status;
 };
 
-// EACH: requests of a thread, their lengths held in registers (2048 requests: 10.9 us
-// against 13.0 us when each pass reads them again).
+// EACH: requests of a thread in a round of kPlanThreads * EACH; a call of one round holds
+// their lengths in registers for both passes (2048 requests: 10.9 us against 13.0 us when
+// each pass reads them again), a call of several reads them twice. Rounds of 8 a thread:
+// 2049 requests 10.9 us, 8192 27.0, 16384 46.0; one round of 32 a thread, whose lengths
+// do not fit the registers, 54.2, 81.2 and 123.
 template <int EACH>
 __global__ void __launch_bounds__(kPlanThreads) kda_kv_plan_kernel(const PlanParams p) {
     extern __shared__ unsigned s_pre[];
@@ -126,68 +130,83 @@ __global__ void __launch_bounds__(kPlanThreads) kda_kv_plan_kernel(const PlanPar
                (b > a && s_tok[r + 1] > (unsigned)p.max_tokens);
     };
 
-    // Each thread owns EACH consecutive requests.
-    const int r0 = tid * EACH;
+    // A round: each thread owns EACH consecutive requests, from r0 on.
+    constexpr int kRound = kPlanThreads * EACH;
     unsigned a[EACH], b[EACH], held[EACH], want[EACH];
+    auto load = [&](int r0) {
 #pragma unroll
-    for (int e = 0; e < EACH; e++) {
-        a[e] = b[e] = 0;
-        if (r0 + e < N) {
-            a[e] = length(p.old_len, r0 + e);
-            b[e] = length(p.new_len, r0 + e);
+        for (int e = 0; e < EACH; e++) {
+            a[e] = b[e] = 0;
+            if (r0 + e < N) {
+                a[e] = length(p.old_len, r0 + e);
+                b[e] = length(p.new_len, r0 + e);
+            }
+        }
+#pragma unroll
+        for (int e = 0; e < EACH; e++) {
+            held[e] = pages(a[e]);
+            want[e] = pages(b[e]);
+        }
+    };
+    unsigned tokens = 0, needed = 0, given = 0, sum;  // of the rounds so far
+    if (tid == 0) s_taken = 0;
+    for (int base = 0; base < N; base += kRound) {
+        const int r0 = base + tid * EACH;
+        load(r0);
+        unsigned tok = 0, take = 0;
+#pragma unroll
+        for (int e = 0; e < EACH; e++) {
+            tok = sat_add(tok, b[e] > a[e] ? b[e] - a[e] : 0u);
+            take = sat_add(take, takes(held[e], want[e]));
+        }
+        tok = sat_add(tokens, block_scan(tok, s_warp, &sum));
+        tokens = sat_add(tokens, sum);
+        take = sat_add(needed, block_scan(take, s_warp, &sum));
+        needed = sat_add(needed, sum);
+#pragma unroll
+        for (int e = 0; e < EACH; e++) {
+            if (r0 + e < N) {
+                s_tok[r0 + e] = tok;
+                s_take[r0 + e] = take;
+            }
+            tok = sat_add(tok, b[e] > a[e] ? b[e] - a[e] : 0u);
+            take = sat_add(take, takes(held[e], want[e]));
         }
     }
-    unsigned tok = 0, take = 0, back = 0, sum;
-    if (tid == 0) s_taken = 0;
-#pragma unroll
-    for (int e = 0; e < EACH; e++) {
-        held[e] = pages(a[e]);
-        want[e] = pages(b[e]);
-        tok = sat_add(tok, b[e] > a[e] ? b[e] - a[e] : 0u);
-        take = sat_add(take, takes(held[e], want[e]));
-    }
-    tok = block_scan(tok, s_warp, &sum);
-    const unsigned tokens = sum;
-    take = block_scan(take, s_warp, &sum);
     if (tid == 0) {
         s_tok[N] = tokens;
-        s_take[N] = sum;
+        s_take[N] = needed;
         if (tokens >= kLenCap) flags |= KDA_DEV_LENGTH;
     }
-#pragma unroll
-    for (int e = 0; e < EACH; e++) {
-        if (r0 + e < N) {
-            s_tok[r0 + e] = tok;
-            s_take[r0 + e] = take;
-        }
-        tok = sat_add(tok, b[e] > a[e] ? b[e] - a[e] : 0u);
-        take = sat_add(take, takes(held[e], want[e]));
-    }
     __syncthreads();
-    unsigned gives[EACH];
+    for (int base = 0; base < N; base += kRound) {
+        const int r0 = base + tid * EACH;
+        if (N > kRound) load(r0);
+        unsigned gives[EACH], back = 0;
 #pragma unroll
-    for (int e = 0; e < EACH; e++) {
-        const int r = r0 + e;
-        gives[e] = 0;
-        if (r >= N) continue;
-        const bool no = refused(r, a[e], b[e], held[e], want[e]);
-        if (no) flags |= KDA_DEV_PAGES;
-        else if (want[e] > held[e]) atomicMax(&s_taken, s_take[r + 1]);
-        // Entries past the row's end were never pages.
-        if (!no && want[e] < held[e] && want[e] < (unsigned)p.max_pages)
-            gives[e] = min(held[e], (unsigned)p.max_pages) - want[e];
-        back = sat_add(back, gives[e]);
-        if (blockIdx.x == 0) {
-            p.kv_len[r] = (int)(no ? a[e] : b[e]);
-            p.cu[r] = (int)s_tok[r];
+        for (int e = 0; e < EACH; e++) {
+            const int r = r0 + e;
+            gives[e] = 0;
+            if (r >= N) continue;
+            const bool no = refused(r, a[e], b[e], held[e], want[e]);
+            if (no) flags |= KDA_DEV_PAGES;
+            else if (want[e] > held[e]) atomicMax(&s_taken, s_take[r + 1]);
+            // Entries past the row's end were never pages.
+            if (!no && want[e] < held[e] && want[e] < (unsigned)p.max_pages)
+                gives[e] = min(held[e], (unsigned)p.max_pages) - want[e];
+            back = sat_add(back, gives[e]);
+            if (blockIdx.x == 0) {
+                p.kv_len[r] = (int)(no ? a[e] : b[e]);
+                p.cu[r] = (int)s_tok[r];
+            }
         }
-    }
-    back = block_scan(back, s_warp, &sum);
-    unsigned given = sum;
+        back = sat_add(given, block_scan(back, s_warp, &sum));
+        given = sat_add(given, sum);
 #pragma unroll
-    for (int e = 0; e < EACH; e++) {
-        if (r0 + e < N) s_back[r0 + e] = back;
-        back = sat_add(back, gives[e]);
+        for (int e = 0; e < EACH; e++) {
+            if (r0 + e < N) s_back[r0 + e] = back;
+            back = sat_add(back, gives[e]);
+        }
     }
     if (tid == 0) s_back[N] = given;
     __syncthreads();
@@ -342,7 +361,7 @@ kda_status_t kda_kv_plan(const int* old_len, const int* new_len, int* block_tabl
     const size_t smem = 3 * ((size_t)N + 1) * 4;
     auto kernel = N <= kPlanThreads        ? kda_kv_plan_kernel<1>
                   : N <= 4 * kPlanThreads ? kda_kv_plan_kernel<4>
-                                          : kda_kv_plan_kernel<kPlanMaxN / kPlanThreads>;
+                                          : kda_kv_plan_kernel<8>;
     int dev = -1;
     const long long most = std::max(device_sms(&dev), 1);
     // Past 48 KB, of which the static part takes some (only the last kernel gets there).
