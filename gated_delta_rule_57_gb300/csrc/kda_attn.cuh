@@ -11,10 +11,11 @@
 // it holds. Lengths live on the device, so the kernels find their items
 // themselves: items are numbered request by request, and a walk over the
 // requests (32 at a time, one per lane) turns a number into an item.
-//   Whole items: CTA c takes items c, c + grid, ...; inside a request the
-//     longest (last tokens) come first and the key heads run fastest, so
-//     concurrent CTAs share the keys of one request in L2 and the short
-//     items fill the end.
+//   Whole items: CTA c takes item c; in bf16 the CTAs that run then take over, in
+//     order, those that have not started, in fp32 items c + grid, ... Inside a
+//     request the longest (last tokens) come first and the key heads run fastest,
+//     so concurrent CTAs share the keys of one request in L2 and the short items
+//     fill the end.
 //   Split items: the key tiles of all items laid end to end are cut into
 //     ranges of equal cost, one per CTA, so few rows over a long cache use every
 //     SM and ragged lengths balance exactly (a tile belongs to the range that

@@ -40,9 +40,10 @@
 // of one group (scores, exponentials, second product) against the other group's two
 // products, and shared memory, which the products' operands and the TMA writes
 // occupy as long as the products take; for single tokens HBM. Measured (32 / 8
-// heads, d = 128): 8 prompts of 8192 tokens 2.66 ms, 1.65 PFLOP/s; one token of 256
-// requests over 1.05 M cached tokens 0.61 ms, 7.0 TB/s; 2 x 4 drafts over 262 k tokens
-// each 0.31 ms, 6.9 TB/s.
+// heads, d = 128): 8 prompts of 8192 tokens 2.46 ms, 1.79 PFLOP/s, alone at 2.07 GHz, and
+// 2.74 ms, 1.60 PFLOP/s, back to back at the power limit (1.65 to 1.70 GHz); one token
+// of 256 requests over 1.05 M cached tokens 0.61 ms, 7.0 TB/s; 2 x 4 drafts over 262 k
+// tokens each 0.31 ms, 6.9 TB/s.
 #include <atomic>
 
 #include "kda_attn.cuh"
@@ -63,7 +64,7 @@ static_assert(2 * kRegsSoftmax + kRegsOther + kRegsResult <= 4 * 128, "more than
 constexpr int kMmaWarp = 8, kLoadWarp = 9, kEdgeWarp = 10;  // and warp 11
 constexpr int kPieces = 4;         // pieces announced ahead
 // Relative time of a key tile for one row tile and for a pair: about 1750 and 2500
-// clocks, measured in a step of two prompts' chunks among single tokens.
+// clocks, measured at d = 128 in a step of two prompts' chunks among single tokens.
 constexpr int kCostSingle = 5, kCostPair = 7;
 // An item beside its key tiles: 4700 clocks of a pair's, measured over 8192 causal tokens.
 constexpr int kItemKeys = 256;
@@ -935,6 +936,9 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
                             u.x = ex2(u.x);
                             u.y = ex2(u.y);
                             sum[(e >> 1) & 1] = add2(sum[(e >> 1) & 1], u);
+                            // to bf16, as the product wants P in V's type (the sum is of
+                            // the unrounded): o is off by 1.8e-3 to 2.3e-3 of its norm,
+                            // 1.6e-3 to 1.7e-3 with P in fp32
                             pk[e / 2] = __uint_as_float(pack2(u.x, u.y));
                         }
                         tmem_st16(ts + b / 2, pk);
@@ -1167,12 +1171,21 @@ cudaError_t launch_t(const AttnArgs& a) {
 // Whole items or ranges. Ranges balance any lengths, but cost a second launch,
 // the parts' stores and a longer start: about 10 us over single tokens, 25 us over
 // pairs of row tiles (18 of their key tiles). Measured, ranges against whole items, us
-// (32 / 8 heads, d = 128, one H = Hkv otherwise):
-//   one token, equal lengths:  1 x 1024 17/12, 1 x 2048 18/17, 1 x 4096 21/27,
-//     16 x 2048 36/26, 64 x 2048 90/84;  lengths to 8192: 32 requests 80/99, 256 618/615
-//   prompts: 2048 54/38, 4 x 2048 152/109, 8192 339/320;  H = 2: 2048 35/28, 8192
-//     106/112;  H = 1: 4096 38/51, 8192 73/86, 16384 177/213
-//   512 new tokens over 32768: 197/323;  2 x 4096 over 16384 1515/1530
+// (32 / 8 heads, one H = Hkv otherwise):
+//                                        d = 128       d = 64
+//   one token, 1 x 1024                    16/12        15/10
+//     1 x 2048, 1 x 4096              18/17, 21/27  17/14, 20/23
+//     16 x 2048, 64 x 2048            35/27, 92/85  22/15, 56/53
+//     lengths to 8192, 32 requests        96/111        58/77
+//     256 requests                       613/610      325/329
+//   prompts, 2048, 4 x 2048         53/39, 135/108 41/32, 107/87
+//     8192                               337/309      288/264
+//     H = 2, 2048, 8192             34/28, 105/113  26/25, 90/99
+//     H = 1, 4096, 8192              38/48, 67/86   30/43, 57/80
+//     H = 1, 16384                       177/207      152/190
+//   512 new tokens over 32768            193/319      144/299
+//   2 x 4096 over 16384                1079/1114      901/896
+// The rule is within 1 % of the better side at both d, but for H = 2, 8192.
 AttnSplit attn_tc_split(int N, int total_q, int max_q, long long max_keys, bool prompt, int Hq,
                         int Hkv, int nsm) {
     AttnSplit sp{};

@@ -447,7 +447,9 @@ kda_status_t kda_decode_multi(const void* q, const void* k, const void* v, const
  * bullet) describes the paged half of the cache that those layers leave. The
  * four calls below serve such a layer: plan a step's pages, write its keys and
  * values, and attend, over whole prompts or over the cache. Heads are grouped:
- * query head i reads key head i / (Hq / Hkv). They share the conventions at
+ * query head i reads key head i / (Hq / Hkv). (The page's own full-attention
+ * layers compress keys and values into a latent; that form is not served, only
+ * stacks whose attention layers keep plain keys and values.) They share the conventions at
  * the top of this file, with these differences:
  *   - q, k and v may be views of one fused projection: token t starts at
  *     t * stride elements, its heads are contiguous ([H, d]). Strides are
@@ -506,8 +508,8 @@ kda_status_t kda_kv_plan(const int* old_len, const int* new_len, int* block_tabl
  *                      skipped; past the cache: skipped, KDA_DEV_PAGES
  *   k_cache, v_cache : [num_pages, Hkv, page_size, d] of type io (in/out)
  *
- * Two tokens with one slot leave either's values. HBM-bound: each byte is read
- * and written once.
+ * Two tokens with one slot leave values of both, in pieces of 16 bytes.
+ * HBM-bound: each byte is read and written once.
  */
 kda_status_t kda_kv_append(const void* k, const void* v, const int* slot_map, void* k_cache,
                            void* v_cache, int T, int Hkv, int d, long long k_stride,
@@ -537,7 +539,9 @@ kda_status_t kda_kv_append(const void* k, const void* v, const int* slot_map, vo
  * to bf16 for the second product (their sum is of the unrounded ones), softmax
  * statistics and sums in fp32. io = KDA_F32: everything in fp32 on the CUDA
  * cores. What later tokens hold (NaN and Inf too) does not reach earlier
- * tokens. KDA_DEV_NONFINITE is set where an o is NaN or Inf.
+ * tokens; a value that is NaN or Inf reaches every row that sees it, however
+ * small its weight, in its channel. KDA_DEV_NONFINITE is set where an o is NaN
+ * or Inf.
  */
 kda_status_t kda_attn_prompt(const void* q, const void* k, const void* v, const int* cu_seqlens,
                              void* o, float* lse, int N, int total, int max_len, int Hq, int Hkv,
@@ -582,8 +586,10 @@ kda_status_t kda_attn_paged(const void* q, const void* k_cache, const void* v_ca
 /*
  * Bytes of device workspace that let kda_attn_prompt (total_q = total, max_q =
  * max_len) and kda_attn_paged split a long row of keys among CTAs: partial
- * results of a few row tiles per SM of the current device; 0 where
- * nothing would be split. NULL or a smaller buffer is accepted and runs unsplit; both
+ * results of a few row tiles per SM of the current device (up to 40 MB on 152
+ * SMs). The answer holds for requests of any number of keys, as the query does not
+ * know theirs: a call whose lengths need no split leaves the buffer unused. 0 where
+ * no length would be split. NULL or a smaller buffer is accepted and runs unsplit; both
  * give the same results up to rounding. 16-byte aligned, not overlapping any
  * other argument, not used by another call in flight; contents are scratch.
  * (size_t)-1 for arguments the calls would reject.
