@@ -590,7 +590,8 @@ kda_status_t kda_attn_paged(const void* q, const void* k_cache, const void* v_ca
  * SMs). The answer holds for requests of any number of keys, as the query does not
  * know theirs: a call whose lengths need no split leaves the buffer unused. 0 where
  * no length would be split. NULL or a smaller buffer is accepted and runs unsplit; both
- * give the same results up to rounding. 16-byte aligned, not overlapping any
+ * give the same results up to rounding (unsplit, a row of more than some 300 million
+ * keys outlasts the kernel's bounded waits: KDA_DEV_TIMEOUT). 16-byte aligned, not overlapping any
  * other argument, not used by another call in flight; contents are scratch.
  * (size_t)-1 for arguments the calls would reject.
  */
