@@ -39,6 +39,10 @@ struct AttnArgs {
     float* lse;  // may be null
     int N, total_q, max_q, Hq, Hkv, d;
     long long q_stride, k_stride, v_stride;  // elements between tokens
+    long long q_head, k_head, v_head;        // elements between heads
+    const void* k_r;     // key channels that all heads share, or null
+    long long kr_stride;
+    int dr;              // how many of them
     int num_pages, page, max_pages;
     float scale;
     float* ws;      // partial results, or null: whole items
@@ -283,6 +287,21 @@ AttnSplit attn_tc_split(int N, int total_q, int max_q, long long max_keys, bool 
                         int Hkv, int nsm);
 AttnSplit attn_simt_split(int N, int total_q, int max_q, long long max_keys, bool prompt, int Hq,
                           int Hkv, int nsm);
+
+// Latent attention: every head's keys are the cached rows, 512 latent channels and dr
+// shared ones, its values the latent channels. k: the cache. Heads beyond a row tile are
+// taken in blocks of equal size, as if they had key heads.
+constexpr int kLatentDim = 512;
+constexpr int kLatentTcRows = 64, kLatentSimtRows = 32;  // rows of a row tile
+inline int latent_head_blocks(int Hq, int rows) {
+    int b = (Hq + rows - 1) / rows;
+    while (Hq % b) b++;
+    return b;
+}
+cudaError_t launch_latent_tc(const AttnArgs& a);    // bf16
+cudaError_t launch_latent_simt(const AttnArgs& a);  // fp32
+AttnSplit latent_tc_split(int N, int total_q, int max_q, long long max_keys, int Hq, int nsm);
+AttnSplit latent_simt_split(int N, int total_q, int max_q, long long max_keys, int Hq, int nsm);
 
 // Keys a request can have: what a row of the block table holds, up to 2^30, so that
 // key numbers a few tiles past the end stay inside 32 bits.

@@ -105,12 +105,14 @@ cudaError_t launch_attn_combine(const AttnSplit& sp, int Hkv, int G, int d, int 
     };
     if (io == KDA_BF16) {
         auto* out = static_cast<__nv_bfloat16*>(o);
-        return d == 128 ? go(kda_attn_combine_kernel<__nv_bfloat16, 128>, out)
-                        : go(kda_attn_combine_kernel<__nv_bfloat16, 64>, out);
+        return d == 512   ? go(kda_attn_combine_kernel<__nv_bfloat16, 512>, out)
+               : d == 128 ? go(kda_attn_combine_kernel<__nv_bfloat16, 128>, out)
+                          : go(kda_attn_combine_kernel<__nv_bfloat16, 64>, out);
     }
     auto* out = static_cast<float*>(o);
-    return d == 128 ? go(kda_attn_combine_kernel<float, 128>, out)
-                    : go(kda_attn_combine_kernel<float, 64>, out);
+    return d == 512   ? go(kda_attn_combine_kernel<float, 512>, out)
+           : d == 128 ? go(kda_attn_combine_kernel<float, 128>, out)
+                      : go(kda_attn_combine_kernel<float, 64>, out);
 }
 
 }  // namespace kda

@@ -73,23 +73,25 @@ constexpr int kItemKeys = 256;
 constexpr long long kWaitClocks = 1LL << 33;
 constexpr float kRaise = 8.f;      // log2 growth of a row maximum that moves its reference
 
-template <int D>
+// DQ channels of queries and keys, D of values and outputs. DQ > D: the last DQ - D of
+// the keys are shared by all heads and have places of their own beside the ring.
+template <int DQ, int D>
 struct TcCfg {
-    static constexpr int TILE_BYTES = kTile * D * 2;
-    static constexpr int STAGES = D == 128 ? 5 : 8;
-    static constexpr int TILES = (2 + STAGES) * TILE_BYTES;
+    static constexpr int DR = DQ - D;
+    static constexpr int TILE_BYTES = kTile * D * 2, Q_BYTES = kTile * DQ * 2;
+    static constexpr int SHARED_BYTES = kTile * DR * 2;
+    static constexpr int STAGES = DR ? 3 : D == 128 ? 5 : 8;
+    static constexpr int TILES = 2 * Q_BYTES + STAGES * TILE_BYTES + 2 * SHARED_BYTES;
 };
 
 struct TcAttnParams {
     AttnShape s;
     AttnSplit sp;
     const int* block_table;  // null: packed prompts
-    const __nv_bfloat16* q;
-    const __nv_bfloat16* k;
     const __nv_bfloat16* v;
     __nv_bfloat16* o;
     float* lse;
-    long long q_stride, k_stride, v_stride;
+    long long v_stride, v_head;
     int num_pages, page, max_pages;
     int box_q;  // tokens of a Q load
     float c;    // scale log2 e
@@ -202,18 +204,18 @@ struct Shared {
     long long sum[kThreadsTc / 32];
     uint32_t tmem;
 };
-template <int D>
+template <int DQ, int D>
 constexpr int tc_smem() {
-    return TcCfg<D>::TILES + (int)sizeof(Shared);
+    return TcCfg<DQ, D>::TILES + (int)sizeof(Shared);
 }
-static_assert(tc_smem<128>() <= 227 * 1024, "shared memory of a CTA");
+static_assert(tc_smem<128, 128>() <= 227 * 1024 && tc_smem<192, 128>() <= 227 * 1024, "shared memory of a CTA");
 
 // Values of key j of a piece; null where its page id is out of range (such pages
 // read as zeros).
 __device__ __forceinline__ const __nv_bfloat16* values_at(const TcAttnParams& p, const Piece& pc,
                                                           int d, int j) {
     if (!p.block_table)
-        return p.v + (size_t)(pc.key0 + j) * p.v_stride + (size_t)pc.h * d;
+        return p.v + (size_t)(pc.key0 + j) * p.v_stride + (size_t)pc.h * p.v_head;
     const int id = p.block_table[(size_t)pc.r * p.max_pages + j / p.page];
     if (id < 0 || id >= p.num_pages) return nullptr;
     return p.v + (((size_t)id * p.s.Hkv + pc.h) * p.page + j % p.page) * d;
@@ -303,18 +305,22 @@ __device__ __forceinline__ int add_cleared(const TcAttnParams& p, const Piece& p
     return flags;
 }
 
-template <int D>
+template <int DQ, int D>
 __global__ void __launch_bounds__(kThreadsTc, 1)
     kda_attn_tc_kernel(const __grid_constant__ CUtensorMap map_q,
                        const __grid_constant__ CUtensorMap map_k,
                        const __grid_constant__ CUtensorMap map_v,
+                       const __grid_constant__ CUtensorMap map_r,  // shared key channels
                        const __grid_constant__ TcAttnParams p) {
-    using C = TcCfg<D>;
+    using C = TcCfg<DQ, D>;
     constexpr int NS = C::STAGES, HALVES = D / 64;
     constexpr uint32_t TM_S = 0, TM_O = 256;
     extern __shared__ __align__(1024) unsigned char sm[];  // 128-byte swizzle: 1024-byte tiles
     unsigned char* sq = sm;                        // two Q tiles
-    unsigned char* skv = sm + 2 * C::TILE_BYTES;   // the ring
+    unsigned char* skv = sm + 2 * C::Q_BYTES;      // the ring
+    // Shared key channels: of even and odd key tiles. They come and go with their key tile:
+    // a place's last user is at least as far back as that of the ring's place (three tiles).
+    unsigned char* srope = skv + NS * C::TILE_BYTES;
     Shared& sh = *reinterpret_cast<Shared*>(sm + C::TILES);
     if (smem_addr(sm) & 1023u) {  // never, by the declaration above
         if (threadIdx.x == 0 && p.d_status) atomicOr(p.d_status, KDA_DEV_TIMEOUT);
@@ -352,6 +358,7 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
             prefetch_tensormap(&map_q);
             prefetch_tensormap(&map_k);
             prefetch_tensormap(&map_v);
+            if (C::DR) prefetch_tensormap(&map_r);
         }
         fence_mbarrier_init();
     }
@@ -377,6 +384,7 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
             // ------------------------------------------------------------ work and loads
             int stage = 0, kv_phase = 0, q_phase = 0, np = 0;
             int asked = 0;  // for further items
+            int nk = 0;     // key tiles so far
             // Paged: a tile is `per` pages (or part of one); lane `pg` of each half
             // loads one. Their ids are read a tile or more ahead of their use.
             const int log2_page = __ffs(p.page) - 1;
@@ -395,13 +403,19 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
                 }
                 return id;
             };
-            auto load_kv = [&](const Piece& pc, const CUtensorMap* map, int kt, int id) {
+            auto load_kv = [&](const Piece& pc, const CUtensorMap* map, int kt, int id, bool keys) {
                 warp_wait(ok, &sh.kv_empty[stage], kv_phase ^ 1);
                 if (!ok) return;
                 unsigned char* dst = skv + stage * C::TILE_BYTES;
                 uint64_t* bar = &sh.kv_full[stage];
-                if (lane == 0) mbar_arrive_expect_tx(bar, C::TILE_BYTES);
+                if (lane == 0)
+                    mbar_arrive_expect_tx(bar, C::TILE_BYTES + (keys ? C::SHARED_BYTES : 0));
                 __syncwarp();
+                if (C::DR && keys) {
+                    if (lane == HALVES)
+                        tma_load_3d(srope + (nk & 1) * C::SHARED_BYTES, &map_r, bar, 0, 0, pc.key0 + kt * kTile);
+                    nk++;
+                }
                 if (half < HALVES) {
                     dst += half * (kTile * 128);
                     if (!p.block_table)
@@ -434,11 +448,11 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
                 if (!ok) return;
                 q_phase ^= 1;
                 if (lane == 0)
-                    mbar_arrive_expect_tx(&sh.q_full, (1 + pc.pair) * HALVES * p.box_q * G * 128);
+                    mbar_arrive_expect_tx(&sh.q_full, (1 + pc.pair) * (DQ / 64) * p.box_q * G * 128);
                 __syncwarp();
-                if (lane < HALVES * (1 + pc.pair)) {
-                    const int w = lane / HALVES, half = lane % HALVES;
-                    tma_load_3d(sq + w * C::TILE_BYTES + half * (kTile * 128), &map_q, &sh.q_full,
+                if (lane < DQ / 64 * (1 + pc.pair)) {
+                    const int w = lane / (DQ / 64), half = lane % (DQ / 64);
+                    tma_load_3d(sq + w * C::Q_BYTES + half * (kTile * 128), &map_q, &sh.q_full,
                                 64 * half, pc.h * G, pc.tok0 + w * tok1);
                 }
                 // Ids of tiles j, j + 1, j + 2 in id[0..2].
@@ -447,11 +461,11 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
 #pragma unroll
                     for (int j = 0; j < 3; j++) id[j] = page_id(pc, pc.kt0 + j);
                 }
-                load_kv(pc, &map_k, pc.kt0, id[0]);
-                if (lead == 2 && n > 1) load_kv(pc, &map_k, pc.kt0 + 1, id[1]);
+                load_kv(pc, &map_k, pc.kt0, id[0], true);
+                if (lead == 2 && n > 1) load_kv(pc, &map_k, pc.kt0 + 1, id[1], true);
                 for (int j = 0; j < n; j++) {
-                    load_kv(pc, &map_v, pc.kt0 + j, id[0]);
-                    if (j + lead < n) load_kv(pc, &map_k, pc.kt0 + j + lead, lead == 1 ? id[1] : id[2]);
+                    load_kv(pc, &map_v, pc.kt0 + j, id[0], false);
+                    if (j + lead < n) load_kv(pc, &map_k, pc.kt0 + j + lead, lead == 1 ? id[1] : id[2], true);
                     id[0] = id[1];
                     id[1] = id[2];
                     if (p.block_table && j + 3 < n) id[2] = page_id(pc, pc.kt0 + j + 3);
@@ -584,7 +598,9 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
             constexpr uint32_t idesc_o = idesc_bf16(kTile, D, 0, 1);
             const uint64_t dq = desc_kmajor(smem_addr(sq));
             const uint64_t dk = desc_kmajor(smem_addr(skv)), dv = desc_mnmajor(smem_addr(skv), kTile);
-            constexpr uint32_t TILE = C::TILE_BYTES >> 4;  // a tile in descriptor units
+            constexpr uint32_t TILE = C::TILE_BYTES >> 4, QTILE = C::Q_BYTES >> 4;  // in descriptor units
+            const uint64_t dr = desc_kmajor(smem_addr(srope));
+            uint32_t rope = 0;  // place of the next key tile's shared channels
             auto next = [&] {
                 if (++stage == NS) {
                     stage = 0;
@@ -597,12 +613,20 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
             };
             auto uniform = [](int x) { return __shfl_sync(0xffffffffu, x, 0); };
             auto scores = [&](int w, uint32_t qtile, uint32_t kstage) {  // S_w = Q_w K^T
-                const uint64_t a = dq + qtile * TILE, b = dk + kstage * TILE;
+                const uint64_t a = dq + qtile * QTILE, b = dk + kstage * TILE;
                 if (elect_one()) {
 #pragma unroll
                     for (int kk = 0; kk < D / 16; kk++)
                         mma_bf16(tbase + TM_S + w * kTile, a + kstep_kmajor(kTile, kk),
                                  b + kstep_kmajor(kTile, kk), idesc_s, kk > 0);
+                    if (C::DR) {
+                        const uint64_t ar = a + kstep_kmajor(kTile, D / 16);
+                        const uint64_t br = dr + rope * (C::SHARED_BYTES >> 4);
+#pragma unroll
+                        for (int kk = 0; kk < C::DR / 16; kk++)
+                            mma_bf16(tbase + TM_S + w * kTile, ar + kstep_kmajor(kTile, kk),
+                                     br + kstep_kmajor(kTile, kk), idesc_s, 1);
+                    }
                     mma_commit(&sh.s_full[w]);
                 }
                 __syncwarp();
@@ -676,6 +700,7 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
                         if (n1 > 0) scores(1, 1, stage);
                         commit(&sh.kv_empty[stage]);
                         next();
+                        rope ^= 1;
                         if (n == 1) commit(&sh.q_empty);
                     }
                     primed = false;
@@ -728,6 +753,7 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
                         if (more) {
                             commit(&sh.kv_empty[ks]);
                             next();
+                            rope ^= 1;
                         }
                         // the rows' last scores are issued
                         if (j + 2 == n || (j + 1 == n && primed && x.n == 1)) commit(&sh.q_empty);
@@ -742,6 +768,7 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
                         scores(j, 0, stage);
                         commit(&sh.kv_empty[stage]);
                         next();
+                        rope ^= 1;
                     }
                     if (n <= 2) commit(&sh.q_empty);
                     if (!ok || !o_free(0) || (n > 1 && !o_free(1))) break;
@@ -761,6 +788,7 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
                             scores(w, 0, ks);
                             commit(&sh.kv_empty[ks]);
                             next();
+                            rope ^= 1;
                             if (j + 3 == n) commit(&sh.q_empty);
                         } else {
                             commit(&sh.o_full[w]);
@@ -1088,11 +1116,11 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
 
 // Rows of packed tokens: [tokens][heads][d], boxes of 64 x heads x tokens.
 bool make_rows(CUtensorMap* m, const void* ptr, int d, int heads, int tokens, long long stride,
-               int box_heads, int box_tokens) {
+               long long head, int box_heads, int box_tokens) {
     auto enc = tensor_map_encoder();
     if (!enc) return false;
     cuuint64_t dims[3] = {(cuuint64_t)d, (cuuint64_t)heads, (cuuint64_t)tokens};
-    cuuint64_t strides[2] = {(cuuint64_t)d * 2, (cuuint64_t)stride * 2};
+    cuuint64_t strides[2] = {(cuuint64_t)head * 2, (cuuint64_t)stride * 2};
     cuuint32_t box[3] = {64, (cuuint32_t)box_heads, (cuuint32_t)box_tokens};
     cuuint32_t es[3] = {1, 1, 1};
     return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(ptr), dims, strides, box,
@@ -1116,7 +1144,7 @@ bool make_cache(CUtensorMap* m, const void* ptr, int d, int page, int heads, int
                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int D>
+template <int DQ, int D>
 cudaError_t launch_t(const AttnArgs& a) {
     const int G = a.Hq / a.Hkv, tok1 = kTile / G;
     int dev = 0;
@@ -1130,14 +1158,11 @@ cudaError_t launch_t(const AttnArgs& a) {
                          a.Hkv, nsm);
     if (p.sp.ctas && a.ws && a.ws_bytes >= attn_split_bytes(p.sp, D)) p.sp.ws = a.ws;
     p.block_table = a.block_table;
-    p.q = static_cast<const __nv_bfloat16*>(a.q);
-    p.k = static_cast<const __nv_bfloat16*>(a.k);
     p.v = static_cast<const __nv_bfloat16*>(a.v);
     p.o = static_cast<__nv_bfloat16*>(a.o);
     p.lse = a.lse;
-    p.q_stride = a.q_stride;
-    p.k_stride = a.k_stride;
     p.v_stride = a.v_stride;
+    p.v_head = a.v_head;
     p.num_pages = a.num_pages;
     p.page = a.page;
     p.max_pages = a.max_pages;
@@ -1145,23 +1170,24 @@ cudaError_t launch_t(const AttnArgs& a) {
     p.c = a.scale * 1.44269504089f;
     p.d_status = a.d_status;
 
-    CUtensorMap mq, mk, mv;
-    bool ok = make_rows(&mq, a.q, D, a.Hq, a.total_q, a.q_stride, G, p.box_q);
+    CUtensorMap mq, mk, mv, mr{};
+    bool ok = make_rows(&mq, a.q, DQ, a.Hq, a.total_q, a.q_stride, a.q_head, G, p.box_q);
     if (a.kv_len)
         ok = ok && make_cache(&mk, a.k, D, a.page, a.Hkv, a.num_pages) &&
              make_cache(&mv, a.v, D, a.page, a.Hkv, a.num_pages);
     else
-        ok = ok && make_rows(&mk, a.k, D, a.Hkv, a.total_q, a.k_stride, 1, kTile) &&
-             make_rows(&mv, a.v, D, a.Hkv, a.total_q, a.v_stride, 1, kTile);
+        ok = ok && make_rows(&mk, a.k, D, a.Hkv, a.total_q, a.k_stride, a.k_head, 1, kTile) &&
+             make_rows(&mv, a.v, D, a.Hkv, a.total_q, a.v_stride, a.v_head, 1, kTile);
+    if (DQ > D) ok = ok && make_rows(&mr, a.k_r, DQ - D, 1, a.total_q, a.kr_stride, DQ - D, 1, kTile);
     if (!ok) return cudaErrorInvalidValue;
-    auto kernel = kda_attn_tc_kernel<D>;
+    auto kernel = kda_attn_tc_kernel<DQ, D>;
     static std::atomic<uint64_t> ready{0};
-    cudaError_t e = allow_shared(kernel, tc_smem<D>(), ready, dev);
+    cudaError_t e = allow_shared(kernel, tc_smem<DQ, D>(), ready, dev);
     if (e != cudaSuccess) return e;
     const long long grid = p.sp.ws ? p.sp.ctas : attn_items_bound(p.s);
     if (grid >= 1LL << 31) return cudaErrorInvalidValue;
-    e = launch_dependent(kernel, dim3((unsigned)grid), dim3(kThreadsTc), tc_smem<D>(), a.stream,
-                         mq, mk, mv, p);
+    e = launch_dependent(kernel, dim3((unsigned)grid), dim3(kThreadsTc), tc_smem<DQ, D>(), a.stream,
+                         mq, mk, mv, mr, p);
     if (e != cudaSuccess || !p.sp.ws) return e;
     return launch_attn_combine(p.sp, a.Hkv, G, D, kTile, a.o, a.lse, KDA_BF16, a.d_status, a.stream);
 }
@@ -1206,7 +1232,8 @@ AttnSplit attn_tc_split(int N, int total_q, int max_q, long long max_keys, bool 
 }
 
 cudaError_t launch_attn_tc(const AttnArgs& a) {
-    return a.d == 128 ? launch_t<128>(a) : launch_t<64>(a);
+    if (a.dr) return launch_t<192, 128>(a);
+    return a.d == 128 ? launch_t<128, 128>(a) : launch_t<64, 64>(a);
 }
 
 }  // namespace kda

@@ -1,0 +1,345 @@
+// Attention over a paged cache of latents on the CUDA cores, every product and sum in 32 bits.
+//
+//     x_ij = scale log2(e) q_i . c_j,  p_ij = 2^{x_ij - m_i},  o_i = sum_j p_ij c_j[0 .. 511] / l_i
+//
+// with one cached row c_j of 512 latent channels and DR rotated ones for all heads. One
+// pass over the keys with a running maximum m_i and sum l_i. A CTA of 256 threads holds
+// 32 rows (token, head) and takes 32 keys at a time through shared memory, the next 32
+// on their way (cp.async) meanwhile; the same tile is keys, then values.
+//   Scores: a thread has 4 rows x 4 keys over every fourth 16-byte vector of the
+//     channels, 8 loads for 64 FFMA; four neighbouring lanes add up.
+//   Outputs: a thread has 8 rows x 8 channels, 4 loads for 64 FFMA.
+// Bound by shared memory and the FFMA pipe alike. Long rows are cut into ranges
+// as the header of kda_attn.cuh says.
+#include <algorithm>
+#include <atomic>
+
+#include "kda_attn.cuh"
+#include "kda_host.cuh"
+
+namespace kda {
+namespace {
+
+constexpr int kRows = kLatentSimtRows, kKeys = 32, kThreads = 256, kDL = kLatentDim;
+constexpr int kLP = kRows + 4;  // floats between keys of the probabilities
+
+struct LatentSimtParams {
+    AttnShape s;
+    AttnSplit sp;
+    const float* q;
+    const float* cache;
+    const int* block_table;
+    float* o;
+    float* lse;
+    long long q_stride, q_head;
+    int num_pages, page, max_pages;
+    float scale;
+    int* d_status;
+};
+
+template <int DR>
+struct SimtCfg {
+    static constexpr int DQ = kDL + DR, LD = DQ + 16;  // rows 16 banks apart
+    static constexpr size_t SMEM = ((size_t)3 * kRows * LD + kKeys * kLP) * 4;
+};
+
+__device__ __forceinline__ void copy16(float* dst, const float* src, bool there) {
+    const int n = there ? 16 : 0;  // the rest is zeros
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(
+                     (uint32_t)__cvta_generic_to_shared(dst)),
+                 "l"(src), "r"(n)
+                 : "memory");
+}
+__device__ __forceinline__ void copies_end() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copies_wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+__device__ __forceinline__ float4 ld4(const float* p) { return *reinterpret_cast<const float4*>(p); }
+
+template <int DR>
+__global__ void __launch_bounds__(kThreads, 1) kda_latent_simt_kernel(const LatentSimtParams p) {
+    using C = SimtCfg<DR>;
+    constexpr int LD = C::LD, V4 = C::DQ / 4;
+    extern __shared__ __align__(16) float sm[];
+    float* sq = sm;
+    float* skv = sq + kRows * LD;           // two tiles
+    float* sp = skv + 2 * kKeys * LD;       // probabilities [key][row]
+    long long* groups = reinterpret_cast<long long*>(sp);  // before the first item
+    static_assert(kAttnGroups * 8 <= kKeys * kLP * 4, "groups fit the probabilities");
+    __shared__ long long s_sum[kThreads / 32];
+    __shared__ float s_corr[kRows];
+    __shared__ int s_lim[kRows];
+
+    pdl_wait();
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int part = lane & 3, kg = lane >> 2;      // scores: channels, keys kg + 8 j, rows warp + 8 i
+    const int r8 = (tid >> 6) * 8, c4 = (tid & 63) * 4;  // outputs: rows r8 .. + 7, channels c4 .., 256 + c4 ..
+    const AttnShape& s = p.s;
+    const float c = p.scale * 1.44269504089f;
+    int flags = 0;
+    AttnWalk walk;
+    struct {
+        int r, t, h;
+        AttnReq q;
+    } it{};
+    long long in, each = 0;
+    const bool split = p.sp.ws != nullptr;
+    if (split) {
+        each = attn_cost_each<kThreads>(s, p.sp.ctas, p.sp.least, groups, s_sum);
+        __syncthreads();
+    }
+    long long cur = split ? blockIdx.x * each : blockIdx.x;
+    const long long end = cur + each;
+    long long start = cur;
+    if (split) walk = attn_walk_at(s, groups, cur);
+    bool have = false;
+    int tile = 0;
+    while (!split || cur < end) {
+        if (!have) {
+            const bool first = split && cur == start;
+            if (!(split ? attn_first_tile(s, walk, &cur, &it.r, &it.q, &it.h, &it.t, &tile) && cur < end
+                        : attn_find<false>(s, walk, cur, &it.r, &it.q, &in))) {
+                if (first && tid == 0) attn_cuts(p.sp, kDL)[blockIdx.x] = AttnCut{};
+                break;
+            }
+            if (first) start = cur;
+            if (!split) {
+                it.t = it.q.nqt - 1 - (int)(in / s.Hkv);
+                it.h = (int)(in % s.Hkv);
+            }
+        }
+        const int G = s.G, tok0 = it.t * it.q.tok;
+        const int rows = min(it.q.tok, it.q.q_len - tok0) * G;
+        const int tiles = attn_item_tiles(s, it.q, it.t);
+        const long long u0 = cur - (long long)tile * kKeys;
+        const int last = split ? attn_tiles_until(s, it.q, u0, tiles, end) : tiles;
+        const int key0 = tile * kKeys, keys = min(attn_item_keys(it.q, it.t), last * kKeys);
+        float* dst = nullptr;
+        if (split) {
+            if (cur == start && tid == 0)
+                attn_cuts(p.sp, kDL)[blockIdx.x] =
+                    AttnCut{each, u0, it.q.q0 + tok0, rows / G, it.h, tile, tiles, kKeys};
+            if (last - tile < tiles)
+                dst = p.sp.ws + attn_slot_floats(p.sp.rows, kDL) * (2 * blockIdx.x + (cur > start ? 1 : 0));
+        }
+        const size_t first = (size_t)it.q.q0 + tok0;  // packed token of row 0
+        __syncthreads();  // the item before is done with shared memory
+        for (int i = tid; i < kRows * V4; i += kThreads) {
+            const int r = i / V4, x = (i - r * V4) * 4;
+            const bool there = r < rows;
+            copy16(sq + r * LD + x,
+                   there ? p.q + (first + r / G) * p.q_stride + (size_t)(it.h * G + r % G) * p.q_head + x : p.q, there);
+        }
+        const int seen0 = it.q.kv - it.q.q_len + tok0;  // keys that row 0's token sees, less one
+        if (tid < kRows) s_lim[tid] = tid < rows ? max(seen0 + tid / G + 1, 0) : 0;
+        auto fetch = [&](int k0, int buf) {
+            if (k0 < keys)
+                for (int i = tid; i < kKeys * V4; i += kThreads) {
+                    const int j = i / V4, x = (i - j * V4) * 4, at = k0 + j;
+                    const float* src = p.cache;
+                    bool there = at < keys;
+                    if (there) {
+                        const int id = p.block_table[(size_t)it.r * p.max_pages + at / p.page];
+                        there = id >= 0 && id < p.num_pages;
+                        if (there) src += ((size_t)id * p.page + at % p.page) * C::DQ + x;
+                        else flags |= KDA_DEV_PAGES;
+                    }
+                    copy16(skv + (buf * kKeys + j) * LD + x, src, there);
+                }
+            copies_end();
+        };
+        float m[4], l[4], acc[8][8];
+#pragma unroll
+        for (int i = 0; i < 4; i++) {
+            m[i] = -INFINITY;
+            l[i] = 0.f;
+        }
+#pragma unroll
+        for (int i = 0; i < 8; i++)
+#pragma unroll
+            for (int e = 0; e < 8; e++) acc[i][e] = 0.f;
+        fetch(key0, 0);
+        int buf = 0;
+        for (int k0 = key0; k0 < keys; k0 += kKeys, buf ^= 1) {
+            fetch(k0 + kKeys, buf ^ 1);
+            copies_wait<1>();
+            __syncthreads();
+            const float* kv = skv + buf * kKeys * LD;
+            float x[4][4] = {};
+#pragma unroll 2
+            for (int e = part * 4; e < C::DQ; e += 16) {
+                float4 a[4], b[4];
+#pragma unroll
+                for (int i = 0; i < 4; i++) a[i] = ld4(sq + (warp + 8 * i) * LD + e);
+#pragma unroll
+                for (int j = 0; j < 4; j++) b[j] = ld4(kv + (kg + 8 * j) * LD + e);
+#pragma unroll
+                for (int i = 0; i < 4; i++)
+#pragma unroll
+                    for (int j = 0; j < 4; j++) {
+                        x[i][j] = fmaf(a[i].x, b[j].x, x[i][j]);
+                        x[i][j] = fmaf(a[i].y, b[j].y, x[i][j]);
+                        x[i][j] = fmaf(a[i].z, b[j].z, x[i][j]);
+                        x[i][j] = fmaf(a[i].w, b[j].w, x[i][j]);
+                    }
+            }
+#pragma unroll
+            for (int i = 0; i < 4; i++) {
+                const int row = warp + 8 * i, lim = s_lim[row];
+                float mx = -INFINITY;
+#pragma unroll
+                for (int j = 0; j < 4; j++) {
+                    x[i][j] += __shfl_xor_sync(0xffffffffu, x[i][j], 1);
+                    x[i][j] += __shfl_xor_sync(0xffffffffu, x[i][j], 2);
+                    x[i][j] = k0 + kg + 8 * j < lim ? x[i][j] * c : -INFINITY;
+                    mx = fmaxf(mx, x[i][j]);
+                }
+#pragma unroll
+                for (int o = 4; o < 32; o <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+                const float mn = fmaxf(m[i], mx);
+                const float ref = mn == -INFINITY ? 0.f : mn;  // a row that sees nothing yet
+                const float corr = exp2f(m[i] - ref);
+                m[i] = mn;
+                l[i] *= corr;
+                float e4 = 0.f;
+#pragma unroll
+                for (int j = 0; j < 4; j++) {
+                    const float e = exp2f(x[i][j] - ref);
+                    l[i] += e;  // of this lane's keys
+                    e4 = part == j ? e : e4;
+                }
+                sp[(kg + 8 * part) * kLP + row] = e4;  // the four lanes have the same sums
+                if (lane == 0) s_corr[row] = corr;
+            }
+            __syncthreads();
+            float f[8];
+#pragma unroll
+            for (int i = 0; i < 8; i++) f[i] = s_corr[r8 + i];
+#pragma unroll
+            for (int i = 0; i < 8; i++)
+#pragma unroll
+                for (int e = 0; e < 8; e++) acc[i][e] *= f[i];
+            // Keys that only some rows see add nothing to the others, whatever they hold.
+            const bool edge = k0 + kKeys > seen0 + 1;
+            auto add = [&](bool guard) {
+#pragma unroll 2
+                for (int j = 0; j < kKeys; j++) {
+                    const float4 v0 = ld4(kv + j * LD + c4), v1 = ld4(kv + j * LD + 256 + c4);
+                    const float4 p0 = ld4(sp + j * kLP + r8), p1 = ld4(sp + j * kLP + r8 + 4);
+                    const float w[8] = {p0.x, p0.y, p0.z, p0.w, p1.x, p1.y, p1.z, p1.w};
+#pragma unroll
+                    for (int i = 0; i < 8; i++) {
+                        if (guard && k0 + j >= s_lim[r8 + i]) continue;
+                        acc[i][0] = fmaf(w[i], v0.x, acc[i][0]);
+                        acc[i][1] = fmaf(w[i], v0.y, acc[i][1]);
+                        acc[i][2] = fmaf(w[i], v0.z, acc[i][2]);
+                        acc[i][3] = fmaf(w[i], v0.w, acc[i][3]);
+                        acc[i][4] = fmaf(w[i], v1.x, acc[i][4]);
+                        acc[i][5] = fmaf(w[i], v1.y, acc[i][5]);
+                        acc[i][6] = fmaf(w[i], v1.z, acc[i][6]);
+                        acc[i][7] = fmaf(w[i], v1.w, acc[i][7]);
+                    }
+                }
+            };
+            if (edge) add(true);
+            else add(false);
+            __syncthreads();  // the tile may be written again
+        }
+        copies_wait<0>();
+        __syncthreads();  // (an item without keys: limits are written)
+#pragma unroll
+        for (int i = 0; i < 4; i++) {
+            const int row = warp + 8 * i;
+#pragma unroll
+            for (int o = 4; o < 32; o <<= 1) l[i] += __shfl_xor_sync(0xffffffffu, l[i], o);
+            if (lane) continue;
+            s_corr[row] = l[i] > 0.f ? 1.f / l[i] : (l[i] == 0.f ? 0.f : l[i]);  // NaN stays
+            if (row >= rows) continue;
+            const size_t at = (first + row / G) * s.Hkv * G + it.h * G + row % G;
+            if (dst) dst[(size_t)p.sp.rows * kDL + row] = l[i] == 0.f ? -INFINITY : m[i] + log2f(l[i]);
+            else if (p.lse) p.lse[at] = l[i] == 0.f ? -INFINITY : (m[i] + log2f(l[i])) * 0.69314718056f;
+        }
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < 8; i++) {
+            const int row = r8 + i;
+            if (row >= rows) break;
+            const float inv = s_corr[row];
+            const size_t at = (first + row / G) * s.Hkv * G + it.h * G + row % G;
+            float* y = dst ? dst + (size_t)row * kDL : p.o + at * kDL;
+#pragma unroll
+            for (int e = 0; e < 8; e++) {
+                acc[i][e] *= inv;
+                flags |= finite_flag(acc[i][e]);
+            }
+            *reinterpret_cast<float4*>(y + c4) = make_float4(acc[i][0], acc[i][1], acc[i][2], acc[i][3]);
+            *reinterpret_cast<float4*>(y + 256 + c4) = make_float4(acc[i][4], acc[i][5], acc[i][6], acc[i][7]);
+        }
+        if (split) {
+            cur = last < tiles ? end
+                               : u0 + attn_cost_before(s, it.q, it.t + 1) - attn_cost_before(s, it.q, it.t);
+            tile = 0;
+            if (++it.t == it.q.nqt) {
+                it.t = 0;
+                it.h++;
+            }
+            have = it.h < s.Hkv;
+        } else {
+            cur += gridDim.x;
+        }
+    }
+    if (blockIdx.x == 0)  // lengths of requests this CTA had no work of
+        for (int i = tid; i < s.N; i += kThreads) walk.bad |= attn_request(s, i).bad != 0;
+    if (walk.bad) flags |= KDA_DEV_LENGTH;
+    report_flags(p.d_status, flags);
+}
+
+template <int DR>
+cudaError_t launch_t(const AttnArgs& a) {
+    LatentSimtParams p{};
+    const int blocks = latent_head_blocks(a.Hq, kRows), G = a.Hq / blocks, tok = kRows / G;
+    int dev = 0;
+    const int nsm = device_sms(&dev);
+    p.s = {a.cu_q, a.kv_len, a.N, a.total_q, a.max_q, attn_kv_cap(a), blocks, G, tok, tok, kKeys, 1, 1, 0};
+    p.q = static_cast<const float*>(a.q);
+    p.cache = static_cast<const float*>(a.k);
+    p.block_table = a.block_table;
+    p.o = static_cast<float*>(a.o);
+    p.lse = a.lse;
+    p.q_stride = a.q_stride;
+    p.q_head = a.q_head;
+    p.num_pages = a.num_pages;
+    p.page = a.page;
+    p.max_pages = a.max_pages;
+    p.scale = a.scale;
+    p.d_status = a.d_status;
+    static std::atomic<uint64_t> ready{0};
+    cudaError_t e = allow_shared(kda_latent_simt_kernel<DR>, SimtCfg<DR>::SMEM, ready, dev);
+    if (e != cudaSuccess) return e;
+    p.sp = latent_simt_split(a.N, a.total_q, a.max_q, p.s.kv_cap, a.Hq, nsm);
+    if (p.sp.ctas && a.ws && a.ws_bytes >= attn_split_bytes(p.sp, kDL)) p.sp.ws = a.ws;
+    const long long grid = p.sp.ws ? p.sp.ctas : std::min(attn_items_bound(p.s), 1LL << 20);
+    e = launch_dependent(kda_latent_simt_kernel<DR>, dim3((unsigned)grid), dim3(kThreads), SimtCfg<DR>::SMEM,
+                         a.stream, p);
+    if (e != cudaSuccess || !p.sp.ws) return e;
+    return launch_attn_combine(p.sp, blocks, G, kDL, kRows, a.o, a.lse, KDA_F32, a.d_status, a.stream);
+}
+
+}  // namespace
+
+AttnSplit latent_simt_split(int N, int total_q, int max_q, long long max_keys, int Hq, int nsm) {
+    AttnSplit sp{};
+    if (N == 0 || total_q == 0 || max_q == 0 || Hq == 0 || nsm == 0) return sp;
+    const int blocks = latent_head_blocks(Hq, kRows), G = Hq / blocks, tok = kRows / G;
+    if (max_keys <= KDA_ATTN_SHORT_KEYS / 16) return sp;
+    if ((long long)total_q / tok * blocks >= 16LL * nsm) return sp;
+    sp.ctas = nsm;
+    sp.least = kKeys;
+    sp.rows = (std::min(max_q, tok) * G + 3) & ~3;  // whole 16-byte vectors
+    return sp;
+}
+
+cudaError_t launch_latent_simt(const AttnArgs& a) { return a.dr ? launch_t<64>(a) : launch_t<0>(a); }
+
+}  // namespace kda

@@ -53,7 +53,7 @@
 extern "C" {
 #endif
 
-#define KDA_ABI_VERSION 3
+#define KDA_ABI_VERSION 4
 
 typedef enum {
     KDA_OK = 0,
@@ -597,6 +597,135 @@ kda_status_t kda_attn_paged(const void* q, const void* k_cache, const void* v_ca
  */
 size_t kda_attn_workspace_size(int N, int total_q, int max_q, int Hq, int Hkv, int d,
                                kda_dtype_t io);
+
+/*
+ * Rotation by position, and layers that keep one latent vector a token
+ * --------------------------------------------------------------------
+ * kda_kv_append_rope is kda_kv_append for layers whose queries and keys are rotated by
+ * position. The others serve attention layers that compress keys and values
+ * into a latent: a token caches one row of dl latent channels and dr channels of a
+ * rotated key part that all heads share (dr = 0: a layer without positions, as the
+ * orkas.ai page "Kimi K3 architecture" has them, section "Sequence: three quarters of
+ * the layers stopped reading everything"). Head h's keys and values are W_h times the
+ * latent. Expanded form: the caller multiplies the latents out and attends over
+ * the heads' own keys and values (kda_attn_latent_prompt: cheap per pair of tokens).
+ * Absorbed form: the caller multiplies queries and outputs by W_h instead, and the
+ * cached rows themselves are keys and, their latent channels, values of every head
+ * (kda_attn_latent_paged: cheap per cached byte).
+ *
+ * Rotation. Pair i of a head's first rot channels (a, b), at position x, becomes
+ *     (a cos t - b sin t, a sin t + b cos t),   t = 2 pi x turns[i] / 2^64
+ * turns[i] is the pair's frequency in turns per token as a 64-bit fraction (for a
+ * frequency f in radians, round(2^64 f / 2 pi) modulo 2^64), so that the angle is as good
+ * at position 2^31 - 1 as at 0. Pairs are channels i and i + rot / 2 (neighbours = 0) or
+ * 2 i and 2 i + 1 (neighbours != 0). Positions may be negative.
+ */
+
+/*
+ * kda_kv_append with rotation: T tokens' queries are rotated into q_out, their keys
+ * rotated and their values copied to their slots.
+ *
+ *   q             : [T, Hq, d] of type io, token stride q_stride (in; Hq = 0: none)
+ *   k, v          : [T, Hkv, d], token strides k_stride, v_stride (in)
+ *   slot_map      : [T] (in) as for kda_kv_append; a token without a slot has its query
+ *                   rotated all the same
+ *   positions     : [T] (in);  turns : [rot / 2] (in), 8-byte aligned
+ *   k_cache, v_cache : [num_pages, Hkv, page_size, d] (in/out)
+ *   q_out         : [T, Hq, d], token stride q_out_stride (out); may be q itself (same
+ *                   stride), else may not overlap an input
+ *   rot           : a multiple of 16 in 16 .. d; channels from rot on are copied
+ *
+ * Strides at most 2^30 elements. The products are in fp32, rounded once. HBM-bound: each byte is read and
+ * written once.
+ */
+kda_status_t kda_kv_append_rope(const void* q, const void* k, const void* v, const int* slot_map,
+                                const int* positions, const long long* turns, void* k_cache,
+                                void* v_cache, void* q_out, int T, int Hq, int Hkv, int d, int rot,
+                                int neighbours, long long q_stride, long long k_stride,
+                                long long v_stride, long long q_out_stride, int num_pages,
+                                int page_size, kda_dtype_t io, int* d_status, void* stream);
+
+/*
+ * Write T tokens' latents and rotated key parts to their slots of a latent cache, and
+ * rotate their queries' part.
+ *
+ *   c        : [T, dl] of type io, token stride c_stride (in);  dl = 512
+ *   k_r      : [T, dr], token stride kr_stride (in);  dr = 64, or 0: none
+ *   q_r      : [T, Hq, dr] (in; Hq = 0: none), strides qr_stride between tokens and
+ *              qr_head between heads (e.g. the last channels of a projection's heads)
+ *   cache    : [num_pages, page_size, dl + dr] (in/out): a row is c, then rotated k_r
+ *   q_out    : [T, Hq, dr] (out), strides q_out_stride and q_out_head; may be q_r itself
+ *   k_out    : [T, dr] or NULL (out), token stride k_out_stride: the rotated k_r again,
+ *              for kda_attn_latent_prompt; may be k_r itself
+ *
+ * slot_map, positions, turns ([dr / 2]) and neighbours as for kda_kv_append_rope (positions
+ * and turns not read for dr = 0). Outputs may not overlap inputs otherwise. Token strides at
+ * most 2^30 elements. HBM-bound.
+ */
+kda_status_t kda_latent_append(const void* c, const void* k_r, const void* q_r, const int* slot_map,
+                               const int* positions, const long long* turns, void* cache,
+                               void* q_out, void* k_out, int T, int Hq, int dl, int dr,
+                               int neighbours, long long c_stride, long long kr_stride,
+                               long long qr_stride, long long qr_head, long long q_out_stride,
+                               long long q_out_head, long long k_out_stride, int num_pages,
+                               int page_size, kda_dtype_t io, int* d_status, void* stream);
+
+/*
+ * Causal attention of each request's last tokens over its paged latent cache (absorbed
+ * form): with c_j the cached rows,
+ *     p_ij = softmax_j(scale q_i . c_j),   o_i = sum_j p_ij c_j[0 .. dl - 1]
+ * for every head of token i.
+ *
+ *   q      : [total_q, Hq, dl + dr] of type io (in), strides q_stride between tokens and
+ *            q_head between heads, in either order; rotated where the cache's rows are
+ *   cache  : [num_pages, page_size, dl + dr] of type io (in);  dl = 512, dr = 0 or 64
+ *   o      : [total_q, Hq, dl] of type io, contiguous (out)
+ *   lse    : [total_q, Hq] fp32 or NULL (out)
+ *   scale  : positive and finite; the caller's (that of the expanded heads)
+ *
+ * Requests, lengths, pages, rows that see nothing, NaN and Inf, and arithmetic as for
+ * kda_attn_paged. A row of the cache counts as a key and as a value: what is not finite in it
+ * reaches every row that sees it and no other. Any number of heads up to 65536: more than 64
+ * are taken in blocks of equal size (prime numbers of heads beyond 64 one by one).
+ */
+kda_status_t kda_attn_latent_paged(const void* q, const void* cache, const int* block_table,
+                                   const int* cu_q, const int* kv_len, void* o, float* lse, int N,
+                                   int total_q, int max_q, int Hq, int dl, int dr,
+                                   long long q_stride, long long q_head, int num_pages,
+                                   int page_size, int max_pages, float scale, kda_dtype_t io,
+                                   void* workspace, size_t ws_bytes, int* d_status, void* stream);
+
+/*
+ * Causal attention over N packed prompts whose heads' keys and values were expanded from
+ * the latents (expanded form): as kda_attn_prompt with a key head for each of H heads and
+ *     q_i . k_j = (first d channels of q) . k_j + (its last dr) . k_r,j
+ *
+ *   q    : [total, H, d + dr] of type io (in);  d = 128, dr = 0 or 64
+ *   k, v : [total, H, d] (in; e.g. both halves of one projection's heads)
+ *   k_r  : [total, dr] (in), token stride kr_stride: rotated key channels that all heads
+ *          share (kda_latent_append's k_out); not read for dr = 0
+ *   o    : [total, H, d] of type io, contiguous (out);  lse : [total, H] fp32 or NULL (out)
+ *
+ * q, k and v have token and head strides (x_stride, x_head) in either order; all strides
+ * are multiples of 16 bytes, token strides at most 2^30 elements. scale: positive and
+ * finite, e.g. 1 / sqrt(d + dr). Workspace: that of kda_attn_workspace_size(N, total,
+ * max_len, H, H, d, io). The rest as for kda_attn_prompt.
+ */
+kda_status_t kda_attn_latent_prompt(const void* q, const void* k, const void* k_r, const void* v,
+                                    const int* cu_seqlens, void* o, float* lse, int N, int total,
+                                    int max_len, int H, int d, int dr, long long q_stride,
+                                    long long q_head, long long k_stride, long long k_head,
+                                    long long kr_stride, long long v_stride, long long v_head,
+                                    float scale, kda_dtype_t io, void* workspace, size_t ws_bytes,
+                                    int* d_status, void* stream);
+
+/* Requests of at most this many keys (max_pages * page_size; half of it for KDA_F32) are
+ * never split by kda_attn_latent_paged: those calls need no workspace. */
+#define KDA_LATENT_SHORT_KEYS 256
+
+/* As kda_attn_workspace_size, for kda_attn_latent_paged. */
+size_t kda_attn_latent_workspace_size(int N, int total_q, int max_q, int Hq, int dl, int dr,
+                                      kda_dtype_t io);
 
 #ifdef __cplusplus
 }
