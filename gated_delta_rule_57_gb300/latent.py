@@ -1,0 +1,210 @@
+"""Binding of the calls for rotation by position and for layers that keep one latent
+vector a token (``include/kda.h``): argument marshalling only, as in ``kda.py``, whose
+conventions (streams, what a call makes, errors) hold here too.
+"""
+from __future__ import annotations
+
+import ctypes
+import fractions
+from typing import Optional
+
+import torch
+
+from . import kda as _k
+from .kda import KDA_ERR_INVALID_ARG, KDA_F32, KDA_LATENT_SHORT_KEYS, KdaError, lib
+
+_PI = fractions.Fraction("3.14159265358979323846264338327950288419716939937510582097494459")
+
+
+def kda_rope_turns(inv_freq, device="cuda"):
+    """Frequencies of the rotation's pairs, in radians per token (a sequence or
+    tensor of rot / 2 numbers, taken as they are in 64 bits, e.g. base ** (-2 i / rot)),
+    as the int64 tensor of 64-bit fractions of a turn that the appends take. Made
+    once, on the host."""
+    if isinstance(inv_freq, torch.Tensor):
+        inv_freq = inv_freq.detach().double().reshape(-1).tolist()
+    turns = [round(fractions.Fraction(float(f)) * 2 ** 63 / _PI) % 2 ** 64 for f in inv_freq]
+    return torch.tensor([t - 2 ** 64 if t >= 2 ** 63 else t for t in turns], dtype=torch.int64, device=device)
+
+
+def _address(t: torch.Tensor):
+    if not t.is_cuda:
+        raise ValueError("KDA tensors must live on a CUDA device")
+    return t.data_ptr()
+
+
+def _heads(name: str, t: torch.Tensor, shape, dtype):
+    """Address, token and head stride of a [T, H, d] tensor whose channels are contiguous."""
+    if t.shape != shape or t.dtype != dtype:
+        raise ValueError(f"{name} must be {list(shape)} of {dtype}")
+    T, H, d = shape
+    st, sh, sd = t.stride()
+    if d > 1 and sd != 1:
+        raise ValueError(f"{name}: the channels of a head must be contiguous")
+    if H <= 1:
+        sh = d
+    return _address(t), st if T > 1 else max(H, 1) * sh, sh
+
+
+def _turns(turns, positions, T):
+    """Addresses of the rotation's frequencies and the tokens' positions, and rot."""
+    if turns.dtype != torch.int64 or turns.dim() != 1:
+        raise ValueError("turns must be an int64 tensor [rot / 2], as kda_rope_turns makes it")
+    if positions.dtype != torch.int32 or positions.dim() != 1 or positions.numel() < T:
+        raise ValueError("positions must be an int32 tensor with an entry per token")
+    return _k._ptr(turns), _k._ptr(positions), 2 * turns.numel()
+
+
+def _slots(slot_map, T):
+    if slot_map.dtype != torch.int32 or slot_map.dim() != 1 or slot_map.numel() < T:
+        raise ValueError("slot_map must be an int32 tensor with an entry per token")
+    return _k._ptr(slot_map)
+
+
+def kda_kv_append_rope(q, k, v, slot_map, positions, turns, k_cache, v_cache, *,
+                       neighbours: bool = False, q_out=None, status: Optional[torch.Tensor] = None,
+                       stream=None):
+    """kda_kv_append with rotation by position: q [T, Hq, d] is rotated into q_out (made
+    here when not given; q itself: in place), k rotated and v copied to their slots.
+    positions: [T] int32; turns: see kda_rope_turns (its length is rot / 2; channels from
+    rot on are copied); neighbours: pairs are channels 2 i, 2 i + 1 instead of i,
+    i + rot / 2. q may be None. Returns q_out."""
+    pages, Hkv, page, d = k_cache.shape
+    T = k.shape[0]
+    io = _k._DTYPE.get(k.dtype)
+    if io is None:
+        raise TypeError(f"unsupported k dtype {k.dtype}")
+    if k.shape != (T, Hkv, d) or v.shape != k.shape or v_cache.shape != k_cache.shape or \
+            k_cache.dtype != k.dtype or v_cache.dtype != k.dtype:
+        raise ValueError("k, v [T, Hkv, d] and the caches must agree in shape and dtype")
+    qp = op = None
+    Hq = qs = os_ = 0
+    if q is not None:
+        Hq = q.shape[1]
+        if q.shape != (T, Hq, d):
+            raise ValueError("q must be [T, Hq, d] with k's T and d")
+        qp, qs = _k._rows("q", q, k.dtype)
+        if q_out is None:
+            q_out = _k._empty((T, Hq, d), q.dtype, q, stream)
+        elif q_out.shape != q.shape:
+            raise ValueError("q_out must have q's shape")
+        op, os_ = _k._rows("q_out", q_out, k.dtype)
+    kp, ks = _k._rows("k", k)
+    vp, vs = _k._rows("v", v, k.dtype)
+    tp, pp, rot = _turns(turns, positions, T)
+    _k._check((_k._lib or lib()).kda_kv_append_rope(
+        qp, kp, vp, _slots(slot_map, T), pp, tp, _k._ptr(k_cache), _k._ptr(v_cache), op, T, Hq, Hkv, d, rot,
+        int(neighbours), qs, ks, vs, os_, pages, page, io, _k._ptr(status), _k._stream(stream)))
+    return q_out
+
+
+def kda_latent_append(c, k_r, slot_map, cache, *, positions=None, turns=None, q_r=None, q_out=None,
+                      k_out=None, neighbours: bool = False, status: Optional[torch.Tensor] = None,
+                      stream=None):
+    """Write the latents c [T, 512] and the rotated key parts k_r [T, 64] (None: a
+    layer without) of T tokens to the slots slot_map [T] of cache [num_pages,
+    page_size, 512 or 576], in place; rotate the queries' part q_r [T, Hq, 64] (a view
+    of any strides) into q_out (made here when not given; q_r itself: in place) and write
+    the rotated key part to k_out [T, 64] too where one is given. positions, turns and
+    neighbours as for kda_kv_append_rope. Returns q_out (None without q_r)."""
+    pages, page, dc = cache.shape
+    T, dl = c.shape
+    io = _k._DTYPE.get(c.dtype)
+    if io is None:
+        raise TypeError(f"unsupported c dtype {c.dtype}")
+    dr = 0 if k_r is None else k_r.shape[1]
+    if dc != dl + dr or cache.dtype != c.dtype:
+        raise ValueError("cache must be [num_pages, page_size, dl + dr] of c's dtype")
+    if k_r is None and (q_r is not None or k_out is not None):
+        raise ValueError("without k_r there are no q_r and k_out")
+    cp, cs, _ = _heads("c", c[:, None], (T, 1, dl), c.dtype)
+    kp = qp = op = kop = tp = pp = None
+    ks = qs = qh = os_ = oh = kos = Hq = 0
+    if k_r is not None:
+        kp, ks, _ = _heads("k_r", k_r[:, None], (T, 1, dr), c.dtype)
+        if turns is None or positions is None:
+            raise ValueError("k_r needs positions and turns")
+        tp, pp, rot = _turns(turns, positions, T)
+        if rot != dr:
+            raise ValueError("turns must have an entry per pair of k_r's channels")
+        if k_out is not None:
+            kop, kos, _ = _heads("k_out", k_out[:, None], (T, 1, dr), c.dtype)
+        if q_r is not None:
+            Hq = q_r.shape[1]
+            qp, qs, qh = _heads("q_r", q_r, (T, Hq, dr), c.dtype)
+            if q_out is None:
+                q_out = _k._empty((T, Hq, dr), c.dtype, c, stream)
+            op, os_, oh = _heads("q_out", q_out, (T, Hq, dr), c.dtype)
+    _k._check((_k._lib or lib()).kda_latent_append(
+        cp, kp, qp, _slots(slot_map, T), pp, tp, _k._ptr(cache), op, kop, T, Hq, dl, dr, int(neighbours), cs, ks,
+        qs, qh, os_, oh, kos, pages, page, io, _k._ptr(status), _k._stream(stream)))
+    return q_out if q_r is not None else None
+
+
+def kda_attn_latent_workspace_size(N: int, total_q: int, max_q: int, Hq: int, dl: int = 512, dr: int = 64,
+                                   io: torch.dtype = torch.bfloat16) -> int:
+    n = lib().kda_attn_latent_workspace_size(N, total_q, max_q, Hq, dl, dr, _k._DTYPE[io])
+    if n == ctypes.c_size_t(-1).value:
+        raise KdaError(KDA_ERR_INVALID_ARG, "unsupported problem size")
+    return int(n)
+
+
+def kda_attn_latent_paged(q, cache, block_table, cu_q, kv_len, *, scale: float, max_q: Optional[int] = None,
+                          o=None, lse=None, want_lse: bool = True, workspace=None,
+                          status: Optional[torch.Tensor] = None, stream=None):
+    """Causal attention of each request's last tokens over its paged latent cache, in
+    the absorbed form: every head's keys are the cached rows, its values their first
+    512 channels. q: [T, Hq, 512 + dr] (a view of any token and head strides); cache:
+    [num_pages, page_size, 512 + dr]; block_table, cu_q, kv_len and max_q as for
+    kda_attn_paged; scale: that of the expanded heads, e.g. (128 + dr) ** -0.5.
+    Returns (o [T, Hq, 512], lse [T, Hq] or None)."""
+    T, Hq, d = q.shape
+    pages, page, dc = cache.shape
+    N, max_pages = block_table.shape
+    io = _k._DTYPE.get(q.dtype)
+    if io is None:
+        raise TypeError(f"unsupported q dtype {q.dtype}")
+    if dc != d or cache.dtype != q.dtype or d < 512:
+        raise ValueError("the cache must be [num_pages, page_size, 512 + dr] of q's channels and dtype")
+    most = T if max_q is None else max_q
+    o, lse = _k._attn_outputs(q, 512, o, lse, want_lse, stream)
+    if workspace is None and max_pages * page > KDA_LATENT_SHORT_KEYS // (2 if io == KDA_F32 else 1):
+        need = (_k._lib or lib()).kda_attn_latent_workspace_size(N, T, most, Hq, 512, d - 512, io)
+        if need != ctypes.c_size_t(-1).value and need:  # the call itself reports bad arguments
+            workspace = _k._empty(need, torch.uint8, q, stream, scratch=True)
+    ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    qp, qs, qh = _heads("q", q, (T, Hq, d), q.dtype)
+    _k._check((_k._lib or lib()).kda_attn_latent_paged(
+        qp, _k._ptr(cache), _k._ints("block_table", block_table, (N, max_pages)), _k._ints("cu_q", cu_q, (N + 1,)),
+        _k._ints("kv_len", kv_len, (N,)), _k._ptr(o), _k._ptr(lse), N, T, most, Hq, 512, d - 512, qs, qh, pages, page,
+        max_pages, scale, io, _k._ptr(workspace), ws_bytes, _k._ptr(status), _k._stream(stream)))
+    return o, lse
+
+
+def kda_attn_latent_prompt(q, k, k_r, v, cu_seqlens, *, max_len: Optional[int] = None,
+                           scale: Optional[float] = None, o=None, lse=None, want_lse: bool = True,
+                           workspace=None, status: Optional[torch.Tensor] = None, stream=None):
+    """Causal attention over packed prompts whose heads' keys and values were expanded
+    from the latents. q: [T, H, 128 + dr]; k, v: [T, H, 128]; k_r: [T, dr], the rotated
+    key channels that all heads share (None: dr = 0); views of any token and head
+    strides; cu_seqlens and max_len as for kda_attn_prompt; scale: None for
+    1 / sqrt(128 + dr). Returns (o [T, H, 128], lse [T, H] or None)."""
+    T, H, dq = q.shape
+    d = k.shape[-1]
+    N = cu_seqlens.numel() - 1
+    dr = 0 if k_r is None else k_r.shape[1]
+    if k.shape != (T, H, d) or v.shape != k.shape or dq != d + dr:
+        raise ValueError("q must be [T, H, d + dr], k and v [T, H, d]")
+    most = T if max_len is None else max_len
+    _, o, lse, workspace, ws_bytes = _k._attn_buffers(q, N, most, most, H, o, lse, want_lse, workspace, stream, d)
+    qp, qs, qh = _heads("q", q, (T, H, dq), q.dtype)
+    kp, ks, kh = _heads("k", k, (T, H, d), q.dtype)
+    vp, vs, vh = _heads("v", v, (T, H, d), q.dtype)
+    rp, rs = None, 0
+    if dr:
+        rp, rs, _ = _heads("k_r", k_r[:, None], (T, 1, dr), q.dtype)
+    _k._check((_k._lib or lib()).kda_attn_latent_prompt(
+        qp, kp, rp, vp, _k._ints("cu_seqlens", cu_seqlens, (N + 1,)), _k._ptr(o), _k._ptr(lse), N, T, most, H, d, dr, qs, qh,
+        ks, kh, rs, vs, vh, dq ** -0.5 if scale is None else scale, _k._DTYPE[q.dtype], _k._ptr(workspace), ws_bytes,
+        _k._ptr(status), _k._stream(stream)))
+    return o, lse

@@ -6,6 +6,7 @@ import torch
 
 import attn_ref
 import latent_ref
+import gated_delta_rule_57_gb300 as pkg
 from gated_delta_rule_57_gb300 import kda
 
 pytestmark = pytest.mark.gpu
@@ -44,7 +45,7 @@ def case(q_lens, kv_lens, hq, dr, page, io, seed=0, spare=0):
 
 def run(q, cache, table, cu, kv, q_lens, scale=0.07, **kw):
     status = ints([0])
-    o, lse = kda.kda_attn_latent_paged(q, cache, table, cu, kv, scale=scale, max_q=max(q_lens), status=status, **kw)
+    o, lse = pkg.kda_attn_latent_paged(q, cache, table, cu, kv, scale=scale, max_q=max(q_lens), status=status, **kw)
     torch.cuda.synchronize()
     return o, lse, int(status)
 

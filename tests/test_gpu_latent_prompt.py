@@ -4,6 +4,7 @@ import torch
 
 import attn_ref
 import latent_ref
+import gated_delta_rule_57_gb300 as pkg
 from gated_delta_rule_57_gb300 import kda
 
 pytestmark = pytest.mark.gpu
@@ -29,7 +30,7 @@ def case(lens, h, dr, io, seed=0):
 
 def run(q, k, k_r, v, cu, lens, **kw):
     status = ints([0])
-    o, lse = kda.kda_attn_latent_prompt(q, k, k_r, v, cu, max_len=max(lens), status=status, **kw)
+    o, lse = pkg.kda_attn_latent_prompt(q, k, k_r, v, cu, max_len=max(lens), status=status, **kw)
     torch.cuda.synchronize()
     return o, lse, int(status)
 

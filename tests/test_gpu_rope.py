@@ -3,6 +3,7 @@ import pytest
 import torch
 
 import latent_ref
+import gated_delta_rule_57_gb300 as pkg
 from gated_delta_rule_57_gb300 import kda
 
 pytestmark = pytest.mark.gpu
@@ -43,20 +44,20 @@ def test_kv_append_rope(io, neighbours, t, hq, hkv, d, rot, page):
     q, k, v = qkv.split([hq, hkv, hkv], 1)
     pos, freq = positions_of(t, g), latent_ref.frequencies(rot)
     slot, live = slots_of(t, pages, page, g)
-    turns, status = kda.kda_rope_turns(freq, device=DEV), ints([0])
+    turns, status = pkg.kda_rope_turns(freq, device=DEV), ints([0])
     (rk, sk), rv = latent_ref.rotate(k, pos, freq, neighbours), vc.clone()
     want, size = kc.double(), torch.zeros(kc.shape, dtype=torch.float64, device=DEV)
     for i, p, r in live:
         want[p, :, r], size[p, :, r], rv[p, :, r] = rk[i], sk[i], v[i]
     ref_q = latent_ref.rotate(q, pos, freq, neighbours)
-    out = kda.kda_kv_append_rope(q, k, v, slot, pos, turns, kc, vc, neighbours=neighbours, status=status)
+    out = pkg.kda_kv_append_rope(q, k, v, slot, pos, turns, kc, vc, neighbours=neighbours, status=status)
     torch.cuda.synchronize()
     latent_ref.check_rotated(out, ref_q)
     latent_ref.check_rotated(kc, (want, size))
     assert torch.equal(vc, rv)
     assert int(status) == (kda.KDA_DEV_PAGES if t > 4 else 0)
     # the queries in place, in the projection itself
-    back = kda.kda_kv_append_rope(q, k, v, slot, pos, turns, kc, vc, neighbours=neighbours, q_out=q)
+    back = pkg.kda_kv_append_rope(q, k, v, slot, pos, turns, kc, vc, neighbours=neighbours, q_out=q)
     torch.cuda.synchronize()
     assert back is q and torch.equal(q, out)
 
@@ -65,7 +66,7 @@ def test_append_without_queries():
     x = torch.randn(5, 2, 64, device=DEV)
     kc, vc = (torch.zeros(1, 2, 16, 64, device=DEV) for _ in range(2))
     i = torch.arange(5, dtype=torch.int32, device=DEV)
-    assert kda.kda_kv_append_rope(None, x, x, i, i, kda.kda_rope_turns(latent_ref.frequencies(64)), kc, vc) is None
+    assert pkg.kda_kv_append_rope(None, x, x, i, i, pkg.kda_rope_turns(latent_ref.frequencies(64)), kc, vc) is None
     torch.cuda.synchronize()
     latent_ref.check_rotated(kc[0, :, :5].transpose(0, 1), latent_ref.rotate(x, i, latent_ref.frequencies(64), False))
     assert torch.equal(vc[0, :, :5].transpose(0, 1), x) and not kc[0, :, 5:].any()
@@ -88,7 +89,7 @@ def test_latent_append(io, neighbours, t, hq, dr, page, order):
     kw = {}
     if dr:
         rk, sk = (x[:, 0] for x in latent_ref.rotate(k_r[:, None], pos, freq, neighbours))
-        kw = dict(positions=pos, turns=kda.kda_rope_turns(freq, device=DEV), k_out=torch.empty(t, 64, dtype=io, device=DEV))
+        kw = dict(positions=pos, turns=pkg.kda_rope_turns(freq, device=DEV), k_out=torch.empty(t, 64, dtype=io, device=DEV))
     for i, p, r in live:
         want[p, r, :512] = c[i].double()
         if dr:
@@ -99,7 +100,7 @@ def test_latent_append(io, neighbours, t, hq, dr, page, order):
         q = torch.zeros((t, hq, 576) if order == "token" else (hq, t, 576), dtype=io, device=DEV)
         q = q if order == "token" else q.transpose(0, 1)
         kw.update(q_r=q_r, q_out=q[..., 512:])
-    out = kda.kda_latent_append(c, k_r, slot, cache, neighbours=neighbours, status=status, **kw)
+    out = pkg.kda_latent_append(c, k_r, slot, cache, neighbours=neighbours, status=status, **kw)
     torch.cuda.synchronize()
     latent_ref.check_rotated(cache, (want, size))
     if dr:
@@ -108,7 +109,7 @@ def test_latent_append(io, neighbours, t, hq, dr, page, order):
         latent_ref.check_rotated(out, latent_ref.rotate(q_r, pos, freq, neighbours))
         assert not q[..., :512].any()
         # in place
-        kda.kda_latent_append(c, k_r, slot, cache, positions=pos, turns=kw["turns"], q_r=q_r, q_out=q_r, k_out=k_r, neighbours=neighbours)
+        pkg.kda_latent_append(c, k_r, slot, cache, positions=pos, turns=kw["turns"], q_r=q_r, q_out=q_r, k_out=k_r, neighbours=neighbours)
         torch.cuda.synchronize()
         assert torch.equal(q_r, out) and torch.equal(k_r, kw["k_out"])
     assert int(status) == (kda.KDA_DEV_PAGES if t > 4 else 0)
