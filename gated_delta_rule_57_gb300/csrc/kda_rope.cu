@@ -11,9 +11,9 @@
 // most) and of sincospif.
 //
 // A token's angles are turned into cos and sin once (rot / 2 pairs, a thread each) and
-// kept in shared memory for all its heads. The token's work is laid out as items of one
-// 16-byte vector, or two where a pair's halves lie in different vectors; a thread keeps
-// the cos and sin of its item in registers while its next item has the same channels.
+// kept in shared memory for all its heads, while the token's first loads are on their
+// way. The token's work is laid out as items of one 16-byte vector, or two where a
+// pair's halves lie in different vectors, a few for each of its threads.
 // Bound by HBM: every byte is read and written once.
 #include "kda_host.cuh"
 #include "kda_internal.cuh"
@@ -45,7 +45,7 @@ struct RopeParams {
     int pairs;             // rot / 2
     int turned, items;     // items of a head of q or k: turned ones, all
     uint32_t items_magic, v_magic;  // of the divisions by items and v_vec
-    int half;              // vectors between a pair's halves; 0: pairs are neighbours
+    int neighbours;        // pairs are neighbours, not halves
     int tpt_log2;          // threads of a token
     long long slots;
     int page;
@@ -92,125 +92,109 @@ struct Vec {
     }
 };
 
-template <typename T>
-__global__ void __launch_bounds__(kRopeThreads) kda_rope_kernel(const RopeParams p) {
+// HALVES: a pair's channels are rot / 2 apart, else neighbours.
+template <typename T, bool HALVES>
+__global__ void __launch_bounds__(kRopeThreads, 4) kda_rope_kernel(const RopeParams p) {
     constexpr int N = Vec<T>::N;
-    // cos and sin of the tokens' pairs (a token has at least 32 threads)
-    __shared__ __align__(16) float2 s_cs[kRopeThreads / 32][kRopeMaxRot / 2];
+    constexpr int PP = HALVES ? N : N / 2;  // pairs of a turned item
+    // cos and sin of the tokens' pairs (a token has at least 32 threads): two pairs a
+    // vector, vector c of item i at c * turned + i, so that neighbouring lanes read
+    // neighbouring vectors.
+    __shared__ float4 s_cs[kRopeThreads / 32][kRopeMaxRot / 4];
     pdl_wait();
     const int tpt = 1 << p.tpt_log2;
     const int sub = threadIdx.x >> p.tpt_log2, i0 = threadIdx.x & (tpt - 1);
     const long long t64 = (long long)blockIdx.x * (kRopeThreads >> p.tpt_log2) + sub;
     const bool live = t64 < p.T;
     const int t = live ? (int)t64 : 0;
-    int flags = 0;
     const int slot = p.slot[t];
-    const bool stored = live && slot >= 0 && slot < p.slots;
-    if (live && slot >= p.slots) flags = KDA_DEV_PAGES;
-    const int id = stored ? slot / p.page : 0, off = stored ? slot - id * p.page : 0;
-    const long long at = id * p.c_page + off * p.c_row;
-    if (p.pairs > 0) {
+    const int half = HALVES ? p.turned : 0;  // vectors between a pair's halves
+    // Items 0 .. nqk - 1: of queries and keys, a head after the other. A turned one i of a
+    // head has vectors i and i + half, the others copy one vector. Then values.
+    const int nqk = (p.Hq + p.Hk) * p.items, n = live ? nqk + p.Hv * p.v_vec : 0;
+    uint4 a[kRopeBatch], b[kRopeBatch];
+    auto load = [&](int e0) {
+#pragma unroll
+        for (int j = 0; j < kRopeBatch; j++) {
+            const int e = e0 + j * tpt;
+            if (e < nqk) {
+                const int h = divide(e, p.items_magic), i = e - h * p.items;
+                const uint4* src = h >= p.Hq ? p.k.p + t * p.k.tok + (h - p.Hq) * p.k.head
+                                             : p.q.p + t * p.q.tok + h * p.q.head;
+                src += i < p.turned ? i : i + half;  // (what is copied follows both halves)
+                a[j] = __ldcs(src);
+                if (HALVES && i < p.turned) b[j] = __ldcs(src + half);
+            } else if (e < n) {
+                a[j] = __ldcs(p.v.p + t * p.v.tok + (e - nqk));
+            }
+        }
+    };
+    load(live ? i0 : n);
+    if (p.pairs > 0) {  // while they are on their way
         const unsigned long long pos = (unsigned long long)(long long)p.pos[t];
         for (int i = i0; i < p.pairs; i += tpt) {
             const unsigned long long turn = pos * (unsigned long long)p.turns[i];
             float s, c;
             sincospif((float)(int)(turn >> 32) * 0x1p-31f, &s, &c);
-            s_cs[sub][i] = make_float2(c, s);
+            const int u = i / PP, w = i % PP;
+            reinterpret_cast<float2*>(&s_cs[sub][(w >> 1) * p.turned + u])[w & 1] = make_float2(c, s);
         }
         __syncthreads();
     }
-    if (!live) return;
-    // Queries and keys. A turned item i of a head: vectors i and i + half (halves), or
-    // vector i (neighbours); the others copy one vector.
-    const int n = (p.Hq + p.Hk) * p.items;
-    int have = -1;
-    float2 cs[N];
-    for (int e0 = i0; e0 < n; e0 += tpt * kRopeBatch) {
-        uint4 a[kRopeBatch], b[kRopeBatch];
+    const bool stored = live && slot >= 0 && slot < p.slots;
+    const int id = stored ? slot / p.page : 0, off = stored ? slot - id * p.page : 0;
+    const long long at = id * p.c_page + off * p.c_row;
+    for (int e0 = i0; e0 < n;) {
 #pragma unroll
         for (int j = 0; j < kRopeBatch; j++) {
             const int e = e0 + j * tpt;
             if (e >= n) continue;
+            if (e >= nqk) {
+                const int v = e - nqk, h = divide(v, p.v_magic);
+                if (stored) p.v_cache[at + h * p.c_head + (v - h * p.v_vec)] = a[j];
+                continue;
+            }
             const int h = divide(e, p.items_magic), i = e - h * p.items;
-            const bool key = h >= p.Hq;
-            if (key && !stored && !p.k_out.p) continue;
-            const uint4* src = key ? p.k.p + t * p.k.tok + (h - p.Hq) * p.k.head
-                                   : p.q.p + t * p.q.tok + h * p.q.head;
-            const int x = i < p.turned ? i : i + p.half;  // (what is copied follows both halves)
-            a[j] = __ldcs(src + x);
-            if (p.half && i < p.turned) b[j] = __ldcs(src + x + p.half);
-        }
+            const bool turned = i < p.turned;
+            if (turned) {
+                const float4* cs = &s_cs[sub][i];
+                Vec<T> u(a[j]), w(HALVES ? b[j] : a[j]);
 #pragma unroll
-        for (int j = 0; j < kRopeBatch; j++) {
-            const int e = e0 + j * tpt;
-            if (e >= n) continue;
-            const int h = divide(e, p.items_magic), i = e - h * p.items;
-            const bool key = h >= p.Hq;
-            if (key && !stored && !p.k_out.p) continue;
-            const int x = i < p.turned ? i : i + p.half;
-            const bool two = p.half && i < p.turned;
-            if (i < p.turned) {
-                Vec<T> u(a[j]);
-                if (p.half) {
-                    if (have != i) {
-#pragma unroll
-                        for (int c = 0; c < N; c++) cs[c] = s_cs[sub][i * N + c];
-                        have = i;
-                    }
-                    Vec<T> w(b[j]);
-#pragma unroll
-                    for (int c = 0; c < N; c++) {
-                        const float ua = u.x[c], ub = w.x[c];
-                        u.x[c] = ua * cs[c].x - ub * cs[c].y;
-                        w.x[c] = ua * cs[c].y + ub * cs[c].x;
-                    }
-                    b[j] = w.pack();
-                } else {
-                    if (have != i) {
-#pragma unroll
-                        for (int c = 0; c < N / 2; c++) cs[c] = s_cs[sub][i * (N / 2) + c];
-                        have = i;
-                    }
-#pragma unroll
-                    for (int c = 0; c < N; c += 2) {
-                        const float ua = u.x[c], ub = u.x[c + 1];
-                        u.x[c] = ua * cs[c / 2].x - ub * cs[c / 2].y;
-                        u.x[c + 1] = ua * cs[c / 2].y + ub * cs[c / 2].x;
+                for (int c = 0; c < PP; c += 2) {
+                    const float4 x = cs[(c >> 1) * p.turned];
+                    if (HALVES) {
+                        const float a0 = u.x[c], a1 = u.x[c + 1], b0 = w.x[c], b1 = w.x[c + 1];
+                        u.x[c] = a0 * x.x - b0 * x.y;
+                        w.x[c] = a0 * x.y + b0 * x.x;
+                        u.x[c + 1] = a1 * x.z - b1 * x.w;
+                        w.x[c + 1] = a1 * x.w + b1 * x.z;
+                    } else {
+                        const float a0 = w.x[2 * c], b0 = w.x[2 * c + 1], a1 = w.x[2 * c + 2], b1 = w.x[2 * c + 3];
+                        u.x[2 * c] = a0 * x.x - b0 * x.y;
+                        u.x[2 * c + 1] = a0 * x.y + b0 * x.x;
+                        u.x[2 * c + 2] = a1 * x.z - b1 * x.w;
+                        u.x[2 * c + 3] = a1 * x.w + b1 * x.z;
                     }
                 }
                 a[j] = u.pack();
+                if (HALVES) b[j] = w.pack();
             }
             auto put = [&](uint4* dst) {
-                dst[x] = a[j];
-                if (two) dst[x + p.half] = b[j];
+                dst += turned ? i : i + half;
+                *dst = a[j];
+                if (HALVES && turned) dst[half] = b[j];
             };
-            if (key) {
+            if (h < p.Hq) {
+                put(p.q_out.p + t * p.q_out.tok + h * p.q_out.head);
+            } else {
                 if (stored) put(p.k_cache + at + (h - p.Hq) * p.c_head + p.k_at);
                 if (p.k_out.p) put(p.k_out.p + t * p.k_out.tok + (h - p.Hq) * p.k_out.head);
-            } else {
-                put(p.q_out.p + t * p.q_out.tok + h * p.q_out.head);
             }
         }
+        e0 += tpt * kRopeBatch;
+        load(e0);
     }
-    // Values (or the latent) are copied.
-    if (stored) {
-        const int nv = p.Hv * p.v_vec;
-        const uint4* src = p.v.p + t * p.v.tok;
-        for (int e0 = i0; e0 < nv; e0 += tpt * kRopeBatch) {
-            uint4 a[kRopeBatch];
-#pragma unroll
-            for (int j = 0; j < kRopeBatch; j++)
-                if (e0 + j * tpt < nv) a[j] = __ldcs(src + e0 + j * tpt);
-#pragma unroll
-            for (int j = 0; j < kRopeBatch; j++) {
-                const int e = e0 + j * tpt;
-                if (e >= nv) continue;
-                const int h = divide(e, p.v_magic);
-                p.v_cache[at + h * p.c_head + (e - h * p.v_vec)] = a[j];
-            }
-        }
-    }
-    report_flags(p.d_status, flags);
+    report_flags(p.d_status, live && slot >= p.slots ? KDA_DEV_PAGES : 0);
 }
 
 // Rows of one tensor: row t starts at p + t * stride bytes and has `row` bytes.
@@ -238,15 +222,16 @@ cudaError_t launch_rope(RopeParams& p, kda_dtype_t io, cudaStream_t stream) {
     p.v_magic = magic_of(p.v_vec);
     const int per = kRopeThreads >> p.tpt_log2;
     const dim3 grid((unsigned)((p.T + per - 1) / per));
-    return io == KDA_BF16
-               ? launch_dependent(kda_rope_kernel<__nv_bfloat16>, grid, dim3(kRopeThreads), 0, stream, p)
-               : launch_dependent(kda_rope_kernel<float>, grid, dim3(kRopeThreads), 0, stream, p);
+    auto kernel = io == KDA_BF16
+                      ? (p.neighbours ? kda_rope_kernel<__nv_bfloat16, false> : kda_rope_kernel<__nv_bfloat16, true>)
+                      : (p.neighbours ? kda_rope_kernel<float, false> : kda_rope_kernel<float, true>);
+    return launch_dependent(kernel, grid, dim3(kRopeThreads), 0, stream, p);
 }
 
 // Items of a head of d channels of which the first rot are turned; V channels a vector.
 void head_items(RopeParams* p, int d, int rot, int neighbours, int V) {
     p->pairs = rot / 2;
-    p->half = neighbours ? 0 : rot / 2 / V;
+    p->neighbours = neighbours != 0;
     p->turned = neighbours ? rot / V : rot / 2 / V;
     p->items = p->turned + (d - rot) / V;
 }

@@ -33,32 +33,47 @@ def _address(t: torch.Tensor):
     return t.data_ptr()
 
 
-def _heads(name: str, t: torch.Tensor, shape, dtype):
+def _heads(name: str, t: torch.Tensor, T, H, d, dtype):
     """Address, token and head stride of a [T, H, d] tensor whose channels are contiguous."""
-    if t.shape != shape or t.dtype != dtype:
-        raise ValueError(f"{name} must be {list(shape)} of {dtype}")
-    T, H, d = shape
+    if t.shape != (T, H, d) or t.dtype != dtype:
+        raise ValueError(f"{name} must be [{T}, {H}, {d}] of {dtype}")
     st, sh, sd = t.stride()
-    if d > 1 and sd != 1:
+    if sd != 1 and d > 1:
         raise ValueError(f"{name}: the channels of a head must be contiguous")
     if H <= 1:
         sh = d
     return _address(t), st if T > 1 else max(H, 1) * sh, sh
 
 
-def _turns(turns, positions, T):
-    """Addresses of the rotation's frequencies and the tokens' positions, and rot."""
+def _packed(name: str, t: torch.Tensor, T, H, d, dtype):
+    """Address and token stride of a [T, H, d] tensor whose heads are contiguous."""
+    p, st, sh = _heads(name, t, T, H, d, dtype)
+    if sh != d:
+        raise ValueError(f"{name}: the heads of a token must be contiguous")
+    return p, st
+
+
+def _flat(name: str, t: torch.Tensor, T, d, dtype):
+    """Address and token stride of a [T, d] tensor whose channels are contiguous."""
+    if t.shape != (T, d) or t.dtype != dtype:
+        raise ValueError(f"{name} must be [{T}, {d}] of {dtype}")
+    st, sd = t.stride()
+    if sd != 1 and d > 1:
+        raise ValueError(f"{name}: the channels of a token must be contiguous")
+    return _address(t), st if T > 1 else d
+
+
+def _per_token(name: str, t: torch.Tensor, T):
+    """Address of an int32 tensor with an entry for each of T tokens, or more."""
+    if t.dtype != torch.int32 or t.dim() != 1 or t.numel() < T:
+        raise ValueError(f"{name} must be an int32 tensor with an entry per token")
+    return _k._ptr(t)
+
+
+def _turns(turns: torch.Tensor):
     if turns.dtype != torch.int64 or turns.dim() != 1:
         raise ValueError("turns must be an int64 tensor [rot / 2], as kda_rope_turns makes it")
-    if positions.dtype != torch.int32 or positions.dim() != 1 or positions.numel() < T:
-        raise ValueError("positions must be an int32 tensor with an entry per token")
-    return _k._ptr(turns), _k._ptr(positions), 2 * turns.numel()
-
-
-def _slots(slot_map, T):
-    if slot_map.dtype != torch.int32 or slot_map.dim() != 1 or slot_map.numel() < T:
-        raise ValueError("slot_map must be an int32 tensor with an entry per token")
-    return _k._ptr(slot_map)
+    return _k._ptr(turns)
 
 
 def kda_kv_append_rope(q, k, v, slot_map, positions, turns, k_cache, v_cache, *,
@@ -70,31 +85,31 @@ def kda_kv_append_rope(q, k, v, slot_map, positions, turns, k_cache, v_cache, *,
     rot on are copied); neighbours: pairs are channels 2 i, 2 i + 1 instead of i,
     i + rot / 2. q may be None. Returns q_out."""
     pages, Hkv, page, d = k_cache.shape
-    T = k.shape[0]
-    io = _k._DTYPE.get(k.dtype)
+    dt = k.dtype
+    io = _k._DTYPE.get(dt)
     if io is None:
-        raise TypeError(f"unsupported k dtype {k.dtype}")
-    if k.shape != (T, Hkv, d) or v.shape != k.shape or v_cache.shape != k_cache.shape or \
-            k_cache.dtype != k.dtype or v_cache.dtype != k.dtype:
-        raise ValueError("k, v [T, Hkv, d] and the caches must agree in shape and dtype")
+        raise TypeError(f"unsupported k dtype {dt}")
+    T = k.shape[0]
+    if v_cache.shape != k_cache.shape or k_cache.dtype != dt or v_cache.dtype != dt:
+        raise ValueError("the caches must be [num_pages, Hkv, page_size, d] of k's dtype")
     qp = op = None
     Hq = qs = os_ = 0
     if q is not None:
         Hq = q.shape[1]
-        if q.shape != (T, Hq, d):
-            raise ValueError("q must be [T, Hq, d] with k's T and d")
-        qp, qs = _k._rows("q", q, k.dtype)
+        qp, qs = _packed("q", q, T, Hq, d, dt)
         if q_out is None:
-            q_out = _k._empty((T, Hq, d), q.dtype, q, stream)
-        elif q_out.shape != q.shape:
-            raise ValueError("q_out must have q's shape")
-        op, os_ = _k._rows("q_out", q_out, k.dtype)
-    kp, ks = _k._rows("k", k)
-    vp, vs = _k._rows("v", v, k.dtype)
-    tp, pp, rot = _turns(turns, positions, T)
-    _k._check((_k._lib or lib()).kda_kv_append_rope(
-        qp, kp, vp, _slots(slot_map, T), pp, tp, _k._ptr(k_cache), _k._ptr(v_cache), op, T, Hq, Hkv, d, rot,
-        int(neighbours), qs, ks, vs, os_, pages, page, io, _k._ptr(status), _k._stream(stream)))
+            q_out = _k._empty((T, Hq, d), dt, q, stream)
+            op, os_ = q_out.data_ptr(), Hq * d
+        else:
+            op, os_ = _packed("q_out", q_out, T, Hq, d, dt)
+    kp, ks = _packed("k", k, T, Hkv, d, dt)
+    vp, vs = _packed("v", v, T, Hkv, d, dt)
+    code = (_k._lib or lib()).kda_kv_append_rope(
+        qp, kp, vp, _per_token("slot_map", slot_map, T), _per_token("positions", positions, T), _turns(turns),
+        _k._ptr(k_cache), _k._ptr(v_cache), op, T, Hq, Hkv, d, 2 * turns.numel(), neighbours, qs, ks, vs, os_, pages,
+        page, io, _k._ptr(status), _k._stream(stream))
+    if code:
+        _k._check(code)
     return q_out
 
 
@@ -109,35 +124,39 @@ def kda_latent_append(c, k_r, slot_map, cache, *, positions=None, turns=None, q_
     neighbours as for kda_kv_append_rope. Returns q_out (None without q_r)."""
     pages, page, dc = cache.shape
     T, dl = c.shape
-    io = _k._DTYPE.get(c.dtype)
+    dt = c.dtype
+    io = _k._DTYPE.get(dt)
     if io is None:
-        raise TypeError(f"unsupported c dtype {c.dtype}")
+        raise TypeError(f"unsupported c dtype {dt}")
     dr = 0 if k_r is None else k_r.shape[1]
-    if dc != dl + dr or cache.dtype != c.dtype:
+    if dc != dl + dr or cache.dtype != dt:
         raise ValueError("cache must be [num_pages, page_size, dl + dr] of c's dtype")
-    if k_r is None and (q_r is not None or k_out is not None):
-        raise ValueError("without k_r there are no q_r and k_out")
-    cp, cs, _ = _heads("c", c[:, None], (T, 1, dl), c.dtype)
+    cp, cs = _flat("c", c, T, dl, dt)
     kp = qp = op = kop = tp = pp = None
     ks = qs = qh = os_ = oh = kos = Hq = 0
-    if k_r is not None:
-        kp, ks, _ = _heads("k_r", k_r[:, None], (T, 1, dr), c.dtype)
+    if k_r is None:
+        if q_r is not None or k_out is not None:
+            raise ValueError("without k_r there are no q_r and k_out")
+    else:
         if turns is None or positions is None:
             raise ValueError("k_r needs positions and turns")
-        tp, pp, rot = _turns(turns, positions, T)
-        if rot != dr:
+        kp, ks = _flat("k_r", k_r, T, dr, dt)
+        tp, pp = _turns(turns), _per_token("positions", positions, T)
+        if 2 * turns.numel() != dr:
             raise ValueError("turns must have an entry per pair of k_r's channels")
         if k_out is not None:
-            kop, kos, _ = _heads("k_out", k_out[:, None], (T, 1, dr), c.dtype)
+            kop, kos = _flat("k_out", k_out, T, dr, dt)
         if q_r is not None:
             Hq = q_r.shape[1]
-            qp, qs, qh = _heads("q_r", q_r, (T, Hq, dr), c.dtype)
+            qp, qs, qh = _heads("q_r", q_r, T, Hq, dr, dt)
             if q_out is None:
-                q_out = _k._empty((T, Hq, dr), c.dtype, c, stream)
-            op, os_, oh = _heads("q_out", q_out, (T, Hq, dr), c.dtype)
-    _k._check((_k._lib or lib()).kda_latent_append(
-        cp, kp, qp, _slots(slot_map, T), pp, tp, _k._ptr(cache), op, kop, T, Hq, dl, dr, int(neighbours), cs, ks,
-        qs, qh, os_, oh, kos, pages, page, io, _k._ptr(status), _k._stream(stream)))
+                q_out = _k._empty((T, Hq, dr), dt, c, stream)
+            op, os_, oh = _heads("q_out", q_out, T, Hq, dr, dt)
+    code = (_k._lib or lib()).kda_latent_append(
+        cp, kp, qp, _per_token("slot_map", slot_map, T), pp, tp, _k._ptr(cache), op, kop, T, Hq, dl, dr, neighbours,
+        cs, ks, qs, qh, os_, oh, kos, pages, page, io, _k._ptr(status), _k._stream(stream))
+    if code:
+        _k._check(code)
     return q_out if q_r is not None else None
 
 
@@ -173,7 +192,7 @@ def kda_attn_latent_paged(q, cache, block_table, cu_q, kv_len, *, scale: float, 
         if need != ctypes.c_size_t(-1).value and need:  # the call itself reports bad arguments
             workspace = _k._empty(need, torch.uint8, q, stream, scratch=True)
     ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
-    qp, qs, qh = _heads("q", q, (T, Hq, d), q.dtype)
+    qp, qs, qh = _heads("q", q, T, Hq, d, q.dtype)
     _k._check((_k._lib or lib()).kda_attn_latent_paged(
         qp, _k._ptr(cache), _k._ints("block_table", block_table, (N, max_pages)), _k._ints("cu_q", cu_q, (N + 1,)),
         _k._ints("kv_len", kv_len, (N,)), _k._ptr(o), _k._ptr(lse), N, T, most, Hq, 512, d - 512, qs, qh, pages, page,
@@ -196,15 +215,14 @@ def kda_attn_latent_prompt(q, k, k_r, v, cu_seqlens, *, max_len: Optional[int] =
     if k.shape != (T, H, d) or v.shape != k.shape or dq != d + dr:
         raise ValueError("q must be [T, H, d + dr], k and v [T, H, d]")
     most = T if max_len is None else max_len
-    _, o, lse, workspace, ws_bytes = _k._attn_buffers(q, N, most, most, H, o, lse, want_lse, workspace, stream, d)
-    qp, qs, qh = _heads("q", q, (T, H, dq), q.dtype)
-    kp, ks, kh = _heads("k", k, (T, H, d), q.dtype)
-    vp, vs, vh = _heads("v", v, (T, H, d), q.dtype)
-    rp, rs = None, 0
-    if dr:
-        rp, rs, _ = _heads("k_r", k_r[:, None], (T, 1, dr), q.dtype)
+    io, o, lse, workspace, ws_bytes = _k._attn_buffers(q, N, most, most, H, o, lse, want_lse, workspace, stream, d)
+    dt = q.dtype
+    qp, qs, qh = _heads("q", q, T, H, dq, dt)
+    kp, ks, kh = _heads("k", k, T, H, d, dt)
+    vp, vs, vh = _heads("v", v, T, H, d, dt)
+    rp, rs = _flat("k_r", k_r, T, dr, dt) if dr else (None, 0)
     _k._check((_k._lib or lib()).kda_attn_latent_prompt(
         qp, kp, rp, vp, _k._ints("cu_seqlens", cu_seqlens, (N + 1,)), _k._ptr(o), _k._ptr(lse), N, T, most, H, d, dr, qs, qh,
-        ks, kh, rs, vs, vh, dq ** -0.5 if scale is None else scale, _k._DTYPE[q.dtype], _k._ptr(workspace), ws_bytes,
+        ks, kh, rs, vs, vh, dq ** -0.5 if scale is None else scale, io, _k._ptr(workspace), ws_bytes,
         _k._ptr(status), _k._stream(stream)))
     return o, lse
