@@ -292,7 +292,8 @@ AttnSplit attn_simt_split(int N, int total_q, int max_q, long long max_keys, boo
 // shared ones, its values the latent channels. k: the cache. Heads beyond a row tile are
 // taken in blocks of equal size, as if they had key heads.
 constexpr int kLatentDim = 512;
-constexpr int kLatentTcRows = 64, kLatentSimtRows = 32;  // rows of a row tile
+constexpr int kLatentSimtRows = 32;  // rows of a row tile
+inline int latent_tc_rows(int max_q, int Hq) { return (long long)max_q * Hq <= 32 ? 32 : 64; }
 inline int latent_head_blocks(int Hq, int rows) {
     int b = (Hq + rows - 1) / rows;
     while (Hq % b) b++;

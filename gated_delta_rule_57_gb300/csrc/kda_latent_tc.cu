@@ -17,11 +17,8 @@
 // One CTA per SM:
 //   warps 0..3  softmax, one row of S per thread (64-row accumulators use 16 lanes of
 //               each warp's 32), the results, and the edge (below)
-//   warp 4      issues the products
-//   warp 5      finds the work and issues the loads
-// A tile comes as units of 128 channels (and one of the rotated ones), two tiles in
-// flight. The first product takes units as they land; the second, when P is there, gives
-// them back. Whichever is ready is issued first.
+//   warps 4, 5  issue the first and the second products
+//   warp 6      finds the work and issues the loads
 //
 // A key past a row's last one gets P = 0 by a select on S. 0 x NaN is NaN, so before the
 // second product the softmax warps clear in shared memory what some rows must not see:
@@ -39,23 +36,27 @@ namespace {
 
 using namespace ptx;
 
-constexpr int kRows = kLatentTcRows, kKeys = 64, kThreadsTc = 192;
-constexpr int kMmaWarp = 4, kLoadWarp = 5;
+constexpr int kThreadsTc = 224;
+constexpr int kScoreWarp = 4, kOutWarp = 5, kLoadWarp = 6;
 constexpr int kDL = kLatentDim;
-constexpr int kBlock = 64 * 128;         // bytes of 64 rows x 64 channels
 constexpr int kUnits = kDL / 128;        // units of a tile's latents
-constexpr int kRing = 2 * kUnits;        // units in shared memory
 constexpr int kPieces = 4;               // pieces announced ahead
 constexpr int kItemKeys = 256;           // what an item costs beside its keys, in keys
 constexpr long long kWaitClocks = 1LL << 33;  // limit of a wait (about 4 s)
 constexpr float kRaise = 8.f;            // log2 growth of a row maximum that moves its reference
-constexpr uint32_t kTmO = 0, kTmS = kUnits * kRows;  // tensor-memory columns
+constexpr int kMaxTiles = 6;             // key tiles in shared memory, at most
 
-template <int DR>
+// RT rows of a row tile, KT keys of a key tile.
+template <int DR, int RT, int KT>
 struct TcCfg {
-    static constexpr int QBLOCKS = (kDL + DR) / 64;
-    static constexpr int Q = QBLOCKS * kBlock, RING = kRing * 2 * kBlock, ROPE = DR ? 2 * kBlock : 0;
-    static constexpr int TILES = Q + RING + ROPE + kBlock;  // and P
+    static constexpr int BLOCKS = (kDL + DR) / 64;             // of 64 channels, of a row
+    static constexpr int QBLOCK = RT * 128, KBLOCK = KT * 128;  // bytes of one
+    static constexpr int Q = BLOCKS * QBLOCK, TILE = BLOCKS * KBLOCK;
+    static constexpr int P = RT * 128;
+    static constexpr int NT = (225 * 1024 - Q - P) / TILE;      // key tiles in shared memory
+    static constexpr int TILES = Q + NT * TILE + P;
+    static constexpr uint32_t TM_O = 0, TM_S = kUnits * RT;     // tensor-memory columns
+    static_assert(NT >= 2 && NT <= kMaxTiles, "key tiles");
 };
 
 struct LatentTcParams {
@@ -81,36 +82,36 @@ struct Piece {
     int slot;        // where a part of an item goes; -1: the whole item
     int end;         // no more pieces
 };
+template <int KT>
 __device__ __forceinline__ int piece_tiles(const Piece& p) {
-    return max(min(p.kt1, (p.keys + kKeys - 1) / kKeys) - p.kt0, 0);
+    return max(min(p.kt1, (p.keys + KT - 1) / KT) - p.kt0, 0);
 }
 // Keys that every row of the item sees: those of its first token.
 __device__ __forceinline__ int seen_by_all(const Piece& p) { return min(max(p.pos0 + 1, 0), p.keys); }
 
 struct Shared {
-    uint64_t full[kRing], empty[kRing];
-    uint64_t rope_full[2], rope_empty[2];
-    uint64_t s_full[2], p_full, pv_done;
+    uint64_t full[kMaxTiles], empty[kMaxTiles];  // of each key tile in shared memory
+    uint64_t s_full[2], s_read[2], p_full, pv_done;
     uint64_t q_full, q_empty;
     uint64_t piece_full[kPieces], piece_empty[kPieces];
     uint64_t next_full;  // the number of the next whole item
-    uint64_t drained;    // all products have ended
+    uint64_t drained[2];  // all products of either kind have ended
     alignas(16) uint4 next;
     Piece pieces[kPieces];
-    alignas(16) float factor[kRows];  // of the rows: of a raised reference, then 1 / l
-    int row_at[kRows];     // row of o of the tile's rows, from its first
-    int lim[kRows];        // keys each row sees
+    alignas(16) float factor[64];  // of the rows: of a raised reference, then 1 / l
+    int row_at[64];        // row of o of the tile's rows, from its first
+    int lim[64];           // keys each row sees
     // Bit i: key seen_by_all + i has values that were cleared (of this piece, or the next).
     uint32_t odd[2][2];
     long long sum[kThreadsTc / 32];
     uint32_t tmem;
 };
-template <int DR>
+template <typename C>
 constexpr int tc_smem() {
-    return TcCfg<DR>::TILES + (int)sizeof(Shared);
+    static_assert(C::TILES + sizeof(Shared) <= 227 * 1024, "shared memory of a CTA");
+    static_assert(kAttnGroups * 8 <= C::P, "cost groups fit P's tile");
+    return C::TILES + (int)sizeof(Shared);
 }
-static_assert(tc_smem<64>() <= 227 * 1024, "shared memory of a CTA");
-static_assert(kAttnGroups * 8 <= kBlock, "cost groups fit P's tile");
 
 __device__ __forceinline__ float ex2(float x) {
     float y;
@@ -167,17 +168,17 @@ __device__ __forceinline__ uint32_t finite_pair(uint32_t x) {  // zeros for the 
     return x & ~((odd >> 15 & 0x00010001u) * 0xffffu);
 }
 
-template <int DR>
+template <int DR, int RT, int KT>
 __global__ void __launch_bounds__(kThreadsTc, 1)
     kda_latent_tc_kernel(const __grid_constant__ CUtensorMap map_q,
                          const __grid_constant__ CUtensorMap map_c,
                          const __grid_constant__ LatentTcParams p) {
-    using C = TcCfg<DR>;
+    using C = TcCfg<DR, RT, KT>;
+    constexpr int NT = C::NT;
     extern __shared__ __align__(1024) unsigned char sm[];  // 128-byte swizzle: 1024-byte tiles
     unsigned char* sq = sm;
-    unsigned char* sring = sm + C::Q;
-    unsigned char* srope = sring + C::RING;
-    unsigned char* sp = srope + C::ROPE;
+    unsigned char* skv = sm + C::Q;
+    unsigned char* sp = skv + NT * C::TILE;
     Shared& sh = *reinterpret_cast<Shared*>(sm + C::TILES);
     long long* groups = reinterpret_cast<long long*>(sp);  // before the first piece
     if (smem_addr(sm) & 1023u) {  // never, by the declaration above
@@ -188,18 +189,18 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
     const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);  // uniform, and known to be
     const int G = p.s.G, Hq = p.s.Hkv * G;
     if (warp == kLoadWarp) {
-        if (lane < kRing) {
+        if (lane < NT) {
             mbar_init(&sh.full[lane], 1);
             mbar_init(&sh.empty[lane], 1);
         }
         if (lane < 2) {
-            mbar_init(&sh.rope_full[lane], 1);
-            mbar_init(&sh.rope_empty[lane], 1);
             mbar_init(&sh.s_full[lane], 1);
+            mbar_init(&sh.s_read[lane], 4);
+            mbar_init(&sh.drained[lane], 1);
         }
         if (lane < kPieces) {
             mbar_init(&sh.piece_full[lane], 1);
-            mbar_init(&sh.piece_empty[lane], 5);  // softmax 4, products
+            mbar_init(&sh.piece_empty[lane], 6);  // softmax 4, products 2
         }
         if (lane == 0) {
             mbar_init(&sh.p_full, 128);
@@ -207,17 +208,16 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
             mbar_init(&sh.q_full, 1);
             mbar_init(&sh.q_empty, 1);
             mbar_init(&sh.next_full, 1);
-            mbar_init(&sh.drained, 1);
             prefetch_tensormap(&map_q);
             prefetch_tensormap(&map_c);
         }
         fence_mbarrier_init();
     }
-    if (warp == kMmaWarp) {
+    if (warp == kScoreWarp) {
         tmem_alloc(&sh.tmem, 512);
         tmem_relinquish();
     }
-    if (tid < kRows) sh.row_at[tid] = tid / G * Hq + tid % G;
+    if (tid < RT) sh.row_at[tid] = tid / G * Hq + tid % G;
     if (tid < 4) sh.odd[tid >> 1][tid & 1] = 0;
     tc_fence_before();
     pdl_wait();
@@ -232,16 +232,16 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
 
     if (warp == kLoadWarp) {
         // ------------------------------------------------------------ work and loads
-        int unit = 0, tile = 0, np = 0, nq = 0;  // units, tiles, pieces, row tiles so far
-        int asked = 0;                           // for further items
+        int tile = 0, slot = 0, phase = 0;  // key tiles so far; the next one's place
+        int np = 0, nq = 0;                 // pieces, row tiles so far
+        int asked = 0;                      // for further items
         bool q_pending = false;
         const int log2_page = __ffs(p.page) - 1;
-        const int per = p.page < kKeys ? kKeys >> log2_page : 1;  // pages of a tile
-        const int pg = lane & (per - 1), half = lane / per;
-        auto page_id = [&](const Piece& pc, int kt) {
+        const int log2_per = p.page < KT ? __ffs(KT) - 1 - log2_page : 0, per = 1 << log2_per;  // pages of a tile
+        auto page_id = [&](const Piece& pc, int kt) {  // of part `lane` of a tile
             int id = p.num_pages;  // past the keys, or no page: beyond the cache, which loads zeros
-            const int j = kt * kKeys + (pg << log2_page);
-            if (half < 2 && j < pc.kv) {
+            const int j = kt * KT + (lane << log2_page);
+            if (lane < per && j < pc.kv) {
                 id = p.block_table[(size_t)pc.r * p.max_pages + (j >> log2_page)];
                 if (id < 0 || id >= p.num_pages) {
                     id = p.num_pages;
@@ -251,14 +251,14 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
             return id;
         };
         auto load_q = [&](const Piece& pc) {
-            if (lane == 0) mbar_arrive_expect_tx(&sh.q_full, C::QBLOCKS * p.box_q * G * 128);
+            if (lane == 0) mbar_arrive_expect_tx(&sh.q_full, C::BLOCKS * p.box_q * G * 128);
             __syncwarp();
-            if (lane < C::QBLOCKS)
-                tma_load_3d(sq + lane * kBlock, &map_q, &sh.q_full, 64 * lane, pc.h * G, pc.tok0);
+            if (lane < C::BLOCKS)
+                tma_load_3d(sq + lane * C::QBLOCK, &map_q, &sh.q_full, 64 * lane, pc.h * G, pc.tok0);
             nq++;
             q_pending = false;
         };
-        // A free place of the ring; the rows of a new piece are loaded as soon as theirs is.
+        // A free place for a tile; the rows of a new piece are loaded as soon as theirs is.
         auto wait_place = [&](const Piece& pc, uint64_t* bar, uint32_t parity) {
             if (q_pending) {
                 const long long t0 = clock64();
@@ -270,13 +270,6 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
             }
             warp_wait(ok, bar, parity);
             return ok;
-        };
-        auto load = [&](unsigned char* dst, uint64_t* bar, int blocks, int ch, int kt, int id) {
-            if (lane == 0) mbar_arrive_expect_tx(bar, blocks * kBlock);
-            __syncwarp();
-            if (half < blocks)
-                tma_load_3d(dst + half * kBlock + (pg << log2_page) * 128, &map_c, bar,
-                            ch + 64 * half, (kt * kKeys) & (p.page - 1), id);
         };
         auto announce = [&](const Piece& pc) {
             const int i = np % kPieces;
@@ -291,27 +284,33 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
         };
         auto process = [&](const Piece& pc) {
             announce(pc);
-            const int n = piece_tiles(pc);
+            const int n = piece_tiles<KT>(pc);
             if (n == 0 || !ok) return;
             q_pending = true;
             int id = page_id(pc, pc.kt0);
-            for (int j = 0; j < n && ok; j++) {
+            for (int j = 0; j < n; j++) {
                 const int kt = pc.kt0 + j;
                 const int next_id = j + 1 < n ? page_id(pc, kt + 1) : 0;
-                if (DR) {
-                    const int s = tile & 1;
-                    if (!wait_place(pc, &sh.rope_empty[s], ((tile >> 1) & 1) ^ 1)) break;
-                    load(srope + s * kBlock, &sh.rope_full[s], 1, kDL, kt, id);
+                if (!wait_place(pc, &sh.empty[slot], phase ^ 1)) break;
+                if (lane == 0) mbar_arrive_expect_tx(&sh.full[slot], C::TILE);
+                __syncwarp();
+                // All blocks together, so that DRAM sees whole rows.
+                for (int i0 = 0; i0 < C::BLOCKS << log2_per; i0 += 32) {
+                    const int i = i0 + lane, blk = i >> log2_per, part = i & (per - 1);
+                    const int page = __shfl_sync(0xffffffffu, id, part);
+                    if (blk < C::BLOCKS)
+                        tma_load_3d(skv + slot * C::TILE + blk * C::KBLOCK + (part << log2_page) * 128, &map_c,
+                                    &sh.full[slot], 64 * blk, (kt * KT) & (p.page - 1), page);
                 }
                 tile++;
-                for (int u = 0; u < kUnits; u++, unit++) {
-                    const int s = unit % kRing;
-                    if (!wait_place(pc, &sh.empty[s], ((unit / kRing) & 1) ^ 1)) break;
-                    load(sring + s * 2 * kBlock, &sh.full[s], 2, 128 * u, kt, id);
+                if (++slot == NT) {
+                    slot = 0;
+                    phase ^= 1;
                 }
-                if (ok && q_pending) {
+                if (q_pending) {
                     warp_wait(ok, &sh.q_empty, (nq & 1) ^ 1);
-                    if (ok) load_q(pc);
+                    if (!ok) break;
+                    load_q(pc);
                 }
                 id = next_id;
             }
@@ -351,7 +350,7 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
             have = attn_first_tile(p.s, walk, &cur, &r, &q, &h, &t, &first) && cur < end;
             start = cur;
             if (have) {
-                cut.cost = q.cost * kKeys;
+                cut.cost = q.cost * KT;
                 cut.u0 = cur - (long long)first * cut.cost;
                 cut.tok0 = q.q0 + t * q.tok;
                 cut.ntok = min(q.tok, q.q_len - t * q.tok);
@@ -384,7 +383,7 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
                 Piece pc = piece_of(r, q, h, t);
                 if (split) {
                     const int n = pc.kt1;
-                    const long long u0 = cur - (long long)first * q.cost * kKeys;
+                    const long long u0 = cur - (long long)first * q.cost * KT;
                     pc.kt0 = first;
                     pc.kt1 = attn_tiles_until(p.s, q, u0, n, end);
                     if (pc.kt1 - pc.kt0 < n) pc.slot = 2 * blockIdx.x + (cur > start ? 1 : 0);
@@ -423,133 +422,97 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
         if (!ok) {
             flags |= KDA_DEV_TIMEOUT;
             // copies in flight land before the CTA leaves
-            for (int i = max(unit - kRing, 0); i < unit; i++)
-                mbar_wait(&sh.full[i % kRing], (i / kRing) & 1, 1LL << 24);
-            if (DR)
-                for (int i = max(tile - 2, 0); i < tile; i++)
-                    mbar_wait(&sh.rope_full[i & 1], (i >> 1) & 1, 1LL << 24);
+            for (int i = 0; i < NT && i < tile; i++) {
+                slot = (slot ? slot : NT) - 1;  // the last tiles, backwards
+                phase ^= slot == NT - 1;
+                mbar_wait(&sh.full[slot], phase, 1LL << 24);
+            }
             if (nq) mbar_wait(&sh.q_full, (nq - 1) & 1, 1LL << 24);
             if (asked) mbar_wait(&sh.next_full, (asked - 1) & 1, 1LL << 24);
         }
-    } else if (warp == kMmaWarp) {
+    } else if (warp == kScoreWarp || warp == kOutWarp) {
         // ------------------------------------------------------------ products
-        constexpr uint32_t idesc_s = idesc_bf16(kRows, kKeys, 0, 0);
-        const uint64_t dq = desc_kmajor(smem_addr(sq)), dk = desc_kmajor(smem_addr(sring));
-        const uint64_t dr = desc_kmajor(smem_addr(srope)), dp = desc_kmajor(smem_addr(sp));
-        const uint64_t dv = desc_mnmajor(smem_addr(sring), kKeys);
-        constexpr uint32_t BLOCK = kBlock >> 4;  // in descriptor units
-        constexpr int STEPS = kUnits + (DR ? 1 : 0);  // of a tile's first product
-        int tq = 0, tp = 0;        // tiles whose first (second) product is issued
-        int step = 0, left = 0;    // of the current tile; tiles left of the current piece
-        int np = 0, nq = 0;
-        bool need_q = false, ended = false;
-        uint32_t add0 = 0, add1 = 0, n0 = 0, n1 = 0;  // of even and odd tiles: not a piece's first; rows
-        bool first = false;
-        int nrow = 0;
-        auto commit = [&](uint64_t* bar) {
-            if (elect_one()) mma_commit(bar);
-            __syncwarp();
+        // What a warp does between two products shows as idle tensor core, so the two kinds
+        // have a warp each, and a tile's are issued in one go, by one lane, from
+        // registers known to be uniform.
+        const bool scores = warp == kScoreWarp;
+        constexpr uint32_t idesc_s = idesc_bf16(64, KT, 0, 0);  // (rows past RT: whatever follows)
+        const uint64_t dq = desc_kmajor(smem_addr(sq)), dk = desc_kmajor(smem_addr(skv));
+        const uint64_t dp = desc_kmajor(smem_addr(sp)), dv = desc_mnmajor(smem_addr(skv), KT);
+        constexpr uint32_t QBLOCK = C::QBLOCK >> 4, KBLOCK = C::KBLOCK >> 4, TILE = C::TILE >> 4;  // descriptor units
+        int t = 0, slot = 0, phase = 0, nq = 0;  // tiles so far; the next one's place; row tiles
+        auto wait = [&](uint64_t* bar, uint32_t parity) {
+            if (!__all_sync(0xffffffffu, mbar_wait(bar, parity, kWaitClocks))) ok = false;
+            return ok;
         };
-        long long t0 = clock64();
-        while (ok && !(ended && tp == tq)) {
-            bool moved = false;
-            if (tp < tq && warp_test(&sh.p_full, tp & 1)) {
-                tc_fence_after();
-                const uint32_t idesc = idesc_bf16(128, 16, 1, 0) + ((((tp & 1 ? n1 : n0) >> 3) - 2) << 17);
-                const uint32_t add = tp & 1 ? add1 : add0;
-                const int u0 = (tp & 1) * kUnits;
-#pragma unroll
-                for (int u = 0; u < kUnits; u++) {
-                    const uint64_t a = dv + (uint32_t)(u0 + u) * 2 * BLOCK;
+        for (int np = 0; ok; np++) {
+            const int i = np % kPieces;
+            if (!wait(&sh.piece_full[i], (np / kPieces) & 1)) break;
+            const Piece& pc = sh.pieces[i];
+            const int end = __shfl_sync(0xffffffffu, pc.end, 0);
+            const int n = __shfl_sync(0xffffffffu, piece_tiles<KT>(pc), 0);
+            const int nrow = __shfl_sync(0xffffffffu, (pc.ntok * G + 15) & ~15, 0);
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&sh.piece_empty[i]);
+            if (end) break;
+            if (scores) {
+                if (n > 0 && !wait(&sh.q_full, nq++ & 1)) break;
+                for (int j = 0; j < n; j++, t++) {
+                    if (!wait(&sh.full[slot], phase)) break;
+                    if (!wait(&sh.s_read[t & 1], ((t >> 1) & 1) ^ 1)) break;
+                    tc_fence_after();
+                    const uint64_t b = dk + (uint32_t)slot * TILE;
+                    const uint32_t d = tbase + C::TM_S + (t & 1) * KT;
                     if (elect_one()) {
 #pragma unroll
-                        for (int kk = 0; kk < kKeys / 16; kk++)
-                            mma_bf16(tbase + kTmO + u * kRows, a + kstep_mnmajor(kk), dp + kstep_kmajor(kRows, kk),
-                                     idesc, kk > 0 ? 1u : add);
-                        mma_commit(&sh.empty[u0 + u]);
-                        if (u == kUnits - 1) mma_commit(&sh.pv_done);
-                    }
-                    __syncwarp();
-                }
-                tp++;
-                moved = true;
-            } else if (!ended && tq - tp < 2) {
-                if (left == 0) {
-                    const int i = np % kPieces;
-                    if (warp_test(&sh.piece_full[i], (np / kPieces) & 1)) {
-                        const Piece& pc = sh.pieces[i];
-                        ended = __shfl_sync(0xffffffffu, pc.end, 0) != 0;
-                        left = __shfl_sync(0xffffffffu, ended ? 0 : piece_tiles(pc), 0);
-                        nrow = __shfl_sync(0xffffffffu, (pc.ntok * G + 15) & ~15, 0);
-                        __syncwarp();
-                        if (lane == 0) mbar_arrive(&sh.piece_empty[i]);
-                        np++;
-                        need_q = left > 0;
-                        first = true;
-                        moved = true;
-                    }
-                } else if (need_q) {
-                    if (warp_test(&sh.q_full, nq & 1)) {
-                        nq++;
-                        need_q = false;
-                        moved = true;
-                    }
-                } else {
-                    const int u = step - (DR ? 1 : 0);  // -1: the rotated channels
-                    const int s = (tq & 1) * kUnits + u;
-                    uint64_t* bar = u < 0 ? &sh.rope_full[tq & 1] : &sh.full[s];
-                    if (warp_test(bar, (tq >> 1) & 1)) {
-                        tc_fence_after();
-                        const uint64_t a = dq + (uint32_t)(u < 0 ? kDL / 64 : 2 * u) * BLOCK;
-                        const uint64_t b = u < 0 ? dr + (tq & 1) * BLOCK : dk + (uint32_t)s * 2 * BLOCK;
-                        const uint32_t d = tbase + kTmS + (tq & 1) * kKeys;
-                        if (elect_one()) {
+                        for (int i = 0; i < C::BLOCKS; i++)
 #pragma unroll
                             for (int kk = 0; kk < 4; kk++)
-                                mma_bf16(d, a + 2 * kk, b + 2 * kk, idesc_s, step > 0 || kk > 0);
-                            if (u >= 0) {
-#pragma unroll
-                                for (int kk = 0; kk < 4; kk++)
-                                    mma_bf16(d, a + BLOCK + 2 * kk, b + BLOCK + 2 * kk, idesc_s, 1);
-                            } else {
-                                mma_commit(&sh.rope_empty[tq & 1]);
-                            }
-                        }
-                        __syncwarp();
-                        if (++step == STEPS) {
-                            commit(&sh.s_full[tq & 1]);
-                            step = 0;
-                            if (tq & 1) {
-                                add1 = !first;
-                                n1 = nrow;
-                            } else {
-                                add0 = !first;
-                                n0 = nrow;
-                            }
-                            first = false;
-                            tq++;
-                            if (--left == 0) commit(&sh.q_empty);
-                        }
-                        moved = true;
+                                mma_bf16(d, dq + (uint32_t)i * QBLOCK + 2 * kk, b + (uint32_t)i * KBLOCK + 2 * kk, idesc_s,
+                                         i > 0 || kk > 0);
+                        mma_commit(&sh.s_full[t & 1]);
+                        if (j + 1 == n) mma_commit(&sh.q_empty);
+                    }
+                    __syncwarp();
+                    if (++slot == NT) {
+                        slot = 0;
+                        phase ^= 1;
                     }
                 }
+            } else {
+                const uint32_t idesc = idesc_bf16(128, 16, 1, 0) + (((uint32_t)(nrow >> 3) - 2) << 17);
+                for (int j = 0; j < n; j++, t++) {
+                    if (!wait(&sh.p_full, t & 1)) break;
+                    tc_fence_after();
+                    const uint64_t a = dv + (uint32_t)slot * TILE;
+                    if (elect_one()) {
+#pragma unroll
+                        for (int u = 0; u < kUnits; u++)
+#pragma unroll
+                            for (int kk = 0; kk < KT / 16; kk++)
+                                mma_bf16(tbase + C::TM_O + u * RT, a + (uint32_t)u * 2 * KBLOCK + kstep_mnmajor(kk),
+                                         dp + 2 * kk, idesc, j > 0 || kk > 0);
+                        mma_commit(&sh.empty[slot]);
+                        mma_commit(&sh.pv_done);
+                    }
+                    __syncwarp();
+                    if (++slot == NT) slot = 0;
+                }
             }
-            const long long now = clock64();
-            if (moved) t0 = now;
-            else if (now - t0 > kWaitClocks) ok = false;
-            ok = __all_sync(0xffffffffu, ok);
         }
         // Products in flight, which write the tensor memory that is freed below and
         // arrive on this CTA's barriers, end before it leaves.
-        commit(&sh.drained);
-        if (!__all_sync(0xffffffffu, mbar_wait(&sh.drained, 0, 1LL << 24))) ok = false;
+        if (elect_one()) mma_commit(&sh.drained[scores]);
+        __syncwarp();
+        if (!__all_sync(0xffffffffu, mbar_wait(&sh.drained[scores], 0, 1LL << 24))) ok = false;
         if (!ok) flags |= KDA_DEV_TIMEOUT;
     } else {
         // ------------------------------------------------------------ softmax and results
         // Row 16 w + i of a 64-row accumulator is lane 32 w + i.
         const int row = 16 * warp + (lane & 15), rtok = row / G;
+        const bool rows_here = 16 * warp < RT;
         const uint32_t tlane = tmem_at(tbase, 32 * warp, 0);
-        int t = 0;  // tiles so far
+        int t = 0, slot = 0, phase = 0;  // tiles so far; the current one's place
         // These warps meet at barriers, so after a wait that gave up they go on without
         // waiting to where all of them stop.
         for (int np = 0;; np++) {
@@ -563,32 +526,44 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
             __syncwarp();
             if (lane == 0) mbar_arrive(&sh.piece_empty[i]);
             if (pc.end) break;
-            const int n = piece_tiles(pc), all = seen_by_all(pc);
-            const bool live = lane < 16 && row < pc.ntok * G;
+            const int n = piece_tiles<KT>(pc), all = seen_by_all(pc);
+            const bool live = lane < 16 && row < pc.ntok * G;  // (at most RT rows)
             // Keys this row sees; a row of nothing masks nothing (never stored).
             const int lim = live ? max(pc.pos0 + rtok + 1, 0) : 0x7fffffff;
-            if (lane < 16) sh.lim[row] = lim;
+            if (lane < 16 && rows_here) sh.lim[row] = lim;
             if (tid < 2) sh.odd[(np & 1) ^ 1][tid] = 0;
             float m = -INFINITY, l = 0.f;  // reference (c S) and sum
             for (int j = 0; j < n; j++, t++) {
-                const int base = (pc.kt0 + j) * kKeys;
+                const int base = (pc.kt0 + j) * KT;
                 warp_wait(ok, &sh.s_full[t & 1], (t >> 1) & 1);
                 tc_fence_after();
-                uint32_t xr[kKeys];
+                uint32_t xr[KT];
                 float* x = reinterpret_cast<float*>(xr);
-                tmem_ld64_async(tlane + kTmS + (t & 1) * kKeys, xr);
-                tmem_wait_ld();
-                tmem_landed<kKeys>(xr);
-                if (__any_sync(0xffffffffu, base + kKeys > lim)) {
+                float top = -INFINITY;
+                if (rows_here) {
+                    const uint32_t ts = tlane + C::TM_S + (t & 1) * KT;
+                    if constexpr (KT == 64) {
+                        tmem_ld64_async(ts, xr);
+                        tmem_wait_ld();
+                        tmem_landed<KT>(xr);
+                    } else {
+                        tmem_ld32(ts, x);
+                    }
+                    tc_fence_before();
+                    if (lane == 0) mbar_arrive(&sh.s_read[t & 1]);
+                    if (__any_sync(0xffffffffu, base + KT > lim)) {
 #pragma unroll
-                    for (int e = 0; e < kKeys; e++) x[e] = base + e < lim ? x[e] : -INFINITY;
+                        for (int e = 0; e < KT; e++) x[e] = base + e < lim ? x[e] : -INFINITY;
+                    }
+                    float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+                    for (int e = 0; e < KT; e += 8)
+#pragma unroll
+                        for (int k = 0; k < 4; k++) mx[k] = fmaxf(fmaxf(mx[k], x[e + k]), x[e + k + 4]);
+                    top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * p.c;
+                } else if (lane == 0) {
+                    mbar_arrive(&sh.s_read[t & 1]);
                 }
-                float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-                for (int e = 0; e < kKeys; e += 8)
-#pragma unroll
-                    for (int k = 0; k < 4; k++) mx[k] = fmaxf(fmaxf(mx[k], x[e + k]), x[e + k + 4]);
-                const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * p.c;
                 if (j == 0) {
                     m = top;
                 } else if (wg_or(live && top > m + kRaise)) {
@@ -596,52 +571,53 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
                     const float a = mn == -INFINITY ? 1.f : ex2(m - mn);
                     m = mn;
                     l *= a;
-                    if (lane < 16) sh.factor[row] = a;
+                    if (lane < 16 && rows_here) sh.factor[row] = a;
                     wg_sync();
                     warp_wait(ok, &sh.pv_done, (t - 1) & 1);  // the sums so far
                     tc_fence_after();
 #pragma unroll 1
-                    for (int b = 0; b < kUnits * kRows; b += 32) {
+                    for (int b = 0; b < kUnits * RT; b += 32) {
                         float y[32];
-                        tmem_ld32(tlane + kTmO + b, y);
+                        tmem_ld32(tlane + C::TM_O + b, y);
 #pragma unroll
-                        for (int e = 0; e < 32; e++) y[e] *= sh.factor[(b & (kRows - 1)) + e];
-                        tmem_st16(tlane + kTmO + b, y);
-                        tmem_st16(tlane + kTmO + b + 16, y + 16);
+                        for (int e = 0; e < 32; e++) y[e] *= sh.factor[(b & (RT - 1)) + e];
+                        tmem_st16(tlane + C::TM_O + b, y);
+                        tmem_st16(tlane + C::TM_O + b + 16, y + 16);
                     }
                     tmem_wait_st();
                 }
-                const float ref = m == -INFINITY ? 0.f : m;
-                float sum[4] = {0.f, 0.f, 0.f, 0.f};
-                uint32_t pk[kKeys / 2];
+                if (rows_here) {
+                    const float ref = m == -INFINITY ? 0.f : m;
+                    float sum[4] = {0.f, 0.f, 0.f, 0.f};
+                    uint32_t pk[KT / 2];
 #pragma unroll
-                for (int e = 0; e < kKeys; e += 2) {
-                    const float u = ex2(fmaf(x[e], p.c, -ref)), v = ex2(fmaf(x[e + 1], p.c, -ref));
-                    sum[e & 2] += u;
-                    sum[(e & 2) + 1] += v;
-                    // to bf16, as the product wants P in the values' type (the sum is of the unrounded)
-                    pk[e / 2] = pack2(u, v);
-                }
-                l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
-                if (t > 0) warp_wait(ok, &sh.pv_done, (t - 1) & 1);  // P of the tile before is read
-                if (lane < 16) {
+                    for (int e = 0; e < KT; e += 2) {
+                        const float u = ex2(fmaf(x[e], p.c, -ref)), v = ex2(fmaf(x[e + 1], p.c, -ref));
+                        sum[e & 2] += u;
+                        sum[(e & 2) + 1] += v;
+                        // to bf16, as the product wants P in the values' type (the sum is of the unrounded)
+                        pk[e / 2] = pack2(u, v);
+                    }
+                    l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+                    if (t > 0) warp_wait(ok, &sh.pv_done, (t - 1) & 1);  // P of the tile before is read
+                    if (lane < 16) {
 #pragma unroll
-                    for (int b = 0; b < 8; b++)
-                        *reinterpret_cast<uint4*>(sp + row * 128 + ((b ^ (row & 7)) << 4)) =
-                            make_uint4(pk[4 * b], pk[4 * b + 1], pk[4 * b + 2], pk[4 * b + 3]);
+                        for (int b = 0; b < KT / 8; b++)
+                            *reinterpret_cast<uint4*>(sp + row * 128 + ((b ^ (row & 7)) << 4)) =
+                                make_uint4(pk[4 * b], pk[4 * b + 1], pk[4 * b + 2], pk[4 * b + 3]);
+                    }
                 }
-                if (base + kKeys > all) {
+                if (base + KT > all) {
                     // Keys that some rows must not see: 16 threads a key.
-                    for (int u = 0; u < kUnits; u++)  // (the copies, seen by this thread)
-                        warp_wait(ok, &sh.full[(t & 1) * kUnits + u], (t >> 1) & 1);
+                    warp_wait(ok, &sh.full[slot], phase);  // (the copies, seen by this thread)
                     const int k0 = max(all - base, 0), k1 = pc.keys - base;
-                    for (int k = k0 + tid / 16; k < kKeys; k += 8) {
+                    for (int k = k0 + tid / 16; k < KT; k += 8) {
                         bool odd = false;
 #pragma unroll
                         for (int b = 0; b < 4; b++) {
                             const int v = (tid & 15) + 16 * b;  // vector of the key's 64
                             uint4* at = reinterpret_cast<uint4*>(
-                                sring + (t & 1) * kUnits * 2 * kBlock + (v >> 3) * kBlock + k * 128 + (v & 7) * 16);
+                                skv + slot * C::TILE + (v >> 3) * C::KBLOCK + k * 128 + (v & 7) * 16);
                             if (k >= k1) {
                                 *at = make_uint4(0, 0, 0, 0);
                             } else {
@@ -660,13 +636,17 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
                 fence_proxy_async_smem();
                 tc_fence_before();
                 mbar_arrive(&sh.p_full);
+                if (++slot == NT) {
+                    slot = 0;
+                    phase ^= 1;
+                }
             }
             if (n > 0) warp_wait(ok, &sh.pv_done, (t - 1) & 1);
             tc_fence_after();
             const size_t at0 = (size_t)pc.tok0 * Hq + (size_t)pc.h * G;
             float* part = pc.slot >= 0 ? p.sp.ws + attn_slot_floats(p.sp.rows, kDL) * pc.slot : nullptr;
             wg_sync();  // (factors of a raised reference are read)
-            if (lane < 16) sh.factor[row] = l == 0.f ? 0.f : 1.f / l;
+            if (lane < 16 && rows_here) sh.factor[row] = l == 0.f ? 0.f : 1.f / l;
             if (live) {
                 if (part) part[(size_t)p.sp.rows * kDL + row] = l == 0.f ? -INFINITY : m + log2f(l);
                 else if (p.lse)
@@ -677,12 +657,12 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
             const uint32_t odd[2] = {sh.odd[np & 1][0], sh.odd[np & 1][1]};
             float fin = 0.f;  // NaN once a value is not finite
 #pragma unroll 1
-            for (int b = 0; b < kUnits * kRows; b += 32) {
-                const int u = b / kRows, r0 = b & (kRows - 1);
+            for (int b = 0; b < kUnits * RT; b += 32) {
+                const int u = b / RT, r0 = b & (RT - 1);
                 const int ch = 128 * u + 32 * warp + lane;
                 if (r0 >= rows) continue;
                 float y[32];
-                if (n > 0) tmem_ld32(tlane + kTmO + b, y);
+                if (n > 0) tmem_ld32(tlane + C::TM_O + b, y);
 #pragma unroll
                 for (int e = 0; e < 32; e++) {
                     const float f = sh.factor[r0 + e];
@@ -734,7 +714,7 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    if (warp == kMmaWarp) tmem_dealloc(tbase, 512);
+    if (warp == kScoreWarp) tmem_dealloc(tbase, 512);
 }
 
 // Rows of queries, [tokens][heads][d], boxes of 64 x heads x tokens.
@@ -750,27 +730,28 @@ bool make_rows(CUtensorMap* m, const AttnArgs& a, int d, int box_heads, int box_
                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// The cache, [pages][page][d], boxes of 64 x (page or 64) tokens.
-bool make_cache(CUtensorMap* m, const AttnArgs& a, int d) {
+// The cache, [pages][page][d], boxes of 64 x (page or `keys`) tokens.
+bool make_cache(CUtensorMap* m, const AttnArgs& a, int d, int keys) {
     auto enc = tensor_map_encoder();
     if (!enc) return false;
     cuuint64_t dims[3] = {(cuuint64_t)d, (cuuint64_t)a.page, (cuuint64_t)a.num_pages};
     cuuint64_t strides[2] = {(cuuint64_t)d * 2, (cuuint64_t)a.page * d * 2};
-    cuuint32_t box[3] = {64, (cuuint32_t)(a.page < kKeys ? a.page : kKeys), 1};
+    cuuint32_t box[3] = {64, (cuuint32_t)(a.page < keys ? a.page : keys), 1};
     cuuint32_t es[3] = {1, 1, 1};
     return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(a.k), dims, strides, box, es,
                CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int DR>
+template <int DR, int RT, int KT>
 cudaError_t launch_t(const AttnArgs& a) {
-    const int blocks = latent_head_blocks(a.Hq, kRows), G = a.Hq / blocks, tok = kRows / G;
+    using C = TcCfg<DR, RT, KT>;
+    const int blocks = latent_head_blocks(a.Hq, RT), G = a.Hq / blocks, tok = RT / G;
     int dev = 0;
     const int nsm = device_sms(&dev);
     if (nsm == 0) return cudaErrorNoDevice;
     LatentTcParams p{};
-    p.s = {a.cu_q, a.kv_len, a.N, a.total_q, a.max_q, attn_kv_cap(a), blocks, G, tok, tok, kKeys, 1, 1, kItemKeys};
+    p.s = {a.cu_q, a.kv_len, a.N, a.total_q, a.max_q, attn_kv_cap(a), blocks, G, tok, tok, KT, 1, 1, kItemKeys};
     p.sp = latent_tc_split(a.N, a.total_q, a.max_q, p.s.kv_cap, a.Hq, nsm);
     if (p.sp.ctas && a.ws && a.ws_bytes >= attn_split_bytes(p.sp, kDL)) p.sp.ws = a.ws;
     p.block_table = a.block_table;
@@ -784,16 +765,16 @@ cudaError_t launch_t(const AttnArgs& a) {
     p.c = a.scale * 1.44269504089f;
     p.d_status = a.d_status;
     CUtensorMap mq, mc;
-    if (!make_rows(&mq, a, kDL + DR, G, p.box_q) || !make_cache(&mc, a, kDL + DR)) return cudaErrorInvalidValue;
-    auto kernel = kda_latent_tc_kernel<DR>;
+    if (!make_rows(&mq, a, kDL + DR, G, p.box_q) || !make_cache(&mc, a, kDL + DR, KT)) return cudaErrorInvalidValue;
+    auto kernel = kda_latent_tc_kernel<DR, RT, KT>;
     static std::atomic<uint64_t> ready{0};
-    cudaError_t e = allow_shared(kernel, tc_smem<DR>(), ready, dev);
+    cudaError_t e = allow_shared(kernel, tc_smem<C>(), ready, dev);
     if (e != cudaSuccess) return e;
     const long long grid = p.sp.ws ? p.sp.ctas : attn_items_bound(p.s);
     if (grid >= 1LL << 31) return cudaErrorInvalidValue;
-    e = launch_dependent(kernel, dim3((unsigned)grid), dim3(kThreadsTc), tc_smem<DR>(), a.stream, mq, mc, p);
+    e = launch_dependent(kernel, dim3((unsigned)grid), dim3(kThreadsTc), tc_smem<C>(), a.stream, mq, mc, p);
     if (e != cudaSuccess || !p.sp.ws) return e;
-    return launch_attn_combine(p.sp, blocks, G, kDL, kRows, a.o, a.lse, KDA_BF16, a.d_status, a.stream);
+    return launch_attn_combine(p.sp, blocks, G, kDL, RT, a.o, a.lse, KDA_BF16, a.d_status, a.stream);
 }
 
 }  // namespace
@@ -801,15 +782,18 @@ cudaError_t launch_t(const AttnArgs& a) {
 AttnSplit latent_tc_split(int N, int total_q, int max_q, long long max_keys, int Hq, int nsm) {
     AttnSplit sp{};
     if (N == 0 || total_q == 0 || max_q == 0 || Hq == 0 || nsm == 0) return sp;
-    const int blocks = latent_head_blocks(Hq, kRows), G = Hq / blocks, tok = kRows / G;
+    const int rt = latent_tc_rows(max_q, Hq), blocks = latent_head_blocks(Hq, rt), G = Hq / blocks, tok = rt / G;
     if (max_keys <= KDA_LATENT_SHORT_KEYS) return sp;
     if ((long long)total_q / tok * blocks >= 8LL * nsm) return sp;
     sp.ctas = nsm;
-    sp.least = 4 * kKeys;
+    sp.least = 256;
     sp.rows = ((max_q < tok ? max_q : tok) * G + 3) & ~3;  // whole 16-byte vectors
     return sp;
 }
 
-cudaError_t launch_latent_tc(const AttnArgs& a) { return a.dr ? launch_t<64>(a) : launch_t<0>(a); }
+cudaError_t launch_latent_tc(const AttnArgs& a) {
+    if (latent_tc_rows(a.max_q, a.Hq) == 32) return a.dr ? launch_t<64, 32, 32>(a) : launch_t<0, 32, 32>(a);
+    return a.dr ? launch_t<64, 64, 32>(a) : launch_t<0, 64, 32>(a);
+}
 
 }  // namespace kda
