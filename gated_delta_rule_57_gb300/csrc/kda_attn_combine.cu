@@ -90,6 +90,76 @@ __global__ void __launch_bounds__(kCombineWarps * 32)
     report_flags(d_status, flags);
 }
 
+// The same for wide rows (D = 512): a warp takes 128 channels of one row. It finds M and
+// the weights first, a part per lane, so that no part's load waits for another's: 8 are in
+// flight.
+template <typename T, int D>
+__global__ void __launch_bounds__(kCombineWarps * 32)
+    kda_attn_combine_wide_kernel(const AttnSplit sp, const int Hkv, const int G, const int tile_rows,
+                                 T* o, float* lse, int* d_status) {
+    pdl_wait();
+    const int b = blockIdx.x + 1;
+    const AttnCut cut = attn_cuts(sp, D)[b];
+    if (cut.ntok == 0 || cut.tile == 0) return;  // no work, or the boundary is an item's too
+    const int c0 = (int)(cut.u0 / cut.each);
+    const int c1 = (int)((cut.u0 + (long long)(cut.n - 1) * cut.cost) / cut.each);
+    const AttnCut start = attn_cuts(sp, D)[c0];
+    const int late = !(start.u0 == cut.u0 && start.tile == 0);
+    constexpr int COLS = D / 128;  // warps of a row
+    const int lane = threadIdx.x & 31, units = cut.ntok * G * COLS, per = tile_rows / G;
+    const int first = ((b - 1 - c0) * gridDim.y + blockIdx.y) * kCombineWarps + (threadIdx.x >> 5);
+    const int step = (c1 - c0) * gridDim.y * kCombineWarps;
+    const size_t slot = attn_slot_floats(sp.rows, D);
+    auto part = [&](int c) { return sp.ws + slot * (2 * (size_t)c + (c == c0 ? late : 0)); };
+    int flags = 0;
+    for (int i = first; i < units; i += step) {
+        const int r = i / COLS, col = i % COLS * 128 + lane * 4, tok = r / G;
+        const int row = tok / per * tile_rows + tok % per * G + r % G;
+        float m = -INFINITY;
+        for (int c = c0 + lane; c <= c1; c += 32) m = fmaxf(m, part(c)[(size_t)sp.rows * D + row]);
+#pragma unroll
+        for (int k = 16; k > 0; k >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, k));
+        float sum = 0.f;
+        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int cb = c0; cb <= c1; cb += 32) {
+            const int n = min(c1 - cb + 1, 32);
+            // (a part in which this row sees nothing has weight 0 and is not read; NaN stays)
+            float w = 0.f;
+            if (lane < n) {
+                const float x = part(cb + lane)[(size_t)sp.rows * D + row];
+                w = x == -INFINITY ? 0.f : exp2f(x - m);
+            }
+            sum += w;
+#pragma unroll 8
+            for (int k = 0; k < n; k++) {
+                const float wk = __shfl_sync(0xffffffffu, w, k);
+                if (wk == 0.f) continue;
+                const float4 y = *reinterpret_cast<const float4*>(part(cb + k) + (size_t)row * D + col);
+                acc.x = fmaf(wk, y.x, acc.x);
+                acc.y = fmaf(wk, y.y, acc.y);
+                acc.z = fmaf(wk, y.z, acc.z);
+                acc.w = fmaf(wk, y.w, acc.w);
+            }
+        }
+#pragma unroll
+        for (int k = 16; k > 0; k >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, k);
+        const size_t at = ((size_t)cut.tok0 + tok) * Hkv * G + (size_t)cut.h * G + r % G;
+        const float inv = sum == 0.f ? 0.f : 1.f / sum;
+        const float y[4] = {acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv};
+        T out[4];
+#pragma unroll
+        for (int e = 0; e < 4; e++) {
+            flags |= finite_flag(y[e]);
+            out[e] = from_f32<T>(y[e]);
+        }
+        if constexpr (sizeof(T) == 4) *reinterpret_cast<float4*>(o + at * D + col) = *reinterpret_cast<float4*>(out);
+        else *reinterpret_cast<uint2*>(o + at * D + col) = *reinterpret_cast<uint2*>(out);
+        if (lse && lane == 0 && i % COLS == 0)
+            lse[at] = sum == 0.f ? -INFINITY : (m + log2f(sum)) * 0.69314718056f;
+    }
+    report_flags(d_status, flags);
+}
+
 }  // namespace
 
 cudaError_t launch_attn_combine(const AttnSplit& sp, int Hkv, int G, int d, int rows_per_tile,
@@ -103,16 +173,24 @@ cudaError_t launch_attn_combine(const AttnSplit& sp, int Hkv, int G, int d, int 
         return launch_dependent(kernel, grid, dim3(kCombineWarps * 32), 0, stream, sp, Hkv, G,
                                 rows_per_tile, out, lse, d_status);
     };
+    if (d == 512) {
+        // Two passes at most, as one boundary may have to do all of an item.
+        const dim3 wide((unsigned)(sp.ctas - 1), (unsigned)((sp.rows * 4 + 2 * kCombineWarps - 1) / (2 * kCombineWarps)));
+        auto go = [&](auto kernel, auto* out) {
+            return launch_dependent(kernel, wide, dim3(kCombineWarps * 32), 0, stream, sp, Hkv, G,
+                                    rows_per_tile, out, lse, d_status);
+        };
+        return io == KDA_BF16 ? go(kda_attn_combine_wide_kernel<__nv_bfloat16, 512>, static_cast<__nv_bfloat16*>(o))
+                              : go(kda_attn_combine_wide_kernel<float, 512>, static_cast<float*>(o));
+    }
     if (io == KDA_BF16) {
         auto* out = static_cast<__nv_bfloat16*>(o);
-        return d == 512   ? go(kda_attn_combine_kernel<__nv_bfloat16, 512>, out)
-               : d == 128 ? go(kda_attn_combine_kernel<__nv_bfloat16, 128>, out)
-                          : go(kda_attn_combine_kernel<__nv_bfloat16, 64>, out);
+        return d == 128 ? go(kda_attn_combine_kernel<__nv_bfloat16, 128>, out)
+                        : go(kda_attn_combine_kernel<__nv_bfloat16, 64>, out);
     }
     auto* out = static_cast<float*>(o);
-    return d == 512   ? go(kda_attn_combine_kernel<float, 512>, out)
-           : d == 128 ? go(kda_attn_combine_kernel<float, 128>, out)
-                      : go(kda_attn_combine_kernel<float, 64>, out);
+    return d == 128 ? go(kda_attn_combine_kernel<float, 128>, out)
+                    : go(kda_attn_combine_kernel<float, 64>, out);
 }
 
 }  // namespace kda
