@@ -646,14 +646,16 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
             const size_t at0 = (size_t)pc.tok0 * Hq + (size_t)pc.h * G;
             float* part = pc.slot >= 0 ? p.sp.ws + attn_slot_floats(p.sp.rows, kDL) * pc.slot : nullptr;
             wg_sync();  // (factors of a raised reference are read)
-            if (lane < 16 && rows_here) sh.factor[row] = l == 0.f ? 0.f : 1.f / l;
+            if (lane < 16 && rows_here) sh.factor[row] = !live || l == 0.f ? 0.f : 1.f / l;
             if (live) {
                 if (part) part[(size_t)p.sp.rows * kDL + row] = l == 0.f ? -INFINITY : m + log2f(l);
                 else if (p.lse)
                     p.lse[at0 + sh.row_at[row]] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.69314718056f;
             }
-            wg_sync();
+            // Rows without any weight: zeros, whatever their accumulators hold.
+            const bool nothing = wg_or(n == 0 || (live && l == 0.f));
             const int rows = pc.ntok * G;
+            const bool in_order = p.s.Hkv == 1 || pc.ntok == 1;  // rows of o
             const uint32_t odd[2] = {sh.odd[np & 1][0], sh.odd[np & 1][1]};
             float fin = 0.f;  // NaN once a value is not finite
 #pragma unroll 1
@@ -664,9 +666,15 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
                 float y[32];
                 if (n > 0) tmem_ld32(tlane + C::TM_O + b, y);
 #pragma unroll
-                for (int e = 0; e < 32; e++) {
-                    const float f = sh.factor[r0 + e];
-                    y[e] = n > 0 && f != 0.f ? y[e] * f : 0.f;
+                for (int e = 0; e < 32; e += 4) {
+                    const float4 f = *reinterpret_cast<const float4*>(&sh.factor[r0 + e]);
+                    const float g[4] = {f.x, f.y, f.z, f.w};
+#pragma unroll
+                    for (int k = 0; k < 4; k++) y[e + k] *= g[k];
+                }
+                if (nothing) {
+#pragma unroll
+                    for (int e = 0; e < 32; e++) y[e] = n > 0 && sh.factor[r0 + e] != 0.f ? y[e] : 0.f;
                 }
                 if (odd[0] | odd[1]) {
                     for (int k = 0; k < 64; k++) {
@@ -682,24 +690,29 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
                             if (key < sh.lim[r0 + e]) y[e] += v;
                     }
                 }
-#pragma unroll
-                for (int e = 0; e < 32; e++)
-                    if (r0 + e < rows) fin = fmaf(y[e], 0.f, fin);
                 if (part) {
+                    float* dst = part + (size_t)r0 * kDL + ch;
 #pragma unroll
                     for (int e = 0; e < 32; e++)
-                        if (r0 + e < rows) part[(size_t)(r0 + e) * kDL + ch] = y[e];
+                        if (r0 + e < rows) {
+                            fin = fmaf(y[e], 0.f, fin);
+                            dst[e * kDL] = y[e];
+                        }
                 } else {
                     // Two rows at a time: even lanes store two channels of the first, odd
                     // lanes of the second.
+                    const bool up = lane & 1;
+                    __nv_bfloat16* dst = p.o + at0 * kDL + (ch & ~1);
 #pragma unroll
                     for (int e = 0; e < 32; e += 2) {
-                        const bool up = lane & 1;
                         const float other = __shfl_xor_sync(0xffffffffu, up ? y[e] : y[e + 1], 1);
-                        const uint32_t two = up ? pack2(other, y[e + 1]) : pack2(y[e], other);
+                        const float lo = up ? other : y[e], hi = up ? y[e + 1] : other;
                         const int rr = r0 + e + up;
-                        if (rr < rows)
-                            *reinterpret_cast<uint32_t*>(p.o + (at0 + sh.row_at[rr]) * kDL + (ch & ~1)) = two;
+                        if (rr < rows) {
+                            fin = fmaf(lo, 0.f, fmaf(hi, 0.f, fin));
+                            const int at = in_order ? rr : sh.row_at[rr];
+                            *reinterpret_cast<uint32_t*>(dst + (size_t)at * kDL) = pack2(lo, hi);
+                        }
                     }
                 }
             }
