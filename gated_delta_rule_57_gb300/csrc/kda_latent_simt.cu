@@ -270,7 +270,7 @@ __global__ void __launch_bounds__(kThreads, 1) kda_latent_simt_kernel(const Late
             float* y = dst ? dst + (size_t)row * kDL : p.o + at * kDL;
 #pragma unroll
             for (int e = 0; e < 8; e++) {
-                acc[i][e] *= inv;
+                acc[i][e] = inv == 0.f ? 0.f : acc[i][e] * inv;  // (a row of no weight: zeros)
                 flags |= finite_flag(acc[i][e]);
             }
             *reinterpret_cast<float4*>(y + c4) = make_float4(acc[i][0], acc[i][1], acc[i][2], acc[i][3]);

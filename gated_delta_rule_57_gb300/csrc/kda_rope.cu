@@ -294,10 +294,13 @@ kda_status_t kda_kv_append_rope(const void* q, const void* k, const void* v, con
         tn{turns, (size_t)rot * 4, (size_t)rot * 4, 1};
     const Rows kc{k_cache, n_c, n_c, 1}, vc{v_cache, n_c, n_c, 1},
         out{q_out, rq, q_out_stride * esz, Hq ? T : 0};
-    for (const Rows& c : {kc, vc, out})
-        for (const Rows& x : {in_q, in_k, in_v, s, ps, tn})
-            if (rows_meet(c, x) && !(c.p == q_out && x.p == q && c.stride == x.stride && Hq > 0 && c.row == x.row && c.n == x.n))
-                return fail(KDA_ERR_INVALID_ARG, "a cache or q_out overlaps an input");
+    const bool in_place = q == q_out && q_stride == q_out_stride;
+    if (!in_place && rows_meet(out, in_q)) return fail(KDA_ERR_INVALID_ARG, "q_out overlaps q");
+    for (const Rows& c : {kc, vc, out}) {
+        for (const Rows& x : {in_k, in_v, s, ps, tn})
+            if (rows_meet(c, x)) return fail(KDA_ERR_INVALID_ARG, "a cache or q_out overlaps an input");
+        if (c.p != q_out && rows_meet(c, in_q)) return fail(KDA_ERR_INVALID_ARG, "a cache overlaps q");
+    }
     if (rows_meet(kc, vc) || rows_meet(kc, out) || rows_meet(vc, out))
         return fail(KDA_ERR_INVALID_ARG, "the caches and q_out overlap");
     const int V = (int)(16 / esz), dv = d / V;
@@ -383,14 +386,14 @@ kda_status_t kda_latent_append(const void* c, const void* k_r, const void* q_r, 
         tn{turns, (size_t)dr * 4, (size_t)dr * 4, dr ? 1 : 0};
     const Rows cc{cache, n_c, n_c, 1}, qo = heads(q_out, q_out_stride, q_out_head),
         ko{k_out, nr, k_out_stride * esz, k_out ? T : 0};
+    const bool q_in_place = q_r == q_out && qr_stride == q_out_stride && qr_head == q_out_head;
+    const bool k_in_place = k_r == k_out && kr_stride == k_out_stride;
+    bool meet = !q_in_place && rows_meet(qo, in_q);
+    meet |= !k_in_place && rows_meet(ko, in_k);
+    meet |= rows_meet(cc, in_q) || rows_meet(cc, in_k) || rows_meet(qo, in_k) || rows_meet(ko, in_q);
     for (const Rows& o : {cc, qo, ko})
-        for (const Rows& x : {in_c, in_k, in_q, s, ps, tn}) {
-            if (!rows_meet(o, x)) continue;
-            if (Hq > 0 && o.p == q_out && x.p == q_r && q_out_stride == qr_stride && q_out_head == qr_head)
-                continue;  // in place
-            if (k_out && o.p == k_out && x.p == k_r && k_out_stride == kr_stride) continue;
-            return fail(KDA_ERR_INVALID_ARG, "the cache, q_out or k_out overlaps an input");
-        }
+        for (const Rows& x : {in_c, s, ps, tn}) meet |= rows_meet(o, x);
+    if (meet) return fail(KDA_ERR_INVALID_ARG, "the cache, q_out or k_out overlaps an input");
     if (rows_meet(cc, qo) || rows_meet(cc, ko) || rows_meet(qo, ko))
         return fail(KDA_ERR_INVALID_ARG, "the cache, q_out and k_out overlap");
     const int V = (int)(16 / esz);

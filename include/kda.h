@@ -685,7 +685,8 @@ kda_status_t kda_latent_append(const void* c, const void* k_r, const void* q_r, 
  *
  * Requests, lengths, pages, rows that see nothing, NaN and Inf, and arithmetic as for
  * kda_attn_paged. A row of the cache counts as a key and as a value: what is not finite in it
- * reaches every row that sees it and no other. Any number of heads up to 65536: more than 64
+ * reaches every row that sees it and no other. A score of -Inf has weight 0; a row of no other
+ * scores counts as one that sees no key. Any number of heads up to 65536: more than 64
  * are taken in blocks of equal size (prime numbers of heads beyond 64 one by one).
  */
 kda_status_t kda_attn_latent_paged(const void* q, const void* cache, const int* block_table,
