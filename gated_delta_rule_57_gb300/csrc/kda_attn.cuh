@@ -292,7 +292,8 @@ AttnSplit attn_simt_split(int N, int total_q, int max_q, long long max_keys, boo
 // shared ones, its values the latent channels. k: the cache. Heads beyond a row tile are
 // taken in blocks of equal size, as if they had key heads.
 constexpr int kLatentDim = 512;
-constexpr int kLatentSimtRows = 32;  // rows of a row tile
+// Rows of a row tile.
+inline int latent_simt_rows(int max_q, int Hq) { return (long long)max_q * Hq <= 8 ? 8 : 32; }
 inline int latent_tc_rows(int max_q, int Hq) { return (long long)max_q * Hq <= 32 ? 32 : 64; }
 inline int latent_head_blocks(int Hq, int rows) {
     int b = (Hq + rows - 1) / rows;
@@ -301,6 +302,7 @@ inline int latent_head_blocks(int Hq, int rows) {
 }
 cudaError_t launch_latent_tc(const AttnArgs& a);    // bf16
 cudaError_t launch_latent_simt(const AttnArgs& a);  // fp32
+cudaError_t launch_latent_prompt_simt(const AttnArgs& a);  // fp32, expanded heads (bf16: launch_attn_tc)
 AttnSplit latent_tc_split(int N, int total_q, int max_q, long long max_keys, int Hq, int nsm);
 AttnSplit latent_simt_split(int N, int total_q, int max_q, long long max_keys, int Hq, int nsm);
 

@@ -302,7 +302,7 @@ kda_status_t kda_attn_latent_prompt(const void* q, const void* k, const void* k_
     a.stream = static_cast<cudaStream_t>(stream);
     st = check_buffers(a, n_q, n_k, n_v, n_r, (size_t)total * H * d * esz);
     if (st != KDA_OK) return st;
-    return launched(io == KDA_BF16 ? launch_attn_tc(a) : launch_attn_simt(a));
+    return launched(io == KDA_BF16 ? launch_attn_tc(a) : launch_latent_prompt_simt(a));
 }
 
 }  // extern "C"

@@ -33,32 +33,28 @@ struct SimtParams {
     const int* block_table;
     void* o;
     float* lse;
-    long long q_stride, k_stride, v_stride, q_head, k_head, v_head;
-    const void* k_r;  // key channels that all heads share (DQ > D)
-    long long kr_stride;
+    long long q_stride, k_stride, v_stride;
     int num_pages, page, max_pages;
     float scale;
     int* d_status;
 };
 
-// DQ channels of queries and keys, D of values and outputs; the keys' last DQ - D are
-// shared by all heads.
-template <int DQ, int D>
+template <int D>
 constexpr size_t simt_smem() {
-    return (size_t)(2 * kRows * (DQ + 4) + kKeys * (D + 4)) * 4;
+    return (size_t)3 * kRows * (D + 4) * 4;
 }
 
 __device__ __forceinline__ float4 load4(const float* p) {
     return *reinterpret_cast<const float4*>(p);
 }
 
-template <int DQ, int D>
+template <int D>
 __global__ void __launch_bounds__(kThreadsSimt, kCtasPerSm) kda_attn_simt_kernel(const SimtParams p) {
-    constexpr int LQ = DQ + 4, LD = D + 4, LP = kKeys + 4, C4 = D / 64;  // C4: float4 columns per thread
+    constexpr int LD = D + 4, LP = kKeys + 4, C4 = D / 64;  // C4: float4 columns per thread
     extern __shared__ __align__(16) float sm[];
     float* sq = sm;
-    float* sk = sq + kRows * LQ;  // also the probabilities, once the scores are done
-    float* sv = sk + kKeys * LQ;
+    float* sk = sq + kRows * LD;  // also the probabilities, once the scores are done
+    float* sv = sk + kKeys * LD;
     float* sp = sk;
 
     __shared__ long long s_groups[kAttnGroups], s_sum[kThreadsSimt / 32];
@@ -121,12 +117,12 @@ __global__ void __launch_bounds__(kThreadsSimt, kCtasPerSm) kda_attn_simt_kernel
         }
         const size_t first = (size_t)it.q.q0 + tok0;  // packed token of row 0
         __syncthreads();
-        for (int i = tid; i < kRows * (DQ / 4); i += kThreadsSimt) {
-            const int r = i / (DQ / 4), c = (i % (DQ / 4)) * 4;
+        for (int i = tid; i < kRows * (D / 4); i += kThreadsSimt) {
+            const int r = i / (D / 4), c = (i % (D / 4)) * 4;
             float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
             if (r < rows)
-                x = load4(gq + (first + r / G) * p.q_stride + (size_t)(it.h * G + r % G) * p.q_head + c);
-            *reinterpret_cast<float4*>(sq + r * LQ + c) = x;
+                x = load4(gq + (first + r / G) * p.q_stride + (size_t)(it.h * G + r % G) * D + c);
+            *reinterpret_cast<float4*>(sq + r * LD + c) = x;
         }
         // Keys that each of this thread's rows sees.
         int lim[4];
@@ -158,34 +154,24 @@ __global__ void __launch_bounds__(kThreadsSimt, kCtasPerSm) kda_attn_simt_kernel
                         }
                     } else {
                         const size_t row = (size_t)it.q.q0 + at;
-                        xk = load4(gk + row * p.k_stride + (size_t)it.h * p.k_head + c);
-                        xv = load4(gv + row * p.v_stride + (size_t)it.h * p.v_head + c);
+                        xk = load4(gk + row * p.k_stride + (size_t)it.h * D + c);
+                        xv = load4(gv + row * p.v_stride + (size_t)it.h * D + c);
                     }
                 }
-                *reinterpret_cast<float4*>(sk + j * LQ + c) = xk;
+                *reinterpret_cast<float4*>(sk + j * LD + c) = xk;
                 *reinterpret_cast<float4*>(sv + j * LD + c) = xv;
-            }
-            if constexpr (DQ > D) {
-                const float* gr = static_cast<const float*>(p.k_r);
-                constexpr int E4 = (DQ - D) / 4;
-                for (int i = tid; i < kKeys * E4; i += kThreadsSimt) {
-                    const int j = i / E4, c = (i % E4) * 4, at = k0 + j;
-                    float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-                    if (at < keys) x = load4(gr + ((size_t)it.q.q0 + at) * p.kr_stride + c);
-                    *reinterpret_cast<float4*>(sk + j * LQ + D + c) = x;
-                }
             }
             __syncthreads();
             float x[4][4] = {};
 #pragma unroll 4
-            for (int e = 0; e < DQ; e += 4) {
+            for (int e = 0; e < D; e += 4) {
                 float4 a[4], b[4];
 #pragma unroll
                 for (int i = 0; i < 4; i++)
-                    a[i] = *reinterpret_cast<const float4*>(sq + (ty * 4 + i) * LQ + e);
+                    a[i] = *reinterpret_cast<const float4*>(sq + (ty * 4 + i) * LD + e);
 #pragma unroll
                 for (int i = 0; i < 4; i++)
-                    b[i] = *reinterpret_cast<const float4*>(sk + (tx + 16 * i) * LQ + e);
+                    b[i] = *reinterpret_cast<const float4*>(sk + (tx + 16 * i) * LD + e);
 #pragma unroll
                 for (int i = 0; i < 4; i++)
 #pragma unroll
@@ -296,7 +282,7 @@ __global__ void __launch_bounds__(kThreadsSimt, kCtasPerSm) kda_attn_simt_kernel
     report_flags(p.d_status, flags);
 }
 
-template <int DQ, int D>
+template <int D>
 cudaError_t launch_t(const AttnArgs& a) {
     const int G = a.Hq / a.Hkv;
     SimtParams p{};
@@ -312,27 +298,22 @@ cudaError_t launch_t(const AttnArgs& a) {
     p.q_stride = a.q_stride;
     p.k_stride = a.k_stride;
     p.v_stride = a.v_stride;
-    p.q_head = a.q_head;
-    p.k_head = a.k_head;
-    p.v_head = a.v_head;
-    p.k_r = a.k_r;
-    p.kr_stride = a.kr_stride;
     p.num_pages = a.num_pages;
     p.page = a.page;
     p.max_pages = a.max_pages;
     p.scale = a.scale;
     p.d_status = a.d_status;
-    cudaError_t e = cudaFuncSetAttribute(kda_attn_simt_kernel<DQ, D>,
+    cudaError_t e = cudaFuncSetAttribute(kda_attn_simt_kernel<D>,
                                          cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         (int)simt_smem<DQ, D>());
+                                         (int)simt_smem<D>());
     if (e != cudaSuccess) return e;
     const int nsm = device_sms();
     p.sp = attn_simt_split(a.N, a.total_q, a.max_q, a.kv_len ? p.s.kv_cap : a.max_q, !a.kv_len, a.Hq,
                            a.Hkv, nsm);
     if (p.sp.ctas && a.ws && a.ws_bytes >= attn_split_bytes(p.sp, D)) p.sp.ws = a.ws;
     const long long grid = p.sp.ws ? p.sp.ctas : std::min(attn_items_bound(p.s), 1LL << 20);
-    e = launch_dependent(kda_attn_simt_kernel<DQ, D>, dim3((unsigned)grid), dim3(kThreadsSimt),
-                         simt_smem<DQ, D>(), a.stream, p);
+    e = launch_dependent(kda_attn_simt_kernel<D>, dim3((unsigned)grid), dim3(kThreadsSimt),
+                         simt_smem<D>(), a.stream, p);
     if (e != cudaSuccess || !p.sp.ws) return e;
     return launch_attn_combine(p.sp, a.Hkv, G, D, kRows, a.o, a.lse, KDA_F32, a.d_status, a.stream);
 }
@@ -357,8 +338,7 @@ AttnSplit attn_simt_split(int N, int total_q, int max_q, long long max_keys, boo
 }
 
 cudaError_t launch_attn_simt(const AttnArgs& a) {
-    if (a.dr) return launch_t<192, 128>(a);
-    return a.d == 128 ? launch_t<128, 128>(a) : launch_t<64, 64>(a);
+    return a.d == 128 ? launch_t<128>(a) : launch_t<64>(a);
 }
 
 }  // namespace kda

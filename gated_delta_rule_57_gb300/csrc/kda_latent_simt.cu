@@ -7,9 +7,10 @@
 // 32 rows (token, head) and takes 32 keys at a time through shared memory, the next 32
 // on their way (cp.async) meanwhile; the same tile is keys, then values.
 //   Scores: a thread has 4 rows x 4 keys over every fourth 16-byte vector of the
-//     channels, 8 loads for 64 FFMA; four neighbouring lanes add up.
-//   Outputs: a thread has 8 rows x 8 channels, 4 loads for 64 FFMA.
-// Bound by shared memory and the FFMA pipe alike. Long rows are cut into ranges
+//     channels, 8 loads for 64 multiply-adds; four neighbouring lanes add up.
+//   Outputs: a thread has 8 rows x 8 channels, 4 loads for 64 multiply-adds.
+// Two of them run in one instruction (fma.rn.f32x2). Where a call has no more than 8 rows a
+// tile (single tokens of few heads) the row tile is 8. Long rows are cut into ranges
 // as the header of kda_attn.cuh says.
 #include <algorithm>
 #include <atomic>
@@ -20,8 +21,7 @@
 namespace kda {
 namespace {
 
-constexpr int kRows = kLatentSimtRows, kKeys = 32, kThreads = 256, kDL = kLatentDim;
-constexpr int kLP = kRows + 4;  // floats between keys of the probabilities
+constexpr int kKeys = 32, kThreads = 256, kDL = kLatentDim;
 
 struct LatentSimtParams {
     AttnShape s;
@@ -37,10 +37,13 @@ struct LatentSimtParams {
     int* d_status;
 };
 
-template <int DR>
+// RT rows of a row tile: 32, or 8 where no more are needed.
+template <int DR, int RT>
 struct SimtCfg {
     static constexpr int DQ = kDL + DR, LD = DQ + 16;  // rows 16 banks apart
-    static constexpr size_t SMEM = ((size_t)3 * kRows * LD + kKeys * kLP) * 4;
+    static constexpr int LP = RT + 4;                  // floats between keys of the probabilities
+    static constexpr int P = kKeys * LP * 4 > kAttnGroups * 8 ? kKeys * LP : kAttnGroups * 2;  // floats
+    static constexpr size_t SMEM = ((size_t)(RT + 2 * kKeys) * LD + P) * 4;
 };
 
 __device__ __forceinline__ void copy16(float* dst, const float* src, bool there) {
@@ -57,24 +60,35 @@ __device__ __forceinline__ void copies_wait() {
 }
 __device__ __forceinline__ float4 ld4(const float* p) { return *reinterpret_cast<const float4*>(p); }
 
-template <int DR>
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+    float2 d;
+    asm("{\n\t.reg .b64 a, b, c, d;\n\t"
+        "mov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\tmov.b64 c, {%6, %7};\n\t"
+        "fma.rn.f32x2 d, a, b, c;\n\tmov.b64 {%0, %1}, d;\n\t}"
+        : "=f"(d.x), "=f"(d.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+    return d;
+}
+
+template <int DR, int RT>
 __global__ void __launch_bounds__(kThreads, 1) kda_latent_simt_kernel(const LatentSimtParams p) {
-    using C = SimtCfg<DR>;
-    constexpr int LD = C::LD, V4 = C::DQ / 4;
+    using C = SimtCfg<DR, RT>;
+    constexpr int LD = C::LD, V4 = C::DQ / 4, LP = C::LP;
+    constexpr int RI = RT / 8, RO = RT / 4;  // rows of a thread in the first, in the second product
     extern __shared__ __align__(16) float sm[];
     float* sq = sm;
-    float* skv = sq + kRows * LD;           // two tiles
+    float* skv = sq + RT * LD;              // two tiles
     float* sp = skv + 2 * kKeys * LD;       // probabilities [key][row]
     long long* groups = reinterpret_cast<long long*>(sp);  // before the first item
-    static_assert(kAttnGroups * 8 <= kKeys * kLP * 4, "groups fit the probabilities");
     __shared__ long long s_sum[kThreads / 32];
-    __shared__ float s_corr[kRows];
-    __shared__ int s_lim[kRows];
+    __shared__ float s_corr[RT];
+    __shared__ int s_lim[RT];
 
     pdl_wait();
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int part = lane & 3, kg = lane >> 2;      // scores: channels, keys kg + 8 j, rows warp + 8 i
-    const int r8 = (tid >> 6) * 8, c4 = (tid & 63) * 4;  // outputs: rows r8 .. + 7, channels c4 .., 256 + c4 ..
+    const int r0 = (tid >> 6) * RO, c4 = (tid & 63) * 4;  // outputs: rows r0 .., channels c4 .., 256 + c4 ..
+    const int log2_page = __ffs(p.page) - 1;
     const AttnShape& s = p.s;
     const float c = p.scale * 1.44269504089f;
     int flags = 0;
@@ -125,40 +139,41 @@ __global__ void __launch_bounds__(kThreads, 1) kda_latent_simt_kernel(const Late
         }
         const size_t first = (size_t)it.q.q0 + tok0;  // packed token of row 0
         __syncthreads();  // the item before is done with shared memory
-        for (int i = tid; i < kRows * V4; i += kThreads) {
+        for (int i = tid; i < RT * V4; i += kThreads) {
             const int r = i / V4, x = (i - r * V4) * 4;
             const bool there = r < rows;
             copy16(sq + r * LD + x,
                    there ? p.q + (first + r / G) * p.q_stride + (size_t)(it.h * G + r % G) * p.q_head + x : p.q, there);
         }
         const int seen0 = it.q.kv - it.q.q_len + tok0;  // keys that row 0's token sees, less one
-        if (tid < kRows) s_lim[tid] = tid < rows ? max(seen0 + tid / G + 1, 0) : 0;
+        if (tid < RT) s_lim[tid] = tid < rows ? max(seen0 + tid / G + 1, 0) : 0;
         auto fetch = [&](int k0, int buf) {
-            if (k0 < keys)
-                for (int i = tid; i < kKeys * V4; i += kThreads) {
-                    const int j = i / V4, x = (i - j * V4) * 4, at = k0 + j;
-                    const float* src = p.cache;
-                    bool there = at < keys;
-                    if (there) {
-                        const int id = p.block_table[(size_t)it.r * p.max_pages + at / p.page];
-                        there = id >= 0 && id < p.num_pages;
-                        if (there) src += ((size_t)id * p.page + at % p.page) * C::DQ + x;
-                        else flags |= KDA_DEV_PAGES;
-                    }
-                    copy16(skv + (buf * kKeys + j) * LD + x, src, there);
+            if (k0 < keys) {  // eight threads a key
+                const int j = tid >> 3, at = k0 + j;
+                const float* src = p.cache;
+                bool there = at < keys;
+                if (there) {
+                    const int id = p.block_table[(size_t)it.r * p.max_pages + (at >> log2_page)];
+                    there = id >= 0 && id < p.num_pages;
+                    if (there) src += (((size_t)id << log2_page) + (at & (p.page - 1))) * C::DQ;
+                    else flags |= KDA_DEV_PAGES;
                 }
+                float* dst = skv + (buf * kKeys + j) * LD;
+                for (int x = (tid & 7) * 4; x < C::DQ; x += 32) copy16(dst + x, there ? src + x : src, there);
+            }
             copies_end();
         };
-        float m[4], l[4], acc[8][8];
+        float m[RI], l[RI];
+        float2 acc[RO][4];
 #pragma unroll
-        for (int i = 0; i < 4; i++) {
+        for (int i = 0; i < RI; i++) {
             m[i] = -INFINITY;
             l[i] = 0.f;
         }
 #pragma unroll
-        for (int i = 0; i < 8; i++)
+        for (int i = 0; i < RO; i++)
 #pragma unroll
-            for (int e = 0; e < 8; e++) acc[i][e] = 0.f;
+            for (int e = 0; e < 4; e++) acc[i][e] = make_float2(0.f, 0.f);
         fetch(key0, 0);
         int buf = 0;
         for (int k0 = key0; k0 < keys; k0 += kKeys, buf ^= 1) {
@@ -166,30 +181,34 @@ __global__ void __launch_bounds__(kThreads, 1) kda_latent_simt_kernel(const Late
             copies_wait<1>();
             __syncthreads();
             const float* kv = skv + buf * kKeys * LD;
-            float x[4][4] = {};
+            float2 y[RI][4];
+#pragma unroll
+            for (int i = 0; i < RI; i++)
+#pragma unroll
+                for (int j = 0; j < 4; j++) y[i][j] = make_float2(0.f, 0.f);
 #pragma unroll 2
             for (int e = part * 4; e < C::DQ; e += 16) {
-                float4 a[4], b[4];
-#pragma unroll
-                for (int i = 0; i < 4; i++) a[i] = ld4(sq + (warp + 8 * i) * LD + e);
+                float4 b[4];
 #pragma unroll
                 for (int j = 0; j < 4; j++) b[j] = ld4(kv + (kg + 8 * j) * LD + e);
 #pragma unroll
-                for (int i = 0; i < 4; i++)
+                for (int i = 0; i < RI; i++) {
+                    const float4 a = ld4(sq + (warp + 8 * i) * LD + e);
 #pragma unroll
                     for (int j = 0; j < 4; j++) {
-                        x[i][j] = fmaf(a[i].x, b[j].x, x[i][j]);
-                        x[i][j] = fmaf(a[i].y, b[j].y, x[i][j]);
-                        x[i][j] = fmaf(a[i].z, b[j].z, x[i][j]);
-                        x[i][j] = fmaf(a[i].w, b[j].w, x[i][j]);
+                        y[i][j] = fma2(make_float2(a.x, a.y), make_float2(b[j].x, b[j].y), y[i][j]);
+                        y[i][j] = fma2(make_float2(a.z, a.w), make_float2(b[j].z, b[j].w), y[i][j]);
                     }
+                }
             }
+            float x[RI][4];
 #pragma unroll
-            for (int i = 0; i < 4; i++) {
+            for (int i = 0; i < RI; i++) {
                 const int row = warp + 8 * i, lim = s_lim[row];
                 float mx = -INFINITY;
 #pragma unroll
                 for (int j = 0; j < 4; j++) {
+                    x[i][j] = y[i][j].x + y[i][j].y;
                     x[i][j] += __shfl_xor_sync(0xffffffffu, x[i][j], 1);
                     x[i][j] += __shfl_xor_sync(0xffffffffu, x[i][j], 2);
                     x[i][j] = k0 + kg + 8 * j < lim ? x[i][j] * c : -INFINITY;
@@ -209,36 +228,42 @@ __global__ void __launch_bounds__(kThreads, 1) kda_latent_simt_kernel(const Late
                     l[i] += e;  // of this lane's keys
                     e4 = part == j ? e : e4;
                 }
-                sp[(kg + 8 * part) * kLP + row] = e4;  // the four lanes have the same sums
+                sp[(kg + 8 * part) * LP + row] = e4;  // the four lanes have the same sums
                 if (lane == 0) s_corr[row] = corr;
             }
             __syncthreads();
-            float f[8];
 #pragma unroll
-            for (int i = 0; i < 8; i++) f[i] = s_corr[r8 + i];
+            for (int i = 0; i < RO; i++) {
+                const float f = s_corr[r0 + i];
 #pragma unroll
-            for (int i = 0; i < 8; i++)
-#pragma unroll
-                for (int e = 0; e < 8; e++) acc[i][e] *= f[i];
+                for (int e = 0; e < 4; e++) {
+                    acc[i][e].x *= f;
+                    acc[i][e].y *= f;
+                }
+            }
             // Keys that only some rows see add nothing to the others, whatever they hold.
             const bool edge = k0 + kKeys > seen0 + 1;
             auto add = [&](bool guard) {
-#pragma unroll 2
+#pragma unroll 4
                 for (int j = 0; j < kKeys; j++) {
                     const float4 v0 = ld4(kv + j * LD + c4), v1 = ld4(kv + j * LD + 256 + c4);
-                    const float4 p0 = ld4(sp + j * kLP + r8), p1 = ld4(sp + j * kLP + r8 + 4);
-                    const float w[8] = {p0.x, p0.y, p0.z, p0.w, p1.x, p1.y, p1.z, p1.w};
+                    float w[RO];
+                    if constexpr (RO == 8) {
+                        const float4 p0 = ld4(sp + j * LP + r0), p1 = ld4(sp + j * LP + r0 + 4);
+                        w[0] = p0.x, w[1] = p0.y, w[2] = p0.z, w[3] = p0.w;
+                        w[4] = p1.x, w[5] = p1.y, w[6] = p1.z, w[7] = p1.w;
+                    } else {
 #pragma unroll
-                    for (int i = 0; i < 8; i++) {
-                        if (guard && k0 + j >= s_lim[r8 + i]) continue;
-                        acc[i][0] = fmaf(w[i], v0.x, acc[i][0]);
-                        acc[i][1] = fmaf(w[i], v0.y, acc[i][1]);
-                        acc[i][2] = fmaf(w[i], v0.z, acc[i][2]);
-                        acc[i][3] = fmaf(w[i], v0.w, acc[i][3]);
-                        acc[i][4] = fmaf(w[i], v1.x, acc[i][4]);
-                        acc[i][5] = fmaf(w[i], v1.y, acc[i][5]);
-                        acc[i][6] = fmaf(w[i], v1.z, acc[i][6]);
-                        acc[i][7] = fmaf(w[i], v1.w, acc[i][7]);
+                        for (int i = 0; i < RO; i++) w[i] = sp[j * LP + r0 + i];
+                    }
+#pragma unroll
+                    for (int i = 0; i < RO; i++) {
+                        if (guard && k0 + j >= s_lim[r0 + i]) continue;
+                        const float2 ww = make_float2(w[i], w[i]);
+                        acc[i][0] = fma2(ww, make_float2(v0.x, v0.y), acc[i][0]);
+                        acc[i][1] = fma2(ww, make_float2(v0.z, v0.w), acc[i][1]);
+                        acc[i][2] = fma2(ww, make_float2(v1.x, v1.y), acc[i][2]);
+                        acc[i][3] = fma2(ww, make_float2(v1.z, v1.w), acc[i][3]);
                     }
                 }
             };
@@ -249,7 +274,7 @@ __global__ void __launch_bounds__(kThreads, 1) kda_latent_simt_kernel(const Late
         copies_wait<0>();
         __syncthreads();  // (an item without keys: limits are written)
 #pragma unroll
-        for (int i = 0; i < 4; i++) {
+        for (int i = 0; i < RI; i++) {
             const int row = warp + 8 * i;
 #pragma unroll
             for (int o = 4; o < 32; o <<= 1) l[i] += __shfl_xor_sync(0xffffffffu, l[i], o);
@@ -262,19 +287,22 @@ __global__ void __launch_bounds__(kThreads, 1) kda_latent_simt_kernel(const Late
         }
         __syncthreads();
 #pragma unroll
-        for (int i = 0; i < 8; i++) {
-            const int row = r8 + i;
+        for (int i = 0; i < RO; i++) {
+            const int row = r0 + i;
             if (row >= rows) break;
             const float inv = s_corr[row];
             const size_t at = (first + row / G) * s.Hkv * G + it.h * G + row % G;
-            float* y = dst ? dst + (size_t)row * kDL : p.o + at * kDL;
+            float* o = dst ? dst + (size_t)row * kDL : p.o + at * kDL;
+            float4 y[2];
 #pragma unroll
-            for (int e = 0; e < 8; e++) {
-                acc[i][e] = inv == 0.f ? 0.f : acc[i][e] * inv;  // (a row of no weight: zeros)
-                flags |= finite_flag(acc[i][e]);
+            for (int e = 0; e < 2; e++) {
+                const float2 a = acc[i][2 * e], b = acc[i][2 * e + 1];
+                // (a row of no weight: zeros)
+                y[e] = inv == 0.f ? make_float4(0.f, 0.f, 0.f, 0.f) : make_float4(a.x * inv, a.y * inv, b.x * inv, b.y * inv);
+                flags |= finite_flag(y[e].x) | finite_flag(y[e].y) | finite_flag(y[e].z) | finite_flag(y[e].w);
             }
-            *reinterpret_cast<float4*>(y + c4) = make_float4(acc[i][0], acc[i][1], acc[i][2], acc[i][3]);
-            *reinterpret_cast<float4*>(y + 256 + c4) = make_float4(acc[i][4], acc[i][5], acc[i][6], acc[i][7]);
+            *reinterpret_cast<float4*>(o + c4) = y[0];
+            *reinterpret_cast<float4*>(o + 256 + c4) = y[1];
         }
         if (split) {
             cur = last < tiles ? end
@@ -295,10 +323,11 @@ __global__ void __launch_bounds__(kThreads, 1) kda_latent_simt_kernel(const Late
     report_flags(p.d_status, flags);
 }
 
-template <int DR>
+template <int DR, int RT>
 cudaError_t launch_t(const AttnArgs& a) {
+    using C = SimtCfg<DR, RT>;
     LatentSimtParams p{};
-    const int blocks = latent_head_blocks(a.Hq, kRows), G = a.Hq / blocks, tok = kRows / G;
+    const int blocks = latent_head_blocks(a.Hq, RT), G = a.Hq / blocks, tok = RT / G;
     int dev = 0;
     const int nsm = device_sms(&dev);
     p.s = {a.cu_q, a.kv_len, a.N, a.total_q, a.max_q, attn_kv_cap(a), blocks, G, tok, tok, kKeys, 1, 1, 0};
@@ -315,15 +344,15 @@ cudaError_t launch_t(const AttnArgs& a) {
     p.scale = a.scale;
     p.d_status = a.d_status;
     static std::atomic<uint64_t> ready{0};
-    cudaError_t e = allow_shared(kda_latent_simt_kernel<DR>, SimtCfg<DR>::SMEM, ready, dev);
+    cudaError_t e = allow_shared(kda_latent_simt_kernel<DR, RT>, C::SMEM, ready, dev);
     if (e != cudaSuccess) return e;
     p.sp = latent_simt_split(a.N, a.total_q, a.max_q, p.s.kv_cap, a.Hq, nsm);
     if (p.sp.ctas && a.ws && a.ws_bytes >= attn_split_bytes(p.sp, kDL)) p.sp.ws = a.ws;
     const long long grid = p.sp.ws ? p.sp.ctas : std::min(attn_items_bound(p.s), 1LL << 20);
-    e = launch_dependent(kda_latent_simt_kernel<DR>, dim3((unsigned)grid), dim3(kThreads), SimtCfg<DR>::SMEM,
+    e = launch_dependent(kda_latent_simt_kernel<DR, RT>, dim3((unsigned)grid), dim3(kThreads), C::SMEM,
                          a.stream, p);
     if (e != cudaSuccess || !p.sp.ws) return e;
-    return launch_attn_combine(p.sp, blocks, G, kDL, kRows, a.o, a.lse, KDA_F32, a.d_status, a.stream);
+    return launch_attn_combine(p.sp, blocks, G, kDL, RT, a.o, a.lse, KDA_F32, a.d_status, a.stream);
 }
 
 }  // namespace
@@ -331,7 +360,7 @@ cudaError_t launch_t(const AttnArgs& a) {
 AttnSplit latent_simt_split(int N, int total_q, int max_q, long long max_keys, int Hq, int nsm) {
     AttnSplit sp{};
     if (N == 0 || total_q == 0 || max_q == 0 || Hq == 0 || nsm == 0) return sp;
-    const int blocks = latent_head_blocks(Hq, kRows), G = Hq / blocks, tok = kRows / G;
+    const int rt = latent_simt_rows(max_q, Hq), blocks = latent_head_blocks(Hq, rt), G = Hq / blocks, tok = rt / G;
     if (max_keys <= KDA_ATTN_SHORT_KEYS / 16) return sp;
     if ((long long)total_q / tok * blocks >= 16LL * nsm) return sp;
     sp.ctas = nsm;
@@ -340,6 +369,9 @@ AttnSplit latent_simt_split(int N, int total_q, int max_q, long long max_keys, i
     return sp;
 }
 
-cudaError_t launch_latent_simt(const AttnArgs& a) { return a.dr ? launch_t<64>(a) : launch_t<0>(a); }
+cudaError_t launch_latent_simt(const AttnArgs& a) {
+    if (latent_simt_rows(a.max_q, a.Hq) == 8) return a.dr ? launch_t<64, 8>(a) : launch_t<0, 8>(a);
+    return a.dr ? launch_t<64, 32>(a) : launch_t<0, 32>(a);
+}
 
 }  // namespace kda
