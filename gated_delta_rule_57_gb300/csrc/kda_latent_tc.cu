@@ -221,6 +221,7 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
     if (tid < 4) sh.odd[tid >> 1][tid & 1] = 0;
     tc_fence_before();
     pdl_wait();
+    pdl_launch();  // the join's CTAs may take their places and wait
     // Cost of this CTA's range (split items); also the barrier after the setup.
     long long each = 0;
     if (p.sp.ws) each = attn_cost_each<kThreadsTc>(p.s, p.sp.ctas, p.sp.least, groups, sh.sum);
@@ -799,7 +800,7 @@ AttnSplit latent_tc_split(int N, int total_q, int max_q, long long max_keys, int
     if (max_keys <= KDA_LATENT_SHORT_KEYS) return sp;
     if ((long long)total_q / tok * blocks >= 8LL * nsm) return sp;
     sp.ctas = nsm;
-    sp.least = 256;
+    sp.least = 128;
     sp.rows = ((max_q < tok ? max_q : tok) * G + 3) & ~3;  // whole 16-byte vectors
     return sp;
 }
