@@ -12,8 +12,8 @@
 //
 // A token's angles are turned into cos and sin once (rot / 2 pairs, a thread each) and
 // kept in shared memory for all its heads, while the token's first loads are on their
-// way. The token's work is laid out as items of one 16-byte vector, or two where a
-// pair's halves lie in different vectors, a few for each of its threads.
+// way. The token's work is laid out as items of two 16-byte vectors, a few for each of its
+// threads (with one where pairs are neighbours, the prompt below took 180 us).
 // Bound by HBM: every byte is read and written once.
 #include "kda_host.cuh"
 #include "kda_internal.cuh"
@@ -41,7 +41,7 @@ struct RopeParams {
     const int* pos;
     const long long* turns;
     int T, Hq, Hk, Hv;
-    int v_vec;             // vectors of a head of v
+    int v_vec, v_half;     // vectors of a head of v; half of those of all its heads
     int pairs;             // rot / 2
     int turned, items;     // items of a head of q or k: turned ones, all
     uint32_t items_magic, v_magic;  // of the divisions by items and v_vec
@@ -96,10 +96,9 @@ struct Vec {
 template <typename T, bool HALVES>
 __global__ void __launch_bounds__(kRopeThreads, 4) kda_rope_kernel(const RopeParams p) {
     constexpr int N = Vec<T>::N;
-    constexpr int PP = HALVES ? N : N / 2;  // pairs of a turned item
-    // cos and sin of the tokens' pairs (a token has at least 32 threads): two pairs a
-    // vector, vector c of item i at c * turned + i, so that neighbouring lanes read
-    // neighbouring vectors.
+    // cos and sin of the tokens' pairs (a token has at least 32 threads), an item's N in the
+    // order of its use: two pairs a vector, vector c of item i at c * turned + i, so that
+    // neighbouring lanes read neighbouring vectors.
     __shared__ float4 s_cs[kRopeThreads / 32][kRopeMaxRot / 4];
     pdl_wait();
     const int tpt = 1 << p.tpt_log2;
@@ -108,10 +107,11 @@ __global__ void __launch_bounds__(kRopeThreads, 4) kda_rope_kernel(const RopePar
     const bool live = t64 < p.T;
     const int t = live ? (int)t64 : 0;
     const int slot = p.slot[t];
-    const int half = HALVES ? p.turned : 0;  // vectors between a pair's halves
+    const int half = p.turned;  // vectors of half of a head's turned channels
     // Items 0 .. nqk - 1: of queries and keys, a head after the other. A turned one i of a
-    // head has vectors i and i + half, the others copy one vector. Then values.
-    const int nqk = (p.Hq + p.Hk) * p.items, n = live ? nqk + p.Hv * p.v_vec : 0;
+    // head has vectors i and i + half, the others copy one vector. Then values, vectors i and
+    // i + v_half.
+    const int nqk = (p.Hq + p.Hk) * p.items, n = live ? nqk + p.v_half : 0;
     uint4 a[kRopeBatch], b[kRopeBatch];
     auto load = [&](int e0) {
 #pragma unroll
@@ -123,9 +123,11 @@ __global__ void __launch_bounds__(kRopeThreads, 4) kda_rope_kernel(const RopePar
                                              : p.q.p + t * p.q.tok + h * p.q.head;
                 src += i < p.turned ? i : i + half;  // (what is copied follows both halves)
                 a[j] = __ldcs(src);
-                if (HALVES && i < p.turned) b[j] = __ldcs(src + half);
+                if (i < p.turned) b[j] = __ldcs(src + half);
             } else if (e < n) {
-                a[j] = __ldcs(p.v.p + t * p.v.tok + (e - nqk));
+                const uint4* src = p.v.p + t * p.v.tok + (e - nqk);
+                a[j] = __ldcs(src);
+                b[j] = __ldcs(src + p.v_half);
             }
         }
     };
@@ -136,7 +138,12 @@ __global__ void __launch_bounds__(kRopeThreads, 4) kda_rope_kernel(const RopePar
             const unsigned long long turn = pos * (unsigned long long)p.turns[i];
             float s, c;
             sincospif((float)(int)(turn >> 32) * 0x1p-31f, &s, &c);
-            const int u = i / PP, w = i % PP;
+            int u = i / N, w = i % N;
+            if (!HALVES) {  // pair i is in vector i / (N / 2)
+                u = i / (N / 2);
+                w = i % (N / 2) + (u < half ? 0 : N / 2);
+                u -= u < half ? 0 : half;
+            }
             reinterpret_cast<float2*>(&s_cs[sub][(w >> 1) * p.turned + u])[w & 1] = make_float2(c, s);
         }
         __syncthreads();
@@ -150,39 +157,41 @@ __global__ void __launch_bounds__(kRopeThreads, 4) kda_rope_kernel(const RopePar
             const int e = e0 + j * tpt;
             if (e >= n) continue;
             if (e >= nqk) {
-                const int v = e - nqk, h = divide(v, p.v_magic);
-                if (stored) p.v_cache[at + h * p.c_head + (v - h * p.v_vec)] = a[j];
+                if (!stored) continue;
+                int v = e - nqk, h = divide(v, p.v_magic);
+                p.v_cache[at + h * p.c_head + (v - h * p.v_vec)] = a[j];
+                v += p.v_half;
+                h = divide(v, p.v_magic);
+                p.v_cache[at + h * p.c_head + (v - h * p.v_vec)] = b[j];
                 continue;
             }
             const int h = divide(e, p.items_magic), i = e - h * p.items;
             const bool turned = i < p.turned;
             if (turned) {
                 const float4* cs = &s_cs[sub][i];
-                Vec<T> u(a[j]), w(HALVES ? b[j] : a[j]);
+                Vec<T> u(a[j]), w(b[j]);
 #pragma unroll
-                for (int c = 0; c < PP; c += 2) {
+                for (int c = 0; c < N; c += 2) {
                     const float4 x = cs[(c >> 1) * p.turned];
-                    if (HALVES) {
-                        const float a0 = u.x[c], a1 = u.x[c + 1], b0 = w.x[c], b1 = w.x[c + 1];
-                        u.x[c] = a0 * x.x - b0 * x.y;
-                        w.x[c] = a0 * x.y + b0 * x.x;
-                        u.x[c + 1] = a1 * x.z - b1 * x.w;
-                        w.x[c + 1] = a1 * x.w + b1 * x.z;
-                    } else {
-                        const float a0 = w.x[2 * c], b0 = w.x[2 * c + 1], a1 = w.x[2 * c + 2], b1 = w.x[2 * c + 3];
-                        u.x[2 * c] = a0 * x.x - b0 * x.y;
-                        u.x[2 * c + 1] = a0 * x.y + b0 * x.x;
-                        u.x[2 * c + 2] = a1 * x.z - b1 * x.w;
-                        u.x[2 * c + 3] = a1 * x.w + b1 * x.z;
-                    }
+                    // two pairs: of channels c and c + 1 of both vectors, or four of one of them
+                    float* y = c < N / 2 ? u.x + 2 * c : w.x + 2 * c - N;
+                    float& a0 = HALVES ? u.x[c] : y[0];
+                    float& b0 = HALVES ? w.x[c] : y[1];
+                    float& a1 = HALVES ? u.x[c + 1] : y[2];
+                    float& b1 = HALVES ? w.x[c + 1] : y[3];
+                    const float c0 = a0, c1 = a1;
+                    a0 = c0 * x.x - b0 * x.y;
+                    b0 = c0 * x.y + b0 * x.x;
+                    a1 = c1 * x.z - b1 * x.w;
+                    b1 = c1 * x.w + b1 * x.z;
                 }
                 a[j] = u.pack();
-                if (HALVES) b[j] = w.pack();
+                b[j] = w.pack();
             }
             auto put = [&](uint4* dst) {
                 dst += turned ? i : i + half;
                 *dst = a[j];
-                if (HALVES && turned) dst[half] = b[j];
+                if (turned) dst[half] = b[j];
             };
             if (h < p.Hq) {
                 put(p.q_out.p + t * p.q_out.tok + h * p.q_out.head);
@@ -215,7 +224,8 @@ bool rows_meet(const Rows& a, const Rows& b) {
 }
 
 cudaError_t launch_rope(RopeParams& p, kda_dtype_t io, cudaStream_t stream) {
-    const int work = (p.Hq + p.Hk) * p.items + p.Hv * p.v_vec;
+    p.v_half = p.Hv * p.v_vec / 2;  // (v_vec is even)
+    const int work = (p.Hq + p.Hk) * p.items + p.v_half;
     p.tpt_log2 = 5;
     while (p.tpt_log2 < 8 && (work >> p.tpt_log2) > kRopeBatch) p.tpt_log2++;
     p.items_magic = magic_of(p.items);
@@ -232,7 +242,7 @@ cudaError_t launch_rope(RopeParams& p, kda_dtype_t io, cudaStream_t stream) {
 void head_items(RopeParams* p, int d, int rot, int neighbours, int V) {
     p->pairs = rot / 2;
     p->neighbours = neighbours != 0;
-    p->turned = neighbours ? rot / V : rot / 2 / V;
+    p->turned = rot / 2 / V;
     p->items = p->turned + (d - rot) / V;
 }
 
