@@ -261,10 +261,11 @@ extern "C" {
 
 kda_status_t kda_kv_append_rope(const void* q, const void* k, const void* v, const int* slot_map,
                                 const int* positions, const long long* turns, void* k_cache,
-                                void* v_cache, void* q_out, int T, int Hq, int Hkv, int d, int rot,
-                                int neighbours, long long q_stride, long long k_stride,
-                                long long v_stride, long long q_out_stride, int num_pages,
-                                int page_size, kda_dtype_t io, int* d_status, void* stream) {
+                                void* v_cache, void* q_out, void* k_out, int T, int Hq, int Hkv, int d,
+                                int rot, int neighbours, long long q_stride, long long k_stride,
+                                long long v_stride, long long q_out_stride, long long k_out_stride,
+                                int num_pages, int page_size, kda_dtype_t io, int* d_status,
+                                void* stream) {
     NvtxRange nvtx_range("kda_kv_append_rope");
     if (T < 0 || Hq < 0 || Hkv < 0 || num_pages < 0 || page_size < 1)
         return fail(KDA_ERR_INVALID_ARG, "T, Hq, Hkv and num_pages must be >= 0, page_size positive");
@@ -281,7 +282,7 @@ kda_status_t kda_kv_append_rope(const void* q, const void* k, const void* v, con
     if ((Hq > 0 && (!q || !q_out)) || (Hkv > 0 && (!k || !v || ((!k_cache || !v_cache) && num_pages > 0))) ||
         !slot_map || !positions || !turns)
         return fail(KDA_ERR_INVALID_ARG, "a NULL pointer");
-    for (const void* x : {q, k, v, (const void*)k_cache, (const void*)v_cache, (const void*)q_out})
+    for (const void* x : {q, k, v, (const void*)k_cache, (const void*)v_cache, (const void*)q_out, (const void*)k_out})
         if (!aligned16(x)) return fail(KDA_ERR_INVALID_ARG, "pointers must be 16-byte aligned");
     if (reinterpret_cast<uintptr_t>(turns) & 7u)
         return fail(KDA_ERR_INVALID_ARG, "turns must be 8-byte aligned");
@@ -295,6 +296,7 @@ kda_status_t kda_kv_append_rope(const void* q, const void* k, const void* v, con
     if (Hkv > 0)
         for (long long s : {k_stride, v_stride})
             if ((st = check_stride(s, (long long)Hkv * d, esz)) != KDA_OK) return st;
+    if (k_out && (st = check_stride(k_out_stride, (long long)Hkv * d, esz)) != KDA_OK) return st;
     size_t n_c;
     if (!mul_ok(&n_c, num_pages, page_size, (size_t)Hkv * d, esz))
         return fail(KDA_ERR_INVALID_ARG, "tensor size overflow");
@@ -303,21 +305,25 @@ kda_status_t kda_kv_append_rope(const void* q, const void* k, const void* v, con
         in_v{v, rk, v_stride * esz, Hkv ? T : 0}, s{slot_map, t4, t4, 1}, ps{positions, t4, t4, 1},
         tn{turns, (size_t)rot * 4, (size_t)rot * 4, 1};
     const Rows kc{k_cache, n_c, n_c, 1}, vc{v_cache, n_c, n_c, 1},
-        out{q_out, rq, q_out_stride * esz, Hq ? T : 0};
-    const bool in_place = q == q_out && q_stride == q_out_stride;
-    if (!in_place && rows_meet(out, in_q)) return fail(KDA_ERR_INVALID_ARG, "q_out overlaps q");
-    for (const Rows& c : {kc, vc, out}) {
-        for (const Rows& x : {in_k, in_v, s, ps, tn})
-            if (rows_meet(c, x)) return fail(KDA_ERR_INVALID_ARG, "a cache or q_out overlaps an input");
-        if (c.p != q_out && rows_meet(c, in_q)) return fail(KDA_ERR_INVALID_ARG, "a cache overlaps q");
-    }
-    if (rows_meet(kc, vc) || rows_meet(kc, out) || rows_meet(vc, out))
-        return fail(KDA_ERR_INVALID_ARG, "the caches and q_out overlap");
+        qo{q_out, rq, q_out_stride * esz, Hq ? T : 0}, ko{k_out, rk, k_out_stride * esz, k_out && Hkv ? T : 0};
+    const bool q_in_place = q == q_out && q_stride == q_out_stride;
+    const bool k_in_place = k == k_out && k_stride == k_out_stride;
+    bool meet = (!q_in_place && rows_meet(qo, in_q)) || (!k_in_place && rows_meet(ko, in_k));
+    meet |= rows_meet(qo, in_k) || rows_meet(ko, in_q);
+    for (const Rows& o : {kc, vc})
+        for (const Rows& x : {in_q, in_k}) meet |= rows_meet(o, x);
+    for (const Rows& o : {kc, vc, qo, ko})
+        for (const Rows& x : {in_v, s, ps, tn}) meet |= rows_meet(o, x);
+    if (meet) return fail(KDA_ERR_INVALID_ARG, "a cache, q_out or k_out overlaps an input");
+    if (rows_meet(kc, vc) || rows_meet(kc, qo) || rows_meet(vc, qo) || rows_meet(kc, ko) || rows_meet(vc, ko) ||
+        rows_meet(qo, ko))
+        return fail(KDA_ERR_INVALID_ARG, "the caches, q_out and k_out overlap");
     const int V = (int)(16 / esz), dv = d / V;
     RopeParams p{};
     p.q = {static_cast<uint4*>(const_cast<void*>(q)), q_stride / V, dv};
     p.q_out = {static_cast<uint4*>(q_out), q_out_stride / V, dv};
     p.k = {static_cast<uint4*>(const_cast<void*>(k)), k_stride / V, dv};
+    p.k_out = {static_cast<uint4*>(k_out), k_out_stride / V, dv};
     p.v = {static_cast<uint4*>(const_cast<void*>(v)), v_stride / V, dv};
     p.k_cache = static_cast<uint4*>(k_cache);
     p.v_cache = static_cast<uint4*>(v_cache);

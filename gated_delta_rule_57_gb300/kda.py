@@ -139,7 +139,7 @@ def lib(build_if_missing: bool = True) -> ctypes.CDLL:
             L.kda_attn_paged.argtypes = [vp] * 8 + [I] * 6 + [ll] + [I] * 3 + [f, I, vp, sz, vp,
                                                                               vp]
             L.kda_attn_paged.restype = I
-            L.kda_kv_append_rope.argtypes = [vp] * 9 + [I] * 6 + [ll] * 4 + [I, I, I, vp, vp]
+            L.kda_kv_append_rope.argtypes = [vp] * 10 + [I] * 6 + [ll] * 5 + [I, I, I, vp, vp]
             L.kda_kv_append_rope.restype = I
             L.kda_latent_append.argtypes = [vp] * 9 + [I] * 5 + [ll] * 7 + [I, I, I, vp, vp]
             L.kda_latent_append.restype = I

@@ -77,10 +77,11 @@ def _turns(turns: torch.Tensor):
 
 
 def kda_kv_append_rope(q, k, v, slot_map, positions, turns, k_cache, v_cache, *,
-                       neighbours: bool = False, q_out=None, status: Optional[torch.Tensor] = None,
-                       stream=None):
+                       neighbours: bool = False, q_out=None, k_out=None,
+                       status: Optional[torch.Tensor] = None, stream=None):
     """kda_kv_append with rotation by position: q [T, Hq, d] is rotated into q_out (made
-    here when not given; q itself: in place), k rotated and v copied to their slots.
+    here when not given; q itself: in place), k rotated and v copied to their slots; the
+    rotated keys go to k_out [T, Hkv, d] too where one is given (k itself: in place).
     positions: [T] int32; turns: see kda_rope_turns (its length is rot / 2; channels from
     rot on are copied); neighbours: pairs are channels 2 i, 2 i + 1 instead of i,
     i + rot / 2. q may be None. Returns q_out."""
@@ -92,8 +93,10 @@ def kda_kv_append_rope(q, k, v, slot_map, positions, turns, k_cache, v_cache, *,
     T = k.shape[0]
     if v_cache.shape != k_cache.shape or k_cache.dtype != dt or v_cache.dtype != dt:
         raise ValueError("the caches must be [num_pages, Hkv, page_size, d] of k's dtype")
-    qp = op = None
-    Hq = qs = os_ = 0
+    qp = op = kop = None
+    Hq = qs = os_ = kos = 0
+    if k_out is not None:
+        kop, kos = _packed("k_out", k_out, T, Hkv, d, dt)
     if q is not None:
         Hq = q.shape[1]
         qp, qs = _packed("q", q, T, Hq, d, dt)
@@ -106,8 +109,8 @@ def kda_kv_append_rope(q, k, v, slot_map, positions, turns, k_cache, v_cache, *,
     vp, vs = _packed("v", v, T, Hkv, d, dt)
     code = (_k._lib or lib()).kda_kv_append_rope(
         qp, kp, vp, _per_token("slot_map", slot_map, T), _per_token("positions", positions, T), _turns(turns),
-        _k._ptr(k_cache), _k._ptr(v_cache), op, T, Hq, Hkv, d, 2 * turns.numel(), neighbours, qs, ks, vs, os_, pages,
-        page, io, _k._ptr(status), _k._stream(stream))
+        _k._ptr(k_cache), _k._ptr(v_cache), op, kop, T, Hq, Hkv, d, 2 * turns.numel(), neighbours, qs, ks, vs, os_,
+        kos, pages, page, io, _k._ptr(status), _k._stream(stream))
     if code:
         _k._check(code)
     return q_out

@@ -633,6 +633,8 @@ size_t kda_attn_workspace_size(int N, int total_q, int max_q, int Hq, int Hkv, i
  *   k_cache, v_cache : [num_pages, Hkv, page_size, d] (in/out)
  *   q_out         : [T, Hq, d], token stride q_out_stride (out); may be q itself (same
  *                   stride), else may not overlap an input
+ *   k_out         : [T, Hkv, d] or NULL, token stride k_out_stride (out): the rotated keys
+ *                   again, for kda_attn_prompt; may be k itself
  *   rot           : a multiple of 16 in 16 .. d; channels from rot on are copied
  *
  * Strides at most 2^30 elements. The products are in fp32, rounded once. HBM-bound: each byte is read and
@@ -640,10 +642,11 @@ size_t kda_attn_workspace_size(int N, int total_q, int max_q, int Hq, int Hkv, i
  */
 kda_status_t kda_kv_append_rope(const void* q, const void* k, const void* v, const int* slot_map,
                                 const int* positions, const long long* turns, void* k_cache,
-                                void* v_cache, void* q_out, int T, int Hq, int Hkv, int d, int rot,
-                                int neighbours, long long q_stride, long long k_stride,
-                                long long v_stride, long long q_out_stride, int num_pages,
-                                int page_size, kda_dtype_t io, int* d_status, void* stream);
+                                void* v_cache, void* q_out, void* k_out, int T, int Hq, int Hkv, int d,
+                                int rot, int neighbours, long long q_stride, long long k_stride,
+                                long long v_stride, long long q_out_stride, long long k_out_stride,
+                                int num_pages, int page_size, kda_dtype_t io, int* d_status,
+                                void* stream);
 
 /*
  * Write T tokens' latents and rotated key parts to their slots of a latent cache, and

@@ -50,16 +50,18 @@ def test_kv_append_rope(io, neighbours, t, hq, hkv, d, rot, page):
     for i, p, r in live:
         want[p, :, r], size[p, :, r], rv[p, :, r] = rk[i], sk[i], v[i]
     ref_q = latent_ref.rotate(q, pos, freq, neighbours)
-    out = pkg.kda_kv_append_rope(q, k, v, slot, pos, turns, kc, vc, neighbours=neighbours, status=status)
+    again = torch.empty(t, hkv, d, dtype=io, device=DEV)
+    out = pkg.kda_kv_append_rope(q, k, v, slot, pos, turns, kc, vc, neighbours=neighbours, k_out=again, status=status)
     torch.cuda.synchronize()
+    latent_ref.check_rotated(again, (rk, sk))
     latent_ref.check_rotated(out, ref_q)
     latent_ref.check_rotated(kc, (want, size))
     assert torch.equal(vc, rv)
     assert int(status) == (kda.KDA_DEV_PAGES if t > 4 else 0)
-    # the queries in place, in the projection itself
-    back = pkg.kda_kv_append_rope(q, k, v, slot, pos, turns, kc, vc, neighbours=neighbours, q_out=q)
+    # in place, in the projection itself
+    back = pkg.kda_kv_append_rope(q, k, v, slot, pos, turns, kc, vc, neighbours=neighbours, q_out=q, k_out=k)
     torch.cuda.synchronize()
-    assert back is q and torch.equal(q, out)
+    assert back is q and torch.equal(q, out) and torch.equal(k, again)
 
 
 def test_append_without_queries():

@@ -16,8 +16,8 @@ def L():
 
 
 def rope(L, **kw):
-    a = dict(q=A[0], k=A[1], v=A[2], slot=A[3], pos=A[4], turns=A[5], kc=A[6], vc=A[7], out=A[8], T=4, Hq=4, Hkv=2, d=64, rot=64,
-             neighbours=0, qs=256, ks=128, vs=128, os=256, pages=16, page=16, io=kda.KDA_BF16, status=None)
+    a = dict(q=A[0], k=A[1], v=A[2], slot=A[3], pos=A[4], turns=A[5], kc=A[6], vc=A[7], out=A[8], ko=A[10], T=4, Hq=4, Hkv=2, d=64, rot=64,
+             neighbours=0, qs=256, ks=128, vs=128, os=256, kos=128, pages=16, page=16, io=kda.KDA_BF16, status=None)
     a.update(kw)
     return L.kda_kv_append_rope(*a.values(), None)
 
@@ -30,7 +30,8 @@ def rope(L, **kw):
     (dict(slot=None), BAD), (dict(pos=None), BAD), (dict(turns=None), BAD), (dict(vc=None), BAD), (dict(q=A[0] + 8), BAD),
     (dict(kc=A[6] + 4), BAD), (dict(turns=A[5] + 4), BAD), (dict(pos=A[4] + 2), BAD), (dict(status=A[9] + 1), BAD),
     (dict(kc=A[0]), BAD), (dict(vc=A[6] + 1024), BAD), (dict(out=A[1]), BAD), (dict(out=A[4]), BAD), (dict(out=A[0] + 16), BAD),
-    (dict(out=A[0], os=512), BAD), (dict(out=A[6]), BAD),
+    (dict(out=A[0], os=512), BAD), (dict(out=A[6]), BAD), (dict(ko=A[2]), BAD), (dict(ko=A[8]), BAD), (dict(ko=A[1] + 16), BAD), (dict(kos=64), BAD),
+    (dict(ko=A[10] + 8), BAD), (dict(ko=A[7]), BAD),
     (dict(T=0, k=None), OK), (dict(Hq=0, Hkv=0, q=None, k=None), OK),
 ])
 def test_kv_append_rope_refuses(L, kw, code):
