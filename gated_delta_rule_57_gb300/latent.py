@@ -28,9 +28,26 @@ def kda_rope_turns(inv_freq, device="cuda"):
 
 
 def _address(t: torch.Tensor):
-    if not t.is_cuda:
-        raise ValueError("KDA tensors must live on a CUDA device")
+    """Address of a tensor of the current device: where a call's kernels run."""
+    device = t.get_device()
+    if device < 0 or device != torch._C._cuda_getDevice():
+        raise ValueError("KDA tensors must live on the current CUDA device")
     return t.data_ptr()
+
+
+def _ptr(t: Optional[torch.Tensor]):
+    if t is None:
+        return None
+    if not t.is_contiguous():
+        raise ValueError("KDA tensors must be contiguous")
+    return _address(t)
+
+
+def _ints(name: str, t: torch.Tensor, *shape):
+    """Address of an int32 tensor of the given shape."""
+    if t.shape != shape or t.dtype != torch.int32:
+        raise ValueError(f"{name} must be an int32 tensor of shape {shape}")
+    return _ptr(t)
 
 
 def _heads(name: str, t: torch.Tensor, T, H, d, dtype):
@@ -67,13 +84,13 @@ def _per_token(name: str, t: torch.Tensor, T):
     """Address of an int32 tensor with an entry for each of T tokens, or more."""
     if t.dtype != torch.int32 or t.dim() != 1 or t.numel() < T:
         raise ValueError(f"{name} must be an int32 tensor with an entry per token")
-    return _k._ptr(t)
+    return _ptr(t)
 
 
 def _turns(turns: torch.Tensor):
     if turns.dtype != torch.int64 or turns.dim() != 1:
         raise ValueError("turns must be an int64 tensor [rot / 2], as kda_rope_turns makes it")
-    return _k._ptr(turns)
+    return _ptr(turns)
 
 
 def kda_kv_append_rope(q, k, v, slot_map, positions, turns, k_cache, v_cache, *,
@@ -109,8 +126,8 @@ def kda_kv_append_rope(q, k, v, slot_map, positions, turns, k_cache, v_cache, *,
     vp, vs = _packed("v", v, T, Hkv, d, dt)
     code = (_k._lib or lib()).kda_kv_append_rope(
         qp, kp, vp, _per_token("slot_map", slot_map, T), _per_token("positions", positions, T), _turns(turns),
-        _k._ptr(k_cache), _k._ptr(v_cache), op, kop, T, Hq, Hkv, d, 2 * turns.numel(), neighbours, qs, ks, vs, os_,
-        kos, pages, page, io, _k._ptr(status), _k._stream(stream))
+        _ptr(k_cache), _ptr(v_cache), op, kop, T, Hq, Hkv, d, 2 * turns.numel(), neighbours, qs, ks, vs, os_,
+        kos, pages, page, io, _ptr(status), _k._stream(stream))
     if code:
         _k._check(code)
     return q_out
@@ -156,8 +173,8 @@ def kda_latent_append(c, k_r, slot_map, cache, *, positions=None, turns=None, q_
                 q_out = _k._empty((T, Hq, dr), dt, c, stream)
             op, os_, oh = _heads("q_out", q_out, T, Hq, dr, dt)
     code = (_k._lib or lib()).kda_latent_append(
-        cp, kp, qp, _per_token("slot_map", slot_map, T), pp, tp, _k._ptr(cache), op, kop, T, Hq, dl, dr, neighbours,
-        cs, ks, qs, qh, os_, oh, kos, pages, page, io, _k._ptr(status), _k._stream(stream))
+        cp, kp, qp, _per_token("slot_map", slot_map, T), pp, tp, _ptr(cache), op, kop, T, Hq, dl, dr, neighbours,
+        cs, ks, qs, qh, os_, oh, kos, pages, page, io, _ptr(status), _k._stream(stream))
     if code:
         _k._check(code)
     return q_out if q_r is not None else None
@@ -197,9 +214,9 @@ def kda_attn_latent_paged(q, cache, block_table, cu_q, kv_len, *, scale: float, 
     ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
     qp, qs, qh = _heads("q", q, T, Hq, d, q.dtype)
     _k._check((_k._lib or lib()).kda_attn_latent_paged(
-        qp, _k._ptr(cache), _k._ints("block_table", block_table, (N, max_pages)), _k._ints("cu_q", cu_q, (N + 1,)),
-        _k._ints("kv_len", kv_len, (N,)), _k._ptr(o), _k._ptr(lse), N, T, most, Hq, 512, d - 512, qs, qh, pages, page,
-        max_pages, scale, io, _k._ptr(workspace), ws_bytes, _k._ptr(status), _k._stream(stream)))
+        qp, _ptr(cache), _ints("block_table", block_table, N, max_pages), _ints("cu_q", cu_q, N + 1),
+        _ints("kv_len", kv_len, N), _ptr(o), _ptr(lse), N, T, most, Hq, 512, d - 512, qs, qh, pages, page,
+        max_pages, scale, io, _ptr(workspace), ws_bytes, _ptr(status), _k._stream(stream)))
     return o, lse
 
 
@@ -225,7 +242,7 @@ def kda_attn_latent_prompt(q, k, k_r, v, cu_seqlens, *, max_len: Optional[int] =
     vp, vs, vh = _heads("v", v, T, H, d, dt)
     rp, rs = _flat("k_r", k_r, T, dr, dt) if dr else (None, 0)
     _k._check((_k._lib or lib()).kda_attn_latent_prompt(
-        qp, kp, rp, vp, _k._ints("cu_seqlens", cu_seqlens, (N + 1,)), _k._ptr(o), _k._ptr(lse), N, T, most, H, d, dr, qs, qh,
-        ks, kh, rs, vs, vh, dq ** -0.5 if scale is None else scale, io, _k._ptr(workspace), ws_bytes,
-        _k._ptr(status), _k._stream(stream)))
+        qp, kp, rp, vp, _ints("cu_seqlens", cu_seqlens, N + 1), _ptr(o), _ptr(lse), N, T, most, H, d, dr, qs, qh,
+        ks, kh, rs, vs, vh, dq ** -0.5 if scale is None else scale, io, _ptr(workspace), ws_bytes,
+        _ptr(status), _k._stream(stream)))
     return o, lse
