@@ -131,38 +131,34 @@ __global__ void __launch_bounds__(kThreads, 1) kda_latent_prompt_simt_kernel(con
         }
         const size_t first = (size_t)it.q.q0 + tok0;  // packed token of row 0
         __syncthreads();  // the item before is done with shared memory
-        for (int i = tid; i < ROWS * (DQ / 4); i += kThreads) {
-            const int r = i / (DQ / 4), x = (i % (DQ / 4)) * 4;
-            const bool there = r < rows;
-            copy16(sq + r * LQ + x, there ? p.q + (first + r) * p.q_stride + it.h * p.q_head + x : p.q, there);
-        }
+        // Rows of 128 channels, a warp a row; of DR channels, 16 lanes a row.
+        const int wr = tid >> 5, wx = (tid & 31) * 4, hx = tx * 4;
+        auto copy_rows = [&](float* dst, int ld, const float* src, long long stride, int n, int there) {
+#pragma unroll 1
+            for (int j = wr; j < n; j += kThreads / 32)
+                copy16(dst + j * ld + wx, j < there ? src + j * stride + wx : src, j < there);
+        };
+        auto copy_ends = [&](float* dst, int ld, const float* src, long long stride, int n, int there) {
+            if constexpr (DR > 0)
+#pragma unroll 1
+                for (int j = ty; j < n; j += kThreads / 16)
+                    copy16(dst + j * ld + hx, j < there ? src + j * stride + hx : src, j < there);
+        };
+        const float* qh = p.q + first * p.q_stride + it.h * p.q_head;
+        copy_rows(sq, LQ, qh, p.q_stride, ROWS, rows);
+        copy_ends(sq + kD, LQ, qh + kD, p.q_stride, ROWS, rows);
         const float* kh = p.k + (size_t)it.q.q0 * p.k_stride + it.h * p.k_head;
+        const float* rh = DR > 0 ? p.k_r + (size_t)it.q.q0 * p.kr_stride : nullptr;
         const float* vh = p.v + (size_t)it.q.q0 * p.v_stride + it.h * p.v_head;
         auto fetch_keys = [&](int k0) {
             if (k0 < keys) {
-                for (int i = tid; i < kKeys * (kD / 4); i += kThreads) {
-                    const int j = i / (kD / 4), x = (i % (kD / 4)) * 4;
-                    const bool there = k0 + j < keys;
-                    copy16(sk + j * LQ + x, there ? kh + (k0 + j) * p.k_stride + x : p.k, there);
-                }
-                if constexpr (DR > 0) {
-                    for (int i = tid; i < kKeys * (DR / 4); i += kThreads) {
-                        const int j = i / (DR / 4), x = (i % (DR / 4)) * 4;
-                        const bool there = k0 + j < keys;
-                        copy16(sk + j * LQ + kD + x,
-                               there ? p.k_r + ((size_t)it.q.q0 + k0 + j) * p.kr_stride + x : p.k_r, there);
-                    }
-                }
+                copy_rows(sk, LQ, kh + k0 * p.k_stride, p.k_stride, kKeys, keys - k0);
+                if (DR > 0) copy_ends(sk + kD, LQ, rh + k0 * p.kr_stride, p.kr_stride, kKeys, keys - k0);
             }
             copies_end();
         };
         auto fetch_values = [&](int k0) {
-            if (k0 < keys)
-                for (int i = tid; i < kKeys * (kD / 4); i += kThreads) {
-                    const int j = i / (kD / 4), x = (i % (kD / 4)) * 4;
-                    const bool there = k0 + j < keys;
-                    copy16(sv + j * kLV + x, there ? vh + (k0 + j) * p.v_stride + x : p.v, there);
-                }
+            if (k0 < keys) copy_rows(sv, kLV, vh + k0 * p.v_stride, p.v_stride, kKeys, keys - k0);
             copies_end();
         };
         fetch_keys(key0);

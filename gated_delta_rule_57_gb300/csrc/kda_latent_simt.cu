@@ -73,7 +73,7 @@ __device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
 template <int DR, int RT>
 __global__ void __launch_bounds__(kThreads, 1) kda_latent_simt_kernel(const LatentSimtParams p) {
     using C = SimtCfg<DR, RT>;
-    constexpr int LD = C::LD, V4 = C::DQ / 4, LP = C::LP;
+    constexpr int LD = C::LD, LP = C::LP;
     constexpr int RI = RT / 8, RO = RT / 4;  // rows of a thread in the first, in the second product
     extern __shared__ __align__(16) float sm[];
     float* sq = sm;
@@ -139,11 +139,10 @@ __global__ void __launch_bounds__(kThreads, 1) kda_latent_simt_kernel(const Late
         }
         const size_t first = (size_t)it.q.q0 + tok0;  // packed token of row 0
         __syncthreads();  // the item before is done with shared memory
-        for (int i = tid; i < RT * V4; i += kThreads) {
-            const int r = i / V4, x = (i - r * V4) * 4;
+        if (const int r = tid >> 3; r < RT) {  // eight threads a row
             const bool there = r < rows;
-            copy16(sq + r * LD + x,
-                   there ? p.q + (first + r / G) * p.q_stride + (size_t)(it.h * G + r % G) * p.q_head + x : p.q, there);
+            const float* src = there ? p.q + (first + r / G) * p.q_stride + (size_t)(it.h * G + r % G) * p.q_head : p.q;
+            for (int x = (tid & 7) * 4; x < C::DQ; x += 32) copy16(sq + r * LD + x, there ? src + x : src, there);
         }
         const int seen0 = it.q.kv - it.q.q_len + tok0;  // keys that row 0's token sees, less one
         if (tid < RT) s_lim[tid] = tid < rows ? max(seen0 + tid / G + 1, 0) : 0;
