@@ -90,25 +90,15 @@ __global__ void __launch_bounds__(kCombineWarps * 32)
     report_flags(d_status, flags);
 }
 
-// The same for wide rows (D = 512): a warp takes 128 channels of one row. It finds M and
-// the weights first, a part per lane, so that no part's load waits for another's: 8 are in
-// flight.
-template <typename T, int D>
-__global__ void __launch_bounds__(kCombineWarps * 32)
-    kda_attn_combine_wide_kernel(const AttnSplit sp, const int Hkv, const int G, const int tile_rows,
-                                 T* o, float* lse, int* d_status) {
-    pdl_wait();
-    const int b = blockIdx.x + 1;
-    const AttnCut cut = attn_cuts(sp, D)[b];
-    if (cut.ntok == 0 || cut.tile == 0) return;  // no work, or the boundary is an item's too
-    const int c0 = (int)(cut.u0 / cut.each);
-    const int c1 = (int)((cut.u0 + (long long)(cut.n - 1) * cut.cost) / cut.each);
-    const AttnCut start = attn_cuts(sp, D)[c0];
-    const int late = !(start.u0 == cut.u0 && start.tile == 0);
-    constexpr int COLS = D / 128;  // warps of a row
+// The same for wide rows (D = 512): a warp finds M and the weights of a row first, a part per
+// lane, so that no part's load waits for another's. It takes all channels of a row that
+// has few parts, 128 of one that has many; 8 loads are in flight either way.
+// Q: quarters of a row that a warp takes.
+template <typename T, int D, int Q>
+__device__ __forceinline__ int join_rows(const AttnSplit& sp, const AttnCut& cut, int c0, int c1, int late, int first,
+                                         int step, int Hkv, int G, int tile_rows, T* o, float* lse) {
+    constexpr int COLS = D / 128 / Q;  // warps of a row
     const int lane = threadIdx.x & 31, units = cut.ntok * G * COLS, per = tile_rows / G;
-    const int first = ((b - 1 - c0) * gridDim.y + blockIdx.y) * kCombineWarps + (threadIdx.x >> 5);
-    const int step = (c1 - c0) * gridDim.y * kCombineWarps;
     const size_t slot = attn_slot_floats(sp.rows, D);
     auto part = [&](int c) { return sp.ws + slot * (2 * (size_t)c + (c == c0 ? late : 0)); };
     int flags = 0;
@@ -120,7 +110,9 @@ __global__ void __launch_bounds__(kCombineWarps * 32)
 #pragma unroll
         for (int k = 16; k > 0; k >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, k));
         float sum = 0.f;
-        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+        float4 acc[Q];
+#pragma unroll
+        for (int q = 0; q < Q; q++) acc[q] = make_float4(0.f, 0.f, 0.f, 0.f);
         for (int cb = c0; cb <= c1; cb += 32) {
             const int n = min(c1 - cb + 1, 32);
             // (a part in which this row sees nothing has weight 0 and is not read; NaN stays)
@@ -130,33 +122,61 @@ __global__ void __launch_bounds__(kCombineWarps * 32)
                 w = x == -INFINITY ? 0.f : exp2f(x - m);
             }
             sum += w;
-#pragma unroll 8
+#pragma unroll 8 / Q
             for (int k = 0; k < n; k++) {
                 const float wk = __shfl_sync(0xffffffffu, w, k);
                 if (wk == 0.f) continue;
-                const float4 y = *reinterpret_cast<const float4*>(part(cb + k) + (size_t)row * D + col);
-                acc.x = fmaf(wk, y.x, acc.x);
-                acc.y = fmaf(wk, y.y, acc.y);
-                acc.z = fmaf(wk, y.z, acc.z);
-                acc.w = fmaf(wk, y.w, acc.w);
+                const float* y = part(cb + k) + (size_t)row * D + col;
+#pragma unroll
+                for (int q = 0; q < Q; q++) {
+                    const float4 v = *reinterpret_cast<const float4*>(y + 128 * q);
+                    acc[q].x = fmaf(wk, v.x, acc[q].x);
+                    acc[q].y = fmaf(wk, v.y, acc[q].y);
+                    acc[q].z = fmaf(wk, v.z, acc[q].z);
+                    acc[q].w = fmaf(wk, v.w, acc[q].w);
+                }
             }
         }
 #pragma unroll
         for (int k = 16; k > 0; k >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, k);
         const size_t at = ((size_t)cut.tok0 + tok) * Hkv * G + (size_t)cut.h * G + r % G;
         const float inv = sum == 0.f ? 0.f : 1.f / sum;
-        const float y[4] = {acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv};
-        T out[4];
 #pragma unroll
-        for (int e = 0; e < 4; e++) {
-            flags |= finite_flag(y[e]);
-            out[e] = from_f32<T>(y[e]);
+        for (int q = 0; q < Q; q++) {
+            const float y[4] = {acc[q].x * inv, acc[q].y * inv, acc[q].z * inv, acc[q].w * inv};
+            T out[4];
+#pragma unroll
+            for (int e = 0; e < 4; e++) {
+                flags |= finite_flag(y[e]);
+                out[e] = from_f32<T>(y[e]);
+            }
+            T* dst = o + at * D + col + 128 * q;
+            if constexpr (sizeof(T) == 4) *reinterpret_cast<float4*>(dst) = *reinterpret_cast<float4*>(out);
+            else *reinterpret_cast<uint2*>(dst) = *reinterpret_cast<uint2*>(out);
         }
-        if constexpr (sizeof(T) == 4) *reinterpret_cast<float4*>(o + at * D + col) = *reinterpret_cast<float4*>(out);
-        else *reinterpret_cast<uint2*>(o + at * D + col) = *reinterpret_cast<uint2*>(out);
         if (lse && lane == 0 && i % COLS == 0)
             lse[at] = sum == 0.f ? -INFINITY : (m + log2f(sum)) * 0.69314718056f;
     }
+    return flags;
+}
+
+template <typename T, int D>
+__global__ void __launch_bounds__(kCombineWarps * 32, 4)
+    kda_attn_combine_wide_kernel(const AttnSplit sp, const int Hkv, const int G, const int tile_rows,
+                                 T* o, float* lse, int* d_status) {
+    pdl_wait();
+    const int b = blockIdx.x + 1;
+    const AttnCut cut = attn_cuts(sp, D)[b];
+    if (cut.ntok == 0 || cut.tile == 0) return;  // no work, or the boundary is an item's too
+    const int c0 = (int)(cut.u0 / cut.each);
+    const int c1 = (int)((cut.u0 + (long long)(cut.n - 1) * cut.cost) / cut.each);
+    const AttnCut start = attn_cuts(sp, D)[c0];
+    const int late = !(start.u0 == cut.u0 && start.tile == 0);
+    const int first = ((b - 1 - c0) * gridDim.y + blockIdx.y) * kCombineWarps + (threadIdx.x >> 5);
+    const int step = (c1 - c0) * gridDim.y * kCombineWarps;
+    const int flags = c1 - c0 < 4
+                          ? join_rows<T, D, D / 128>(sp, cut, c0, c1, late, first, step, Hkv, G, tile_rows, o, lse)
+                          : join_rows<T, D, 1>(sp, cut, c0, c1, late, first, step, Hkv, G, tile_rows, o, lse);
     report_flags(d_status, flags);
 }
 
@@ -174,8 +194,8 @@ cudaError_t launch_attn_combine(const AttnSplit& sp, int Hkv, int G, int d, int 
                                 rows_per_tile, out, lse, d_status);
     };
     if (d == 512) {
-        // Two passes at most, as one boundary may have to do all of an item.
-        const dim3 wide((unsigned)(sp.ctas - 1), (unsigned)((sp.rows * 4 + 2 * kCombineWarps - 1) / (2 * kCombineWarps)));
+        // A warp for each row, as one boundary may have to do all of an item.
+        const dim3 wide((unsigned)(sp.ctas - 1), (unsigned)((sp.rows + kCombineWarps - 1) / kCombineWarps));
         auto go = [&](auto kernel, auto* out) {
             return launch_dependent(kernel, wide, dim3(kCombineWarps * 32), 0, stream, sp, Hkv, G,
                                     rows_per_tile, out, lse, d_status);
