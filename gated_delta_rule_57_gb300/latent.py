@@ -5,7 +5,6 @@ conventions (streams, what a call makes, errors) hold here too.
 from __future__ import annotations
 
 import ctypes
-import fractions
 from typing import Optional
 
 import torch
@@ -13,7 +12,7 @@ import torch
 from . import kda as _k
 from .kda import KDA_ERR_INVALID_ARG, KDA_F32, KDA_LATENT_SHORT_KEYS, KdaError, lib
 
-_PI = fractions.Fraction("3.14159265358979323846264338327950288419716939937510582097494459")
+_PI = (314159265358979323846264338327950288419716939937510582097494459 << 200) // 10 ** 62  # pi 2^200
 
 
 def kda_rope_turns(inv_freq, device="cuda"):
@@ -23,74 +22,92 @@ def kda_rope_turns(inv_freq, device="cuda"):
     once, on the host."""
     if isinstance(inv_freq, torch.Tensor):
         inv_freq = inv_freq.detach().double().reshape(-1).tolist()
-    turns = [round(fractions.Fraction(float(f)) * 2 ** 63 / _PI) % 2 ** 64 for f in inv_freq]
-    return torch.tensor([t - 2 ** 64 if t >= 2 ** 63 else t for t in turns], dtype=torch.int64, device=device)
+    turns = []
+    for f in inv_freq:
+        n, d = float(f).as_integer_ratio()
+        x = (n << 264) // (d * _PI) + 1 >> 1  # 2^63 f / pi, rounded
+        turns.append((x + 2 ** 63) % 2 ** 64 - 2 ** 63)
+    return torch.tensor(turns, dtype=torch.int64, device=device)
 
 
-def _address(t: torch.Tensor):
-    """Address of a tensor of the current device: where a call's kernels run."""
+def _device(t: torch.Tensor) -> int:
+    """Number of a call's device: its first tensor's, which is to be the current one, where
+    the call's kernels run."""
     device = t.get_device()
     if device < 0 or device != torch._C._cuda_getDevice():
         raise ValueError("KDA tensors must live on the current CUDA device")
+    return device
+
+
+def _ptr(dev: int, t: Optional[torch.Tensor]):
+    if t is None:
+        return None
+    if t.get_device() != dev:
+        raise ValueError("KDA tensors must live on one CUDA device")
+    if not t.is_contiguous():
+        raise ValueError("KDA tensors must be contiguous")
     return t.data_ptr()
 
 
-def _ptr(t: Optional[torch.Tensor]):
-    if t is None:
-        return None
-    if not t.is_contiguous():
-        raise ValueError("KDA tensors must be contiguous")
-    return _address(t)
-
-
-def _ints(name: str, t: torch.Tensor, *shape):
+def _ints(dev: int, name: str, t: torch.Tensor, *shape):
     """Address of an int32 tensor of the given shape."""
-    if t.shape != shape or t.dtype != torch.int32:
+    if t.shape != shape or t.dtype is not torch.int32:
         raise ValueError(f"{name} must be an int32 tensor of shape {shape}")
-    return _ptr(t)
+    return _ptr(dev, t)
 
 
-def _heads(name: str, t: torch.Tensor, T, H, d, dtype):
+def _heads(dev: int, name: str, t: torch.Tensor, T, H, d, dtype):
     """Address, token and head stride of a [T, H, d] tensor whose channels are contiguous."""
-    if t.shape != (T, H, d) or t.dtype != dtype:
+    if t.shape != (T, H, d) or t.dtype is not dtype:
         raise ValueError(f"{name} must be [{T}, {H}, {d}] of {dtype}")
     st, sh, sd = t.stride()
     if sd != 1 and d > 1:
         raise ValueError(f"{name}: the channels of a head must be contiguous")
     if H <= 1:
         sh = d
-    return _address(t), st if T > 1 else max(H, 1) * sh, sh
+    if t.get_device() != dev:
+        raise ValueError("KDA tensors must live on one CUDA device")
+    return t.data_ptr(), st if T > 1 else max(H, 1) * sh, sh
 
 
-def _packed(name: str, t: torch.Tensor, T, H, d, dtype):
+def _packed(dev: int, name: str, t: torch.Tensor, T, H, d, dtype):
     """Address and token stride of a [T, H, d] tensor whose heads are contiguous."""
-    p, st, sh = _heads(name, t, T, H, d, dtype)
-    if sh != d:
+    if t.shape != (T, H, d) or t.dtype is not dtype:
+        raise ValueError(f"{name} must be [{T}, {H}, {d}] of {dtype}")
+    st, sh, sd = t.stride()
+    if sd != 1 and d > 1 or sh != d and H > 1:
         raise ValueError(f"{name}: the heads of a token must be contiguous")
-    return p, st
+    if t.get_device() != dev:
+        raise ValueError("KDA tensors must live on one CUDA device")
+    return t.data_ptr(), st if T > 1 else H * d
 
 
-def _flat(name: str, t: torch.Tensor, T, d, dtype):
+def _flat(dev: int, name: str, t: torch.Tensor, T, d, dtype):
     """Address and token stride of a [T, d] tensor whose channels are contiguous."""
-    if t.shape != (T, d) or t.dtype != dtype:
+    if t.shape != (T, d) or t.dtype is not dtype:
         raise ValueError(f"{name} must be [{T}, {d}] of {dtype}")
     st, sd = t.stride()
     if sd != 1 and d > 1:
         raise ValueError(f"{name}: the channels of a token must be contiguous")
-    return _address(t), st if T > 1 else d
+    if t.get_device() != dev:
+        raise ValueError("KDA tensors must live on one CUDA device")
+    return t.data_ptr(), st if T > 1 else d
 
 
-def _per_token(name: str, t: torch.Tensor, T):
+def _per_token(dev: int, name: str, t: torch.Tensor, T):
     """Address of an int32 tensor with an entry for each of T tokens, or more."""
-    if t.dtype != torch.int32 or t.dim() != 1 or t.numel() < T:
+    shape = t.shape
+    if len(shape) != 1 or shape[0] < T or t.dtype is not torch.int32:
         raise ValueError(f"{name} must be an int32 tensor with an entry per token")
-    return _ptr(t)
+    return _ptr(dev, t)
 
 
-def _turns(turns: torch.Tensor):
-    if turns.dtype != torch.int64 or turns.dim() != 1:
+def _turns(dev: int, t: torch.Tensor):
+    """Address of a rotation's frequencies, and the channels that it turns."""
+    shape = t.shape
+    if len(shape) != 1 or t.dtype is not torch.int64:
         raise ValueError("turns must be an int64 tensor [rot / 2], as kda_rope_turns makes it")
-    return _ptr(turns)
+    return _ptr(dev, t), 2 * shape[0]
 
 
 def kda_kv_append_rope(q, k, v, slot_map, positions, turns, k_cache, v_cache, *,
@@ -108,26 +125,28 @@ def kda_kv_append_rope(q, k, v, slot_map, positions, turns, k_cache, v_cache, *,
     if io is None:
         raise TypeError(f"unsupported k dtype {dt}")
     T = k.shape[0]
-    if v_cache.shape != k_cache.shape or k_cache.dtype != dt or v_cache.dtype != dt:
+    dev = _device(k)
+    if v_cache.shape != (pages, Hkv, page, d) or k_cache.dtype is not dt or v_cache.dtype is not dt:
         raise ValueError("the caches must be [num_pages, Hkv, page_size, d] of k's dtype")
     qp = op = kop = None
     Hq = qs = os_ = kos = 0
     if k_out is not None:
-        kop, kos = _packed("k_out", k_out, T, Hkv, d, dt)
+        kop, kos = _packed(dev, "k_out", k_out, T, Hkv, d, dt)
     if q is not None:
         Hq = q.shape[1]
-        qp, qs = _packed("q", q, T, Hq, d, dt)
+        qp, qs = _packed(dev, "q", q, T, Hq, d, dt)
         if q_out is None:
             q_out = _k._empty((T, Hq, d), dt, q, stream)
             op, os_ = q_out.data_ptr(), Hq * d
         else:
-            op, os_ = _packed("q_out", q_out, T, Hq, d, dt)
-    kp, ks = _packed("k", k, T, Hkv, d, dt)
-    vp, vs = _packed("v", v, T, Hkv, d, dt)
+            op, os_ = _packed(dev, "q_out", q_out, T, Hq, d, dt)
+    kp, ks = _packed(dev, "k", k, T, Hkv, d, dt)
+    vp, vs = _packed(dev, "v", v, T, Hkv, d, dt)
+    tp, rot = _turns(dev, turns)
     code = (_k._lib or lib()).kda_kv_append_rope(
-        qp, kp, vp, _per_token("slot_map", slot_map, T), _per_token("positions", positions, T), _turns(turns),
-        _ptr(k_cache), _ptr(v_cache), op, kop, T, Hq, Hkv, d, 2 * turns.numel(), neighbours, qs, ks, vs, os_,
-        kos, pages, page, io, _ptr(status), _k._stream(stream))
+        qp, kp, vp, _per_token(dev, "slot_map", slot_map, T), _per_token(dev, "positions", positions, T), tp,
+        _ptr(dev, k_cache), _ptr(dev, v_cache), op, kop, T, Hq, Hkv, d, rot, neighbours, qs, ks, vs, os_,
+        kos, pages, page, io, _ptr(dev, status), _k._stream(stream))
     if code:
         _k._check(code)
     return q_out
@@ -148,10 +167,11 @@ def kda_latent_append(c, k_r, slot_map, cache, *, positions=None, turns=None, q_
     io = _k._DTYPE.get(dt)
     if io is None:
         raise TypeError(f"unsupported c dtype {dt}")
+    dev = _device(c)
     dr = 0 if k_r is None else k_r.shape[1]
     if dc != dl + dr or cache.dtype != dt:
         raise ValueError("cache must be [num_pages, page_size, dl + dr] of c's dtype")
-    cp, cs = _flat("c", c, T, dl, dt)
+    cp, cs = _flat(dev, "c", c, T, dl, dt)
     kp = qp = op = kop = tp = pp = None
     ks = qs = qh = os_ = oh = kos = Hq = 0
     if k_r is None:
@@ -160,21 +180,21 @@ def kda_latent_append(c, k_r, slot_map, cache, *, positions=None, turns=None, q_
     else:
         if turns is None or positions is None:
             raise ValueError("k_r needs positions and turns")
-        kp, ks = _flat("k_r", k_r, T, dr, dt)
-        tp, pp = _turns(turns), _per_token("positions", positions, T)
-        if 2 * turns.numel() != dr:
+        kp, ks = _flat(dev, "k_r", k_r, T, dr, dt)
+        (tp, rot), pp = _turns(dev, turns), _per_token(dev, "positions", positions, T)
+        if rot != dr:
             raise ValueError("turns must have an entry per pair of k_r's channels")
         if k_out is not None:
-            kop, kos = _flat("k_out", k_out, T, dr, dt)
+            kop, kos = _flat(dev, "k_out", k_out, T, dr, dt)
         if q_r is not None:
             Hq = q_r.shape[1]
-            qp, qs, qh = _heads("q_r", q_r, T, Hq, dr, dt)
+            qp, qs, qh = _heads(dev, "q_r", q_r, T, Hq, dr, dt)
             if q_out is None:
                 q_out = _k._empty((T, Hq, dr), dt, c, stream)
-            op, os_, oh = _heads("q_out", q_out, T, Hq, dr, dt)
+            op, os_, oh = _heads(dev, "q_out", q_out, T, Hq, dr, dt)
     code = (_k._lib or lib()).kda_latent_append(
-        cp, kp, qp, _per_token("slot_map", slot_map, T), pp, tp, _ptr(cache), op, kop, T, Hq, dl, dr, neighbours,
-        cs, ks, qs, qh, os_, oh, kos, pages, page, io, _ptr(status), _k._stream(stream))
+        cp, kp, qp, _per_token(dev, "slot_map", slot_map, T), pp, tp, _ptr(dev, cache), op, kop, T, Hq, dl, dr, neighbours,
+        cs, ks, qs, qh, os_, oh, kos, pages, page, io, _ptr(dev, status), _k._stream(stream))
     if code:
         _k._check(code)
     return q_out if q_r is not None else None
@@ -206,17 +226,18 @@ def kda_attn_latent_paged(q, cache, block_table, cu_q, kv_len, *, scale: float, 
     if dc != d or cache.dtype != q.dtype or d < 512:
         raise ValueError("the cache must be [num_pages, page_size, 512 + dr] of q's channels and dtype")
     most = T if max_q is None else max_q
+    dev = _device(q)
     o, lse = _k._attn_outputs(q, 512, o, lse, want_lse, stream)
     if workspace is None and max_pages * page > KDA_LATENT_SHORT_KEYS // (2 if io == KDA_F32 else 1):
         need = (_k._lib or lib()).kda_attn_latent_workspace_size(N, T, most, Hq, 512, d - 512, io)
         if need != ctypes.c_size_t(-1).value and need:  # the call itself reports bad arguments
             workspace = _k._empty(need, torch.uint8, q, stream, scratch=True)
     ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
-    qp, qs, qh = _heads("q", q, T, Hq, d, q.dtype)
+    qp, qs, qh = _heads(dev, "q", q, T, Hq, d, q.dtype)
     _k._check((_k._lib or lib()).kda_attn_latent_paged(
-        qp, _ptr(cache), _ints("block_table", block_table, N, max_pages), _ints("cu_q", cu_q, N + 1),
-        _ints("kv_len", kv_len, N), _ptr(o), _ptr(lse), N, T, most, Hq, 512, d - 512, qs, qh, pages, page,
-        max_pages, scale, io, _ptr(workspace), ws_bytes, _ptr(status), _k._stream(stream)))
+        qp, _ptr(dev, cache), _ints(dev, "block_table", block_table, N, max_pages), _ints(dev, "cu_q", cu_q, N + 1),
+        _ints(dev, "kv_len", kv_len, N), _ptr(dev, o), _ptr(dev, lse), N, T, most, Hq, 512, d - 512, qs, qh, pages, page,
+        max_pages, scale, io, _ptr(dev, workspace), ws_bytes, _ptr(dev, status), _k._stream(stream)))
     return o, lse
 
 
@@ -235,14 +256,15 @@ def kda_attn_latent_prompt(q, k, k_r, v, cu_seqlens, *, max_len: Optional[int] =
     if k.shape != (T, H, d) or v.shape != k.shape or dq != d + dr:
         raise ValueError("q must be [T, H, d + dr], k and v [T, H, d]")
     most = T if max_len is None else max_len
+    dev = _device(q) if q.dtype in _k._DTYPE else -1
     io, o, lse, workspace, ws_bytes = _k._attn_buffers(q, N, most, most, H, o, lse, want_lse, workspace, stream, d)
     dt = q.dtype
-    qp, qs, qh = _heads("q", q, T, H, dq, dt)
-    kp, ks, kh = _heads("k", k, T, H, d, dt)
-    vp, vs, vh = _heads("v", v, T, H, d, dt)
-    rp, rs = _flat("k_r", k_r, T, dr, dt) if dr else (None, 0)
+    qp, qs, qh = _heads(dev, "q", q, T, H, dq, dt)
+    kp, ks, kh = _heads(dev, "k", k, T, H, d, dt)
+    vp, vs, vh = _heads(dev, "v", v, T, H, d, dt)
+    rp, rs = _flat(dev, "k_r", k_r, T, dr, dt) if dr else (None, 0)
     _k._check((_k._lib or lib()).kda_attn_latent_prompt(
-        qp, kp, rp, vp, _ints("cu_seqlens", cu_seqlens, N + 1), _ptr(o), _ptr(lse), N, T, most, H, d, dr, qs, qh,
-        ks, kh, rs, vs, vh, dq ** -0.5 if scale is None else scale, io, _ptr(workspace), ws_bytes,
-        _ptr(status), _k._stream(stream)))
+        qp, kp, rp, vp, _ints(dev, "cu_seqlens", cu_seqlens, N + 1), _ptr(dev, o), _ptr(dev, lse), N, T, most, H, d, dr, qs, qh,
+        ks, kh, rs, vs, vh, dq ** -0.5 if scale is None else scale, io, _ptr(dev, workspace), ws_bytes,
+        _ptr(dev, status), _k._stream(stream)))
     return o, lse

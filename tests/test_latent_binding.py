@@ -25,7 +25,7 @@ CALLS = {
 
 @pytest.fixture
 def fakes(made, monkeypatch):  # noqa: F811
-    monkeypatch.setattr(latent, "_address", lambda t: t.data_ptr())  # (all tensors here are the host's)
+    monkeypatch.setattr(latent, "_device", lambda t: t.get_device())  # (all tensors here are the host's)
     return made
 
 
