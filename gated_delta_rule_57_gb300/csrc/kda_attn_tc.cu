@@ -10,10 +10,11 @@
 //
 // One CTA per SM, four warpgroups:
 //   warps 0..3, 4..7  two softmax groups, one row of S per thread
-//   warp 8            issues the products
+//   warp 8            issues the products (at DQ = 192: of the first group)
 //   warp 9            finds the work and issues the loads
 //   warp 10           clears V of what some rows must not see
-//   warp 11           adds that to the finished rows which see it
+//   warp 11           adds that to the finished rows which see it (at DQ = 192 warp 10 does,
+//                     and this one issues the second group's products)
 //   warps 12..15      the results: O / l, merging, stores
 // Every wait has a limit, after which the kernel reports KDA_DEV_TIMEOUT.
 // A group's loop: S (TMEM, 128 lanes x 128 columns fp32) -> registers, mask,
@@ -61,7 +62,7 @@ constexpr int kThreadsTc = 512;
 // Registers per thread: launched with 128 (65536 in all), then by warpgroup.
 constexpr int kRegsSoftmax = 192, kRegsOther = 64, kRegsResult = 64;
 static_assert(2 * kRegsSoftmax + kRegsOther + kRegsResult <= 4 * 128, "more than launched with");
-constexpr int kMmaWarp = 8, kLoadWarp = 9, kEdgeWarp = 10;  // and warp 11
+constexpr int kMmaWarp = 8, kLoadWarp = 9, kEdgeWarp = 10, kMmaWarp1 = 11;
 constexpr int kPieces = 4;         // pieces announced ahead
 // Relative time of a key tile for one row tile and for a pair: about 1750 and 2500
 // clocks, measured at d = 128 in a step of two prompts' chunks among single tokens.
@@ -81,6 +82,12 @@ struct TcCfg {
     static constexpr int TILE_BYTES = kTile * D * 2, Q_BYTES = kTile * DQ * 2;
     static constexpr int SHARED_BYTES = kTile * DR * 2;
     static constexpr int STAGES = DR ? 3 : D == 128 ? 5 : 8;
+    // Issuing warps: one for both groups, in a fixed order, or one for each. What such a warp
+    // does between two products shows as idle tensor core unless the other's run, but the
+    // order keeps the groups half a step apart. Measured, one against two, us (32 heads): DQ = 192,
+    // 4 prompts of 8192 1800/1614, 24 ragged 490/460; DQ = D = 128 (8 key heads), 8 of 8192 2461/2633,
+    // ragged 318/370, a mixed step over pages 463/521.
+    static constexpr bool TWO_ISSUE = DR > 0;
     static constexpr int TILES = 2 * Q_BYTES + STAGES * TILE_BYTES + 2 * SHARED_BYTES;
 };
 
@@ -192,7 +199,7 @@ struct Shared {
     uint64_t odd_full[kPieces];     // all V tiles of a piece are cleared
     uint64_t rows_full[kPieces];    // all its rows are written
     uint64_t next_full;             // the number of the next whole item
-    uint64_t drained;               // all products have ended
+    uint64_t drained[2];            // all products (of a group) have ended
     alignas(16) uint4 next;
     Piece pieces[kPieces];
     // Keys of a piece with values that were cleared: bit i, key seen_by_all + i.
@@ -332,7 +339,8 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
     if (warp == 1) {
         if (lane < NS) {
             mbar_init(&sh.kv_full[lane], 1);
-            mbar_init(&sh.kv_empty[lane], 2);  // read by the products, seen by the V warp
+            // read by the products, seen by the V warp
+            mbar_init(&sh.kv_empty[lane], C::TWO_ISSUE ? 3 : 2);
             mbar_init(&sh.v_ready[lane], 1);
         }
         if (lane < 2) {
@@ -343,18 +351,19 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
             mbar_init(&sh.ml_full[lane], 128);
             mbar_init(&sh.ml_free[lane], 128);
             mbar_init(&sh.o_free[lane], 128);
+            mbar_init(&sh.drained[lane], 1);
         }
         if (lane < kPieces) {
             mbar_init(&sh.piece_full[lane], 1);
-            mbar_init(&sh.piece_empty[lane], 15);  // softmax 8, products, V 2, results 4
+            // softmax 8, products and V 3 (TWO_ISSUE: products 2, V), results 4
+            mbar_init(&sh.piece_empty[lane], 15);
             mbar_init(&sh.odd_full[lane], 1);
             mbar_init(&sh.rows_full[lane], 4);
         }
         if (lane == 0) {
             mbar_init(&sh.next_full, 1);
-            mbar_init(&sh.drained, 1);
             mbar_init(&sh.q_full, 1);
-            mbar_init(&sh.q_empty, 1);
+            mbar_init(&sh.q_empty, C::TWO_ISSUE ? 2 : 1);
             prefetch_tensormap(&map_q);
             prefetch_tensormap(&map_k);
             prefetch_tensormap(&map_v);
@@ -587,7 +596,142 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
                 mbar_wait(&sh.q_full, q_phase ^ 1, 1LL << 24);
                 if (asked) mbar_wait(&sh.next_full, (asked - 1) & 1, 1LL << 24);
             }
-        } else if (warp == kMmaWarp) {
+        } else if (C::TWO_ISSUE && (warp == kMmaWarp || warp == kMmaWarp1)) {
+            // ------------------------------------------------------------ products, a warp a group
+            // Both warps see every tile of the ring go by, in its order, and give it back:
+            // after the products of theirs that read it, or at once. All of it is uniform,
+            // so that stages and descriptors stay in uniform registers, and one elected lane
+            // issues.
+            const int w = warp == kMmaWarp ? 0 : 1;
+            int stage = 0, kv_phase = 0, np = 0;
+            int nq = 0, tiles = 0, uses = 0;  // row tiles, key tiles of the group, pieces with any, so far
+            constexpr uint32_t idesc_s = idesc_bf16(kTile, kTile, 0, 0);
+            constexpr uint32_t idesc_o = idesc_bf16(kTile, D, 0, 1);
+            const uint64_t dq = desc_kmajor(smem_addr(sq));
+            const uint64_t dk = desc_kmajor(smem_addr(skv)), dv = desc_mnmajor(smem_addr(skv), kTile);
+            constexpr uint32_t TILE = C::TILE_BYTES >> 4, QTILE = C::Q_BYTES >> 4;  // in descriptor units
+            const uint64_t dr = desc_kmajor(smem_addr(srope));
+            uint32_t rope = 0;  // place of the next key tile's shared channels
+            const uint32_t ds = tbase + TM_S + w * kTile, dout = tbase + TM_O + w * D;
+            auto next = [&] {
+                if (++stage == NS) {
+                    stage = 0;
+                    kv_phase ^= 1;
+                }
+            };
+            auto wait = [&](uint64_t* bar, uint32_t parity) {
+                if (!__all_sync(0xffffffffu, mbar_wait(bar, parity, kWaitClocks))) ok = false;
+                return ok;
+            };
+            auto uniform = [](int x) { return __shfl_sync(0xffffffffu, x, 0); };
+            auto commit = [&](uint64_t* bar) {
+                if (elect_one()) mma_commit(bar);
+                __syncwarp();
+            };
+            // A tile of the other group's: there, so that its barrier's phase is this one. (Given
+            // back behind this warp's products, so that what the ring gives back, and the
+            // shared channels of earlier tiles with it, is read.)
+            auto skip = [&] {
+                if (!wait(&sh.kv_full[stage], kv_phase)) return false;
+                commit(&sh.kv_empty[stage]);
+                next();
+                return true;
+            };
+            // S = Q K^T with the ring's next tile; `last` of the piece for these rows.
+            auto scores = [&](uint32_t qtile, bool last) {
+                if (!wait(&sh.kv_full[stage], kv_phase)) return false;
+                tc_fence_after();
+                const uint64_t a = dq + qtile * QTILE, b = dk + stage * TILE;
+                if (elect_one()) {
+#pragma unroll
+                    for (int kk = 0; kk < D / 16; kk++)
+                        mma_bf16(ds, a + kstep_kmajor(kTile, kk), b + kstep_kmajor(kTile, kk), idesc_s, kk > 0);
+                    if (C::DR) {
+                        const uint64_t ar = a + kstep_kmajor(kTile, D / 16);
+                        const uint64_t br = dr + rope * (C::SHARED_BYTES >> 4);
+#pragma unroll
+                        for (int kk = 0; kk < C::DR / 16; kk++)
+                            mma_bf16(ds, ar + kstep_kmajor(kTile, kk), br + kstep_kmajor(kTile, kk), idesc_s, 1);
+                    }
+                    mma_commit(&sh.s_full[w]);
+                    mma_commit(&sh.kv_empty[stage]);
+                    if (last) mma_commit(&sh.q_empty);
+                }
+                __syncwarp();
+                next();
+                return true;
+            };
+            // O += P V with the ring's next tile, one half of its keys after the other.
+            auto outputs = [&](uint32_t add, bool last) {
+                if (!wait(&sh.v_ready[stage], kv_phase)) return false;
+                const uint64_t b = dv + stage * TILE;
+#pragma unroll
+                for (int half = 0; half < 2; half++) {
+                    if (!wait(&sh.p_full[w][half], tiles & 1)) return false;
+                    tc_fence_after();
+                    if (elect_one()) {
+#pragma unroll
+                        for (int i = 0; i < kTile / 32; i++) {
+                            const int kk = half * (kTile / 32) + i;
+                            mma_bf16_ta(dout, ds + 8 * kk, b + kstep_mnmajor(kk), idesc_o, kk > 0 ? 1 : add);
+                        }
+                        if (half) {
+                            mma_commit(&sh.kv_empty[stage]);
+                            if (last) mma_commit(&sh.o_full[w]);
+                        }
+                    }
+                    __syncwarp();
+                }
+                tiles++;
+                next();
+                return true;
+            };
+            while (ok) {
+                const int i = np % kPieces;
+                if (!wait(&sh.piece_full[i], (np / kPieces) & 1)) break;
+                const Piece& pc = sh.pieces[i];
+                const int end = uniform(pc.end), n = uniform(piece_tiles(pc)), pair = uniform(pc.pair);
+                const int mine = uniform(group_share(pc, w, tok1).n);
+                if (lane == 0) mbar_arrive(&sh.piece_empty[i]);
+                np++;
+                if (end) break;
+                if (n == 0) continue;
+                if (!wait(&sh.q_full, nq++ & 1)) break;
+                if (mine == 0) commit(&sh.q_empty);
+                if (pair) {
+                    // Two row tiles on every key tile.
+                    if (!(mine > 0 ? scores(w, mine == 1) : skip())) break;
+                    rope ^= 1;
+                    // What O held is read.
+                    if (mine > 0 && !wait(&sh.o_free[w], (uses++ & 1) ^ 1)) break;
+                    for (int j = 0; j < n && ok; j++) {
+                        if (!(j < mine ? outputs(j > 0, j + 1 == mine) : skip())) break;
+                        if (j + 1 == n) break;
+                        if (!(j + 1 < mine ? scores(w, j + 2 == mine) : skip())) break;
+                        rope ^= 1;
+                    }
+                } else {
+                    // One row tile, key tiles in turn to the two groups; two of them lead.
+                    for (int j = 0; j < 2 && j < n && ok; j++) {
+                        if (!(j == w ? scores(0, mine == 1) : skip())) break;
+                        rope ^= 1;
+                    }
+                    if (!ok || (mine > 0 && !wait(&sh.o_free[w], (uses++ & 1) ^ 1))) break;
+                    for (int j = 0; j < n && ok; j++) {
+                        const bool own = (j & 1) == w;
+                        if (!(own ? outputs(j > 1, j + 2 >= n) : skip())) break;
+                        if (j + 2 >= n) continue;
+                        if (!(own ? scores(0, j + 4 >= n) : skip())) break;
+                        rope ^= 1;
+                    }
+                }
+            }
+            // Products in flight, which write the tensor memory that is freed below and
+            // arrive on this CTA's barriers, end before it leaves.
+            commit(&sh.drained[w]);
+            if (!__all_sync(0xffffffffu, mbar_wait(&sh.drained[w], 0, 1LL << 24))) ok = false;
+            if (!ok) flags |= KDA_DEV_TIMEOUT;
+        } else if (!C::TWO_ISSUE && warp == kMmaWarp) {
             // ------------------------------------------------------------ products
             // What this warp does between two products shows as idle tensor core.
             // All of it is uniform, so that stages and descriptors stay in uniform
@@ -598,9 +742,7 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
             constexpr uint32_t idesc_o = idesc_bf16(kTile, D, 0, 1);
             const uint64_t dq = desc_kmajor(smem_addr(sq));
             const uint64_t dk = desc_kmajor(smem_addr(skv)), dv = desc_mnmajor(smem_addr(skv), kTile);
-            constexpr uint32_t TILE = C::TILE_BYTES >> 4, QTILE = C::Q_BYTES >> 4;  // in descriptor units
-            const uint64_t dr = desc_kmajor(smem_addr(srope));
-            uint32_t rope = 0;  // place of the next key tile's shared channels
+            constexpr uint32_t TILE = C::TILE_BYTES >> 4;  // a tile in descriptor units
             auto next = [&] {
                 if (++stage == NS) {
                     stage = 0;
@@ -613,20 +755,12 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
             };
             auto uniform = [](int x) { return __shfl_sync(0xffffffffu, x, 0); };
             auto scores = [&](int w, uint32_t qtile, uint32_t kstage) {  // S_w = Q_w K^T
-                const uint64_t a = dq + qtile * QTILE, b = dk + kstage * TILE;
+                const uint64_t a = dq + qtile * TILE, b = dk + kstage * TILE;
                 if (elect_one()) {
 #pragma unroll
                     for (int kk = 0; kk < D / 16; kk++)
                         mma_bf16(tbase + TM_S + w * kTile, a + kstep_kmajor(kTile, kk),
                                  b + kstep_kmajor(kTile, kk), idesc_s, kk > 0);
-                    if (C::DR) {
-                        const uint64_t ar = a + kstep_kmajor(kTile, D / 16);
-                        const uint64_t br = dr + rope * (C::SHARED_BYTES >> 4);
-#pragma unroll
-                        for (int kk = 0; kk < C::DR / 16; kk++)
-                            mma_bf16(tbase + TM_S + w * kTile, ar + kstep_kmajor(kTile, kk),
-                                     br + kstep_kmajor(kTile, kk), idesc_s, 1);
-                    }
                     mma_commit(&sh.s_full[w]);
                 }
                 __syncwarp();
@@ -700,7 +834,6 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
                         if (n1 > 0) scores(1, 1, stage);
                         commit(&sh.kv_empty[stage]);
                         next();
-                        rope ^= 1;
                         if (n == 1) commit(&sh.q_empty);
                     }
                     primed = false;
@@ -753,8 +886,7 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
                         if (more) {
                             commit(&sh.kv_empty[ks]);
                             next();
-                            rope ^= 1;
-                        }
+                            }
                         // the rows' last scores are issued
                         if (j + 2 == n || (j + 1 == n && primed && x.n == 1)) commit(&sh.q_empty);
                     }
@@ -768,7 +900,6 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
                         scores(j, 0, stage);
                         commit(&sh.kv_empty[stage]);
                         next();
-                        rope ^= 1;
                     }
                     if (n <= 2) commit(&sh.q_empty);
                     if (!ok || !o_free(0) || (n > 1 && !o_free(1))) break;
@@ -788,8 +919,7 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
                             scores(w, 0, ks);
                             commit(&sh.kv_empty[ks]);
                             next();
-                            rope ^= 1;
-                            if (j + 3 == n) commit(&sh.q_empty);
+                                if (j + 3 == n) commit(&sh.q_empty);
                         } else {
                             commit(&sh.o_full[w]);
                         }
@@ -799,8 +929,8 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
             }
             // Products in flight, which write the tensor memory that is freed below and
             // arrive on this CTA's barriers, end before it leaves.
-            commit(&sh.drained);
-            if (!__all_sync(0xffffffffu, mbar_wait(&sh.drained, 0, 1LL << 24))) ok = false;
+            commit(&sh.drained[0]);
+            if (!__all_sync(0xffffffffu, mbar_wait(&sh.drained[0], 0, 1LL << 24))) ok = false;
             if (!ok) flags |= KDA_DEV_TIMEOUT;
         } else if (warp == kEdgeWarp) {
             // ------------------------------------------------------------ V at the edge
@@ -815,8 +945,7 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
                 if (!ok) break;
                 const Piece pc = sh.pieces[i];
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&sh.piece_empty[i]);
-                np++;
+                if (!C::TWO_ISSUE && lane == 0) mbar_arrive(&sh.piece_empty[i]);
                 if (pc.end) break;
                 if (lane < 8) sh.odd[i][lane] = 0;  // (those of the piece before are done with)
                 __syncwarp();
@@ -848,7 +977,21 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
                     }
                 }
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&sh.odd_full[i]);
+                if (!C::TWO_ISSUE) {
+                    if (lane == 0) mbar_arrive(&sh.odd_full[i]);
+                } else {  // what was cleared is added to the finished rows that see it
+                    const uint32_t odd = lane < 8 ? sh.odd[i][lane] : 0;
+                    if (__any_sync(0xffffffffu, odd != 0)) {
+                        warp_wait(ok, &sh.rows_full[i], (np / kPieces) & 1);
+                        if (ok)
+                            flags |= add_cleared<D>(
+                                p, pc, odd,
+                                pc.slot >= 0 ? p.sp.ws + attn_slot_floats(p.sp.rows, D) * pc.slot : nullptr);
+                    }
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&sh.piece_empty[i]);
+                }
+                np++;
             }
             if (!ok) flags |= KDA_DEV_TIMEOUT;
         } else {
