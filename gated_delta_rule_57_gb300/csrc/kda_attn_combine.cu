@@ -90,80 +90,66 @@ __global__ void __launch_bounds__(kCombineWarps * 32)
     report_flags(d_status, flags);
 }
 
-// The same for wide rows (D = 512): a warp finds M and the weights of a row first, a part per
-// lane, so that no part's load waits for another's. It takes all channels of a row that
-// has few parts, 128 of one that has many; 8 loads are in flight either way.
-// Q: quarters of a row that a warp takes.
-template <typename T, int D, int Q>
-__device__ __forceinline__ int join_rows(const AttnSplit& sp, const AttnCut& cut, int c0, int c1, int late, int first,
-                                         int step, int Hkv, int G, int tile_rows, T* o, float* lse) {
-    constexpr int COLS = D / 128 / Q;  // warps of a row
-    const int lane = threadIdx.x & 31, units = cut.ntok * G * COLS, per = tile_rows / G;
-    const size_t slot = attn_slot_floats(sp.rows, D);
-    auto part = [&](int c) { return sp.ws + slot * (2 * (size_t)c + (c == c0 ? late : 0)); };
-    int flags = 0;
-    for (int i = first; i < units; i += step) {
-        const int r = i / COLS, col = i % COLS * 128 + lane * 4, tok = r / G;
-        const int row = tok / per * tile_rows + tok % per * G + r % G;
+// The same for wide rows (D = 512), M and the weights first, so that no part's load waits for
+// another's. The parts of an item, where the workspace has them.
+template <int D>
+struct Parts {
+    const AttnSplit& sp;
+    int c0, c1, late, row_tile, G;
+    __device__ __forceinline__ const float* at(int c) const {
+        return sp.ws + attn_slot_floats(sp.rows, D) * (2 * (size_t)c + (c == c0 ? late : 0));
+    }
+    __device__ __forceinline__ int row(int r) const {  // of the tile, of the item's row r
+        const int tok = r / G, per = row_tile / G;
+        return tok / per * row_tile + tok % per * G + r % G;
+    }
+    __device__ __forceinline__ float sum_of(int c, int row) const { return at(c)[(size_t)sp.rows * D + row]; }
+    // The largest of all parts' sums, by a warp.
+    __device__ __forceinline__ float largest(int row) const {
         float m = -INFINITY;
-        for (int c = c0 + lane; c <= c1; c += 32) m = fmaxf(m, part(c)[(size_t)sp.rows * D + row]);
+        for (int c = c0 + (threadIdx.x & 31); c <= c1; c += 32) m = fmaxf(m, sum_of(c, row));
 #pragma unroll
         for (int k = 16; k > 0; k >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, k));
-        float sum = 0.f;
-        float4 acc[Q];
-#pragma unroll
-        for (int q = 0; q < Q; q++) acc[q] = make_float4(0.f, 0.f, 0.f, 0.f);
-        for (int cb = c0; cb <= c1; cb += 32) {
-            const int n = min(c1 - cb + 1, 32);
-            // (a part in which this row sees nothing has weight 0 and is not read; NaN stays)
-            float w = 0.f;
-            if (lane < n) {
-                const float x = part(cb + lane)[(size_t)sp.rows * D + row];
-                w = x == -INFINITY ? 0.f : exp2f(x - m);
-            }
-            sum += w;
-#pragma unroll 8 / Q
-            for (int k = 0; k < n; k++) {
-                const float wk = __shfl_sync(0xffffffffu, w, k);
-                if (wk == 0.f) continue;
-                const float* y = part(cb + k) + (size_t)row * D + col;
-#pragma unroll
-                for (int q = 0; q < Q; q++) {
-                    const float4 v = *reinterpret_cast<const float4*>(y + 128 * q);
-                    acc[q].x = fmaf(wk, v.x, acc[q].x);
-                    acc[q].y = fmaf(wk, v.y, acc[q].y);
-                    acc[q].z = fmaf(wk, v.z, acc[q].z);
-                    acc[q].w = fmaf(wk, v.w, acc[q].w);
-                }
-            }
-        }
-#pragma unroll
-        for (int k = 16; k > 0; k >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, k);
-        const size_t at = ((size_t)cut.tok0 + tok) * Hkv * G + (size_t)cut.h * G + r % G;
-        const float inv = sum == 0.f ? 0.f : 1.f / sum;
-#pragma unroll
-        for (int q = 0; q < Q; q++) {
-            const float y[4] = {acc[q].x * inv, acc[q].y * inv, acc[q].z * inv, acc[q].w * inv};
-            T out[4];
-#pragma unroll
-            for (int e = 0; e < 4; e++) {
-                flags |= finite_flag(y[e]);
-                out[e] = from_f32<T>(y[e]);
-            }
-            T* dst = o + at * D + col + 128 * q;
-            if constexpr (sizeof(T) == 4) *reinterpret_cast<float4*>(dst) = *reinterpret_cast<float4*>(out);
-            else *reinterpret_cast<uint2*>(dst) = *reinterpret_cast<uint2*>(out);
-        }
-        if (lse && lane == 0 && i % COLS == 0)
-            lse[at] = sum == 0.f ? -INFINITY : (m + log2f(sum)) * 0.69314718056f;
+        return m;
     }
+    // A part's weight; one in which the row sees nothing has weight 0 and is not read. NaN stays.
+    __device__ __forceinline__ float weight(int c, int row, float m) const {
+        const float x = sum_of(c, row);
+        return x == -INFINITY ? 0.f : exp2f(x - m);
+    }
+};
+__device__ __forceinline__ void add(float4& acc, float w, const float* y) {
+    const float4 v = *reinterpret_cast<const float4*>(y);
+    acc.x = fmaf(w, v.x, acc.x);
+    acc.y = fmaf(w, v.y, acc.y);
+    acc.z = fmaf(w, v.z, acc.z);
+    acc.w = fmaf(w, v.w, acc.w);
+}
+template <typename T>
+__device__ __forceinline__ int put(T* dst, float4 acc, float inv) {
+    const float y[4] = {acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv};
+    T out[4];
+    int flags = 0;
+#pragma unroll
+    for (int e = 0; e < 4; e++) {
+        flags |= finite_flag(y[e]);
+        out[e] = from_f32<T>(y[e]);
+    }
+    if constexpr (sizeof(T) == 4) *reinterpret_cast<float4*>(dst) = *reinterpret_cast<float4*>(out);
+    else *reinterpret_cast<uint2*>(dst) = *reinterpret_cast<uint2*>(out);
     return flags;
 }
+
+// Few parts: a warp takes a row. Many (more than kFewParts): a CTA takes 128 channels of a row, its
+// warps every eighth part each, added up in their order.
+constexpr int kFewParts = 16;
 
 template <typename T, int D>
 __global__ void __launch_bounds__(kCombineWarps * 32, 4)
     kda_attn_combine_wide_kernel(const AttnSplit sp, const int Hkv, const int G, const int tile_rows,
                                  T* o, float* lse, int* d_status) {
+    __shared__ float4 s_acc[kCombineWarps][32];
+    __shared__ float s_sum[kCombineWarps];
     pdl_wait();
     const int b = blockIdx.x + 1;
     const AttnCut cut = attn_cuts(sp, D)[b];
@@ -171,12 +157,72 @@ __global__ void __launch_bounds__(kCombineWarps * 32, 4)
     const int c0 = (int)(cut.u0 / cut.each);
     const int c1 = (int)((cut.u0 + (long long)(cut.n - 1) * cut.cost) / cut.each);
     const AttnCut start = attn_cuts(sp, D)[c0];
-    const int late = !(start.u0 == cut.u0 && start.tile == 0);
-    const int first = ((b - 1 - c0) * gridDim.y + blockIdx.y) * kCombineWarps + (threadIdx.x >> 5);
-    const int step = (c1 - c0) * gridDim.y * kCombineWarps;
-    const int flags = c1 - c0 < 4
-                          ? join_rows<T, D, D / 128>(sp, cut, c0, c1, late, first, step, Hkv, G, tile_rows, o, lse)
-                          : join_rows<T, D, 1>(sp, cut, c0, c1, late, first, step, Hkv, G, tile_rows, o, lse);
+    const Parts<D> parts{sp, c0, c1, !(start.u0 == cut.u0 && start.tile == 0), tile_rows, G};
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, rows = cut.ntok * G;
+    const int cta = (b - 1 - c0) * gridDim.y + blockIdx.y, ctas = (c1 - c0) * gridDim.y;
+    constexpr int Q = D / 128;
+    auto out_row = [&](int r) {
+        return ((size_t)cut.tok0 + r / G) * Hkv * G + (size_t)cut.h * G + r % G;
+    };
+    int flags = 0;
+    if (c1 - c0 < kFewParts) {
+        for (int r = cta * kCombineWarps + warp; r < rows; r += ctas * kCombineWarps) {
+            const int row = parts.row(r);
+            const float m = parts.largest(row);
+            const float w = lane <= c1 - c0 ? parts.weight(c0 + lane, row, m) : 0.f;
+            float4 acc[Q];
+#pragma unroll
+            for (int q = 0; q < Q; q++) acc[q] = make_float4(0.f, 0.f, 0.f, 0.f);
+            float sum = 0.f;
+#pragma unroll 2
+            for (int k = 0; k <= c1 - c0; k++) {
+                const float wk = __shfl_sync(0xffffffffu, w, k);
+                if (wk == 0.f) continue;
+                sum += wk;
+#pragma unroll
+                for (int q = 0; q < Q; q++) add(acc[q], wk, parts.at(c0 + k) + (size_t)row * D + 128 * q + lane * 4);
+            }
+            const float inv = sum == 0.f ? 0.f : 1.f / sum;
+#pragma unroll
+            for (int q = 0; q < Q; q++) flags |= put(o + out_row(r) * D + 128 * q + lane * 4, acc[q], inv);
+            if (lse && lane == 0) lse[out_row(r)] = sum == 0.f ? -INFINITY : (m + log2f(sum)) * 0.69314718056f;
+        }
+    } else {
+        for (int i = cta; i < rows * Q; i += ctas) {
+            const int r = i / Q, row = parts.row(r), col = i % Q * 128 + lane * 4;
+            const float m = parts.largest(row);
+            float sum = 0.f;
+            float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+            for (int cb = c0 + warp; cb <= c1; cb += 32 * kCombineWarps) {
+                const int n = min((c1 - cb) / kCombineWarps + 1, 32);  // parts cb, cb + 8, ...
+                const float w = lane < n ? parts.weight(cb + kCombineWarps * lane, row, m) : 0.f;
+#pragma unroll 8
+                for (int k = 0; k < n; k++) {
+                    const float wk = __shfl_sync(0xffffffffu, w, k);
+                    if (wk == 0.f) continue;
+                    sum += wk;
+                    add(acc, wk, parts.at(cb + kCombineWarps * k) + (size_t)row * D + col);
+                }
+            }
+            __syncthreads();  // what was there is read
+            s_acc[warp][lane] = acc;
+            if (lane == 0) s_sum[warp] = sum;
+            __syncthreads();
+            if (warp == 0) {
+                for (int k = 1; k < kCombineWarps; k++) {
+                    const float4 y = s_acc[k][lane];
+                    acc.x += y.x;
+                    acc.y += y.y;
+                    acc.z += y.z;
+                    acc.w += y.w;
+                    sum += s_sum[k];
+                }
+                flags |= put(o + out_row(r) * D + col, acc, sum == 0.f ? 0.f : 1.f / sum);
+                if (lse && lane == 0 && i % Q == 0)
+                    lse[out_row(r)] = sum == 0.f ? -INFINITY : (m + log2f(sum)) * 0.69314718056f;
+            }
+        }
+    }
     report_flags(d_status, flags);
 }
 
