@@ -360,7 +360,7 @@ AttnSplit latent_simt_split(int N, int total_q, int max_q, long long max_keys, i
     AttnSplit sp{};
     if (N == 0 || total_q == 0 || max_q == 0 || Hq == 0 || nsm == 0) return sp;
     const int rt = latent_simt_rows(max_q, Hq), blocks = latent_head_blocks(Hq, rt), G = Hq / blocks, tok = rt / G;
-    if (max_keys <= KDA_ATTN_SHORT_KEYS / 16) return sp;
+    if (max_keys <= KDA_LATENT_SHORT_KEYS / 2) return sp;
     if ((long long)total_q / tok * blocks >= 16LL * nsm) return sp;
     sp.ctas = nsm;
     sp.least = kKeys;

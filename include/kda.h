@@ -448,9 +448,8 @@ kda_status_t kda_decode_multi(const void* q, const void* k, const void* v, const
  * four calls below serve such a layer: plan a step's pages, write its keys and
  * values, and attend, over whole prompts or over the cache. Heads are grouped:
  * query head i reads key head i / (Hq / Hkv). (The page's own full-attention
- * layers compress keys and values into a latent; that form is not served, only
- * stacks whose attention layers keep plain keys and values.) They share the conventions at
- * the top of this file, with these differences:
+ * layers compress keys and values into a latent: the calls after these four.) They share
+ * the conventions at the top of this file, with these differences:
  *   - q, k and v may be views of one fused projection: token t starts at
  *     t * stride elements, its heads are contiguous ([H, d]). Strides are
  *     multiples of 16 bytes.
@@ -619,6 +618,9 @@ size_t kda_attn_workspace_size(int N, int total_q, int max_q, int Hq, int Hkv, i
  * frequency f in radians, round(2^64 f / 2 pi) modulo 2^64), so that the angle is as good
  * at position 2^31 - 1 as at 0. Pairs are channels i and i + rot / 2 (neighbours = 0) or
  * 2 i and 2 i + 1 (neighbours != 0). Positions may be negative.
+ *
+ * Alignment, int arrays, device-side reports and strides (multiples of 16 bytes) as for the
+ * four calls above.
  */
 
 /*
@@ -637,8 +639,8 @@ size_t kda_attn_workspace_size(int N, int total_q, int max_q, int Hq, int Hkv, i
  *                   again, for kda_attn_prompt; may be k itself
  *   rot           : a multiple of 16 in 16 .. d; channels from rot on are copied
  *
- * Strides at most 2^30 elements. The products are in fp32, rounded once. HBM-bound: each byte is read and
- * written once.
+ * Strides at most 2^30 elements. The products are in fp32, rounded once. HBM-bound: each byte
+ * is read and written once.
  */
 kda_status_t kda_kv_append_rope(const void* q, const void* k, const void* v, const int* slot_map,
                                 const int* positions, const long long* turns, void* k_cache,

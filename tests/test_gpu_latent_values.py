@@ -367,3 +367,63 @@ def test_drawn_calls(seed):
     ws = rng.choice(workspaces(n, total, total if most is None else most, hq, dr, io))
     o, lse, status = paged(q, cache, table, cu, kv, most, workspace=ws)
     check_spoiled(o, lse, ref, hit, gone, status)
+
+
+@pytest.mark.parametrize("seed", range(60))
+def test_drawn_prompts(seed):
+    rng = random.Random(1000 + seed)
+    while True:
+        io, dr, h = rng.choice([BF, BF, BF, F32]), rng.choice([0, 64, 64]), rng.choice([1, 2, 3, 5, 8, 16])
+        lens = [max(0, log_int(rng, 1, rng.choice([5, 100, 700, 2600])) - rng.choice([0, 0, 1])) for _ in range(rng.choice([1, 2, 3, rng.randint(1, 30)]))]
+        if 0 < sum(lens) and sum(x * x for x in lens) * h <= 3e7:
+            break
+    q, k, k_r, v, cu = prompt_case(lens, h, dr, io, seed=seed)
+    if rng.random() < 0.5:  # tokens inside heads
+        q, v = (x.transpose(0, 1).contiguous().transpose(0, 1) for x in (q, v))
+    ref = latent_ref.prompt(q, k, k_r, v, lens, (128 + dr) ** -0.5)
+    hit, gone = torch.zeros(sum(lens), h, 128, dtype=torch.bool, device=DEV), torch.zeros(sum(lens), h, dtype=torch.bool, device=DEV)
+    starts = cu.tolist()
+    for _ in range(0 if rng.random() < 0.5 else rng.randint(1, 4)):
+        r = rng.randrange(len(lens))
+        if lens[r] == 0:
+            continue
+        at, head, c = starts[r] + rng.randrange(lens[r]), rng.randrange(h), rng.randrange(128)
+        rows = slice(at, starts[r + 1])
+        if rng.random() < 0.5:
+            v[at, head, c] = NAN
+            hit[rows, head, c] = True
+        elif dr and rng.random() < 0.5:
+            k_r[at, c % dr] = NAN
+            hit[rows], gone[rows] = True, True
+        else:
+            k[at, head, c] = NAN
+            hit[rows, head], gone[rows, head] = True, True
+    need = kda.kda_attn_workspace_size(len(lens), sum(lens), max(lens), h, h, 128, io)
+    ws = rng.choice([None, torch.full((max(need, 4) // 4,), NAN, device=DEV), torch.empty(0, device=DEV)])
+    status = ints([0])
+    o, lse = pkg.kda_attn_latent_prompt(q, k, k_r, v, cu, max_len=rng.choice([None, max(lens)]), workspace=ws, status=status)
+    torch.cuda.synchronize()
+    assert torch.equal(~torch.isfinite(o), hit) and torch.equal(torch.isnan(lse), gone)
+    attn_ref.check(torch.where(hit, ref[0].to(io), o), torch.where(gone, ref[1].float(), lse), ref)
+    assert int(status) == (kda.KDA_DEV_NONFINITE if hit.any() else 0)
+
+
+@pytest.mark.parametrize("io", DTYPES)
+def test_calls_at_once_on_two_streams(io):
+    """Each with the workspace that it makes: the bits of calls alone."""
+    cases = [case([1, 3], [5000, 4000], 8, 64, 64, io, seed=1), case([2] * 9, [700] * 9, 40, 0, 16, io, seed=2)]
+    prompts = [prompt_case([2500, 3], 2, 64, io, seed=3), prompt_case([100, 900], 5, 0, io, seed=4)]
+
+    def calls(i):
+        return (*pkg.kda_attn_latent_paged(*cases[i], scale=SCALE, max_q=3), *pkg.kda_attn_latent_prompt(*prompts[i]))
+
+    alone = [calls(i) for i in range(2)]
+    torch.cuda.synchronize()
+    streams, got = [torch.cuda.Stream() for _ in range(2)], []
+    for _ in range(10):
+        for i, s in enumerate(streams):
+            with torch.cuda.stream(s):
+                got.append((i, calls(i)))
+    torch.cuda.synchronize()
+    for i, out in got:
+        assert all(torch.equal(x, y) for x, y in zip(alone[i], out))
