@@ -15,10 +15,11 @@
 // second product is as narrow as they are (a multiple of 16).
 //
 // One CTA per SM:
-//   warps 0..3  softmax, one row of S per thread (64-row accumulators use 16 lanes of
-//               each warp's 32), the results, and the edge (below)
-//   warps 4, 5  issue the first and the second products
-//   warp 6      finds the work and issues the loads
+//   warps 0..3   softmax, one row of S per thread (64-row accumulators use 16 lanes of
+//                each warp's 32), and the edge (below)
+//   warps 4..7   the results
+//   warps 8, 9   issue the first and the second products
+//   warp 10      finds the work and issues the loads
 //
 // A key past a row's last one gets P = 0 by a select on S. 0 x NaN is NaN, so before the
 // second product the softmax warps clear in shared memory what some rows must not see:
@@ -36,8 +37,8 @@ namespace {
 
 using namespace ptx;
 
-constexpr int kThreadsTc = 224;
-constexpr int kScoreWarp = 4, kOutWarp = 5, kLoadWarp = 6;
+constexpr int kThreadsTc = 352;
+constexpr int kScoreWarp = 8, kOutWarp = 9, kLoadWarp = 10;
 constexpr int kDL = kLatentDim;
 constexpr int kUnits = kDL / 128;        // units of a tile's latents
 constexpr int kPieces = 4;               // pieces announced ahead
@@ -55,7 +56,8 @@ struct TcCfg {
     static constexpr int P = RT * 128;
     static constexpr int NT = (225 * 1024 - Q - P) / TILE;      // key tiles in shared memory
     static constexpr int TILES = Q + NT * TILE + P;
-    static constexpr uint32_t TM_O = 0, TM_S = kUnits * RT;     // tensor-memory columns
+    static constexpr int NO = RT == 32 ? 2 : 1;                 // results in tensor memory
+    static constexpr uint32_t TM_O = 0, TM_S = NO * kUnits * RT;  // its columns
     static_assert(NT >= 2 && NT <= kMaxTiles, "key tiles");
 };
 
@@ -94,15 +96,16 @@ struct Shared {
     uint64_t s_full[2], s_read[2], p_full, pv_done;
     uint64_t q_full, q_empty;
     uint64_t piece_full[kPieces], piece_empty[kPieces];
-    uint64_t next_full;  // the number of the next whole item
+    uint64_t sums_full[kPieces], o_full[kPieces];  // of a piece: its rows' sums, its products
+    uint64_t o_free[2];   // a result in tensor memory is read
+    uint64_t next_full;   // the number of the next whole item
     uint64_t drained[2];  // all products of either kind have ended
     alignas(16) uint4 next;
     Piece pieces[kPieces];
-    alignas(16) float factor[64];  // of the rows: of a raised reference, then 1 / l
-    int row_at[64];        // row of o of the tile's rows, from its first
-    int lim[64];           // keys each row sees
-    // Bit i: key seen_by_all + i has values that were cleared (of this piece, or the next).
-    uint32_t odd[2][2];
+    alignas(16) float factor[64];        // of the rows of a raised reference
+    alignas(16) float inv[kPieces][64];  // 1 / l of a piece's rows; 0: a row without weight, or none
+    int row_at[64];                      // row of o of the tile's rows, from its first
+    uint32_t odd[kPieces][2];  // bit i: key seen_by_all + i has values that were cleared
     long long sum[kThreadsTc / 32];
     uint32_t tmem;
 };
@@ -197,10 +200,13 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
             mbar_init(&sh.s_full[lane], 1);
             mbar_init(&sh.s_read[lane], 4);
             mbar_init(&sh.drained[lane], 1);
+            mbar_init(&sh.o_free[lane], 128);
         }
         if (lane < kPieces) {
             mbar_init(&sh.piece_full[lane], 1);
-            mbar_init(&sh.piece_empty[lane], 6);  // softmax 4, products 2
+            mbar_init(&sh.piece_empty[lane], 10);  // softmax 4, products 2, results 4
+            mbar_init(&sh.sums_full[lane], 128);
+            mbar_init(&sh.o_full[lane], 1);
         }
         if (lane == 0) {
             mbar_init(&sh.p_full, 128);
@@ -218,7 +224,6 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
         tmem_relinquish();
     }
     if (tid < RT) sh.row_at[tid] = tid / G * Hq + tid % G;
-    if (tid < 4) sh.odd[tid >> 1][tid & 1] = 0;
     tc_fence_before();
     pdl_wait();
     pdl_launch();  // the join's CTAs may take their places and wait
@@ -441,7 +446,7 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
         const uint64_t dq = desc_kmajor(smem_addr(sq)), dk = desc_kmajor(smem_addr(skv));
         const uint64_t dp = desc_kmajor(smem_addr(sp)), dv = desc_mnmajor(smem_addr(skv), KT);
         constexpr uint32_t QBLOCK = C::QBLOCK >> 4, KBLOCK = C::KBLOCK >> 4, TILE = C::TILE >> 4;  // descriptor units
-        int t = 0, slot = 0, phase = 0, nq = 0;  // tiles so far; the next one's place; row tiles
+        int t = 0, slot = 0, phase = 0, nq = 0;  // tiles so far; the next one's place; pieces with tiles
         auto wait = [&](uint64_t* bar, uint32_t parity) {
             if (!__all_sync(0xffffffffu, mbar_wait(bar, parity, kWaitClocks))) ok = false;
             return ok;
@@ -466,11 +471,11 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
                     const uint32_t d = tbase + C::TM_S + (t & 1) * KT;
                     if (elect_one()) {
 #pragma unroll
-                        for (int i = 0; i < C::BLOCKS; i++)
+                        for (int c = 0; c < C::BLOCKS; c++)
 #pragma unroll
                             for (int kk = 0; kk < 4; kk++)
-                                mma_bf16(d, dq + (uint32_t)i * QBLOCK + 2 * kk, b + (uint32_t)i * KBLOCK + 2 * kk, idesc_s,
-                                         i > 0 || kk > 0);
+                                mma_bf16(d, dq + (uint32_t)c * QBLOCK + 2 * kk, b + (uint32_t)c * KBLOCK + 2 * kk, idesc_s,
+                                         c > 0 || kk > 0);
                         mma_commit(&sh.s_full[t & 1]);
                         if (j + 1 == n) mma_commit(&sh.q_empty);
                     }
@@ -482,6 +487,9 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
                 }
             } else {
                 const uint32_t idesc = idesc_bf16(128, 16, 1, 0) + (((uint32_t)(nrow >> 3) - 2) << 17);
+                const int buf = nq % C::NO;
+                const uint32_t d = tbase + C::TM_O + buf * kUnits * RT;
+                if (n > 0 && !wait(&sh.o_free[buf], ((nq++ / C::NO) & 1) ^ 1)) break;
                 for (int j = 0; j < n; j++, t++) {
                     if (!wait(&sh.p_full, t & 1)) break;
                     tc_fence_after();
@@ -491,10 +499,11 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
                         for (int u = 0; u < kUnits; u++)
 #pragma unroll
                             for (int kk = 0; kk < KT / 16; kk++)
-                                mma_bf16(tbase + C::TM_O + u * RT, a + (uint32_t)u * 2 * KBLOCK + kstep_mnmajor(kk),
+                                mma_bf16(d + u * RT, a + (uint32_t)u * 2 * KBLOCK + kstep_mnmajor(kk),
                                          dp + 2 * kk, idesc, j > 0 || kk > 0);
                         mma_commit(&sh.empty[slot]);
                         mma_commit(&sh.pv_done);
+                        if (j + 1 == n) mma_commit(&sh.o_full[i]);
                     }
                     __syncwarp();
                     if (++slot == NT) slot = 0;
@@ -507,32 +516,30 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
         __syncwarp();
         if (!__all_sync(0xffffffffu, mbar_wait(&sh.drained[scores], 0, 1LL << 24))) ok = false;
         if (!ok) flags |= KDA_DEV_TIMEOUT;
-    } else {
-        // ------------------------------------------------------------ softmax and results
+    } else if (warp < 4) {
+        // ------------------------------------------------------------ softmax
         // Row 16 w + i of a 64-row accumulator is lane 32 w + i.
         const int row = 16 * warp + (lane & 15), rtok = row / G;
         const bool rows_here = 16 * warp < RT;
         const uint32_t tlane = tmem_at(tbase, 32 * warp, 0);
-        int t = 0, slot = 0, phase = 0;  // tiles so far; the current one's place
+        int t = 0, slot = 0, phase = 0, buf = 0;  // tiles so far; the current one's place; O's
         // These warps meet at barriers, so after a wait that gave up they go on without
         // waiting to where all of them stop.
         for (int np = 0;; np++) {
             const int i = np % kPieces;
             warp_wait(ok, &sh.piece_full[i], (np / kPieces) & 1);
+            if (tid < 2) sh.odd[i][tid] = 0;  // (its last piece is done with)
             if (wg_or(!ok)) {
                 ok = false;
                 break;
             }
             const Piece pc = sh.pieces[i];
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&sh.piece_empty[i]);
             if (pc.end) break;
             const int n = piece_tiles<KT>(pc), all = seen_by_all(pc);
             const bool live = lane < 16 && row < pc.ntok * G;  // (at most RT rows)
             // Keys this row sees; a row of nothing masks nothing (never stored).
             const int lim = live ? max(pc.pos0 + rtok + 1, 0) : 0x7fffffff;
-            if (lane < 16 && rows_here) sh.lim[row] = lim;
-            if (tid < 2) sh.odd[(np & 1) ^ 1][tid] = 0;
+            const uint32_t to = tlane + C::TM_O + buf * kUnits * RT;
             float m = -INFINITY, l = 0.f;  // reference (c S) and sum
             for (int j = 0; j < n; j++, t++) {
                 const int base = (pc.kt0 + j) * KT;
@@ -579,11 +586,11 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
 #pragma unroll 1
                     for (int b = 0; b < kUnits * RT; b += 32) {
                         float y[32];
-                        tmem_ld32(tlane + C::TM_O + b, y);
+                        tmem_ld32(to + b, y);
 #pragma unroll
                         for (int e = 0; e < 32; e++) y[e] *= sh.factor[(b & (RT - 1)) + e];
-                        tmem_st16(tlane + C::TM_O + b, y);
-                        tmem_st16(tlane + C::TM_O + b + 16, y + 16);
+                        tmem_st16(to + b, y);
+                        tmem_st16(to + b + 16, y + 16);
                     }
                     tmem_wait_st();
                 }
@@ -631,7 +638,7 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
                             }
                         }
                         const int bit = base + k - all;
-                        if (odd) atomicOr(&sh.odd[np & 1][bit >> 5 & 1], 1u << (bit & 31));
+                        if (odd) atomicOr(&sh.odd[i][bit >> 5 & 1], 1u << (bit & 31));
                     }
                 }
                 fence_proxy_async_smem();
@@ -642,40 +649,71 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
                     phase ^= 1;
                 }
             }
-            if (n > 0) warp_wait(ok, &sh.pv_done, (t - 1) & 1);
+            // What the results need, and the rows' sums. (The slot is used again once these warps
+            // and the results' are done with the piece.)
+            if (lane < 16 && rows_here) sh.inv[i][row] = !live || l == 0.f ? 0.f : 1.f / l;
+            if (live) {
+                if (pc.slot >= 0)
+                    p.sp.ws[attn_slot_floats(p.sp.rows, kDL) * pc.slot + (size_t)p.sp.rows * kDL + row] =
+                        l == 0.f ? -INFINITY : m + log2f(l);
+                else if (p.lse)
+                    p.lse[(size_t)pc.tok0 * Hq + (size_t)pc.h * G + sh.row_at[row]] =
+                        l == 0.f ? -INFINITY : (m + log2f(l)) * 0.69314718056f;
+            }
+            mbar_arrive(&sh.sums_full[i]);
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&sh.piece_empty[i]);
+            if (n > 0 && ++buf == C::NO) buf = 0;
+        }
+        if (!ok) flags |= KDA_DEV_TIMEOUT;
+    } else {
+        // ------------------------------------------------------------ results
+        // In warps of their own, so that the next piece's scores need not wait (nor, at 32
+        // rows, its products: there are two results in tensor memory).
+        const uint32_t tlane = tmem_at(tbase, 32 * (warp & 3), 0);
+        int buf = 0;
+        uint32_t o_phase = 0;  // of the pieces' products, a bit a slot
+        for (int np = 0; ok; np++) {
+            const int i = np % kPieces;
+            warp_wait(ok, &sh.piece_full[i], (np / kPieces) & 1);
+            if (!ok) break;
+            const Piece pc = sh.pieces[i];
+            if (pc.end) break;
+            const int n = piece_tiles<KT>(pc), all = seen_by_all(pc), rows = pc.ntok * G;
+            warp_wait(ok, &sh.sums_full[i], (np / kPieces) & 1);
+            if (n > 0) {
+                warp_wait(ok, &sh.o_full[i], o_phase >> i & 1);
+                o_phase ^= 1u << i;
+            }
+            if (!ok) break;
             tc_fence_after();
+            const uint32_t to = tlane + C::TM_O + buf * kUnits * RT;
             const size_t at0 = (size_t)pc.tok0 * Hq + (size_t)pc.h * G;
             float* part = pc.slot >= 0 ? p.sp.ws + attn_slot_floats(p.sp.rows, kDL) * pc.slot : nullptr;
-            wg_sync();  // (factors of a raised reference are read)
-            if (lane < 16 && rows_here) sh.factor[row] = !live || l == 0.f ? 0.f : 1.f / l;
-            if (live) {
-                if (part) part[(size_t)p.sp.rows * kDL + row] = l == 0.f ? -INFINITY : m + log2f(l);
-                else if (p.lse)
-                    p.lse[at0 + sh.row_at[row]] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.69314718056f;
-            }
             // Rows without any weight: zeros, whatever their accumulators hold.
-            const bool nothing = wg_or(n == 0 || (live && l == 0.f));
-            const int rows = pc.ntok * G;
+            bool empty_row = false;
+            for (int r = lane; r < rows; r += 32) empty_row |= sh.inv[i][r] == 0.f;
+            const bool nothing = n == 0 || __any_sync(0xffffffffu, empty_row);
             const bool in_order = p.s.Hkv == 1 || pc.ntok == 1;  // rows of o
-            const uint32_t odd[2] = {sh.odd[np & 1][0], sh.odd[np & 1][1]};
+            const uint32_t odd[2] = {sh.odd[i][0], sh.odd[i][1]};
             float fin = 0.f;  // NaN once a value is not finite
 #pragma unroll 1
             for (int b = 0; b < kUnits * RT; b += 32) {
                 const int u = b / RT, r0 = b & (RT - 1);
-                const int ch = 128 * u + 32 * warp + lane;
+                const int ch = 128 * u + 32 * (warp & 3) + lane;
                 if (r0 >= rows) continue;
                 float y[32];
-                if (n > 0) tmem_ld32(tlane + C::TM_O + b, y);
+                if (n > 0) tmem_ld32(to + b, y);
 #pragma unroll
                 for (int e = 0; e < 32; e += 4) {
-                    const float4 f = *reinterpret_cast<const float4*>(&sh.factor[r0 + e]);
+                    const float4 f = *reinterpret_cast<const float4*>(&sh.inv[i][r0 + e]);
                     const float g[4] = {f.x, f.y, f.z, f.w};
 #pragma unroll
                     for (int k = 0; k < 4; k++) y[e + k] *= g[k];
                 }
                 if (nothing) {
 #pragma unroll
-                    for (int e = 0; e < 32; e++) y[e] = n > 0 && sh.factor[r0 + e] != 0.f ? y[e] : 0.f;
+                    for (int e = 0; e < 32; e++) y[e] = n > 0 && sh.inv[i][r0 + e] != 0.f ? y[e] : 0.f;
                 }
                 if (odd[0] | odd[1]) {
                     for (int k = 0; k < 64; k++) {
@@ -688,7 +726,7 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
                         if (!finite_flag(v)) continue;
 #pragma unroll
                         for (int e = 0; e < 32; e++)
-                            if (key < sh.lim[r0 + e]) y[e] += v;
+                            if (key < pc.pos0 + (r0 + e) / G + 1) y[e] += v;
                     }
                 }
                 if (part) {
@@ -719,7 +757,12 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
             }
             if (!(fin == 0.f)) flags |= KDA_DEV_NONFINITE;
             tc_fence_before();
-            wg_sync();  // limits and factors are read
+            if (n > 0) {
+                mbar_arrive(&sh.o_free[buf]);
+                if (++buf == C::NO) buf = 0;
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&sh.piece_empty[i]);
         }
         if (!ok) flags |= KDA_DEV_TIMEOUT;
     }
