@@ -19,7 +19,9 @@
 //                each warp's 32), and the edge (below)
 //   warps 4..7   the results
 //   warps 8, 9   issue the first and the second products
-//   warp 10      finds the work and issues the loads
+//   warp 10      issues the loads
+//   warp 11      finds the work, ahead of the loads: from a request's lengths to its first
+//                tile takes some 5000 clocks, which stood between any two items before
 //
 // A key past a row's last one gets P = 0 by a select on S. 0 x NaN is NaN, so before the
 // second product the softmax warps clear in shared memory what some rows must not see:
@@ -37,8 +39,8 @@ namespace {
 
 using namespace ptx;
 
-constexpr int kThreadsTc = 352;
-constexpr int kScoreWarp = 8, kOutWarp = 9, kLoadWarp = 10;
+constexpr int kThreadsTc = 384;
+constexpr int kScoreWarp = 8, kOutWarp = 9, kLoadWarp = 10, kPlanWarp = 11;
 constexpr int kDL = kLatentDim;
 constexpr int kUnits = kDL / 128;        // units of a tile's latents
 constexpr int kPieces = 4;               // pieces announced ahead
@@ -95,7 +97,7 @@ struct Shared {
     uint64_t full[kMaxTiles], empty[kMaxTiles];  // of each key tile in shared memory
     uint64_t s_full[2], s_read[2], p_full, pv_done;
     uint64_t q_full, q_empty;
-    uint64_t piece_full[kPieces], piece_empty[kPieces];
+    uint64_t piece_full[kPieces], piece_empty[kPieces], piece_taken[kPieces];  // (taken: its loads begin)
     uint64_t sums_full[kPieces], o_full[kPieces];  // of a piece: its rows' sums, its products
     uint64_t o_free[2];   // a result in tensor memory is read
     uint64_t next_full;   // the number of the next whole item
@@ -204,7 +206,8 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
         }
         if (lane < kPieces) {
             mbar_init(&sh.piece_full[lane], 1);
-            mbar_init(&sh.piece_empty[lane], 10);  // softmax 4, products 2, results 4
+            mbar_init(&sh.piece_empty[lane], 11);  // softmax 4, products 2, results 4, loads
+            mbar_init(&sh.piece_taken[lane], 1);
             mbar_init(&sh.sums_full[lane], 128);
             mbar_init(&sh.o_full[lane], 1);
         }
@@ -237,10 +240,9 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
     bool ok = true;
 
     if (warp == kLoadWarp) {
-        // ------------------------------------------------------------ work and loads
+        // ------------------------------------------------------------ loads
         int tile = 0, slot = 0, phase = 0;  // key tiles so far; the next one's place
-        int np = 0, nq = 0;                 // pieces, row tiles so far
-        int asked = 0;                      // for further items
+        int nq = 0;                         // row tiles so far
         bool q_pending = false;
         const int log2_page = __ffs(p.page) - 1;
         const int log2_per = p.page < KT ? __ffs(KT) - 1 - log2_page : 0, per = 1 << log2_per;  // pages of a tile
@@ -277,32 +279,40 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
             warp_wait(ok, bar, parity);
             return ok;
         };
-        auto announce = [&](const Piece& pc) {
+        int id_ahead = 0;
+        bool ahead = false;  // id_ahead: of the next piece's first tile
+        for (int np = 0; ok; np++) {
             const int i = np % kPieces;
-            warp_wait(ok, &sh.piece_empty[i], ((np / kPieces) & 1) ^ 1);
-            if (!ok) return;
-            if (lane == 0) {
-                sh.pieces[i] = pc;
-                mbar_arrive(&sh.piece_full[i]);
-            }
-            np++;
+            warp_wait(ok, &sh.piece_full[i], (np / kPieces) & 1);
+            if (!ok) break;
+            const Piece pc = sh.pieces[i];
             __syncwarp();
-        };
-        auto process = [&](const Piece& pc) {
-            announce(pc);
+            if (lane == 0) {
+                mbar_arrive(&sh.piece_taken[i]);
+                mbar_arrive(&sh.piece_empty[i]);
+            }
+            if (pc.end) break;
             const int n = piece_tiles<KT>(pc);
-            if (n == 0 || !ok) return;
+            if (n == 0) continue;
             q_pending = true;
-            int id = page_id(pc, pc.kt0);
+            int id = ahead ? id_ahead : page_id(pc, pc.kt0);
+            ahead = false;
             for (int j = 0; j < n; j++) {
                 const int kt = pc.kt0 + j;
-                const int next_id = j + 1 < n ? page_id(pc, kt + 1) : 0;
+                int next_id = 0;
+                if (j + 1 < n) {
+                    next_id = page_id(pc, kt + 1);
+                } else if (const int k = (np + 1) % kPieces; warp_test(&sh.piece_full[k], ((np + 1) / kPieces) & 1)) {
+                    const Piece& nx = sh.pieces[k];
+                    ahead = !nx.end && piece_tiles<KT>(nx) > 0;
+                    if (ahead) id_ahead = page_id(nx, nx.kt0);
+                }
                 if (!wait_place(pc, &sh.empty[slot], phase ^ 1)) break;
                 if (lane == 0) mbar_arrive_expect_tx(&sh.full[slot], C::TILE);
                 __syncwarp();
                 // All blocks together, so that DRAM sees whole rows.
                 for (int i0 = 0; i0 < C::BLOCKS << log2_per; i0 += 32) {
-                    const int i = i0 + lane, blk = i >> log2_per, part = i & (per - 1);
+                    const int x = i0 + lane, blk = x >> log2_per, part = x & (per - 1);
                     const int page = __shfl_sync(0xffffffffu, id, part);
                     if (blk < C::BLOCKS)
                         tma_load_3d(skv + slot * C::TILE + blk * C::KBLOCK + (part << log2_page) * 128, &map_c,
@@ -320,6 +330,30 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
                 }
                 id = next_id;
             }
+        }
+        if (!ok) {
+            flags |= KDA_DEV_TIMEOUT;
+            // copies in flight land before the CTA leaves
+            for (int i = 0; i < NT && i < tile; i++) {
+                slot = (slot ? slot : NT) - 1;  // the last tiles, backwards
+                phase ^= slot == NT - 1;
+                mbar_wait(&sh.full[slot], phase, 1LL << 24);
+            }
+            if (nq) mbar_wait(&sh.q_full, (nq - 1) & 1, 1LL << 24);
+        }
+    } else if (warp == kPlanWarp) {
+        // ------------------------------------------------------------ work
+        int np = 0, asked = 0;  // pieces announced; items asked for
+        auto announce = [&](const Piece& pc) {
+            const int i = np % kPieces;
+            warp_wait(ok, &sh.piece_empty[i], ((np / kPieces) & 1) ^ 1);
+            if (!ok) return;
+            if (lane == 0) {
+                sh.pieces[i] = pc;
+                mbar_arrive(&sh.piece_full[i]);
+            }
+            np++;
+            __syncwarp();
         };
         auto piece_of = [&](int r, const AttnReq& q, int h, int t) {
             Piece pc;
@@ -368,15 +402,7 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
             if (!have) cur = end;
         }
         while (ok && (!split || cur < end)) {
-            if (!split) {
-                if (lane == 0) {
-                    mbar_arrive_expect_tx(&sh.next_full, 16);
-                    clc_try_cancel(&sh.next, &sh.next_full);
-                }
-                asked++;
-                __syncwarp();
-                if (cur < walk.base) walk = AttnWalk{};
-            }
+            if (!split && cur < walk.base) walk = AttnWalk{};
             if (!have) {
                 have = split ? attn_first_tile(p.s, walk, &cur, &r, &q, &h, &t, &first)
                              : attn_find<false>(p.s, walk, cur, &r, &q, &in);
@@ -402,12 +428,21 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
                     }
                     have = h < p.s.Hkv;
                 }
-                process(pc);
+                announce(pc);
+                // Another item is asked for once this one's loads begin, so that what a CTA has
+                // ahead is one.
+                if (!split) warp_wait(ok, &sh.piece_taken[(np - 1) % kPieces], ((np - 1) / kPieces) & 1);
             } else if (split) {
                 break;
             }
-            if (!split) {
+            if (!split && ok) {
                 have = false;
+                if (lane == 0) {
+                    mbar_arrive_expect_tx(&sh.next_full, 16);
+                    clc_try_cancel(&sh.next, &sh.next_full);
+                }
+                asked++;
+                __syncwarp();
                 warp_wait(ok, &sh.next_full, (asked - 1) & 1);
                 const int x = ok ? __shfl_sync(0xffffffffu, clc_answer(&sh.next), 0) : -1;
                 if (x < 0) break;
@@ -427,14 +462,7 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
         announce(last);
         if (!ok) {
             flags |= KDA_DEV_TIMEOUT;
-            // copies in flight land before the CTA leaves
-            for (int i = 0; i < NT && i < tile; i++) {
-                slot = (slot ? slot : NT) - 1;  // the last tiles, backwards
-                phase ^= slot == NT - 1;
-                mbar_wait(&sh.full[slot], phase, 1LL << 24);
-            }
-            if (nq) mbar_wait(&sh.q_full, (nq - 1) & 1, 1LL << 24);
-            if (asked) mbar_wait(&sh.next_full, (asked - 1) & 1, 1LL << 24);
+            if (asked) mbar_wait(&sh.next_full, (asked - 1) & 1, 1LL << 24);  // an answer on its way lands
         }
     } else if (warp == kScoreWarp || warp == kOutWarp) {
         // ------------------------------------------------------------ products
