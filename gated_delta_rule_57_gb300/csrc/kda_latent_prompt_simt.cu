@@ -339,6 +339,7 @@ cudaError_t launch_t(const AttnArgs& a) {
     using C = SimtCfg<DR, RI>;
     int dev = 0;
     const int nsm = device_sms(&dev);
+    if (nsm == 0) return cudaErrorNoDevice;
     PromptSimtParams p{};
     p.s = {a.cu_q, nullptr, a.N, a.total_q, a.max_q, 0, a.Hq, 1, C::ROWS, C::ROWS, kKeys, 1, 1, 0};
     p.q = static_cast<const float*>(a.q);
@@ -360,13 +361,21 @@ cudaError_t launch_t(const AttnArgs& a) {
     cudaError_t e = allow_shared(kda_latent_prompt_simt_kernel<DR, RI>, C::SMEM, ready, dev);
     if (e != cudaSuccess) return e;
     // Ranges unless rows have few key tiles, or there are enough items to fill the SMs evenly.
-    if (nsm > 0 && a.max_q > 2 * kKeys && (long long)a.total_q / C::ROWS * a.Hq < 16LL * nsm) {
+    // Measured, ranges against whole items, us: 2 prompts of 256 tokens x 8 heads 33/73, 8 x 16 heads
+    // 121/144, 32 x 16 heads 396/407, 4 of 2048 x 32 heads 3790/3770; of 128 tokens 2 x 8 heads 32/41, but
+    // 16 x 16 heads 93/81.
+    if (a.max_q > 2 * kKeys && (long long)a.total_q / C::ROWS * a.Hq < 16LL * nsm) {
         p.sp.ctas = nsm;
         p.sp.least = kKeys;
         p.sp.rows = std::min((a.max_q + 3) & ~3, C::ROWS);  // whole 16-byte vectors
         if (a.ws && a.ws_bytes >= attn_split_bytes(p.sp, kD)) p.sp.ws = a.ws;
     }
-    const long long grid = p.sp.ws ? p.sp.ctas : std::min(attn_items_bound(p.s), 1LL << 20);
+    // Whole items: a CTA for each, which evens out long ones, or one per SM, which walks over the
+    // requests once instead of for every item. Measured, a CTA an item against one per SM, us: 8
+    // prompts of 2048 x 32 heads 7500/7730, 40 of 100 .. 1000 x 32 4570/4860, 64 of 128 x 32 565/564; 200
+    // of 1 .. 128 x 16 719/694, 256 of 33 x 32 919/695, 1000 of 128 x 8 3250/2110, 4864 of 64 x 2 6710/916.
+    const long long most = a.N > 64 ? nsm : 1 << 20;
+    const long long grid = p.sp.ws ? p.sp.ctas : std::min(attn_items_bound(p.s), most);
     e = launch_dependent(kda_latent_prompt_simt_kernel<DR, RI>, dim3((unsigned)grid), dim3(kThreads), C::SMEM,
                          a.stream, p);
     if (e != cudaSuccess || !p.sp.ws) return e;
@@ -376,7 +385,11 @@ cudaError_t launch_t(const AttnArgs& a) {
 }  // namespace
 
 cudaError_t launch_latent_prompt_simt(const AttnArgs& a) {
-    if (a.max_q <= 64) return a.dr ? launch_t<64, 4>(a) : launch_t<0, 4>(a);
+    // Row tiles of 64 or 128. Small ones waste less of a short prompt, on keys behind the diagonal and
+    // in the last tile; large ones read keys and values half as often. Measured, 64 against 128, us: 64
+    // prompts of 64 tokens x 16 heads 110/167, 64 of 128 270/286, 16 of 200 x 8 heads 112/119, 16 of 300
+    // 160/205; 8 of 512 x 16 heads 344/329, 4 of 2048 x 32 heads 4460/3790.
+    if (a.max_q <= 384) return a.dr ? launch_t<64, 4>(a) : launch_t<0, 4>(a);
     return a.dr ? launch_t<64, 8>(a) : launch_t<0, 8>(a);
 }
 

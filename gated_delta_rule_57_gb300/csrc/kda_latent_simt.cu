@@ -329,6 +329,7 @@ cudaError_t launch_t(const AttnArgs& a) {
     const int blocks = latent_head_blocks(a.Hq, RT), G = a.Hq / blocks, tok = RT / G;
     int dev = 0;
     const int nsm = device_sms(&dev);
+    if (nsm == 0) return cudaErrorNoDevice;
     p.s = {a.cu_q, a.kv_len, a.N, a.total_q, a.max_q, attn_kv_cap(a), blocks, G, tok, tok, kKeys, 1, 1, 0};
     p.q = static_cast<const float*>(a.q);
     p.cache = static_cast<const float*>(a.k);
@@ -347,7 +348,7 @@ cudaError_t launch_t(const AttnArgs& a) {
     if (e != cudaSuccess) return e;
     p.sp = latent_simt_split(a.N, a.total_q, a.max_q, p.s.kv_cap, a.Hq, nsm);
     if (p.sp.ctas && a.ws && a.ws_bytes >= attn_split_bytes(p.sp, kDL)) p.sp.ws = a.ws;
-    const long long grid = p.sp.ws ? p.sp.ctas : std::min(attn_items_bound(p.s), 1LL << 20);
+    const long long grid = p.sp.ws ? p.sp.ctas : std::min(attn_items_bound(p.s), (long long)nsm);  // one per SM
     e = launch_dependent(kda_latent_simt_kernel<DR, RT>, dim3((unsigned)grid), dim3(kThreads), C::SMEM,
                          a.stream, p);
     if (e != cudaSuccess || !p.sp.ws) return e;
@@ -360,8 +361,11 @@ AttnSplit latent_simt_split(int N, int total_q, int max_q, long long max_keys, i
     AttnSplit sp{};
     if (N == 0 || total_q == 0 || max_q == 0 || Hq == 0 || nsm == 0) return sp;
     const int rt = latent_simt_rows(max_q, Hq), blocks = latent_head_blocks(Hq, rt), G = Hq / blocks, tok = rt / G;
-    if (max_keys <= KDA_LATENT_SHORT_KEYS / 2) return sp;
-    if ((long long)total_q / tok * blocks >= 16LL * nsm) return sp;
+    // Ranges, unless the keys are so few that their join costs more. Measured, ranges against whole
+    // items, us: of 32 keys 4 requests x 8 heads 12.4/9.7, 64 x 32 heads 19/17; of 64 keys
+    // 14.6/14.0 and 31/25; of 128 keys 15/24 and 38/43, 1024 requests x 16 heads 290/292; 4864 of 256
+    // keys x 16 heads 2400/2420.
+    if (max_keys <= KDA_LATENT_SHORT_KEYS / 4) return sp;
     sp.ctas = nsm;
     sp.least = kKeys;
     sp.rows = (std::min(max_q, tok) * G + 3) & ~3;  // whole 16-byte vectors
@@ -369,6 +373,8 @@ AttnSplit latent_simt_split(int N, int total_q, int max_q, long long max_keys, i
 }
 
 cudaError_t launch_latent_simt(const AttnArgs& a) {
+    // (8 rows against 32: 1 request of 2048 keys x 4 heads 14 us against 19, 16 of 2048 x 8 heads 45
+    // against 74, 64 of 1024 80 against 136)
     if (latent_simt_rows(a.max_q, a.Hq) == 8) return a.dr ? launch_t<64, 8>(a) : launch_t<0, 8>(a);
     return a.dr ? launch_t<64, 32>(a) : launch_t<0, 32>(a);
 }

@@ -36,7 +36,7 @@ KDA_F32 = 1
 # Requests of at most this many keys (a sixteenth of it in fp32) are never split.
 KDA_ATTN_SHORT_KEYS = 2048
 
-# The same for kda_attn_latent_paged (half of it in fp32).
+# The same for kda_attn_latent_paged (a quarter of it in fp32).
 KDA_LATENT_SHORT_KEYS = 256
 
 KDA_DEV_DECAY_RANGE = 0x1

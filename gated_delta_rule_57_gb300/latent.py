@@ -228,7 +228,7 @@ def kda_attn_latent_paged(q, cache, block_table, cu_q, kv_len, *, scale: float, 
     most = T if max_q is None else max_q
     dev = _device(q)
     o, lse = _k._attn_outputs(q, 512, o, lse, want_lse, stream)
-    if workspace is None and max_pages * page > KDA_LATENT_SHORT_KEYS // (2 if io == KDA_F32 else 1):
+    if workspace is None and max_pages * page > KDA_LATENT_SHORT_KEYS // (4 if io == KDA_F32 else 1):
         need = (_k._lib or lib()).kda_attn_latent_workspace_size(N, T, most, Hq, 512, d - 512, io)
         if need != ctypes.c_size_t(-1).value and need:  # the call itself reports bad arguments
             workspace = _k._empty(need, torch.uint8, q, stream, scratch=True)

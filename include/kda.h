@@ -725,7 +725,7 @@ kda_status_t kda_attn_latent_prompt(const void* q, const void* k, const void* k_
                                     float scale, kda_dtype_t io, void* workspace, size_t ws_bytes,
                                     int* d_status, void* stream);
 
-/* Requests of at most this many keys (max_pages * page_size; half of it for KDA_F32) are
+/* Requests of at most this many keys (max_pages * page_size; a quarter of it for KDA_F32) are
  * never split by kda_attn_latent_paged: those calls need no workspace. */
 #define KDA_LATENT_SHORT_KEYS 256
 

@@ -427,3 +427,26 @@ def test_calls_at_once_on_two_streams(io):
     torch.cuda.synchronize()
     for i, out in got:
         assert all(torch.equal(x, y) for x, y in zip(alone[i], out))
+
+
+@pytest.mark.parametrize("io", DTYPES)
+@pytest.mark.parametrize("n,longest,hq", [(800, 64, 4), (400, 60, 1), (350, 500, 3), (320, 700, 2)])
+def test_many_requests(io, n, longest, hq):
+    """More items than SMs, whole or in ranges, of requests of any length and none."""
+    rng = random.Random(n + longest)
+    kv_lens = [rng.choice([longest, 0, 1, rng.randint(1, longest)]) for _ in range(n)]
+    q_lens = [rng.choice([1, 1, 1, 0, 2]) for _ in range(n)]
+    q, cache, table, cu, kv = case(q_lens, kv_lens, hq, 64, 16, io)
+    o, lse, status = paged(q, cache, table, cu, kv, 2)
+    attn_ref.check(o, lse, latent_ref.paged(q, cache, table, q_lens, kv_lens, SCALE))
+    assert int(status) == 0
+
+
+@pytest.mark.parametrize("io", DTYPES)
+@pytest.mark.parametrize("n,longest,h", [(65, 64, 3), (300, 40, 2), (200, 380, 1), (70, 400, 1)])
+def test_many_prompts(io, n, longest, h):
+    rng = random.Random(n + longest)
+    lens = [rng.choice([longest, 0, 1, rng.randint(1, longest)]) for _ in range(n)]
+    q, k, k_r, v, cu = prompt_case(lens, h, 64, io)
+    o, lse = pkg.kda_attn_latent_prompt(q, k, k_r, v, cu, max_len=longest)
+    attn_ref.check(o, lse, latent_ref.prompt(q, k, k_r, v, lens, 192 ** -0.5))
