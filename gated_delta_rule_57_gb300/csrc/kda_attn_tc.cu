@@ -886,7 +886,7 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
                         if (more) {
                             commit(&sh.kv_empty[ks]);
                             next();
-                            }
+                        }
                         // the rows' last scores are issued
                         if (j + 2 == n || (j + 1 == n && primed && x.n == 1)) commit(&sh.q_empty);
                     }
@@ -919,7 +919,7 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
                             scores(w, 0, ks);
                             commit(&sh.kv_empty[ks]);
                             next();
-                                if (j + 3 == n) commit(&sh.q_empty);
+                            if (j + 3 == n) commit(&sh.q_empty);
                         } else {
                             commit(&sh.o_full[w]);
                         }

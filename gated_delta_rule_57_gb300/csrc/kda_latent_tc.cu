@@ -868,8 +868,15 @@ AttnSplit latent_tc_split(int N, int total_q, int max_q, long long max_keys, int
     AttnSplit sp{};
     if (N == 0 || total_q == 0 || max_q == 0 || Hq == 0 || nsm == 0) return sp;
     const int rt = latent_tc_rows(max_q, Hq), blocks = latent_head_blocks(Hq, rt), G = Hq / blocks, tok = rt / G;
-    if (max_keys <= KDA_LATENT_SHORT_KEYS) return sp;
-    if ((long long)total_q / tok * blocks >= 8LL * nsm) return sp;
+    // Whole items, given out as CTAs become free, or ranges of one cost. Ranges end together,
+    // but cost some 6 us for the parts, their join and more pieces; whole items end up to one
+    // item apart. Measured, ranges against whole, us, 152 SMs: 256 requests of 256 keys x 16 heads
+    // 28/22, of 512 46/37, of 1024 68/60, 608 of 1024 x 32 heads 128/122, 2432 459/446; but 40 of
+    // 1024 x 16 22/29, of 2048 30/50, and with lengths drawn from 1 on 200 of 512 28/30, of 1024
+    // 42/50, 400 of 1024 61/64, 608 of 2048 133/148, of 1024 82/84, of 512 56/51.
+    const long long items = (long long)total_q / (max_q < tok ? max_q : tok) * blocks;  // at least
+    if (max_keys <= KDA_LATENT_SHORT_KEYS || (max_keys <= 512 && 2 * items >= nsm)) return sp;
+    if (items >= (max_keys < 2048 ? max_keys / 256 : 8) * nsm) return sp;
     sp.ctas = nsm;
     sp.least = 128;
     sp.rows = ((max_q < tok ? max_q : tok) * G + 3) & ~3;  // whole 16-byte vectors
@@ -877,6 +884,10 @@ AttnSplit latent_tc_split(int N, int total_q, int max_q, long long max_keys, int
 }
 
 cudaError_t launch_latent_tc(const AttnArgs& a) {
+    // Row tiles of 32 where calls have no more rows, with room for five key tiles and two results
+    // (against 64 with four and one: 256 requests of 4096 keys x 16 heads 194 us against 202, 64 x 32 heads 66
+    // against 69, 3 of 700 x 8 heads 15.7 against 16.4); of 64 above, as a tile's products are bound by
+    // its reads from shared memory, the same for 64 rows as for 32.
     if (latent_tc_rows(a.max_q, a.Hq) == 32) return a.dr ? launch_t<64, 32, 32>(a) : launch_t<0, 32, 32>(a);
     return a.dr ? launch_t<64, 64, 32>(a) : launch_t<0, 64, 32>(a);
 }
