@@ -132,7 +132,10 @@ def kda_kv_append_rope(q, k, v, slot_map, positions, turns, k_cache, v_cache, *,
     Hq = qs = os_ = kos = 0
     if k_out is not None:
         kop, kos = _packed(dev, "k_out", k_out, T, Hkv, d, dt)
-    if q is not None:
+    if q is None:
+        if q_out is not None:
+            raise ValueError("without q there is no q_out")
+    else:
         Hq = q.shape[1]
         qp, qs = _packed(dev, "q", q, T, Hq, d, dt)
         if q_out is None:
@@ -175,8 +178,8 @@ def kda_latent_append(c, k_r, slot_map, cache, *, positions=None, turns=None, q_
     kp = qp = op = kop = tp = pp = None
     ks = qs = qh = os_ = oh = kos = Hq = 0
     if k_r is None:
-        if q_r is not None or k_out is not None:
-            raise ValueError("without k_r there are no q_r and k_out")
+        if q_r is not None or q_out is not None or k_out is not None:
+            raise ValueError("without k_r there are no q_r, q_out and k_out")
     else:
         if turns is None or positions is None:
             raise ValueError("k_r needs positions and turns")
@@ -186,7 +189,10 @@ def kda_latent_append(c, k_r, slot_map, cache, *, positions=None, turns=None, q_
             raise ValueError("turns must have an entry per pair of k_r's channels")
         if k_out is not None:
             kop, kos = _flat(dev, "k_out", k_out, T, dr, dt)
-        if q_r is not None:
+        if q_r is None:
+            if q_out is not None:
+                raise ValueError("without q_r there is no q_out")
+        else:
             Hq = q_r.shape[1]
             qp, qs, qh = _heads(dev, "q_r", q_r, T, Hq, dr, dt)
             if q_out is None:

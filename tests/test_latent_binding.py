@@ -81,6 +81,9 @@ def test_refuses(error, call):
     lambda: pkg.kda_kv_append_rope(*QKV, i32(T).long(), i32(T), TURNS, bf(9, H, 16, 64), bf(9, H, 16, 64)),
     lambda: pkg.kda_kv_append_rope(*QKV, i32(T), i32(T), TURNS.double(), bf(9, H, 16, 64), bf(9, H, 16, 64)),
     lambda: pkg.kda_kv_append_rope(*QKV, i32(T), i32(T), TURNS, bf(9, H, 16, 64), bf(9, H, 16, 64), q_out=bf(T, H, 128)),
+    lambda: pkg.kda_kv_append_rope(None, *QKV[1:], i32(T), i32(T), TURNS, bf(9, H, 16, 64), bf(9, H, 16, 64), q_out=bf(T, H, 64)),
+    lambda: pkg.kda_latent_append(bf(T, 512), None, i32(T), bf(9, 16, 512), q_out=bf(T, H, 64)),
+    lambda: pkg.kda_latent_append(bf(T, 512), bf(T, 64), i32(T), bf(9, 16, 576), positions=i32(T), turns=TURNS, q_out=bf(T, H, 64)),
     lambda: pkg.kda_latent_append(bf(512, T).t(), bf(T, 64), i32(T), bf(9, 16, 576), positions=i32(T), turns=TURNS),
     lambda: pkg.kda_latent_append(bf(T, 512), bf(T, 64), i32(T), bf(9, 16, 576), positions=i32(T), turns=TURNS[:16]),
     lambda: pkg.kda_latent_append(bf(T, 512), bf(T, 64), i32(T), bf(9, 16, 576), positions=i32(T), turns=TURNS, q_r=bf(T, H, 32)),
