@@ -64,6 +64,7 @@ constexpr int kRegsSoftmax = 192, kRegsOther = 64, kRegsResult = 64;
 static_assert(2 * kRegsSoftmax + kRegsOther + kRegsResult <= 4 * 128, "more than launched with");
 constexpr int kMmaWarp = 8, kLoadWarp = 9, kEdgeWarp = 10, kMmaWarp1 = 11;
 constexpr int kPieces = 4;         // pieces announced ahead
+constexpr int kAskAhead = 6;       // key tiles left to load of a whole item when the next is asked for
 // Relative time of a key tile for one row tile and for a pair: about 1750 and 2500
 // clocks, measured at d = 128 in a step of two prompts' chunks among single tokens.
 constexpr int kCostSingle = 5, kCostPair = 7;
@@ -449,12 +450,24 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
                 np++;
                 __syncwarp();
             };
+            // Whole items: another one is asked for when this one's last loads are due. (At its first
+            // ones, a CTA with a long item took a further one away from those about to end: a
+            // prompt of 8192 tokens took 182 us with 8 heads of 192 channels, 146 now, and 121 with
+            // 8 of 128, 90 now. 4864 prompts of 64 tokens x 2 heads take 330 us, 322 before.)
+            auto ask = [&] {
+                if (lane == 0) {
+                    mbar_arrive_expect_tx(&sh.next_full, 16);
+                    clc_try_cancel(&sh.next, &sh.next_full);
+                }
+                asked++;
+                __syncwarp();
+            };
             auto process = [&](const Piece& pc) {
                 announce(pc);
                 const int n = piece_tiles(pc), lead = pc.pair ? 1 : 2;
-                if (n == 0 || !ok) return;
+                if (n == 0 || !ok) return false;
                 warp_wait(ok, &sh.q_empty, q_phase ^ 1);
-                if (!ok) return;
+                if (!ok) return false;
                 q_phase ^= 1;
                 if (lane == 0)
                     mbar_arrive_expect_tx(&sh.q_full, (1 + pc.pair) * (DQ / 64) * p.box_q * G * 128);
@@ -473,12 +486,14 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
                 load_kv(pc, &map_k, pc.kt0, id[0], true);
                 if (lead == 2 && n > 1) load_kv(pc, &map_k, pc.kt0 + 1, id[1], true);
                 for (int j = 0; j < n; j++) {
+                    if (!p.sp.ws && j == max(n - kAskAhead, 0)) ask();
                     load_kv(pc, &map_v, pc.kt0 + j, id[0], false);
                     if (j + lead < n) load_kv(pc, &map_k, pc.kt0 + j + lead, lead == 1 ? id[1] : id[2], true);
                     id[0] = id[1];
                     id[1] = id[2];
                     if (p.block_table && j + 3 < n) id[2] = page_id(pc, pc.kt0 + j + 3);
                 }
+                return true;
             };
             auto piece_of = [&](int r, const AttnReq& q, int h, int t) {
                 Piece pc;
@@ -531,15 +546,7 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
                 if (!have) cur = end;
             }
             while (ok && (!split || cur < end)) {
-                if (!split) {
-                    if (lane == 0) {
-                        mbar_arrive_expect_tx(&sh.next_full, 16);
-                        clc_try_cancel(&sh.next, &sh.next_full);
-                    }
-                    asked++;
-                    __syncwarp();
-                    if (cur < walk.base) walk = AttnWalk{};
-                }
+                if (!split && cur < walk.base) walk = AttnWalk{};
                 if (!have) {
                     have = split ? attn_first_tile(p.s, walk, &cur, &r, &q, &h, &t, &tile)
                                  : attn_find<false>(p.s, walk, cur, &r, &q, &in);
@@ -548,6 +555,7 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
                         h = (int)(in % p.s.Hkv);
                     }
                 }
+                bool asks = false;  // for the next item, among its loads
                 if (have) {
                     Piece pc = piece_of(r, q, h, t);
                     if (split) {
@@ -565,11 +573,12 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
                         }
                         have = h < p.s.Hkv;
                     }
-                    process(pc);
+                    asks = process(pc);
                 } else if (split) {
                     break;
                 }
                 if (!split) {
+                    if (!asks) ask();
                     have = false;
                     warp_wait(ok, &sh.next_full, (asked - 1) & 1);
                     const int x = ok ? __shfl_sync(0xffffffffu, clc_answer(&sh.next), 0) : -1;

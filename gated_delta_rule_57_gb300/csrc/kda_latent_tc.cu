@@ -44,6 +44,7 @@ constexpr int kScoreWarp = 8, kOutWarp = 9, kLoadWarp = 10, kPlanWarp = 11;
 constexpr int kDL = kLatentDim;
 constexpr int kUnits = kDL / 128;        // units of a tile's latents
 constexpr int kPieces = 4;               // pieces announced ahead
+constexpr int kAskAhead = 4;             // tiles left to load of an item when the next one is asked for
 constexpr int kItemKeys = 256;           // what an item costs beside its keys, in keys
 constexpr long long kWaitClocks = 1LL << 33;  // limit of a wait (about 4 s)
 constexpr float kRaise = 8.f;            // log2 growth of a row maximum that moves its reference
@@ -97,7 +98,7 @@ struct Shared {
     uint64_t full[kMaxTiles], empty[kMaxTiles];  // of each key tile in shared memory
     uint64_t s_full[2], s_read[2], p_full, pv_done;
     uint64_t q_full, q_empty;
-    uint64_t piece_full[kPieces], piece_empty[kPieces], piece_taken[kPieces];  // (taken: its loads begin)
+    uint64_t piece_full[kPieces], piece_empty[kPieces], piece_taken[kPieces];  // (taken: its last loads are due)
     uint64_t sums_full[kPieces], o_full[kPieces];  // of a piece: its rows' sums, its products
     uint64_t o_free[2];   // a result in tensor memory is read
     uint64_t next_full;   // the number of the next whole item
@@ -287,17 +288,18 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
             if (!ok) break;
             const Piece pc = sh.pieces[i];
             __syncwarp();
+            const int n = piece_tiles<KT>(pc);
             if (lane == 0) {
-                mbar_arrive(&sh.piece_taken[i]);
+                if (n <= kAskAhead) mbar_arrive(&sh.piece_taken[i]);
                 mbar_arrive(&sh.piece_empty[i]);
             }
             if (pc.end) break;
-            const int n = piece_tiles<KT>(pc);
             if (n == 0) continue;
             q_pending = true;
             int id = ahead ? id_ahead : page_id(pc, pc.kt0);
             ahead = false;
             for (int j = 0; j < n; j++) {
+                if (lane == 0 && j > 0 && j == n - kAskAhead) mbar_arrive(&sh.piece_taken[i]);
                 const int kt = pc.kt0 + j;
                 int next_id = 0;
                 if (j + 1 < n) {
@@ -429,8 +431,8 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
                     have = h < p.s.Hkv;
                 }
                 announce(pc);
-                // Another item is asked for once this one's loads begin, so that what a CTA has
-                // ahead is one.
+                // Another item is asked for when this one's last loads are due: not before, or it
+                // would wait here while other CTAs have nothing to do.
                 if (!split) warp_wait(ok, &sh.piece_taken[(np - 1) % kPieces], ((np - 1) / kPieces) & 1);
             } else if (split) {
                 break;
