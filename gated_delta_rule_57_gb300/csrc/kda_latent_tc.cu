@@ -27,6 +27,15 @@
 // second product the softmax warps clear in shared memory what some rows must not see:
 // rows of keys past the item's last (stale slots) whole; of the keys that only some rows
 // see the values that are not finite. Those are noted and added to the rows that see them.
+//
+// What bounds it. Few rows: HBM. 256 single tokens of 32 heads over 1.06 M cached tokens take 206 us,
+// 5.9 TB/s (87 % of a copy's rate; some 15 us are the start, the parts and their join). Full
+// tiles: the products, whose operands come out of shared memory. An MMA of 64 x 32 takes 30 clocks, one of
+// 128 x 64 49, so a tile of 64 rows and 32 keys 36 x 30 + 8 x 49 = 1470, which is 880 TFLOP/s;
+// 2 x 4 draft tokens of 32 heads over 262147 keys take 178 us, 820 TFLOP/s with the join. Tiles of 64 keys
+// would take 2080 clocks for twice the keys, but only two of them fit beside 64 rows, and
+// their loads are then waited for (202 us against 182 at the time). 16 heads fill half of a tile's 32 rows,
+// which costs nothing while HBM is the bound.
 #include <atomic>
 
 #include "kda_attn.cuh"
@@ -47,7 +56,9 @@ constexpr int kPieces = 4;               // pieces announced ahead
 constexpr int kAskAhead = 4;             // tiles left to load of an item when the next one is asked for
 constexpr int kItemKeys = 256;           // what an item costs beside its keys, in keys
 constexpr long long kWaitClocks = 1LL << 33;  // limit of a wait (about 4 s)
-constexpr float kRaise = 8.f;            // log2 growth of a row maximum that moves its reference
+// Log2 growth of a row maximum that moves its reference: P then stays below 2^8, and a raise costs a
+// pass over the results.
+constexpr float kRaise = 8.f;
 constexpr int kMaxTiles = 6;             // key tiles in shared memory, at most
 
 // RT rows of a row tile, KT keys of a key tile.
@@ -880,7 +891,7 @@ AttnSplit latent_tc_split(int N, int total_q, int max_q, long long max_keys, int
     if (max_keys <= KDA_LATENT_SHORT_KEYS || (max_keys <= 512 && 2 * items >= nsm)) return sp;
     if (items >= (max_keys < 2048 ? max_keys / 256 : 8) * nsm) return sp;
     sp.ctas = nsm;
-    sp.least = 128;
+    sp.least = 128;  // keys of a range: 3 requests to 700 keys x 8 heads 17.3 us, with 256 20.3, with 64 17.9
     sp.rows = ((max_q < tok ? max_q : tok) * G + 3) & ~3;  // whole 16-byte vectors
     return sp;
 }

@@ -619,6 +619,8 @@ size_t kda_attn_workspace_size(int N, int total_q, int max_q, int Hq, int Hkv, i
  * at position 2^31 - 1 as at 0. Pairs are channels i and i + rot / 2 (neighbours = 0) or
  * 2 i and 2 i + 1 (neighbours != 0). Positions may be negative.
  *
+ * Two tokens with one slot leave values of both, in pieces of 16 bytes, as with kda_kv_append.
+ *
  * Alignment, int arrays, device-side reports and strides (multiples of 16 bytes) as for the
  * four calls above.
  */
@@ -729,7 +731,8 @@ kda_status_t kda_attn_latent_prompt(const void* q, const void* k, const void* k_
  * never split by kda_attn_latent_paged: those calls need no workspace. */
 #define KDA_LATENT_SHORT_KEYS 256
 
-/* As kda_attn_workspace_size, for kda_attn_latent_paged. */
+/* As kda_attn_workspace_size, for kda_attn_latent_paged (up to 40 MB on 152 SMs). Unsplit, a row
+ * of more than some 150 million keys outlasts the kernel's bounded waits: KDA_DEV_TIMEOUT. */
 size_t kda_attn_latent_workspace_size(int N, int total_q, int max_q, int Hq, int dl, int dr,
                                       kda_dtype_t io);
 
