@@ -450,3 +450,40 @@ def test_many_prompts(io, n, longest, h):
     q, k, k_r, v, cu = prompt_case(lens, h, 64, io)
     o, lse = pkg.kda_attn_latent_prompt(q, k, k_r, v, cu, max_len=longest)
     attn_ref.check(o, lse, latent_ref.prompt(q, k, k_r, v, lens, 192 ** -0.5))
+
+
+@pytest.mark.parametrize("io", DTYPES)
+def test_calls_without_work(io):
+    """No tokens, no requests, no heads: nothing is read or written, outputs have their shapes."""
+    def x(*shape):
+        return torch.zeros(shape, dtype=io, device=DEV)
+    cache, kc, turns = x(4, 16, 576).fill_(3), x(4, 2, 16, 64).fill_(3), pkg.kda_rope_turns([1.0] * 32)
+    status, none = ints([0]), ints([])
+    for t, n, h in [(0, 0, 4), (0, 3, 4), (5, 0, 4), (5, 1, 0)]:
+        cu = ints([0] * n + [t])
+        o, lse = pkg.kda_attn_latent_paged(x(t, h, 576), cache, ints([[0]] * n).view(n, 1), cu, ints([1] * n), scale=1.0, status=status)
+        assert o.shape == (t, h, 512) and lse.shape == (t, h)
+        o, lse = pkg.kda_attn_latent_prompt(x(t, h, 192), x(t, h, 128), x(t, 64), x(t, h, 128), cu, status=status)
+        assert o.shape == (t, h, 128) and lse.shape == (t, h)
+    assert pkg.kda_latent_append(x(0, 512), x(0, 64), none, cache, positions=none, turns=turns, q_r=x(0, 2, 64)).shape == (0, 2, 64)
+    assert pkg.kda_kv_append_rope(x(0, 3, 64), x(0, 2, 64), x(0, 2, 64), none, none, turns, kc, kc.clone()).shape == (0, 3, 64)
+    torch.cuda.synchronize()
+    assert int(status) == 0 and (cache == 3).all() and (kc == 3).all()
+
+
+@pytest.mark.parametrize("io", DTYPES)
+def test_queries_or_keys_alone(io):
+    """A call that rotates only queries, and one that only appends."""
+    q, k, v = (torch.randn(7, 2, 64, device=DEV).to(io) for _ in range(3))
+    freq = latent_ref.frequencies(64)
+    turns, at, slots = pkg.kda_rope_turns(freq), ints(list(range(50, 57))), ints(list(range(7)))
+    kc, vc = (torch.full((1, 2, 16, 64), 5.0, dtype=io, device=DEV) for _ in range(2))
+    assert pkg.kda_kv_append_rope(None, k, v, slots, at, turns, kc, vc) is None
+    torch.cuda.synchronize()
+    latent_ref.check_rotated(kc[0, :, :7].transpose(0, 1), latent_ref.rotate(k, at, freq, False))
+    assert torch.equal(vc[0, :, :7].transpose(0, 1), v) and (kc[0, :, 7:] == 5).all() and (vc[0, :, 7:] == 5).all()
+    none = torch.empty(7, 0, 64, dtype=io, device=DEV)
+    empty = torch.empty(1, 0, 16, 64, dtype=io, device=DEV)
+    out = pkg.kda_kv_append_rope(q, none, none, slots, at, turns, empty, empty)
+    torch.cuda.synchronize()
+    latent_ref.check_rotated(out, latent_ref.rotate(q, at, freq, False))
