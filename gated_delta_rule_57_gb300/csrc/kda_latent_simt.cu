@@ -6,17 +6,18 @@
 // pass over the keys with a running maximum m_i and sum l_i. A CTA of 256 threads holds
 // 32 rows (token, head) and takes 32 keys at a time through shared memory, the next 32
 // on their way (cp.async) meanwhile; the same tile is keys, then values.
-//   Scores: a thread has 4 rows x 4 keys over every fourth 16-byte vector of the
-//     channels, 8 loads for 64 multiply-adds; four neighbouring lanes add up.
+//   Scores: a warp has 4 rows x 32 keys, a thread 4 x 16 of them over every 16th 16-byte vector
+//     of the channels, 20 loads for 256 multiply-adds; the 16 lanes of half a warp then add up,
+//     each step giving half of a lane's scores away, so that each ends with 4 whole ones of one row.
 //   Outputs: a thread has 8 rows x 8 channels, 4 loads for 64 multiply-adds.
 // Two of them run in one instruction (fma.rn.f32x2). Where a call has no more than 8 rows a
 // tile (single tokens of few heads) the row tile is 8. Long rows are cut into ranges
 // as the header of kda_attn.cuh says.
 //
-// Bound by shared memory: the 8 loads of 16 bytes a lane take 32 clocks of its 128 bytes a clock, the 64
-// multiply-adds 16 of the FMA pipes. A mixed step of 9 requests to 2049 keys (two chunks of 33
-// tokens among single ones, 8 heads) takes 68 us, 21 TFLOP/s of 74. (Single
-// multiply-adds took 73 us where these took 71.)
+// Bound by shared memory and the FMA pipes alike: 20 loads of 16 bytes a lane take 80 clocks of its 128
+// bytes a clock, 256 multiply-adds 64 clocks. A mixed step of 9 requests to 2049 keys (two chunks of 33
+// tokens among single ones, 8 heads) takes 57 us, 25 TFLOP/s of 74; with 4 x 4 scores a thread (8 loads for 64,
+// four lanes adding up, every lane's exponentials four times) 68; 64 requests of 2048 keys x 16 heads 213 and 259.
 #include <algorithm>
 #include <atomic>
 
@@ -80,6 +81,8 @@ __global__ void __launch_bounds__(kThreads, 1) kda_latent_simt_kernel(const Late
     using C = SimtCfg<DR, RT>;
     constexpr int LD = C::LD, LP = C::LP;
     constexpr int RI = RT / 8, RO = RT / 4;  // rows of a thread in the first, in the second product
+    constexpr int NV = RI;                   // scores that a thread ends up with, of one row
+    constexpr int SPAN = 16 / RI;            // lanes of such a row in a half warp
     extern __shared__ __align__(16) float sm[];
     float* sq = sm;
     float* skv = sq + RT * LD;              // two tiles
@@ -91,7 +94,8 @@ __global__ void __launch_bounds__(kThreads, 1) kda_latent_simt_kernel(const Late
 
     pdl_wait();
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int part = lane & 3, kg = lane >> 2;      // scores: channels, keys kg + 8 j, rows warp + 8 i
+    const int part = lane & 15, key16 = lane & 16;  // scores: channels 4 part + 64 i, keys key16 .. + 15
+    const int row1 = RI * warp + part / SPAN, key1 = key16 + part % SPAN * NV;  // softmax: row, first key
     const int r0 = (tid >> 6) * RO, c4 = (tid & 63) * 4;  // outputs: rows r0 .., channels c4 .., 256 + c4 ..
     const int log2_page = __ffs(p.page) - 1;
     const AttnShape& s = p.s;
@@ -167,13 +171,8 @@ __global__ void __launch_bounds__(kThreads, 1) kda_latent_simt_kernel(const Late
             }
             copies_end();
         };
-        float m[RI], l[RI];
+        float m = -INFINITY, l = 0.f;  // (l: of this lane's keys)
         float2 acc[RO][4];
-#pragma unroll
-        for (int i = 0; i < RI; i++) {
-            m[i] = -INFINITY;
-            l[i] = 0.f;
-        }
 #pragma unroll
         for (int i = 0; i < RO; i++)
 #pragma unroll
@@ -185,56 +184,66 @@ __global__ void __launch_bounds__(kThreads, 1) kda_latent_simt_kernel(const Late
             copies_wait<1>();
             __syncthreads();
             const float* kv = skv + buf * kKeys * LD;
-            float2 y[RI][4];
+            float v[16 * RI];
+            {
+                float2 y[RI][16];
 #pragma unroll
-            for (int i = 0; i < RI; i++)
+                for (int i = 0; i < RI; i++)
 #pragma unroll
-                for (int j = 0; j < 4; j++) y[i][j] = make_float2(0.f, 0.f);
-#pragma unroll 2
-            for (int e = part * 4; e < C::DQ; e += 16) {
-                float4 b[4];
+                    for (int j = 0; j < 16; j++) y[i][j] = make_float2(0.f, 0.f);
+#pragma unroll 1
+                for (int e = part * 4; e < C::DQ; e += 64) {
+                    float4 a[RI];
 #pragma unroll
-                for (int j = 0; j < 4; j++) b[j] = ld4(kv + (kg + 8 * j) * LD + e);
+                    for (int i = 0; i < RI; i++) a[i] = ld4(sq + (RI * warp + i) * LD + e);
 #pragma unroll
-                for (int i = 0; i < RI; i++) {
-                    const float4 a = ld4(sq + (warp + 8 * i) * LD + e);
+                    for (int j = 0; j < 16; j++) {
+                        const float4 b = ld4(kv + (key16 + j) * LD + e);
 #pragma unroll
-                    for (int j = 0; j < 4; j++) {
-                        y[i][j] = fma2(make_float2(a.x, a.y), make_float2(b[j].x, b[j].y), y[i][j]);
-                        y[i][j] = fma2(make_float2(a.z, a.w), make_float2(b[j].z, b[j].w), y[i][j]);
+                        for (int i = 0; i < RI; i++) {
+                            y[i][j] = fma2(make_float2(a[i].x, a[i].y), make_float2(b.x, b.y), y[i][j]);
+                            y[i][j] = fma2(make_float2(a[i].z, a[i].w), make_float2(b.z, b.w), y[i][j]);
+                        }
                     }
                 }
+#pragma unroll
+                for (int i = 0; i < RI; i++)
+#pragma unroll
+                    for (int j = 0; j < 16; j++) v[16 * i + j] = y[i][j].x + y[i][j].y;
             }
-            float x[RI][4];
+            // The 16 lanes' sums meet: at each step a lane gives half of its scores away and adds up
+            // the other half, so that it ends with NV whole ones.
 #pragma unroll
-            for (int i = 0; i < RI; i++) {
-                const int row = warp + 8 * i, lim = s_lim[row];
-                float mx = -INFINITY;
+            for (int o = 8, n = 8 * RI; o > 0; o >>= 1, n >>= 1) {
+                const bool up = part & o;
 #pragma unroll
-                for (int j = 0; j < 4; j++) {
-                    x[i][j] = y[i][j].x + y[i][j].y;
-                    x[i][j] += __shfl_xor_sync(0xffffffffu, x[i][j], 1);
-                    x[i][j] += __shfl_xor_sync(0xffffffffu, x[i][j], 2);
-                    x[i][j] = k0 + kg + 8 * j < lim ? x[i][j] * c : -INFINITY;
-                    mx = fmaxf(mx, x[i][j]);
+                for (int k = 0; k < n; k++) {
+                    const float give = up ? v[k] : v[k + n];
+                    v[k] = (up ? v[k + n] : v[k]) + __shfl_xor_sync(0xffffffffu, give, o);
                 }
-#pragma unroll
-                for (int o = 4; o < 32; o <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-                const float mn = fmaxf(m[i], mx);
-                const float ref = mn == -INFINITY ? 0.f : mn;  // a row that sees nothing yet
-                const float corr = exp2f(m[i] - ref);
-                m[i] = mn;
-                l[i] *= corr;
-                float e4 = 0.f;
-#pragma unroll
-                for (int j = 0; j < 4; j++) {
-                    const float e = exp2f(x[i][j] - ref);
-                    l[i] += e;  // of this lane's keys
-                    e4 = part == j ? e : e4;
-                }
-                sp[(kg + 8 * part) * LP + row] = e4;  // the four lanes have the same sums
-                if (lane == 0) s_corr[row] = corr;
             }
+            const int lim = s_lim[row1];
+            float mx = -INFINITY;
+#pragma unroll
+            for (int j = 0; j < NV; j++) {
+                v[j] = k0 + key1 + j < lim ? v[j] * c : -INFINITY;
+                mx = fmaxf(mx, v[j]);
+            }
+#pragma unroll
+            for (int o = 1; o < SPAN; o <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
+            const float mn = fmaxf(m, mx);
+            const float ref = mn == -INFINITY ? 0.f : mn;  // a row that sees nothing yet
+            const float corr = exp2f(m - ref);
+            m = mn;
+            l *= corr;
+#pragma unroll
+            for (int j = 0; j < NV; j++) {
+                const float e = exp2f(v[j] - ref);
+                l += e;
+                sp[(key1 + j) * LP + row1] = e;
+            }
+            if (lane % SPAN == 0 && lane < 16) s_corr[row1] = corr;
             __syncthreads();
 #pragma unroll
             for (int i = 0; i < RO; i++) {
@@ -278,16 +287,15 @@ __global__ void __launch_bounds__(kThreads, 1) kda_latent_simt_kernel(const Late
         copies_wait<0>();
         __syncthreads();  // (an item without keys: limits are written)
 #pragma unroll
-        for (int i = 0; i < RI; i++) {
-            const int row = warp + 8 * i;
-#pragma unroll
-            for (int o = 4; o < 32; o <<= 1) l[i] += __shfl_xor_sync(0xffffffffu, l[i], o);
-            if (lane) continue;
-            s_corr[row] = l[i] > 0.f ? 1.f / l[i] : (l[i] == 0.f ? 0.f : l[i]);  // NaN stays
-            if (row >= rows) continue;
-            const size_t at = (first + row / G) * s.Hkv * G + it.h * G + row % G;
-            if (dst) dst[(size_t)p.sp.rows * kDL + row] = l[i] == 0.f ? -INFINITY : m[i] + log2f(l[i]);
-            else if (p.lse) p.lse[at] = l[i] == 0.f ? -INFINITY : (m[i] + log2f(l[i])) * 0.69314718056f;
+        for (int o = 1; o < SPAN; o <<= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
+        l += __shfl_xor_sync(0xffffffffu, l, 16);
+        if (lane % SPAN == 0 && lane < 16) {
+            s_corr[row1] = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);  // NaN stays
+            if (row1 < rows) {
+                const size_t at = (first + row1 / G) * s.Hkv * G + it.h * G + row1 % G;
+                if (dst) dst[(size_t)p.sp.rows * kDL + row1] = l == 0.f ? -INFINITY : m + log2f(l);
+                else if (p.lse) p.lse[at] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.69314718056f;
+            }
         }
         __syncthreads();
 #pragma unroll
@@ -367,9 +375,9 @@ AttnSplit latent_simt_split(int N, int total_q, int max_q, long long max_keys, i
     if (N == 0 || total_q == 0 || max_q == 0 || Hq == 0 || nsm == 0) return sp;
     const int rt = latent_simt_rows(max_q, Hq), blocks = latent_head_blocks(Hq, rt), G = Hq / blocks, tok = rt / G;
     // Ranges, unless the keys are so few that their join costs more. Measured, ranges against whole
-    // items, us: of 32 keys 4 requests x 8 heads 12.4/9.7, 64 x 32 heads 19/17; of 64 keys
-    // 14.6/14.0 and 31/25; of 128 keys 15/24 and 38/43, 1024 requests x 16 heads 290/292; 4864 of 256
-    // keys x 16 heads 2400/2420.
+    // items, us: of 32 keys 4 requests x 8 heads 12.3/9.4, 64 x 32 heads 17/14; of 64 keys
+    // 14.1/13.7 and 26/21; of 128 keys 15/23 and 33/36, 1024 requests x 16 heads 240/242; 4864 of 256
+    // keys x 16 heads 1970/1990.
     if (max_keys <= KDA_LATENT_SHORT_KEYS / 4) return sp;
     sp.ctas = nsm;
     sp.least = kKeys;
@@ -378,8 +386,8 @@ AttnSplit latent_simt_split(int N, int total_q, int max_q, long long max_keys, i
 }
 
 cudaError_t launch_latent_simt(const AttnArgs& a) {
-    // (8 rows against 32: 1 request of 2048 keys x 4 heads 14 us against 19, 16 of 2048 x 8 heads 45
-    // against 74, 64 of 1024 80 against 136)
+    // (8 rows against 32: 1 request of 2048 keys x 4 heads 14 us against 17, 16 of 2048 x 8 heads 43
+    // against 62, 64 of 1024 78 against 113)
     if (latent_simt_rows(a.max_q, a.Hq) == 8) return a.dr ? launch_t<64, 8>(a) : launch_t<0, 8>(a);
     return a.dr ? launch_t<64, 32>(a) : launch_t<0, 32>(a);
 }
