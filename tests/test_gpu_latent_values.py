@@ -487,3 +487,31 @@ def test_queries_or_keys_alone(io):
     out = pkg.kda_kv_append_rope(q, none, none, slots, at, turns, empty, empty)
     torch.cuda.synchronize()
     latent_ref.check_rotated(out, latent_ref.rotate(q, at, freq, False))
+
+
+@pytest.mark.parametrize("io", DTYPES)
+@pytest.mark.parametrize("x", [NAN, INF])
+def test_a_bad_query_is_its_own_rows(io, x):
+    """NaN or Inf in a head's query: that head's row of that token and no other, whole and in ranges.
+    (Inf: among the keys that such a row sees here there is one whose score is +Inf.)"""
+    q_lens, kv_lens, hq = [3, 1, 2], [700, 3000, 40], 20
+    q, cache, table, cu, kv = case(q_lens, kv_lens, hq, 64, 64, io)
+    ref = latent_ref.paged(q, cache, table, q_lens, kv_lens, SCALE)
+    hit = torch.zeros(6, hq, dtype=torch.bool, device=DEV)
+    for t, h, c in [(0, 3, 0), (2, 19, 511), (3, 7, 570), (5, 0, 100)]:
+        q[t, h, c] = x
+        hit[t, h] = True
+    for ws in workspaces(3, 6, 3, hq, 64, io):
+        o, lse, status = paged(q, cache, table, cu, kv, 3, workspace=ws)
+        check_spoiled(o, lse, ref, hit[..., None].expand(-1, -1, 512), hit, status)
+    lens = [300, 70, 2500]
+    q, k, k_r, v, cu = prompt_case(lens, 2, 64, io)
+    ref = latent_ref.prompt(q, k, k_r, v, lens, 192 ** -0.5)
+    hit = torch.zeros(sum(lens), 2, dtype=torch.bool, device=DEV)
+    for t, h, c in [(299, 0, 5), (100, 1, 191), (310, 1, 127), (2000, 0, 130)]:
+        q[t, h, c] = x
+        hit[t, h] = True
+    o, lse = pkg.kda_attn_latent_prompt(q, k, k_r, v, cu, max_len=2500)
+    torch.cuda.synchronize()
+    assert torch.equal(~torch.isfinite(o), hit[..., None].expand_as(o)) and torch.equal(torch.isnan(lse), hit)
+    attn_ref.check(torch.where(hit[..., None], ref[0].to(io), o), torch.where(hit, ref[1].float(), lse), ref)
