@@ -17,7 +17,8 @@
 // Bound by shared memory and the FMA pipes alike: 20 loads of 16 bytes a lane take 80 clocks of its 128
 // bytes a clock, 256 multiply-adds 64 clocks. A mixed step of 9 requests to 2049 keys (two chunks of 33
 // tokens among single ones, 8 heads) takes 57 us, 25 TFLOP/s of 74; with 4 x 4 scores a thread (8 loads for 64,
-// four lanes adding up, every lane's exponentials four times) 68; 64 requests of 2048 keys x 16 heads 213 and 259.
+// four lanes adding up, every lane's exponentials four times) 68. Warps whose rows are not there leave the pipes to
+// the others: 64 requests of 2048 keys x 16 heads 142 us, 213 without.
 #include <algorithm>
 #include <atomic>
 
@@ -184,66 +185,68 @@ __global__ void __launch_bounds__(kThreads, 1) kda_latent_simt_kernel(const Late
             copies_wait<1>();
             __syncthreads();
             const float* kv = skv + buf * kKeys * LD;
-            float v[16 * RI];
-            {
-                float2 y[RI][16];
+            if (RI * warp < rows) {  // (warps without rows leave the pipes to the others)
+                float v[16 * RI];
+                {
+                    float2 y[RI][16];
 #pragma unroll
-                for (int i = 0; i < RI; i++)
+                    for (int i = 0; i < RI; i++)
 #pragma unroll
-                    for (int j = 0; j < 16; j++) y[i][j] = make_float2(0.f, 0.f);
+                        for (int j = 0; j < 16; j++) y[i][j] = make_float2(0.f, 0.f);
 #pragma unroll 1
-                for (int e = part * 4; e < C::DQ; e += 64) {
-                    float4 a[RI];
+                    for (int e = part * 4; e < C::DQ; e += 64) {
+                        float4 a[RI];
 #pragma unroll
-                    for (int i = 0; i < RI; i++) a[i] = ld4(sq + (RI * warp + i) * LD + e);
+                        for (int i = 0; i < RI; i++) a[i] = ld4(sq + (RI * warp + i) * LD + e);
 #pragma unroll
-                    for (int j = 0; j < 16; j++) {
-                        const float4 b = ld4(kv + (key16 + j) * LD + e);
+                        for (int j = 0; j < 16; j++) {
+                            const float4 b = ld4(kv + (key16 + j) * LD + e);
 #pragma unroll
-                        for (int i = 0; i < RI; i++) {
-                            y[i][j] = fma2(make_float2(a[i].x, a[i].y), make_float2(b.x, b.y), y[i][j]);
-                            y[i][j] = fma2(make_float2(a[i].z, a[i].w), make_float2(b.z, b.w), y[i][j]);
+                            for (int i = 0; i < RI; i++) {
+                                y[i][j] = fma2(make_float2(a[i].x, a[i].y), make_float2(b.x, b.y), y[i][j]);
+                                y[i][j] = fma2(make_float2(a[i].z, a[i].w), make_float2(b.z, b.w), y[i][j]);
+                            }
                         }
                     }
+#pragma unroll
+                    for (int i = 0; i < RI; i++)
+#pragma unroll
+                        for (int j = 0; j < 16; j++) v[16 * i + j] = y[i][j].x + y[i][j].y;
+                }
+                // The 16 lanes' sums meet: at each step a lane gives half of its scores away and adds up
+                // the other half, so that it ends with NV whole ones.
+#pragma unroll
+                for (int o = 8, n = 8 * RI; o > 0; o >>= 1, n >>= 1) {
+                    const bool up = part & o;
+#pragma unroll
+                    for (int k = 0; k < n; k++) {
+                        const float give = up ? v[k] : v[k + n];
+                        v[k] = (up ? v[k + n] : v[k]) + __shfl_xor_sync(0xffffffffu, give, o);
+                    }
+                }
+                const int lim = s_lim[row1];
+                float mx = -INFINITY;
+#pragma unroll
+                for (int j = 0; j < NV; j++) {
+                    v[j] = k0 + key1 + j < lim ? v[j] * c : -INFINITY;
+                    mx = fmaxf(mx, v[j]);
                 }
 #pragma unroll
-                for (int i = 0; i < RI; i++)
+                for (int o = 1; o < SPAN; o <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+                mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
+                const float mn = fmaxf(m, mx);
+                const float ref = mn == -INFINITY ? 0.f : mn;  // a row that sees nothing yet
+                const float corr = exp2f(m - ref);
+                m = mn;
+                l *= corr;
 #pragma unroll
-                    for (int j = 0; j < 16; j++) v[16 * i + j] = y[i][j].x + y[i][j].y;
-            }
-            // The 16 lanes' sums meet: at each step a lane gives half of its scores away and adds up
-            // the other half, so that it ends with NV whole ones.
-#pragma unroll
-            for (int o = 8, n = 8 * RI; o > 0; o >>= 1, n >>= 1) {
-                const bool up = part & o;
-#pragma unroll
-                for (int k = 0; k < n; k++) {
-                    const float give = up ? v[k] : v[k + n];
-                    v[k] = (up ? v[k + n] : v[k]) + __shfl_xor_sync(0xffffffffu, give, o);
+                for (int j = 0; j < NV; j++) {
+                    const float e = exp2f(v[j] - ref);
+                    l += e;
+                    sp[(key1 + j) * LP + row1] = e;
                 }
+                if (lane % SPAN == 0 && lane < 16) s_corr[row1] = corr;
             }
-            const int lim = s_lim[row1];
-            float mx = -INFINITY;
-#pragma unroll
-            for (int j = 0; j < NV; j++) {
-                v[j] = k0 + key1 + j < lim ? v[j] * c : -INFINITY;
-                mx = fmaxf(mx, v[j]);
-            }
-#pragma unroll
-            for (int o = 1; o < SPAN; o <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
-            const float mn = fmaxf(m, mx);
-            const float ref = mn == -INFINITY ? 0.f : mn;  // a row that sees nothing yet
-            const float corr = exp2f(m - ref);
-            m = mn;
-            l *= corr;
-#pragma unroll
-            for (int j = 0; j < NV; j++) {
-                const float e = exp2f(v[j] - ref);
-                l += e;
-                sp[(key1 + j) * LP + row1] = e;
-            }
-            if (lane % SPAN == 0 && lane < 16) s_corr[row1] = corr;
             __syncthreads();
 #pragma unroll
             for (int i = 0; i < RO; i++) {
@@ -256,9 +259,9 @@ __global__ void __launch_bounds__(kThreads, 1) kda_latent_simt_kernel(const Late
             }
             // Keys that only some rows see add nothing to the others, whatever they hold.
             const bool edge = k0 + kKeys > seen0 + 1;
-            auto add = [&](bool guard) {
+            auto add = [&](bool guard, int nk) {
 #pragma unroll 4
-                for (int j = 0; j < kKeys; j++) {
+                for (int j = 0; j < nk; j++) {
                     const float4 v0 = ld4(kv + j * LD + c4), v1 = ld4(kv + j * LD + 256 + c4);
                     float w[RO];
                     if constexpr (RO == 8) {
@@ -280,8 +283,10 @@ __global__ void __launch_bounds__(kThreads, 1) kda_latent_simt_kernel(const Late
                     }
                 }
             };
-            if (edge) add(true);
-            else add(false);
+            if (r0 < rows) {
+                if (edge) add(true, min(keys - k0, kKeys));
+                else add(false, kKeys);
+            }
             __syncthreads();  // the tile may be written again
         }
         copies_wait<0>();
@@ -375,9 +380,9 @@ AttnSplit latent_simt_split(int N, int total_q, int max_q, long long max_keys, i
     if (N == 0 || total_q == 0 || max_q == 0 || Hq == 0 || nsm == 0) return sp;
     const int rt = latent_simt_rows(max_q, Hq), blocks = latent_head_blocks(Hq, rt), G = Hq / blocks, tok = rt / G;
     // Ranges, unless the keys are so few that their join costs more. Measured, ranges against whole
-    // items, us: of 32 keys 4 requests x 8 heads 12.3/9.4, 64 x 32 heads 17/14; of 64 keys
-    // 14.1/13.7 and 26/21; of 128 keys 15/23 and 33/36, 1024 requests x 16 heads 240/242; 4864 of 256
-    // keys x 16 heads 1970/1990.
+    // items, us: of 32 keys 4 requests x 8 heads 12.0/9.3, 64 x 32 heads 17/15; of 64 keys
+    // 13.9/13.7 and 27/22; of 128 keys 14/23 and 34/36, 1024 requests x 16 heads 169/169; 4864 of 256
+    // keys x 16 heads 1313/1334.
     if (max_keys <= KDA_LATENT_SHORT_KEYS / 4) return sp;
     sp.ctas = nsm;
     sp.least = kKeys;
@@ -386,8 +391,8 @@ AttnSplit latent_simt_split(int N, int total_q, int max_q, long long max_keys, i
 }
 
 cudaError_t launch_latent_simt(const AttnArgs& a) {
-    // (8 rows against 32: 1 request of 2048 keys x 4 heads 14 us against 17, 16 of 2048 x 8 heads 43
-    // against 62, 64 of 1024 78 against 113)
+    // (8 rows against 32, us: 1 request of 2048 keys x 4 heads 12/14, 4 of 4096 x 1 head 20/28, 64 of 100 x 2
+    // heads 16/20, 9 of 2000 x 6 28/31; with 8 heads there is no difference, 16 of 2048 44/43)
     if (latent_simt_rows(a.max_q, a.Hq) == 8) return a.dr ? launch_t<64, 8>(a) : launch_t<0, 8>(a);
     return a.dr ? launch_t<64, 32>(a) : launch_t<0, 32>(a);
 }
