@@ -638,3 +638,18 @@ def kda_attn_paged(q, k_cache, v_cache, block_table, cu_q, kv_len, *,
                                 max_pages, d ** -0.5 if scale is None else scale, io,
                                 _ptr(workspace), ws_bytes, _ptr(status), _stream(stream)))
     return o, lse
+
+
+# The calls of `latent.py` under this module's name too. (It takes this module's helpers,
+# so it comes last; names are looked up, as it stays the one place where they are defined.)
+from . import latent as _latent  # noqa: E402
+
+
+def __getattr__(name):
+    if name in _latent.__all__:
+        return getattr(_latent, name)
+    raise AttributeError(f"module {__name__!r} has no attribute {name!r}")
+
+
+def __dir__():
+    return sorted({*globals(), *_latent.__all__})

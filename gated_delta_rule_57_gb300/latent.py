@@ -1,6 +1,7 @@
 """Binding of the calls for rotation by position and for layers that keep one latent
 vector a token (``include/kda.h``): argument marshalling only, as in ``kda.py``, whose
-conventions (streams, what a call makes, errors) hold here too.
+conventions (streams, what a call makes, errors) hold here too. The calls are attributes of
+`kda` as well, as all others are.
 """
 from __future__ import annotations
 
@@ -11,6 +12,9 @@ import torch
 
 from . import kda as _k
 from .kda import KDA_ERR_INVALID_ARG, KDA_F32, KDA_LATENT_SHORT_KEYS, KdaError, lib
+
+__all__ = ["kda_rope_turns", "kda_kv_append_rope", "kda_latent_append", "kda_attn_latent_workspace_size",
+           "kda_attn_latent_paged", "kda_attn_latent_prompt"]
 
 _PI = (314159265358979323846264338327950288419716939937510582097494459 << 200) // 10 ** 62  # pi 2^200
 
