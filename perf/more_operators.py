@@ -228,7 +228,7 @@ def prepare(case, seed):
         freq = _frequencies(rot)
         s.update(slot=slot, live=live, pos=_positions(case, gen), freq=freq.to(DEV), rot=rot, neighbours=case["pairs"] == "neighbours")
         if own and rot:
-            import gated_delta_rule_57_gb300 as kda
+            from gated_delta_rule_57_gb300 import kda
             s["turns"] = kda.kda_rope_turns(freq, device=DEV)
         if case["op"] == "rope":
             hq, hkv, d = case["hq"], case["hkv"], case["d"]
@@ -277,7 +277,7 @@ def run(s):
 
 
 def _framework(s):
-    import gated_delta_rule_57_gb300 as kda
+    from gated_delta_rule_57_gb300 import kda
     if s["op"] == "rope":
         q = kda.kda_kv_append_rope(s["q"], s["k"], s["v"], s["slot"], s["pos"], s["turns"], s["kc"], s["vc"], neighbours=s["neighbours"])
         return {"q": q, "kc": s["kc"], "vc": s["vc"]}
