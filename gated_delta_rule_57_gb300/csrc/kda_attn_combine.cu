@@ -91,7 +91,10 @@ __global__ void __launch_bounds__(kCombineWarps * 32)
 }
 
 // The same for wide rows (D = 512), M and the weights first, so that no part's load waits for
-// another's. The parts of an item, where the workspace has them.
+// another's. Every part counts, with a weight that underflowed to 0 too, and with one of 0 where a
+// row's scores are all -Inf: what is not finite in it stays, as 0 x NaN. (Where a row sees no key of
+// a part, the part holds zeros.) A row without weight in any part is zeros. The parts of an item,
+// where the workspace has them.
 template <int D>
 struct Parts {
     const AttnSplit& sp;
@@ -112,7 +115,7 @@ struct Parts {
         for (int k = 16; k > 0; k >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, k));
         return m;
     }
-    // A part's weight; one in which the row sees nothing has weight 0 and is not read. NaN stays.
+    // A part's weight, 0 for one without scores above -Inf. NaN stays.
     __device__ __forceinline__ float weight(int c, int row, float m) const {
         const float x = sum_of(c, row);
         return x == -INFINITY ? 0.f : exp2f(x - m);
@@ -127,11 +130,12 @@ __device__ __forceinline__ void add(float4& acc, float w, const float* y) {
 }
 template <typename T>
 __device__ __forceinline__ int put(T* dst, float4 acc, float inv) {
-    const float y[4] = {acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv};
+    float y[4] = {acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv};
     T out[4];
     int flags = 0;
 #pragma unroll
     for (int e = 0; e < 4; e++) {
+        if (inv == 0.f) y[e] = 0.f;  // a row of no weight
         flags |= finite_flag(y[e]);
         out[e] = from_f32<T>(y[e]);
     }
@@ -180,7 +184,6 @@ __global__ void __launch_bounds__(kCombineWarps * 32, 4)
 #pragma unroll 2
             for (int k = 0; k <= c1 - c0; k++) {
                 const float wk = __shfl_sync(0xffffffffu, w, k);
-                if (wk == 0.f) continue;
                 sum += wk;
 #pragma unroll
                 for (int q = 0; q < Q; q++) add(acc[q], wk, parts.at(c0 + k) + (size_t)row * D + 128 * q + lane * 4);
@@ -202,7 +205,6 @@ __global__ void __launch_bounds__(kCombineWarps * 32, 4)
 #pragma unroll 8
                 for (int k = 0; k < n; k++) {
                     const float wk = __shfl_sync(0xffffffffu, w, k);
-                    if (wk == 0.f) continue;
                     sum += wk;
                     add(acc, wk, parts.at(cb + kCombineWarps * k) + (size_t)row * D + col);
                 }

@@ -314,9 +314,11 @@ __global__ void __launch_bounds__(kThreads, 1) kda_latent_simt_kernel(const Late
 #pragma unroll
             for (int e = 0; e < 2; e++) {
                 const float2 a = acc[i][2 * e], b = acc[i][2 * e + 1];
-                // (a row of no weight: zeros)
-                y[e] = inv == 0.f ? make_float4(0.f, 0.f, 0.f, 0.f) : make_float4(a.x * inv, a.y * inv, b.x * inv, b.y * inv);
-                flags |= finite_flag(y[e].x) | finite_flag(y[e].y) | finite_flag(y[e].z) | finite_flag(y[e].w);
+                // (a row of no weight: zeros; in a part 0 x NaN stays, as the row may have weight in others)
+                y[e] = inv == 0.f && !dst ? make_float4(0.f, 0.f, 0.f, 0.f)
+                                          : make_float4(a.x * inv, a.y * inv, b.x * inv, b.y * inv);
+                // (of parts the join looks at the joined rows)
+                if (!dst) flags |= finite_flag(y[e].x) | finite_flag(y[e].y) | finite_flag(y[e].z) | finite_flag(y[e].w);
             }
             *reinterpret_cast<float4*>(o + c4) = y[0];
             *reinterpret_cast<float4*>(o + 256 + c4) = y[1];

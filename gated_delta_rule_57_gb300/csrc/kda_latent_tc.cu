@@ -731,13 +731,14 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
             const uint32_t to = tlane + C::TM_O + buf * kUnits * RT;
             const size_t at0 = (size_t)pc.tok0 * Hq + (size_t)pc.h * G;
             float* part = pc.slot >= 0 ? p.sp.ws + attn_slot_floats(p.sp.rows, kDL) * pc.slot : nullptr;
-            // Rows without any weight: zeros, whatever their accumulators hold.
+            // Rows without any weight: zeros, whatever their accumulators hold. In a part 0 times that,
+            // 0 or NaN, as the row may have weight in others.
             bool empty_row = false;
             for (int r = lane; r < rows; r += 32) empty_row |= sh.inv[i][r] == 0.f;
-            const bool nothing = n == 0 || __any_sync(0xffffffffu, empty_row);
+            const bool nothing = n == 0 || (!part && __any_sync(0xffffffffu, empty_row));
             const bool in_order = p.s.Hkv == 1 || pc.ntok == 1;  // rows of o
             const uint32_t odd[2] = {sh.odd[i][0], sh.odd[i][1]};
-            float fin = 0.f;  // NaN once a value is not finite
+            float fin = 0.f;  // NaN once a value is not finite (of parts the join looks at the joined rows)
 #pragma unroll 1
             for (int b = 0; b < kUnits * RT; b += 32) {
                 const int u = b / RT, r0 = b & (RT - 1);
@@ -774,10 +775,7 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
                     float* dst = part + (size_t)r0 * kDL + ch;
 #pragma unroll
                     for (int e = 0; e < 32; e++)
-                        if (r0 + e < rows) {
-                            fin = fmaf(y[e], 0.f, fin);
-                            dst[e * kDL] = y[e];
-                        }
+                        if (r0 + e < rows) dst[e * kDL] = y[e];
                 } else {
                     // Two rows at a time: even lanes store two channels of the first, odd
                     // lanes of the second.
