@@ -95,6 +95,10 @@ __global__ void __launch_bounds__(kThreadsSimt, kCtasPerSm) kda_attn_simt_kernel
                 break;
             }
             if (first) start = cur;
+            if (!split && it.q.bad) {
+                cur += gridDim.x;
+                continue;
+            }
             if (!split) {
                 it.t = it.q.nqt - 1 - (int)(in / s.Hkv);
                 it.h = (int)(in % s.Hkv);
@@ -277,7 +281,7 @@ __global__ void __launch_bounds__(kThreadsSimt, kCtasPerSm) kda_attn_simt_kernel
         }
     }
     if (blockIdx.x == 0)  // lengths of requests this CTA had no work of
-        for (int i = tid; i < s.N; i += kThreadsSimt) walk.bad |= attn_request(s, i).bad != 0;
+        for (int i = tid; i < s.N; i += kThreadsSimt) walk.bad |= attn_request<true>(s, i).bad != 0;
     if (walk.bad) flags |= KDA_DEV_LENGTH;
     report_flags(p.d_status, flags);
 }

@@ -127,6 +127,10 @@ __global__ void __launch_bounds__(kThreads, 1) kda_latent_prompt_simt_kernel(con
                 break;
             }
             if (first) start = cur;
+            if (!split && it.q.bad) {
+                cur += gridDim.x;
+                continue;
+            }
             if (!split) {
                 it.t = it.q.nqt - 1 - (int)(in / s.Hkv);
                 it.h = (int)(in % s.Hkv);
@@ -377,7 +381,7 @@ __global__ void __launch_bounds__(kThreads, 1) kda_latent_prompt_simt_kernel(con
         }
     }
     if (blockIdx.x == 0)  // lengths of requests this CTA had no work of
-        for (int i = tid; i < s.N; i += kThreads) walk.bad |= attn_request(s, i).bad != 0;
+        for (int i = tid; i < s.N; i += kThreads) walk.bad |= attn_request<true>(s, i).bad != 0;
     if (walk.bad) flags |= KDA_DEV_LENGTH;
     report_flags(p.d_status, flags);
 }

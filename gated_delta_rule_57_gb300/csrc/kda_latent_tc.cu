@@ -422,6 +422,7 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
                 if (!split && have) {
                     t = q.nqt - 1 - (int)(in / p.s.Hkv);
                     h = (int)(in % p.s.Hkv);
+                    have = !q.bad;
                 }
             }
             if (have) {
@@ -467,7 +468,7 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
             }
         }
         if (reports) {  // lengths of requests this CTA had no work of too
-            for (int i = lane; i < p.s.N; i += 32) walk.bad |= attn_request(p.s, i).bad != 0;
+            for (int i = lane; i < p.s.N; i += 32) walk.bad |= attn_request<true>(p.s, i).bad != 0;
             if (walk.bad) flags |= KDA_DEV_LENGTH;
         }
         Piece last{};
