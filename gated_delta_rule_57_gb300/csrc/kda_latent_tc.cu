@@ -767,9 +767,10 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
                         const float v =
                             __bfloat162float(p.cache[((size_t)id * p.page + key % p.page) * (kDL + DR) + ch]);
                         if (!finite_flag(v)) continue;
+                        // (a row of no weight stays zeros)
 #pragma unroll
                         for (int e = 0; e < 32; e++)
-                            if (key < pc.pos0 + (r0 + e) / G + 1) y[e] += v;
+                            if (key < pc.pos0 + (r0 + e) / G + 1 && (part || sh.inv[i][r0 + e] != 0.f)) y[e] += v;
                     }
                 }
                 if (part) {

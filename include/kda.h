@@ -693,9 +693,11 @@ kda_status_t kda_latent_append(const void* c, const void* k_r, const void* q_r, 
  *
  * Requests, lengths, pages, rows that see nothing, NaN and Inf, and arithmetic as for
  * kda_attn_paged. A row of the cache counts as a key and as a value: what is not finite in it
- * reaches every row that sees it and no other. A score of -Inf has weight 0; a row of no other
- * scores counts as one that sees no key. Any number of heads up to 65536: more than 64
- * are taken in blocks of equal size (prime numbers of heads beyond 64 one by one).
+ * reaches every row that sees it and no other. A score of -Inf has weight 0, in o everywhere but in
+ * the channels that are not finite in its cached row; a row of no other scores counts as one that
+ * sees no key (o = 0, lse = -inf). So it is with a workspace and without one. Any number of heads
+ * up to 65536: more than 64 are taken in blocks of equal size (prime numbers of heads beyond 64 one
+ * by one).
  */
 kda_status_t kda_attn_latent_paged(const void* q, const void* cache, const int* block_table,
                                    const int* cu_q, const int* kv_len, void* o, float* lse, int N,

@@ -78,9 +78,9 @@ def test_a_stretch_of_minus_infinity_leaves_nan_in_its_channel(io, ws, kv, lo, h
 
 @pytest.mark.parametrize("io", DTYPES)
 @pytest.mark.parametrize("ws", [False, True])
-@pytest.mark.parametrize("n,kv,heads", [(1, 3, 4), (1, 900, 8), (1, 9000, 64)])
+@pytest.mark.parametrize("n,kv,heads", [(1, 3, 4), (2, 2, 1), (3, 40, 8), (4, 900, 8), (2, 4, 64), (64, 900, 1), (4, 9000, 5)])
 def test_tokens_of_no_other_scores_see_nothing(io, ws, n, kv, heads):
-    """Every key of theirs scores -Inf."""
+    """Every key of theirs scores -Inf, those that only the later ones see too."""
     q, cache, rows = inputs(n, heads, kv, 64, io, n)
     rows[:kv, CHANNEL] = INF
     o, lse, status = call(q, cache, kv, ws)
