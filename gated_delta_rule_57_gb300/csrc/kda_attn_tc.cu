@@ -317,13 +317,19 @@ __device__ __forceinline__ int add_cleared(const TcAttnParams& p, const Piece& p
     return flags;
 }
 
-template <int DQ, int D>
+// r: of the shared key channels, where there are any.
+template <int DR>
+struct TcMaps {
+    CUtensorMap q, k, v, r;
+};
+template <>
+struct TcMaps<0> {
+    CUtensorMap q, k, v;
+};
+
+template <int DQ, int D, bool EARLY>
 __global__ void __launch_bounds__(kThreadsTc, 1)
-    kda_attn_tc_kernel(const __grid_constant__ CUtensorMap map_q,
-                       const __grid_constant__ CUtensorMap map_k,
-                       const __grid_constant__ CUtensorMap map_v,
-                       const __grid_constant__ CUtensorMap map_r,  // shared key channels
-                       const __grid_constant__ TcAttnParams p) {
+    kda_attn_tc_kernel(const __grid_constant__ TcMaps<DQ - D> maps, const __grid_constant__ TcAttnParams p) {
     using C = TcCfg<DQ, D>;
     constexpr int NS = C::STAGES, HALVES = D / 64;
     constexpr uint32_t TM_S = 0, TM_O = 256;
@@ -369,10 +375,10 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
             mbar_init(&sh.next_full, 1);
             mbar_init(&sh.q_full, 1);
             mbar_init(&sh.q_empty, C::TWO_ISSUE ? 2 : 1);
-            prefetch_tensormap(&map_q);
-            prefetch_tensormap(&map_k);
-            prefetch_tensormap(&map_v);
-            if (C::DR) prefetch_tensormap(&map_r);
+            prefetch_tensormap(&maps.q);
+            prefetch_tensormap(&maps.k);
+            prefetch_tensormap(&maps.v);
+            if constexpr (C::DR > 0) prefetch_tensormap(&maps.r);
         }
         fence_mbarrier_init();
     }
@@ -425,10 +431,12 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
                 if (lane == 0)
                     mbar_arrive_expect_tx(bar, C::TILE_BYTES + (keys ? C::SHARED_BYTES : 0));
                 __syncwarp();
-                if (C::DR && keys) {
-                    if (lane == HALVES)
-                        tma_load_3d(srope + (nk & 1) * C::SHARED_BYTES, &map_r, bar, 0, 0, pc.key0 + kt * kTile);
-                    nk++;
+                if constexpr (C::DR > 0) {
+                    if (keys) {
+                        if (lane == HALVES)
+                            tma_load_3d(srope + (nk & 1) * C::SHARED_BYTES, &maps.r, bar, 0, 0, pc.key0 + kt * kTile);
+                        nk++;
+                    }
                 }
                 if (half < HALVES) {
                     dst += half * (kTile * 128);
@@ -454,10 +462,9 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
                 np++;
                 __syncwarp();
             };
-            // Whole items: another one is asked for when this one's last loads are due. (At its first
-            // ones, a CTA with a long item took a further one away from those about to end: a
-            // prompt of 8192 tokens took 182 us with 8 heads of 192 channels, 146 now, and 121 with
-            // 8 of 128, 90 now. 4864 prompts of 64 tokens x 2 heads take 330 us, 322 before.)
+            // Whole items: another one is asked for when this one's last loads are due (at its first
+            // ones, a CTA with a long item takes a further one away from those about to end), or,
+            // EARLY, before this one is looked up: see launch_t.
             auto ask = [&] {
                 if (lane == 0) {
                     mbar_arrive_expect_tx(&sh.next_full, 16);
@@ -478,7 +485,7 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
                 __syncwarp();
                 if (lane < DQ / 64 * (1 + pc.pair)) {
                     const int w = lane / (DQ / 64), half = lane % (DQ / 64);
-                    tma_load_3d(sq + w * C::Q_BYTES + half * (kTile * 128), &map_q, &sh.q_full,
+                    tma_load_3d(sq + w * C::Q_BYTES + half * (kTile * 128), &maps.q, &sh.q_full,
                                 64 * half, pc.h * G, pc.tok0 + w * tok1);
                 }
                 // Ids of tiles j, j + 1, j + 2 in id[0..2].
@@ -487,12 +494,12 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
 #pragma unroll
                     for (int j = 0; j < 3; j++) id[j] = page_id(pc, pc.kt0 + j);
                 }
-                load_kv(pc, &map_k, pc.kt0, id[0], true);
-                if (lead == 2 && n > 1) load_kv(pc, &map_k, pc.kt0 + 1, id[1], true);
+                load_kv(pc, &maps.k, pc.kt0, id[0], true);
+                if (lead == 2 && n > 1) load_kv(pc, &maps.k, pc.kt0 + 1, id[1], true);
                 for (int j = 0; j < n; j++) {
-                    if (!p.sp.ws && j == max(n - kAskAhead, 0)) ask();
-                    load_kv(pc, &map_v, pc.kt0 + j, id[0], false);
-                    if (j + lead < n) load_kv(pc, &map_k, pc.kt0 + j + lead, lead == 1 ? id[1] : id[2], true);
+                    if (!EARLY && !p.sp.ws && j == max(n - kAskAhead, 0)) ask();
+                    load_kv(pc, &maps.v, pc.kt0 + j, id[0], false);
+                    if (j + lead < n) load_kv(pc, &maps.k, pc.kt0 + j + lead, lead == 1 ? id[1] : id[2], true);
                     id[0] = id[1];
                     id[1] = id[2];
                     if (p.block_table && j + 3 < n) id[2] = page_id(pc, pc.kt0 + j + 3);
@@ -550,7 +557,10 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
                 if (!have) cur = end;
             }
             while (ok && (!split || cur < end)) {
-                if (!split && cur < walk.base) walk = AttnWalk{};
+                if (!split) {
+                    if (EARLY) ask();
+                    if (cur < walk.base) walk = AttnWalk{};
+                }
                 if (!have) {
                     have = split ? attn_first_tile(p.s, walk, &cur, &r, &q, &h, &t, &tile)
                                  : attn_find<false>(p.s, walk, cur, &r, &q, &in);
@@ -583,7 +593,7 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
                     break;
                 }
                 if (!split) {
-                    if (!asks) ask();
+                    if (!EARLY && !asks) ask();
                     have = false;
                     warp_wait(ok, &sh.next_full, (asked - 1) & 1);
                     const int x = ok ? __shfl_sync(0xffffffffu, clc_answer(&sh.next), 0) : -1;
@@ -1327,24 +1337,30 @@ cudaError_t launch_t(const AttnArgs& a) {
     p.c = a.scale * 1.44269504089f;
     p.d_status = a.d_status;
 
-    CUtensorMap mq, mk, mv, mr{};
-    bool ok = make_rows(&mq, a.q, DQ, a.Hq, a.total_q, a.q_stride, a.q_head, G, p.box_q);
+    TcMaps<DQ - D> m;
+    bool ok = make_rows(&m.q, a.q, DQ, a.Hq, a.total_q, a.q_stride, a.q_head, G, p.box_q);
     if (a.kv_len)
-        ok = ok && make_cache(&mk, a.k, D, a.page, a.Hkv, a.num_pages) &&
-             make_cache(&mv, a.v, D, a.page, a.Hkv, a.num_pages);
+        ok = ok && make_cache(&m.k, a.k, D, a.page, a.Hkv, a.num_pages) &&
+             make_cache(&m.v, a.v, D, a.page, a.Hkv, a.num_pages);
     else
-        ok = ok && make_rows(&mk, a.k, D, a.Hkv, a.total_q, a.k_stride, a.k_head, 1, kTile) &&
-             make_rows(&mv, a.v, D, a.Hkv, a.total_q, a.v_stride, a.v_head, 1, kTile);
-    if (DQ > D) ok = ok && make_rows(&mr, a.k_r, DQ - D, 1, a.total_q, a.kr_stride, DQ - D, 1, kTile);
+        ok = ok && make_rows(&m.k, a.k, D, a.Hkv, a.total_q, a.k_stride, a.k_head, 1, kTile) &&
+             make_rows(&m.v, a.v, D, a.Hkv, a.total_q, a.v_stride, a.v_head, 1, kTile);
+    if constexpr (DQ > D) ok = ok && make_rows(&m.r, a.k_r, DQ - D, 1, a.total_q, a.kr_stride, DQ - D, 1, kTile);
     if (!ok) return cudaErrorInvalidValue;
-    auto kernel = kda_attn_tc_kernel<DQ, D>;
-    static std::atomic<uint64_t> ready{0};
-    cudaError_t e = allow_shared(kernel, tc_smem<DQ, D>(), ready, dev);
+    // Whole items, when the next one is asked for. With keys of up to two tiles the answer's way shows if
+    // it is asked for among the loads; with more, a CTA with a long item took a further one that others
+    // could have begun. Measured, early against late, us (heads of 128 channels): 4864 prompts of 64 tokens x 2
+    // heads 321/332, 1000 of 128 x 8 246/251, 500 of 200 x 8 190/191, of 1 to 128 x 8 on 2 2000 223/221; 256
+    // of 384 x 8 235/222, 8192 tokens x 8 119/88 (x 8 of 192 channels 182/146).
+    const bool early = !p.sp.ws && (a.kv_len ? p.s.kv_cap : a.max_q) <= 2 * kTile;
+    auto kernel = early ? kda_attn_tc_kernel<DQ, D, true> : kda_attn_tc_kernel<DQ, D, false>;
+    static std::atomic<uint64_t> ready[2];
+    cudaError_t e = allow_shared(kernel, tc_smem<DQ, D>(), ready[early], dev);
     if (e != cudaSuccess) return e;
     const long long grid = p.sp.ws ? p.sp.ctas : attn_items_bound(p.s);
     if (grid >= 1LL << 31) return cudaErrorInvalidValue;
     e = launch_dependent(kernel, dim3((unsigned)grid), dim3(kThreadsTc), tc_smem<DQ, D>(), a.stream,
-                         mq, mk, mv, mr, p);
+                         m, p);
     if (e != cudaSuccess || !p.sp.ws) return e;
     return launch_attn_combine(p.sp, a.Hkv, G, D, kTile, a.o, a.lse, KDA_BF16, a.d_status, a.stream);
 }
