@@ -71,7 +71,7 @@ def _heads(dev: int, name: str, t: torch.Tensor, T, H, d, dtype):
         sh = d
     if t.get_device() != dev:
         raise ValueError("KDA tensors must live on one CUDA device")
-    return t.data_ptr(), st if T > 1 else max(H, 1) * sh, sh
+    return t.data_ptr(), st if T > 1 else d, sh  # (one token's stride says nothing: the least that is taken)
 
 
 def _packed(dev: int, name: str, t: torch.Tensor, T, H, d, dtype):
