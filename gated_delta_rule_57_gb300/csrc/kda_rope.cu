@@ -5,10 +5,12 @@
 //     (a, b) -> (a cos t - b sin t, a sin t + b cos t),   t = position * frequency
 //
 // Angles. A frequency is held in turns a token, as a 64-bit fraction f / 2^64: the
-// product position * f modulo 2^64 is then exact, its top 32 bits are the angle to 2^-32
-// of a turn (1.5e-9 rad) at any position, and no 64-bit floating point is needed (a
-// rate of 1/64 here). What is left are the roundings of the fraction to fp32 (1.9e-7 rad at
-// most) and of sincospif.
+// product position * f modulo 2^64 is then exact at any position, and no 64-bit floating
+// point is needed (a rate of 1/64 here). The nearest quarter turn is taken off in whole numbers
+// and turned back by signs and an exchange, so that what is rounded to fp32 is an eighth of a turn
+// at most, to 2^-34: cos and sin are off by less than 3.1 x 2^-24 of themselves and 4e-10, near
+// their zeros too. (A fraction of half a turn rounded to fp32 is off by 9.4e-8 rad. 65536 latents
+// below take 115.5 us, 114.8 so, and 116.6 with all bits of the eighth, by a 64-bit conversion.)
 //
 // A token's angles are turned into cos and sin once (rot / 2 pairs, a thread each) and
 // kept in shared memory for all its heads, while the token's first loads are on their
@@ -139,8 +141,16 @@ __global__ void __launch_bounds__(kRopeThreads, 4) kda_rope_kernel(const RopePar
         const unsigned long long pos = (unsigned long long)(long long)p.pos[t];
         for (int i = i0; i < p.pairs; i += tpt) {
             const unsigned long long turn = pos * (unsigned long long)p.turns[i];
+            const uint32_t rest = (uint32_t)(turn >> 30);  // signed: less the nearest quarter
+            const uint32_t quarter = (uint32_t)(turn >> 62) + (rest >> 31);
             float s, c;
-            sincospif((float)(int)(turn >> 32) * 0x1p-31f, &s, &c);
+            sincospif((float)(int)rest * 0x1p-33f, &s, &c);
+            if (quarter & 1) {
+                const float x = c;
+                c = -s;
+                s = x;
+            }
+            if (quarter & 2) c = -c, s = -s;
             int u = i / N, w = i % N;
             if (!HALVES) {  // pair i is in vector i / (N / 2)
                 u = i / (N / 2);
