@@ -7,12 +7,12 @@
 // only when the maximum passes it by more than 8) and l its running sum.
 //
 // Layout. A row of O has 512 fp32 channels: 64 rows take half of the tensor memory if the
-// channels are its lanes, four accumulators of 128 channels x 64 rows, and the scores
-// fit beside them. So the first product has the rows (token, head) as M (64) and 64
-// keys as N, the second the channels as M (4 x 128) and the rows as N. One tile of 64
-// cached rows in shared memory is the K-major B operand of the first and the MN-major A
-// operand of the second; P goes through shared memory as its B operand. At few rows the
-// second product is as narrow as they are (a multiple of 16).
+// channels are its lanes, four accumulators of 128 channels x 64 rows, and two tiles of scores
+// fit beside them; of 32 rows two O do. So the first product has the rows (token, head) as M (64, of
+// which 32 or 64 count) and 32 keys as N, the second the channels as M (4 x 128) and the rows as
+// N. One tile of 32 cached rows in shared memory is the K-major B operand of the first and the
+// MN-major A operand of the second; P goes through shared memory as its B operand. At few rows
+// the second product is as narrow as they are (a multiple of 16).
 //
 // One CTA per SM:
 //   warps 0..3   softmax, one row of S per thread (64-row accumulators use 16 lanes of
@@ -60,12 +60,13 @@ constexpr long long kWaitClocks = 1LL << 33;  // limit of a wait (about 4 s)
 // pass over the results.
 constexpr float kRaise = 8.f;
 constexpr int kMaxTiles = 6;             // key tiles in shared memory, at most
+constexpr int kKeys = 32;                // keys of a key tile
 
-// RT rows of a row tile, KT keys of a key tile.
-template <int DR, int RT, int KT>
+// RT rows of a row tile.
+template <int DR, int RT>
 struct TcCfg {
     static constexpr int BLOCKS = (kDL + DR) / 64;             // of 64 channels, of a row
-    static constexpr int QBLOCK = RT * 128, KBLOCK = KT * 128;  // bytes of one
+    static constexpr int QBLOCK = RT * 128, KBLOCK = kKeys * 128;  // bytes of one
     static constexpr int Q = BLOCKS * QBLOCK, TILE = BLOCKS * KBLOCK;
     static constexpr int P = RT * 128;
     static constexpr int NT = (225 * 1024 - Q - P) / TILE;      // key tiles in shared memory
@@ -98,9 +99,8 @@ struct Piece {
     int slot;        // where a part of an item goes; -1: the whole item
     int end;         // no more pieces
 };
-template <int KT>
 __device__ __forceinline__ int piece_tiles(const Piece& p) {
-    return max(min(p.kt1, (p.keys + KT - 1) / KT) - p.kt0, 0);
+    return max(min(p.kt1, (p.keys + kKeys - 1) / kKeys) - p.kt0, 0);
 }
 // Keys that every row of the item sees: those of its first token.
 __device__ __forceinline__ int seen_by_all(const Piece& p) { return min(max(p.pos0 + 1, 0), p.keys); }
@@ -185,12 +185,12 @@ __device__ __forceinline__ uint32_t finite_pair(uint32_t x) {  // zeros for the 
     return x & ~((odd >> 15 & 0x00010001u) * 0xffffu);
 }
 
-template <int DR, int RT, int KT>
+template <int DR, int RT>
 __global__ void __launch_bounds__(kThreadsTc, 1)
     kda_latent_tc_kernel(const __grid_constant__ CUtensorMap map_q,
                          const __grid_constant__ CUtensorMap map_c,
                          const __grid_constant__ LatentTcParams p) {
-    using C = TcCfg<DR, RT, KT>;
+    using C = TcCfg<DR, RT>;
     constexpr int NT = C::NT;
     extern __shared__ __align__(1024) unsigned char sm[];  // 128-byte swizzle: 1024-byte tiles
     unsigned char* sq = sm;
@@ -257,10 +257,10 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
         int nq = 0;                         // row tiles so far
         bool q_pending = false;
         const int log2_page = __ffs(p.page) - 1;
-        const int log2_per = p.page < KT ? __ffs(KT) - 1 - log2_page : 0, per = 1 << log2_per;  // pages of a tile
+        const int log2_per = p.page < kKeys ? __ffs(kKeys) - 1 - log2_page : 0, per = 1 << log2_per;  // pages of a tile
         auto page_id = [&](const Piece& pc, int kt) {  // of part `lane` of a tile
             int id = p.num_pages;  // past the keys, or no page: beyond the cache, which loads zeros
-            const int j = kt * KT + (lane << log2_page);
+            const int j = kt * kKeys + (lane << log2_page);
             if (lane < per && j < pc.kv) {
                 id = p.block_table[(size_t)pc.r * p.max_pages + (j >> log2_page)];
                 if (id < 0 || id >= p.num_pages) {
@@ -299,7 +299,7 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
             if (!ok) break;
             const Piece pc = sh.pieces[i];
             __syncwarp();
-            const int n = piece_tiles<KT>(pc);
+            const int n = piece_tiles(pc);
             if (lane == 0) {
                 if (n <= kAskAhead) mbar_arrive(&sh.piece_taken[i]);
                 mbar_arrive(&sh.piece_empty[i]);
@@ -317,7 +317,7 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
                     next_id = page_id(pc, kt + 1);
                 } else if (const int k = (np + 1) % kPieces; warp_test(&sh.piece_full[k], ((np + 1) / kPieces) & 1)) {
                     const Piece& nx = sh.pieces[k];
-                    ahead = !nx.end && piece_tiles<KT>(nx) > 0;
+                    ahead = !nx.end && piece_tiles(nx) > 0;
                     if (ahead) id_ahead = page_id(nx, nx.kt0);
                 }
                 if (!wait_place(pc, &sh.empty[slot], phase ^ 1)) break;
@@ -329,7 +329,7 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
                     const int page = __shfl_sync(0xffffffffu, id, part);
                     if (blk < C::BLOCKS)
                         tma_load_3d(skv + slot * C::TILE + blk * C::KBLOCK + (part << log2_page) * 128, &map_c,
-                                    &sh.full[slot], 64 * blk, (kt * KT) & (p.page - 1), page);
+                                    &sh.full[slot], 64 * blk, (kt * kKeys) & (p.page - 1), page);
                 }
                 tile++;
                 if (++slot == NT) {
@@ -403,7 +403,7 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
             have = attn_first_tile(p.s, walk, &cur, &r, &q, &h, &t, &first) && cur < end;
             start = cur;
             if (have) {
-                cut.cost = q.cost * KT;
+                cut.cost = q.cost * kKeys;
                 cut.u0 = cur - (long long)first * cut.cost;
                 cut.tok0 = q.q0 + t * q.tok;
                 cut.ntok = min(q.tok, q.q_len - t * q.tok);
@@ -429,7 +429,7 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
                 Piece pc = piece_of(r, q, h, t);
                 if (split) {
                     const int n = pc.kt1;
-                    const long long u0 = cur - (long long)first * q.cost * KT;
+                    const long long u0 = cur - (long long)first * q.cost * kKeys;
                     pc.kt0 = first;
                     pc.kt1 = attn_tiles_until(p.s, q, u0, n, end);
                     if (pc.kt1 - pc.kt0 < n) pc.slot = 2 * blockIdx.x + (cur > start ? 1 : 0);
@@ -484,9 +484,9 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
         // have a warp each, and a tile's are issued in one go, by one lane, from
         // registers known to be uniform.
         const bool scores = warp == kScoreWarp;
-        constexpr uint32_t idesc_s = idesc_bf16(64, KT, 0, 0);  // (rows past RT: whatever follows)
+        constexpr uint32_t idesc_s = idesc_bf16(64, kKeys, 0, 0);  // (rows past RT: whatever follows)
         const uint64_t dq = desc_kmajor(smem_addr(sq)), dk = desc_kmajor(smem_addr(skv));
-        const uint64_t dp = desc_kmajor(smem_addr(sp)), dv = desc_mnmajor(smem_addr(skv), KT);
+        const uint64_t dp = desc_kmajor(smem_addr(sp)), dv = desc_mnmajor(smem_addr(skv), kKeys);
         constexpr uint32_t QBLOCK = C::QBLOCK >> 4, KBLOCK = C::KBLOCK >> 4, TILE = C::TILE >> 4;  // descriptor units
         int t = 0, slot = 0, phase = 0, nq = 0;  // tiles so far; the next one's place; pieces with tiles
         auto wait = [&](uint64_t* bar, uint32_t parity) {
@@ -498,7 +498,7 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
             if (!wait(&sh.piece_full[i], (np / kPieces) & 1)) break;
             const Piece& pc = sh.pieces[i];
             const int end = __shfl_sync(0xffffffffu, pc.end, 0);
-            const int n = __shfl_sync(0xffffffffu, piece_tiles<KT>(pc), 0);
+            const int n = __shfl_sync(0xffffffffu, piece_tiles(pc), 0);
             const int nrow = __shfl_sync(0xffffffffu, (pc.ntok * G + 15) & ~15, 0);
             __syncwarp();
             if (lane == 0) mbar_arrive(&sh.piece_empty[i]);
@@ -510,7 +510,7 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
                     if (!wait(&sh.s_read[t & 1], ((t >> 1) & 1) ^ 1)) break;
                     tc_fence_after();
                     const uint64_t b = dk + (uint32_t)slot * TILE;
-                    const uint32_t d = tbase + C::TM_S + (t & 1) * KT;
+                    const uint32_t d = tbase + C::TM_S + (t & 1) * kKeys;
                     if (elect_one()) {
 #pragma unroll
                         for (int c = 0; c < C::BLOCKS; c++)
@@ -540,7 +540,7 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
 #pragma unroll
                         for (int u = 0; u < kUnits; u++)
 #pragma unroll
-                            for (int kk = 0; kk < KT / 16; kk++)
+                            for (int kk = 0; kk < kKeys / 16; kk++)
                                 mma_bf16(d + u * RT, a + (uint32_t)u * 2 * KBLOCK + kstep_mnmajor(kk),
                                          dp + 2 * kk, idesc, j > 0 || kk > 0);
                         mma_commit(&sh.empty[slot]);
@@ -577,37 +577,29 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
             }
             const Piece pc = sh.pieces[i];
             if (pc.end) break;
-            const int n = piece_tiles<KT>(pc), all = seen_by_all(pc);
+            const int n = piece_tiles(pc), all = seen_by_all(pc);
             const bool live = lane < 16 && row < pc.ntok * G;  // (at most RT rows)
             // Keys this row sees; a row of nothing masks nothing (never stored).
             const int lim = live ? max(pc.pos0 + rtok + 1, 0) : 0x7fffffff;
             const uint32_t to = tlane + C::TM_O + buf * kUnits * RT;
             float m = -INFINITY, l = 0.f;  // reference (c S) and sum
             for (int j = 0; j < n; j++, t++) {
-                const int base = (pc.kt0 + j) * KT;
+                const int base = (pc.kt0 + j) * kKeys;
                 warp_wait(ok, &sh.s_full[t & 1], (t >> 1) & 1);
                 tc_fence_after();
-                uint32_t xr[KT];
-                float* x = reinterpret_cast<float*>(xr);
+                float x[kKeys];
                 float top = -INFINITY;
                 if (rows_here) {
-                    const uint32_t ts = tlane + C::TM_S + (t & 1) * KT;
-                    if constexpr (KT == 64) {
-                        tmem_ld64_async(ts, xr);
-                        tmem_wait_ld();
-                        tmem_landed<KT>(xr);
-                    } else {
-                        tmem_ld32(ts, x);
-                    }
+                    tmem_ld32(tlane + C::TM_S + (t & 1) * kKeys, x);
                     tc_fence_before();
                     if (lane == 0) mbar_arrive(&sh.s_read[t & 1]);
-                    if (__any_sync(0xffffffffu, base + KT > lim)) {
+                    if (__any_sync(0xffffffffu, base + kKeys > lim)) {
 #pragma unroll
-                        for (int e = 0; e < KT; e++) x[e] = base + e < lim ? x[e] : -INFINITY;
+                        for (int e = 0; e < kKeys; e++) x[e] = base + e < lim ? x[e] : -INFINITY;
                     }
                     float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-                    for (int e = 0; e < KT; e += 8)
+                    for (int e = 0; e < kKeys; e += 8)
 #pragma unroll
                         for (int k = 0; k < 4; k++) mx[k] = fmaxf(fmaxf(mx[k], x[e + k]), x[e + k + 4]);
                     top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * p.c;
@@ -639,9 +631,9 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
                 if (rows_here) {
                     const float ref = m == -INFINITY ? 0.f : m;
                     float sum[4] = {0.f, 0.f, 0.f, 0.f};
-                    uint32_t pk[KT / 2];
+                    uint32_t pk[kKeys / 2];
 #pragma unroll
-                    for (int e = 0; e < KT; e += 2) {
+                    for (int e = 0; e < kKeys; e += 2) {
                         const float u = ex2(fmaf(x[e], p.c, -ref)), v = ex2(fmaf(x[e + 1], p.c, -ref));
                         sum[e & 2] += u;
                         sum[(e & 2) + 1] += v;
@@ -652,16 +644,16 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
                     if (t > 0) warp_wait(ok, &sh.pv_done, (t - 1) & 1);  // P of the tile before is read
                     if (lane < 16) {
 #pragma unroll
-                        for (int b = 0; b < KT / 8; b++)
+                        for (int b = 0; b < kKeys / 8; b++)
                             *reinterpret_cast<uint4*>(sp + row * 128 + ((b ^ (row & 7)) << 4)) =
                                 make_uint4(pk[4 * b], pk[4 * b + 1], pk[4 * b + 2], pk[4 * b + 3]);
                     }
                 }
-                if (base + KT > all) {
+                if (base + kKeys > all) {
                     // Keys that some rows must not see: 16 threads a key.
                     warp_wait(ok, &sh.full[slot], phase);  // (the copies, seen by this thread)
                     const int k0 = max(all - base, 0), k1 = pc.keys - base;
-                    for (int k = k0 + tid / 16; k < KT; k += 8) {
+                    for (int k = k0 + tid / 16; k < kKeys; k += 8) {
                         bool odd = false;
 #pragma unroll
                         for (int b = 0; b < 4; b++) {
@@ -721,7 +713,7 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
             if (!ok) break;
             const Piece pc = sh.pieces[i];
             if (pc.end) break;
-            const int n = piece_tiles<KT>(pc), all = seen_by_all(pc), rows = pc.ntok * G;
+            const int n = piece_tiles(pc), all = seen_by_all(pc), rows = pc.ntok * G;
             warp_wait(ok, &sh.sums_full[i], (np / kPieces) & 1);
             if (n > 0) {
                 warp_wait(ok, &sh.o_full[i], o_phase >> i & 1);
@@ -828,28 +820,28 @@ bool make_rows(CUtensorMap* m, const AttnArgs& a, int d, int box_heads, int box_
                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// The cache, [pages][page][d], boxes of 64 x (page or `keys`) tokens.
-bool make_cache(CUtensorMap* m, const AttnArgs& a, int d, int keys) {
+// The cache, [pages][page][d], boxes of 64 x (page or kKeys) tokens.
+bool make_cache(CUtensorMap* m, const AttnArgs& a, int d) {
     auto enc = tensor_map_encoder();
     if (!enc) return false;
     cuuint64_t dims[3] = {(cuuint64_t)d, (cuuint64_t)a.page, (cuuint64_t)a.num_pages};
     cuuint64_t strides[2] = {(cuuint64_t)d * 2, (cuuint64_t)a.page * d * 2};
-    cuuint32_t box[3] = {64, (cuuint32_t)(a.page < keys ? a.page : keys), 1};
+    cuuint32_t box[3] = {64, (cuuint32_t)(a.page < kKeys ? a.page : kKeys), 1};
     cuuint32_t es[3] = {1, 1, 1};
     return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(a.k), dims, strides, box, es,
                CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int DR, int RT, int KT>
+template <int DR, int RT>
 cudaError_t launch_t(const AttnArgs& a) {
-    using C = TcCfg<DR, RT, KT>;
+    using C = TcCfg<DR, RT>;
     const int blocks = latent_head_blocks(a.Hq, RT), G = a.Hq / blocks, tok = RT / G;
     int dev = 0;
     const int nsm = device_sms(&dev);
     if (nsm == 0) return cudaErrorNoDevice;
     LatentTcParams p{};
-    p.s = {a.cu_q, a.kv_len, a.N, a.total_q, a.max_q, attn_kv_cap(a), blocks, G, tok, tok, KT, 1, 1, kItemKeys};
+    p.s = {a.cu_q, a.kv_len, a.N, a.total_q, a.max_q, attn_kv_cap(a), blocks, G, tok, tok, kKeys, 1, 1, kItemKeys};
     p.sp = latent_tc_split(a.N, a.total_q, a.max_q, p.s.kv_cap, a.Hq, nsm);
     if (p.sp.ctas && a.ws && a.ws_bytes >= attn_split_bytes(p.sp, kDL)) p.sp.ws = a.ws;
     p.block_table = a.block_table;
@@ -863,8 +855,8 @@ cudaError_t launch_t(const AttnArgs& a) {
     p.c = a.scale * 1.44269504089f;
     p.d_status = a.d_status;
     CUtensorMap mq, mc;
-    if (!make_rows(&mq, a, kDL + DR, G, p.box_q) || !make_cache(&mc, a, kDL + DR, KT)) return cudaErrorInvalidValue;
-    auto kernel = kda_latent_tc_kernel<DR, RT, KT>;
+    if (!make_rows(&mq, a, kDL + DR, G, p.box_q) || !make_cache(&mc, a, kDL + DR)) return cudaErrorInvalidValue;
+    auto kernel = kda_latent_tc_kernel<DR, RT>;
     static std::atomic<uint64_t> ready{0};
     cudaError_t e = allow_shared(kernel, tc_smem<C>(), ready, dev);
     if (e != cudaSuccess) return e;
@@ -901,8 +893,8 @@ cudaError_t launch_latent_tc(const AttnArgs& a) {
     // (against 64 with four and one: 256 requests of 4096 keys x 16 heads 194 us against 202, 64 x 32 heads 66
     // against 69, 3 of 700 x 8 heads 15.7 against 16.4); of 64 above, as a tile's products are bound by
     // its reads from shared memory, the same for 64 rows as for 32.
-    if (latent_tc_rows(a.max_q, a.Hq) == 32) return a.dr ? launch_t<64, 32, 32>(a) : launch_t<0, 32, 32>(a);
-    return a.dr ? launch_t<64, 64, 32>(a) : launch_t<0, 64, 32>(a);
+    if (latent_tc_rows(a.max_q, a.Hq) == 32) return a.dr ? launch_t<64, 32>(a) : launch_t<0, 32>(a);
+    return a.dr ? launch_t<64, 64>(a) : launch_t<0, 64>(a);
 }
 
 }  // namespace kda
