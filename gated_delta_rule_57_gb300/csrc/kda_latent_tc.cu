@@ -875,13 +875,22 @@ AttnSplit latent_tc_split(int N, int total_q, int max_q, long long max_keys, int
     const int rt = latent_tc_rows(max_q, Hq), blocks = latent_head_blocks(Hq, rt), G = Hq / blocks, tok = rt / G;
     // Whole items, given out as CTAs become free, or ranges of one cost. Ranges end together,
     // but cost some 6 us for the parts, their join and more pieces; whole items end up to one
-    // item apart. Measured, ranges against whole, us, 152 SMs: 256 requests of 256 keys x 16 heads
-    // 28/22, of 512 46/37, of 1024 68/60, 608 of 1024 x 32 heads 128/122, 2432 459/446; but 40 of
-    // 1024 x 16 22/29, of 2048 30/50, and with lengths drawn from 1 on 200 of 512 28/30, of 1024
-    // 42/50, 400 of 1024 61/64, 608 of 2048 133/148, of 1024 82/84, of 512 56/51.
+    // item apart. Measured, ranges against whole, us, 152 SMs, one token a request, 16 heads (32 are alike).
+    // Requests of equal length, and of lengths drawn from 1 up to it:
+    //   256 keys, 256 requests         30/22
+    //   512       40, 256, 608         20/18, 46/36, 75/69        20/18, 34/29, 57/49
+    //   1024      40, 152, 400         22/28, 42/37, 95/85        21/28, 33/30, 65/60
+    //   1536      76, 152, 608         41/39, 56/50, 176/170      27/37, 45/43, 107/108
+    //   2048      152, 608, 4864       68/62, 225/220             50/52, 131/135, 873/865
+    //   4096, 8192  608; 1216          406/399; 1546/1538         239/263; 839/896
+    // What a request may have is not what it has, and one long request among many short ones is a chain on
+    // one SM, of 21 ns a key: 1215 to 2048 keys and one of 131072 283/2712, 1216 with logarithms drawn, to 8192
+    // 227/306, to 32768 673/1007. So beyond 2048 keys whole items need so many that this chain
+    // is short against them (5 us each and more): 20000 to 300 keys in tables of 2048 1355/1050, 4864 to
+    // 2048 above; 3000 to 300 in tables of 32768, 171/160, are ranges.
     const long long items = (long long)total_q / (max_q < tok ? max_q : tok) * blocks;  // at least
     if (max_keys <= KDA_LATENT_SHORT_KEYS || (max_keys <= 512 && 2 * items >= nsm)) return sp;
-    if (items >= (max_keys < 2048 ? max_keys / 256 : 8) * nsm) return sp;
+    if ((max_keys < 2048 && items >= nsm) || items >= max_keys / 64 * nsm) return sp;
     sp.ctas = nsm;
     sp.least = 128;  // keys of a range: 3 requests to 700 keys x 8 heads 17.3 us, with 256 20.3, with 64 17.9
     sp.rows = ((max_q < tok ? max_q : tok) * G + 3) & ~3;  // whole 16-byte vectors
