@@ -297,11 +297,12 @@ cudaError_t launch_attn_tc(const AttnArgs& a);    // bf16
 cudaError_t launch_attn_simt(const AttnArgs& a);  // fp32
 
 // How a call on `nsm` SMs divides a kernel's work: CTAs and rows of a slot of its
-// split form, or ctas = 0 for whole items. max_keys: no request has more keys.
-AttnSplit attn_tc_split(int N, int total_q, int max_q, long long max_keys, bool prompt, int Hq,
-                        int Hkv, int nsm);
-AttnSplit attn_simt_split(int N, int total_q, int max_q, long long max_keys, bool prompt, int Hq,
-                          int Hkv, int nsm);
+// split form, or ctas = 0 for whole items. max_keys: no request has more keys; shared: some key
+// channels are all heads'.
+AttnSplit attn_tc_split(int N, int total_q, int max_q, long long max_keys, bool prompt, bool shared,
+                        int Hq, int Hkv, int nsm);
+AttnSplit attn_simt_split(int N, int total_q, int max_q, long long max_keys, bool prompt, bool shared,
+                          int Hq, int Hkv, int nsm);
 
 // Latent attention: every head's keys are the cached rows, 512 latent channels and dr
 // shared ones, its values the latent channels. k: the cache. Heads beyond a row tile are

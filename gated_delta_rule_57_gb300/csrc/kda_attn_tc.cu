@@ -1321,8 +1321,8 @@ cudaError_t launch_t(const AttnArgs& a) {
     p.s = {a.cu_q, a.kv_len, a.N, a.total_q, a.max_q,
            attn_kv_cap(a), a.Hkv, G, tok1, 2 * tok1,
            kTile, kCostSingle, kCostPair, kItemKeys};
-    p.sp = attn_tc_split(a.N, a.total_q, a.max_q, a.kv_len ? p.s.kv_cap : a.max_q, !a.kv_len, a.Hq,
-                         a.Hkv, nsm);
+    p.sp = attn_tc_split(a.N, a.total_q, a.max_q, a.kv_len ? p.s.kv_cap : a.max_q, !a.kv_len, DQ > D,
+                         a.Hq, a.Hkv, nsm);
     if (p.sp.ctas && a.ws && a.ws_bytes >= attn_split_bytes(p.sp, D)) p.sp.ws = a.ws;
     p.block_table = a.block_table;
     p.v = static_cast<const __nv_bfloat16*>(a.v);
@@ -1369,24 +1369,29 @@ cudaError_t launch_t(const AttnArgs& a) {
 
 // Whole items or ranges. Ranges balance any lengths, but cost a second launch,
 // the parts' stores and a longer start: about 10 us over single tokens, 25 us over
-// pairs of row tiles (18 of their key tiles). Measured, ranges against whole items, us
-// (32 / 8 heads, one H = Hkv otherwise):
-//                                        d = 128       d = 64
-//   one token, 1 x 1024                    16/12        15/10
-//     1 x 2048, 1 x 4096              18/17, 21/27  17/14, 20/23
-//     16 x 2048, 64 x 2048            35/27, 92/85  22/15, 56/53
-//     lengths to 8192, 32 requests        96/111        58/77
-//     256 requests                       613/610      325/329
-//   prompts, 2048, 4 x 2048         53/39, 135/108 41/32, 107/87
-//     8192                               337/309      288/264
-//     H = 2, 2048, 8192             34/28, 105/113  26/25, 90/99
-//     H = 1, 4096, 8192              38/48, 67/86   30/43, 57/80
-//     H = 1, 16384                       177/207      152/190
-//   512 new tokens over 32768            193/319      144/299
-//   2 x 4096 over 16384                1079/1114      901/896
-// The rule is within 1 % of the better side at both d, but for H = 2, 8192.
-AttnSplit attn_tc_split(int N, int total_q, int max_q, long long max_keys, bool prompt, int Hq,
-                        int Hkv, int nsm) {
+// pairs of row tiles, and with one issuing warp a tile takes a quarter longer in them. Measured,
+// ranges against whole items, us (Hq / Hkv heads; 32 / 8 where none are given):
+//                                             d = 128      d = 64
+//   one token, 1 x 1024                         16/12       17/12
+//     1 x 2048, 1 x 4096                  18/17, 21/28  19/16, 22/24
+//     16 x 2048, 64 x 2048                36/27, 94/86  23/15, 57/54
+//     lengths to 8192, 32 requests                92/95       56/64
+//     256 requests                              606/588     322/322
+//   prompts, 2048, 4 x 2048              55/31, 141/106 45/27, 117/86
+//     8192                                      340/311     293/265
+//     8 / 2, 4096, 8192                    51/48, 109/88  43/45, 95/82
+//     4 / 1, 3000, 4096, 8192     35/40, 42/49, 70/87  27/34, 31/44, 58/80
+//     4 / 4, 8192, 12288, 16384 72/87, 120/127, 186/170  60/80, 102/116, 155/152
+//     5 / 5, 8192, 12288                  96/102, 167/129  68/80, 119/116
+//     6 / 6, 4096, 8192, 12288    48/49, 93/89, 166/135  38/44, 79/80, 136/116
+//     2 / 2, 8192 alone, with 3000 and 500    50/87, 54/86  39/80, 43/80
+//   512 new tokens over 32768                   195/323     148/304
+//   2 x 4096 over 16384                       1145/1125     913/917
+// The rule is within 5 % of the better side of these. With shared key channels (192 of them, two issuing
+// warps) there is no such quarter: 6 heads x 8192 132/147, 8 x 4096 67/77, 7 x 8192 149/148, 8 x 8192
+// 166/148, 4 x 16384 284/284, 6 x 12288 248/217.
+AttnSplit attn_tc_split(int N, int total_q, int max_q, long long max_keys, bool prompt, bool shared,
+                        int Hq, int Hkv, int nsm) {
     AttnSplit sp{};
     if (N == 0 || total_q == 0 || max_q == 0 || Hkv == 0 || nsm == 0) return sp;
     const int G = Hq / Hkv, tok1 = kTile / G;
@@ -1394,9 +1399,9 @@ AttnSplit attn_tc_split(int N, int total_q, int max_q, long long max_keys, bool 
     const long long items = (long long)total_q / (2 * tok1) * Hkv;
     if (max_q > tok1) {
         // Prompts: half the longest item is the mean one. Whole unless the longest
-        // passes an even share of all of them by more than what ranges cost.
-        const long long longest = (max_keys + kTile - 1) / kTile;
-        if (prompt ? longest - longest * items / (2 * nsm) <= 18 : items >= 8LL * nsm) return sp;
+        // passes an even share of all of them by more than what ranges cost, 17 tiles.
+        const long long longest = (max_keys + kTile - 1) / kTile, share = longest * items / (2 * nsm);
+        if (prompt ? longest - share - (shared ? 0 : share / 4) <= 17 : items >= 8LL * nsm) return sp;
     }
     sp.ctas = nsm;
     sp.least = 2 * kCostPair * kTile;
