@@ -266,7 +266,8 @@ __device__ __forceinline__ AttnWalk attn_walk_at(const AttnShape& s, const long 
 // Partial results of split items in the workspace: slot 2 c holds the part of
 // CTA c's range that starts where the range does, slot 2 c + 1 the one that
 // ends where it does. Per slot: rows x d outputs (each the softmax over its
-// part), then rows log-sums in base 2. After the slots, one AttnCut per CTA.
+// part), then rows log-sums in base 2: -Inf where a row sees no key of the part (or, but for latents,
+// has no weight in it). After the slots, one AttnCut per CTA.
 struct AttnSplit {
     float* ws;      // null: whole items
     int ctas;       // CTAs the tiles are divided among
@@ -281,6 +282,8 @@ struct AttnCut {
     int h, tile, n;  // key head; the tile's number in the item; tiles of the item
     int cost;        // of a tile
 };
+// Latents: the log-sum where a row sees keys of a part, but all their scores are -Inf.
+constexpr float kAttnNoWeight = -3.4028234663852886e38f;
 inline __host__ __device__ size_t attn_slot_floats(int rows, int d) { return (size_t)rows * (d + 1); }
 inline __host__ __device__ AttnCut* attn_cuts(const AttnSplit& sp, int d) {
     return reinterpret_cast<AttnCut*>(sp.ws + 2 * (size_t)sp.ctas * attn_slot_floats(sp.rows, d));

@@ -91,10 +91,9 @@ __global__ void __launch_bounds__(kCombineWarps * 32)
 }
 
 // The same for wide rows (D = 512), M and the weights first, so that no part's load waits for
-// another's. Every part counts, with a weight that underflowed to 0 too, and with one of 0 where a
-// row's scores are all -Inf: what is not finite in it stays, as 0 x NaN. (Where a row sees no key of
-// a part, the part holds zeros.) A row without weight in any part is zeros. The parts of an item,
-// where the workspace has them.
+// another's. Every part of which a row sees keys counts, with a weight that underflowed to 0 too, and
+// with one of 0 where its scores are all -Inf: what is not finite in it stays, as 0 x NaN. A row
+// without weight in any part is zeros. The parts of an item, where the workspace has them.
 template <int D>
 struct Parts {
     const AttnSplit& sp;
@@ -115,10 +114,10 @@ struct Parts {
         for (int k = 16; k > 0; k >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, k));
         return m;
     }
-    // A part's weight, 0 for one without scores above -Inf. NaN stays.
+    // A part's weight; below 0 for one of which the row sees no key. NaN stays.
     __device__ __forceinline__ float weight(int c, int row, float m) const {
         const float x = sum_of(c, row);
-        return x == -INFINITY ? 0.f : exp2f(x - m);
+        return x == -INFINITY ? -1.f : x == kAttnNoWeight ? 0.f : exp2f(x - m);
     }
 };
 __device__ __forceinline__ void add(float4& acc, float w, const float* y) {
@@ -184,6 +183,7 @@ __global__ void __launch_bounds__(kCombineWarps * 32, 4)
 #pragma unroll 2
             for (int k = 0; k <= c1 - c0; k++) {
                 const float wk = __shfl_sync(0xffffffffu, w, k);
+                if (wk < 0.f) continue;
                 sum += wk;
 #pragma unroll
                 for (int q = 0; q < Q; q++) add(acc[q], wk, parts.at(c0 + k) + (size_t)row * D + 128 * q + lane * 4);
@@ -202,9 +202,10 @@ __global__ void __launch_bounds__(kCombineWarps * 32, 4)
             for (int cb = c0 + warp; cb <= c1; cb += 32 * kCombineWarps) {
                 const int n = min((c1 - cb) / kCombineWarps + 1, 32);  // parts cb, cb + 8, ...
                 const float w = lane < n ? parts.weight(cb + kCombineWarps * lane, row, m) : 0.f;
-#pragma unroll 8
+#pragma unroll 4  // (8: registers spill)
                 for (int k = 0; k < n; k++) {
                     const float wk = __shfl_sync(0xffffffffu, w, k);
+                    if (wk < 0.f) continue;
                     sum += wk;
                     add(acc, wk, parts.at(cb + kCombineWarps * k) + (size_t)row * D + col);
                 }

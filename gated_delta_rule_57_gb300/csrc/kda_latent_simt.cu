@@ -302,7 +302,9 @@ __global__ void __launch_bounds__(kThreads, 1) kda_latent_simt_kernel(const Late
             s_corr[row1] = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);  // NaN stays
             if (row1 < rows) {
                 const size_t at = (first + row1 / G) * s.Hkv * G + it.h * G + row1 % G;
-                if (dst) dst[(size_t)p.sp.rows * kDL + row1] = l == 0.f ? -INFINITY : m + log2f(l);
+                if (dst)
+                    dst[(size_t)p.sp.rows * kDL + row1] =
+                        l != 0.f ? m + log2f(l) : key0 < s_lim[row1] ? kAttnNoWeight : -INFINITY;
                 else if (p.lse) p.lse[at] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.69314718056f;
             }
         }

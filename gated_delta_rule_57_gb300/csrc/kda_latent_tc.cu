@@ -689,7 +689,7 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
             if (live) {
                 if (pc.slot >= 0)
                     p.sp.ws[attn_slot_floats(p.sp.rows, kDL) * pc.slot + (size_t)p.sp.rows * kDL + row] =
-                        l == 0.f ? -INFINITY : m + log2f(l);
+                        l != 0.f ? m + log2f(l) : pc.kt0 * kKeys < lim ? kAttnNoWeight : -INFINITY;
                 else if (p.lse)
                     p.lse[(size_t)pc.tok0 * Hq + (size_t)pc.h * G + sh.row_at[row]] =
                         l == 0.f ? -INFINITY : (m + log2f(l)) * 0.69314718056f;
