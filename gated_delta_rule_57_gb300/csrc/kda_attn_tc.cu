@@ -90,8 +90,9 @@ struct TcCfg {
     // Issuing warps: one for both groups, in a fixed order, or one for each. What such a warp
     // does between two products shows as idle tensor core unless the other's run, but the
     // order keeps the groups half a step apart. Measured, one against two, us (32 heads): DQ = 192,
-    // 4 prompts of 8192 1800/1614, 24 ragged 490/460; DQ = D = 128 (8 key heads), 8 of 8192 2461/2633,
-    // ragged 318/370, a mixed step over pages 463/521.
+    // 4 prompts of 8192 1800/1614, 24 ragged 490/460; DQ = D = 128 (8 key heads), 8 of 8192 2465/2855,
+    // ragged 318/370, a mixed step over pages 463/521; with 32 key heads, 4 of 8192 1327/1643, 24
+    // ragged 1083/1258.
     static constexpr bool TWO_ISSUE = DR > 0;
     static constexpr int TILES = 2 * Q_BYTES + STAGES * TILE_BYTES + 2 * SHARED_BYTES;
 };

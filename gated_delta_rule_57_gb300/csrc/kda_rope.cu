@@ -17,9 +17,10 @@
 // way. The token's work is laid out as items of two 16-byte vectors, a few for each of its
 // threads (with one vector where pairs are neighbours, the latents below took 180 us).
 //
-// Bound by HBM: every byte is read and written once. Measured in bf16: 65536 tokens of 32 query
-// and 8 key heads of 128 channels 240 us, 6.7 TB/s; 65536 latents with 32 query heads 118 us, 5.9 TB/s;
-// 256 tokens 4.9 and 4.3 us, the latency of a launch, a load, the angles and a store.
+// Bound by HBM: every byte is read and written once. Measured in bf16, calls one after another from a
+// graph, with outputs made beforehand: 65536 tokens of 32 query and 8 key heads of 128 channels 237 us,
+// 6.8 TB/s; 65536 latents with 32 query heads, expanded, 115 us, 6.0 TB/s; 256 tokens 3.1 and 2.7 us, the
+// latency of a launch, a load, the angles and a store.
 #include "kda_host.cuh"
 #include "kda_internal.cuh"
 
@@ -240,9 +241,10 @@ cudaError_t launch_rope(RopeParams& p, kda_dtype_t io, cudaStream_t stream) {
     p.v_half = p.Hv * p.v_vec / 2;  // (v_vec is even)
     const int work = (p.Hq + p.Hk) * p.items + p.v_half;
     // Threads of a token: as few as two batches of items each allow, and more while the
-    // call has too few tokens for two CTAs an SM. Measured with 32, 64, 128, 256, us: 65536 tokens of
-    // 32 + 8 + 8 heads 238/236/240/307, of 8 + 1 + 1 heads 62/84/126/206, latents with 32 query heads
-    // 106/113/152/230; 256 tokens 7.7/5.2/4.5/4.5, 4.6/4.1/3.9/3.7, 5.3/4.2/4.1/3.7.
+    // call has too few tokens for two CTAs an SM. Measured as above with 32, 64, 128, 256, us: 65536 tokens
+    // of 32 + 8 + 8 heads 238/236/240/318, of 8 + 1 + 1 heads 68/89/132/223, latents with 32 query heads
+    // 115/131/174/244 (absorbed 115/130/173/242); 256 tokens 6.6/4.3/3.2/3.2, 3.6/2.9/2.7/2.6,
+    // 4.4/3.4/3.1/2.7.
     int dev = 0;
     const long long fill = 2LL * device_sms(&dev) * kRopeThreads;
     p.tpt_log2 = 5;

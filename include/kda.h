@@ -531,7 +531,8 @@ kda_status_t kda_kv_append(const void* k, const void* v, const int* slot_map, vo
  *   max_len    : no prompt is longer; one that is, or a cu_seqlens that
  *                decreases or passes total, sets KDA_DEV_LENGTH and that
  *                prompt's rows are not written, nor those of a prompt that then
- *                starts inside the second one before it
+ *                starts inside the second one before it (rows that two prompts
+ *                share in another way hold either's)
  *   scale      : positive and finite
  *   workspace, ws_bytes : see kda_attn_workspace_size
  *
