@@ -28,11 +28,11 @@
 // rows of keys past the item's last (stale slots) whole; of the keys that only some rows
 // see the values that are not finite. Those are noted and added to the rows that see them.
 //
-// What bounds it. Few rows: HBM. 256 single tokens of 32 heads over 1.06 M cached tokens take 206 us,
-// 5.9 TB/s (87 % of a copy's rate; some 15 us are the start, the parts and their join). Full
+// What bounds it. Few rows: HBM. 256 single tokens of 32 heads over 1.06 M cached tokens take 201 us,
+// 6.1 TB/s (90 % of a copy's rate; some 15 us are the start, the parts and their join). Full
 // tiles: the products, whose operands come out of shared memory. An MMA of 64 x 32 takes 30 clocks, one of
 // 128 x 64 49, so a tile of 64 rows and 32 keys 36 x 30 + 8 x 49 = 1470, which is 880 TFLOP/s;
-// 2 x 4 draft tokens of 32 heads over 262147 keys take 178 us, 820 TFLOP/s with the join. Tiles of 64 keys
+// 2 x 4 draft tokens of 32 heads over 262147 keys take 171 us, 850 TFLOP/s with the join. Tiles of 64 keys
 // would take 2080 clocks for twice the keys, but only two of them fit beside 64 rows, and
 // their loads are then waited for (202 us against 182 at the time). 16 heads fill half of a tile's 32 rows,
 // which costs nothing while HBM is the bound.
