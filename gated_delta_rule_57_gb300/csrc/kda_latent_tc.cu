@@ -885,12 +885,13 @@ AttnSplit latent_tc_split(int N, int total_q, int max_q, long long max_keys, int
     //   4096, 8192  608; 1216          406/399; 1546/1538         239/263; 839/896
     // What a request may have is not what it has, and one long request among many short ones is a chain on
     // one SM, of 21 ns a key: 1215 to 2048 keys and one of 131072 283/2712, 1216 with logarithms drawn, to 8192
-    // 227/306, to 32768 673/1007. So beyond 2048 keys whole items need so many that this chain
-    // is short against them (5 us each and more): 20000 to 300 keys in tables of 2048 1355/1050, 4864 to
-    // 2048 above; 3000 to 300 in tables of 32768, 171/160, are ranges.
+    // 227/306, to 32768 673/1007. So beyond 2048 keys whole items need so many that this chain is at most
+    // half as long as they take (5 us each and more): 20000 to 300 keys in tables of 2048 1355/1050, 256 of 67
+    // heads (17152 items) to 8192 11605/9376; 4864 to 8192, logarithms drawn, 864/884 and 3000 to 300 in tables
+    // of 32768, 171/160, are ranges.
     const long long items = (long long)total_q / (max_q < tok ? max_q : tok) * blocks;  // at least
     if (max_keys <= KDA_LATENT_SHORT_KEYS || (max_keys <= 512 && 2 * items >= nsm)) return sp;
-    if ((max_keys < 2048 && items >= nsm) || items >= max_keys / 64 * nsm) return sp;
+    if ((max_keys < 2048 && items >= nsm) || items >= max_keys / 128 * nsm) return sp;
     sp.ctas = nsm;
     sp.least = 128;  // keys of a range: 3 requests to 700 keys x 8 heads 17.3 us, with 256 20.3, with 64 17.9
     sp.rows = ((max_q < tok ? max_q : tok) * G + 3) & ~3;  // whole 16-byte vectors
