@@ -241,11 +241,13 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
     if (tid < RT) sh.row_at[tid] = tid / G * Hq + tid % G;
     tc_fence_before();
     pdl_wait();
-    pdl_launch();  // the join's CTAs may take their places and wait
     // Cost of this CTA's range (split items); also the barrier after the setup.
     long long each = 0;
     if (p.sp.ws) each = attn_cost_each<kThreadsTc>(p.s, p.sp.ctas, p.sp.least, groups, sh.sum);
     __syncthreads();
+    // The join's CTAs may take their places and wait. (Not before this CTA has its tensor memory: a kernel that
+    // took some and waited for this one could hold what this one needs.)
+    pdl_launch();
     tc_fence_after();
     const uint32_t tbase = sh.tmem;
     int flags = 0;
