@@ -145,9 +145,9 @@ __device__ __forceinline__ int put(T* dst, float4 acc, float inv) {
 
 // Few parts: a warp takes a row. Many (more than kFewParts): a CTA takes 128 channels of a row, its
 // warps every eighth part each, added up in their order. Bound by the latency of a row's loads, first
-// the sums, then the parts. Measured with the attention before it: 76 parts (2 x 4 drafts over 262 k tokens)
-// 182 us, with a warp a row 187 and through the kernel above 206; 1 request of 65536 keys x 64 heads
-// 33 against 57; 5 parts (3 requests to 700 keys) 18.5 us, shared by a CTA's warps 25.
+// the sums, then the parts. Measured with the attention before it, when chosen: 76 parts (2 x 4 drafts over
+// 262 k tokens) 182 us, with a warp a row 187 and through the kernel above 206; 1 request of 65536 keys x 64
+// heads 33 against 57; 5 parts (3 requests to 700 keys) 18.5 us, shared by a CTA's warps 25. Now 171, 33 and 15.3.
 constexpr int kFewParts = 16;
 
 template <typename T, int D>

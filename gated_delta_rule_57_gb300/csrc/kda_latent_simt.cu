@@ -16,7 +16,7 @@
 //
 // Bound by shared memory and the FMA pipes alike: 20 loads of 16 bytes a lane take 80 clocks of its 128
 // bytes a clock, 256 multiply-adds 64 clocks. A mixed step of 9 requests to 2049 keys (two chunks of 33
-// tokens among single ones, 8 heads) takes 57 us, 25 TFLOP/s of 74; with 4 x 4 scores a thread (8 loads for 64,
+// tokens among single ones, 8 heads) takes 55 us, 26 TFLOP/s of 74; with 4 x 4 scores a thread (8 loads for 64,
 // four lanes adding up, every lane's exponentials four times) 68. Warps whose rows are not there leave the pipes to
 // the others: 64 requests of 2048 keys x 16 heads 142 us, 213 without.
 #include <algorithm>
